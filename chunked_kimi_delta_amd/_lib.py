@@ -32,6 +32,23 @@ class KdaFwdArgs(ctypes.Structure):
     ]
 
 
+class GdnArgs(ctypes.Structure):
+    """Mirror of gdn_args (include/gdn.h)."""
+    _fields_ = [
+        ("B", ctypes.c_int32), ("T", ctypes.c_int32), ("N", ctypes.c_int32),
+        ("H", ctypes.c_int32), ("HV", ctypes.c_int32), ("K", ctypes.c_int32),
+        ("V", ctypes.c_int32), ("io", ctypes.c_int32),
+        ("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+        ("g", ctypes.c_void_p), ("beta", ctypes.c_void_p),
+        ("scale", ctypes.c_float),
+        ("cu_seqlens", ctypes.c_void_p), ("initial_state", ctypes.c_void_p),
+        ("o", ctypes.c_void_p), ("final_state", ctypes.c_void_p),
+        ("qk_l2norm", ctypes.c_int32), ("beta_sigmoid", ctypes.c_int32),
+        ("gate", ctypes.c_int32), ("gate_lower_bound", ctypes.c_float),
+        ("A_log", ctypes.c_void_p), ("dt_bias", ctypes.c_void_p),
+    ]
+
+
 def library_path() -> str:
     return os.environ.get("KDA_FWD_LIB", os.path.join(HERE, LIB_NAME))
 
@@ -66,6 +83,17 @@ def load():
     lib.kda_bwd.argtypes = ([ctypes.POINTER(KdaFwdArgs), ctypes.c_void_p, ctypes.c_void_p,
                              ctypes.c_void_p, ctypes.c_size_t] + [ctypes.c_void_p] * 9)
     lib.kda_bwd.restype = ctypes.c_int
+    gdn, ptr = ctypes.POINTER(GdnArgs), ctypes.c_void_p
+    lib.gdn_fwd_workspace_bytes.argtypes = [gdn]
+    lib.gdn_fwd_workspace_bytes.restype = ctypes.c_size_t
+    lib.gdn_fwd.argtypes = [gdn, ptr, ctypes.c_size_t, ptr]
+    lib.gdn_fwd.restype = ctypes.c_int
+    lib.gdn_step.argtypes = [gdn, ptr, ptr, ctypes.c_int32, ptr]
+    lib.gdn_step.restype = ctypes.c_int
+    lib.act8_pack.argtypes = [ptr, ctypes.c_int32, ctypes.c_int64, ctypes.c_int32, ptr, ptr, ptr]
+    lib.act8_pack.restype = ctypes.c_int
+    lib.act8_unpack.argtypes = [ptr, ptr, ctypes.c_int32, ctypes.c_int64, ctypes.c_int32, ptr, ptr]
+    lib.act8_unpack.restype = ctypes.c_int
     lib.kda_strerror.argtypes = [ctypes.c_int]
     lib.kda_strerror.restype = ctypes.c_char_p
     lib.kda_version.argtypes = []

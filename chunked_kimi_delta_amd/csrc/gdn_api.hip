@@ -1,0 +1,212 @@
+// gdn_api.hip -- the extern "C" boundary of the gated delta rule (include/gdn.h): argument
+// checks, workspace layout and the launches on the caller's stream. Host side only.
+#include <math.h>
+
+#include "gdn.h"
+#include "gdn_internal.h"
+
+namespace {
+
+using namespace gdn;
+
+bool aligned(const void *p, uintptr_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
+size_t align256(size_t x) { return (x + 255) / 256 * 256; }
+
+kda_status check_shapes(const gdn_args *a)
+{
+    if (!a) return KDA_ERR_INVALID_ARG;
+    if (a->B < 1 || a->T < 0 || a->N < 0 || a->H < 1 || a->HV < 1 || a->HV % a->H)
+        return KDA_ERR_INVALID_ARG;
+    if (a->cu_seqlens) {
+        if (a->B != 1 || a->N < 1) return KDA_ERR_INVALID_ARG;
+    } else if (a->N != a->B) {
+        return KDA_ERR_INVALID_ARG;
+    }
+    if ((a->K != 64 && a->K != 128) || (a->V != 64 && a->V != 128)) return KDA_ERR_UNSUPPORTED;
+    if (a->io != KDA_BF16 && a->io != KDA_FP32) return KDA_ERR_UNSUPPORTED;
+    // grid sizes, and 32-bit offsets inside the 64 rows of a chunk
+    const int64_t tt = (int64_t)a->B * a->T;
+    if (a->HV > 32768 || (int64_t)a->N * a->HV > INT32_MAX || tt / CT + a->N > INT32_MAX)
+        return KDA_ERR_UNSUPPORTED;
+    return KDA_OK;
+}
+
+kda_status check_pre(const gdn_args *a)
+{
+    if (a->gate != KDA_GATE_NONE && a->gate != KDA_GATE_SOFTPLUS && a->gate != KDA_GATE_BOUNDED)
+        return KDA_ERR_UNSUPPORTED;
+    if (a->gate == KDA_GATE_NONE) return KDA_OK;
+    if (!a->A_log || !aligned(a->A_log, 4) || !aligned(a->dt_bias, 4)) return KDA_ERR_INVALID_ARG;
+    if (a->gate == KDA_GATE_BOUNDED &&
+        !(a->gate_lower_bound < 0.f && a->gate_lower_bound > -INFINITY))
+        return KDA_ERR_INVALID_ARG;
+    return KDA_OK;
+}
+
+Pre pre_of(const gdn_args *a)
+{
+    return Pre{a->qk_l2norm != 0, a->beta_sigmoid != 0, a->gate, a->gate_lower_bound, a->A_log,
+               a->dt_bias};
+}
+
+float scale_of(const gdn_args *a)
+{
+    return a->scale > 0.f && !isnan(a->scale) ? a->scale : 1.0f / sqrtf((float)a->K);
+}
+
+// A dense batch of short sequences takes the recurrence: a chunk has a fixed cost of 64 tokens.
+bool recurrent(const gdn_args *a) { return !a->cu_seqlens && a->T <= 16; }
+
+struct Layout {                     // byte offsets in the workspace
+    int64_t tt, slots;
+    size_t q, k, total;             // three bf16 planes each of q and k (fp32 io)
+};
+
+Layout layout(const gdn_args *a)
+{
+    Layout L = {};
+    L.tt = (int64_t)a->B * a->T;
+    L.slots = L.tt / CT + a->N;
+    const bool f32 = a->io == KDA_FP32;
+    L.q = (size_t)L.slots * a->HV * (f32 ? Rec<3>::BYTES : Rec<2>::BYTES);
+    const size_t planes = f32 ? align256((size_t)L.tt * a->H * a->K * 6) : 0;
+    L.k = L.q + planes;
+    L.total = L.k + planes;
+    return L;
+}
+
+template <class F>
+hipError_t by_dims(int K, int V, F f)
+{
+    using std::integral_constant;
+    if (K == 64)
+        return V == 64 ? f(integral_constant<int, 64>(), integral_constant<int, 64>())
+                       : f(integral_constant<int, 64>(), integral_constant<int, 128>());
+    return V == 64 ? f(integral_constant<int, 128>(), integral_constant<int, 64>())
+                   : f(integral_constant<int, 128>(), integral_constant<int, 128>());
+}
+
+kda_status run_recurrent(const gdn_args *a, const float *h0, float *ht, const int32_t *index,
+                         int32_t slots, hipStream_t st)
+{
+    // rows are the grid's second dimension
+    StepParams p = {};
+    p.T = a->T;
+    p.H = a->H;
+    p.HV = a->HV;
+    p.G = a->HV / a->H;
+    p.scale = scale_of(a);
+    p.pre = pre_of(a);
+    const int64_t e = a->io == KDA_FP32 ? 4 : 2;
+    for (int b = 0; b < a->N; b += 65535) {
+        const int64_t tok = (int64_t)b * a->T, state = (int64_t)b * a->HV * a->K * a->V;
+        p.B = a->N - b < 65535 ? a->N - b : 65535;
+        p.q = (const uint8_t *)a->q + tok * a->H * a->K * e;
+        p.k = (const uint8_t *)a->k + tok * a->H * a->K * e;
+        p.v = (const uint8_t *)a->v + tok * a->HV * a->V * e;
+        p.g = (const uint8_t *)a->g + tok * a->HV * e;
+        p.beta = (const uint8_t *)a->beta + tok * a->HV * e;
+        p.o = (uint8_t *)a->o + tok * a->HV * a->V * e;
+        p.index = index ? index + b : nullptr;
+        p.h0 = h0 && !index ? h0 + state : h0;
+        p.ht = ht && !index ? ht + state : ht;
+        p.slots = index ? slots : p.B;
+        const hipError_t er = by_dims(a->K, a->V, [&](auto k, auto v) {
+            return launch_recurrent<decltype(k)::value, decltype(v)::value>(p, a->io == KDA_FP32, st);
+        });
+        if (er != hipSuccess) return KDA_ERR_HIP;
+    }
+    return KDA_OK;
+}
+
+kda_status check_tensors(const gdn_args *a)
+{
+    const void *ptrs[] = {a->q, a->k, a->v, a->g, a->beta, a->o};
+    if ((int64_t)a->B * a->T > 0)
+        for (const void *p : ptrs)
+            if (!p || !aligned(p, 16)) return KDA_ERR_INVALID_ARG;
+    const void *opt[] = {a->initial_state, a->final_state, a->cu_seqlens};
+    for (const void *p : opt)
+        if (!aligned(p, 16)) return KDA_ERR_INVALID_ARG;
+    return check_pre(a);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t gdn_fwd_workspace_bytes(const gdn_args *a)
+{
+    if (check_shapes(a) != KDA_OK || recurrent(a)) return 0;
+    return layout(a).total;
+}
+
+kda_status gdn_fwd(const gdn_args *a, void *workspace, size_t ws_bytes, void *stream)
+{
+    kda_status st = check_shapes(a);
+    if (st != KDA_OK) return st;
+    if ((st = check_tensors(a)) != KDA_OK) return st;
+    hipStream_t hs = (hipStream_t)stream;
+    if (recurrent(a)) {
+        if (a->N == 0) return KDA_OK;
+        return run_recurrent(a, a->initial_state, a->final_state, nullptr, 0, hs);
+    }
+    const Layout L = layout(a);
+    if (L.tt > 0 && (!workspace || ws_bytes < L.total || !aligned(workspace, 256)))
+        return KDA_ERR_WORKSPACE;
+    uint8_t *const ws = (uint8_t *)workspace;
+    const bool f32 = a->io == KDA_FP32;
+    Params p = {};
+    p.seq.cu = a->cu_seqlens;
+    p.seq.T = a->T;
+    p.seq.T_total = L.tt;
+    p.seq.N = a->N;
+    p.seq.n_slots = (int32_t)L.slots;
+    p.H = a->H;
+    p.HV = a->HV;
+    p.G = a->HV / a->H;
+    p.scale = scale_of(a);
+    p.g = a->g;
+    p.beta = a->beta;
+    p.h0 = a->initial_state;
+    p.o = a->o;
+    p.ht = a->final_state;
+    p.rec = ws;
+    p.pre = pre_of(a);
+    p.v = a->v;
+    p.q[0] = (const uint16_t *)a->q;
+    p.k[0] = (const uint16_t *)a->k;
+    if (f32 && L.tt > 0) {
+        const int64_t n = L.tt * a->H * a->K;
+        if (launch_split_planes((const float *)a->q, n, (uint16_t *)(ws + L.q), hs) != hipSuccess ||
+            launch_split_planes((const float *)a->k, n, (uint16_t *)(ws + L.k), hs) != hipSuccess)
+            return KDA_ERR_HIP;
+        for (int i = 0; i < 3; ++i) {
+            p.q[i] = (const uint16_t *)(ws + L.q) + i * n;
+            p.k[i] = (const uint16_t *)(ws + L.k) + i * n;
+        }
+    }
+    if (L.tt > 0) {
+        const hipError_t e = a->K == 64 ? launch_prepare<64>(p, f32, hs) : launch_prepare<128>(p, f32, hs);
+        if (e != hipSuccess) return KDA_ERR_HIP;
+    }
+    const hipError_t e = by_dims(a->K, a->V, [&](auto k, auto v) {
+        return launch_state<decltype(k)::value, decltype(v)::value>(p, f32, hs);
+    });
+    return e == hipSuccess ? KDA_OK : KDA_ERR_HIP;
+}
+
+kda_status gdn_step(const gdn_args *a, float *state, const int32_t *state_indices, int32_t slots,
+                    void *stream)
+{
+    kda_status st = check_shapes(a);
+    if (st != KDA_OK) return st;
+    if (a->cu_seqlens || slots < 0 || (!state_indices && slots < a->B)) return KDA_ERR_INVALID_ARG;
+    if ((st = check_tensors(a)) != KDA_OK) return st;
+    if (a->T == 0) return KDA_OK;
+    if ((slots > 0 && !state) || !aligned(state, 16) || !aligned(state_indices, 4))
+        return KDA_ERR_INVALID_ARG;
+    return run_recurrent(a, state, state, state_indices, slots, (hipStream_t)stream);
+}
+
+}  // extern "C"

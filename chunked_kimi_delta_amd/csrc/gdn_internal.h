@@ -1,0 +1,216 @@
+// gdn_internal.h -- device-side building blocks of the gated delta rule (one decay per token
+// and value head) on gfx950. Lane layouts are those of kda_internal.h.
+//
+// A sequence is cut into chunks of 64 tokens (four 16-token tiles). With Gam the in-chunk
+// cumsum of g, gam its last value, D_ij = e^{Gam_i - Gam_j} and S the state at the chunk's
+// start, a chunk is
+//     R = V - e^Gam . (K S)                         e = A R,  A = (I + L)^-1,
+//     o = scale e^Gam . (Q S) + M e                 L_ij = D_ij beta_j k_i.k_j   (i > j)
+//     S <- e^gam S + K^T (beta e^{gam - Gam} . e)   M_ij = scale D_ij beta_j q_i.k_j  (i >= j)
+// where e_t is the residual v_t - S_{t-1}^T k_t of the token recurrence itself (beta enters
+// after it). With one decay per token every decay is a scalar of a row: K, Q and V enter the
+// matrix products as they are stored, and the decays, beta and the L2-norm factors are row
+// scales of the products' results.
+//
+// Operands with more than 8 significant bits (S, R, e, A, M, fp32 inputs) are split into bf16
+// parts, x = x0 + x1 (+ x2), and a product takes the pairs i + j < parts: two parts hold 17 bits
+// (bf16 io), three hold 24 (fp32 io, whose q and k come as three planes). So an fp32 state is an
+// fp32-class result for either io type.
+#pragma once
+
+#include "kda_internal.h"
+
+namespace gdn {
+
+using kda::bf16x8;
+using kda::f32x4;
+using kda::mfma32;
+using kda::SeqGeom;
+using kda::zero4;
+
+constexpr int CT = 64;                  // tokens per chunk
+
+struct Pre {
+    int32_t qk_l2norm, beta_sigmoid, gate;
+    float lower_bound;
+    const float *A_log, *dt_bias;       // [HV] (dt_bias may be null)
+};
+
+struct Params {
+    SeqGeom seq;                        // n_slots counts 64-token chunk slots
+    int32_t H, HV, G;
+    float scale;
+    const uint16_t *q[3], *k[3];        // bf16 io: q and k; fp32 io: their three bf16 planes
+    const void *v, *g, *beta;           // io dtype
+    const float *h0;
+    void *o;                            // io dtype
+    float *ht;
+    uint8_t *rec;                       // chunk records
+    Pre pre;
+};
+
+// Arguments of the recurrence (gdn_step, and gdn_fwd for short dense batches).
+struct StepParams {
+    int32_t B, T, H, HV, G;
+    float scale;
+    const void *q, *k, *v, *g, *beta;
+    void *o;
+    const float *h0;                    // row b's state: h0 / ht at index[b] (or b)
+    float *ht;
+    const int32_t *index;
+    int32_t slots;
+    Pre pre;
+};
+
+// Record of one (value head, chunk slot). A and M are lower triangular; their 16-row tiles t
+// are stored as 16x16x32 operand fragments over the tokens 32 s .. 32 s + 31, s <= t / 2, in
+// the order (0,0) (1,0) (2,0) (2,1) (3,0) (3,1): lane (g, m) holds row 16 t + m, elements e < 4
+// token 32 s + 4 g + e and e >= 4 token 32 s + 16 + 4 g + e - 4 (so that two C-layout tiles are
+// the other operand, as they are).
+//   A and M, each [parts][6][64 lanes][8] bf16; then fp32 row scales of the chunk's 64 tokens:
+//   RA = e^Gam rk, RB = beta e^{gam - Gam} rk, RC = scale e^Gam rq (rk, rq the L2-norm factors),
+//   and EG [1] = e^gam (one KiB-aligned block, so it is copied to LDS in 1 KiB steps).
+template <int X>
+struct Rec {
+    static constexpr int FR = 1024, MAT = 6 * FR;       // one fragment, one part of a matrix
+    static constexpr int A = 0, M = X * MAT;
+    static constexpr int RA = 2 * X * MAT, RB = RA + 256, RC = RB + 256, EG = RC + 256;
+    static constexpr int BYTES = RA + FR;
+};
+
+__host__ __device__ constexpr int frag_index(int t, int s) { return t < 2 ? t : 2 * t - 2 + s; }
+
+// ------------------------------------------------------------------------------- operands
+
+template <int X>
+struct Parts {
+    bf16x8 p[X];
+};
+
+// Eight values (two C-layout tiles) as X bf16 parts.
+template <int X>
+__device__ __forceinline__ Parts<X> split(f32x4 x, f32x4 y) {
+    Parts<X> r;
+#pragma unroll
+    for (int k = 0; k < X; ++k) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            r.p[k][i] = (__bf16)x[i];
+            r.p[k][4 + i] = (__bf16)y[i];
+        }
+        if (k + 1 < X) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                x[i] -= (float)r.p[k][i];
+                y[i] -= (float)r.p[k][4 + i];
+            }
+        }
+    }
+    return r;
+}
+
+template <int XA, int XB>
+__device__ __forceinline__ f32x4 mm(const Parts<XA> &a, const Parts<XB> &b, f32x4 c) {
+    constexpr int X = XA > XB ? XA : XB;
+#pragma unroll
+    for (int i = 0; i < XA; ++i)
+#pragma unroll
+        for (int j = 0; j < XB; ++j)
+            if (i + j < X) c = mfma32(a.p[i], b.p[j], c);
+    return c;
+}
+
+typedef __attribute__((address_space(3))) uint8_t lds_u8;
+typedef __attribute__((ext_vector_type(4))) short s16x4;
+
+__device__ __forceinline__ bf16x8 lds_b128(const uint8_t *p) { return *(const bf16x8 *)p; }
+// the parts of an operand, `step` bytes apart
+template <int X>
+__device__ __forceinline__ Parts<X> lds_parts(const uint8_t *p, int step) {
+    Parts<X> r;
+#pragma unroll
+    for (int i = 0; i < X; ++i) r.p[i] = lds_b128(p + i * step);
+    return r;
+}
+
+// Transposing read: within 16 lanes, lane j reads four 16-bit values of row j / 4 at its own
+// address and lane m receives column m of rows 0 .. 3 (m = 4 (j % 4) + element).
+__device__ __forceinline__ s16x4 lds_tr(const uint8_t *p) {
+    return __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+        (__attribute__((address_space(3))) s16x4 *)(lds_u8 *)p);
+}
+__device__ __forceinline__ bf16x8 join(s16x4 a, s16x4 b) {
+    return __builtin_bit_cast(bf16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+__device__ __forceinline__ f32x4 widen(s16x4 a) {
+    f32x4 r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = __uint_as_float((uint32_t)(uint16_t)a[i] << 16);
+    return r;
+}
+
+// A staged matrix has 64 rows of W bf16 in 16-byte pieces; piece p of row r lies at place
+// p ^ (r % pieces) of its row, so that sixteen rows at one piece touch all banks.
+template <int W>
+__device__ __forceinline__ int piece_at(int row, int piece) {
+    constexpr int NP = W / 8;
+    return (row * NP + (piece ^ (row & (NP - 1)))) * 16;
+}
+
+__device__ __forceinline__ void copy16_to_lds(const void *src, uint8_t *dst) {
+    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)src,
+                                     (__attribute__((address_space(3))) void *)(lds_u8 *)dst, 16,
+                                     0, 0);
+}
+
+// Stage rows 0 .. 63 of a [tokens][stride] matrix into LDS (W columns, layout piece_at); rows
+// from nv on repeat row nv - 1, so that every read lies inside the sequence (the row scales and
+// operands that meet them are zero). NW waves share the work; no wait.
+template <int W, int NW>
+__device__ __forceinline__ void stage_rows(const uint16_t *src, int64_t stride, int nv,
+                                           uint8_t *dst, int wave, int lane) {
+    constexpr int NP = W / 8, STEPS = 64 * NP / 64;
+#pragma unroll
+    for (int q = 0; q < STEPS / NW; ++q) {
+        const int step = q * NW + wave;
+        const int at = step * 64 + lane, row = at / NP, piece = (at % NP) ^ (row & (NP - 1));
+        const int rr = row < nv ? row : nv - 1;
+        copy16_to_lds(src + rr * stride + piece * 8, dst + step * 1024);
+    }
+}
+
+// Stage `kib` KiB of consecutive memory.
+template <int NW>
+__device__ __forceinline__ void stage_block(const uint8_t *src, int kib, uint8_t *dst, int wave,
+                                            int lane) {
+    for (int step = wave; step < kib; step += NW)
+        copy16_to_lds(src + step * 1024 + lane * 16, dst + step * 1024);
+}
+
+// ------------------------------------------------------------------------------- pre-stage
+
+__device__ __forceinline__ float exact_sigmoid(float x) { return 1.f / (1.f + expf(-x)); }
+
+// The log decay of raw input x (bias not added yet).
+__device__ __forceinline__ float activate_gate(const Pre &pre, float x, int j) {
+    if (pre.gate == 0) return x;
+    if (pre.dt_bias) x += pre.dt_bias[j];
+    const float a = expf(pre.A_log[j]);
+    if (pre.gate == 1) return -a * (fmaxf(x, 0.f) + log1pf(expf(-fabsf(x))));
+    return pre.lower_bound * exact_sigmoid(a * x);
+}
+
+__device__ __forceinline__ float load_io(const void *p, int64_t i, bool f32) {
+    return f32 ? ((const float *)p)[i] : kda::bf16_bits_to_f32(((const uint16_t *)p)[i]);
+}
+
+}  // namespace gdn
+
+// Host-side launchers (defined next to their kernels).
+namespace gdn {
+// fp32 x [n] as three bf16 planes, n values apart
+hipError_t launch_split_planes(const float *x, int64_t n, uint16_t *planes, hipStream_t st);
+template <int K> hipError_t launch_prepare(const Params &p, bool f32, hipStream_t st);
+template <int K, int V> hipError_t launch_state(const Params &p, bool f32, hipStream_t st);
+template <int K, int V> hipError_t launch_recurrent(const StepParams &p, bool f32, hipStream_t st);
+}  // namespace gdn

@@ -1,0 +1,174 @@
+"""The gated delta rule with one decay per token and value head (include/gdn.h): argument
+marshalling only, as in api.py."""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from ._lib import GdnArgs, load, strerror
+from .api import _GATES, _IO, _check, _ptr
+
+
+def _arguments(q, k, v, g, beta, scale, cu_seqlens, initial_state, use_qk_l2norm,
+               use_beta_sigmoid, gate, A_log, dt_bias, gate_lower_bound):
+    """Checked gdn_args of the inputs; o and the final state are the caller's to set."""
+    dt, dev = q.dtype, q.device
+    if dt not in _IO:
+        raise TypeError(f"unsupported io dtype {dt} (bf16 or fp32)")
+    if dev.type != "cuda":
+        raise ValueError("inputs must be on a HIP device")
+    if q.dim() != 4 or v.dim() != 4:
+        raise ValueError("q must be [B, T, H, K] and v [B, T, HV, V]")
+    B, T, H, K = q.shape
+    HV, V = v.shape[2], v.shape[3]
+    _check(q, "q", dt, (B, T, H, K), dev)
+    _check(k, "k", dt, (B, T, H, K), dev)
+    _check(v, "v", dt, (B, T, HV, V), dev)
+    _check(g, "g", dt, (B, T, HV), dev)
+    _check(beta, "beta", dt, (B, T, HV), dev)
+    N = B
+    if cu_seqlens is not None:
+        if cu_seqlens.dtype != torch.int64 or cu_seqlens.device != dev or cu_seqlens.dim() != 1:
+            raise ValueError("cu_seqlens must be a 1-D int64 tensor on the inputs' device")
+        if not cu_seqlens.is_contiguous():
+            raise ValueError("cu_seqlens must be contiguous")
+        N = cu_seqlens.numel() - 1
+    if initial_state is not None:
+        _check(initial_state, "initial_state", torch.float32, (N, HV, K, V), dev)
+    if gate not in _GATES:
+        raise ValueError(f"gate must be None, 'softplus' or 'bounded' (got {gate!r})")
+    a = GdnArgs()
+    a.B, a.T, a.N, a.H, a.HV, a.K, a.V, a.io = B, T, N, H, HV, K, V, _IO[dt]
+    a.q, a.k, a.v, a.g, a.beta = (q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
+                                  beta.data_ptr())
+    a.scale = float("nan") if scale is None else float(scale)
+    if cu_seqlens is not None:
+        a.cu_seqlens = cu_seqlens.data_ptr()
+    if initial_state is not None:
+        a.initial_state = initial_state.data_ptr()
+    a.qk_l2norm = int(bool(use_qk_l2norm))
+    a.beta_sigmoid = int(bool(use_beta_sigmoid))
+    if gate is not None:
+        if A_log is None:
+            raise ValueError("a gate needs A_log")
+        _check(A_log, "A_log", torch.float32, (HV,), dev)
+        if dt_bias is not None:
+            _check(dt_bias, "dt_bias", torch.float32, (HV,), dev)
+        a.gate = _GATES[gate]
+        a.gate_lower_bound = float(gate_lower_bound)
+        a.A_log, a.dt_bias = _ptr(A_log), _ptr(dt_bias)
+    return a
+
+
+def _call(fn, name, dev, stream, *args):
+    """Enqueue on `stream` (default: torch's current stream of `dev`), with `dev` current."""
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    if torch.cuda.current_device() == dev.index:
+        st = fn(*args, stream.cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, stream.cuda_stream)
+    if st != 0:
+        raise RuntimeError(f"{name} failed: {strerror(st)} ({st})")
+
+
+class GdnFwdPlan:
+    """Validated arguments for repeated gdn_fwd calls on the same tensors.
+
+    q, k [B,T,H,K]; v [B,T,HV,V]; g, beta [B,T,HV] (all bf16 or all fp32, contiguous, on one HIP
+    device): g is the log decay of a token's whole state. cu_seqlens, initial_state, the outputs
+    o and final_state and the pre-stage keywords are KdaFwdPlan's, with dt_bias fp32 [HV]. K and
+    V are 64 or 128; any length, zero included.
+    """
+
+    def __init__(self, q, k, v, g, beta, scale=None, cu_seqlens=None, initial_state=None,
+                 output_final_state=True, workspace=None, o=None, final_state=None,
+                 use_qk_l2norm=False, use_beta_sigmoid=False, gate=None, A_log=None,
+                 dt_bias=None, gate_lower_bound=-5.0):
+        self.lib = load()
+        a = _arguments(q, k, v, g, beta, scale, cu_seqlens, initial_state, use_qk_l2norm,
+                       use_beta_sigmoid, gate, A_log, dt_bias, gate_lower_bound)
+        dev = self.device = q.device
+        self.o = torch.empty_like(v) if o is None else o
+        if o is not None:
+            _check(o, "o", v.dtype, v.shape, dev)
+        a.o = self.o.data_ptr()
+        self.final_state = None
+        if output_final_state:
+            shape = (a.N, a.HV, a.K, a.V)
+            self.final_state = (torch.empty(shape, dtype=torch.float32, device=dev)
+                                if final_state is None else final_state)
+            if final_state is not None:
+                _check(final_state, "final_state", torch.float32, shape, dev)
+            a.final_state = self.final_state.data_ptr()
+        self.args = a
+        self._keep = (q, k, v, g, beta, cu_seqlens, initial_state, A_log, dt_bias)
+        # 0: refused (the call says why), or the recurrence, which needs none
+        with torch.cuda.device(dev):
+            need = int(self.lib.gdn_fwd_workspace_bytes(ctypes.byref(a)))
+        if workspace is None:
+            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+        else:
+            _check(workspace, "workspace", torch.uint8, workspace.shape, dev)
+            if workspace.numel() < need:
+                raise ValueError(f"workspace too small: {workspace.numel()} < {need} bytes")
+        self.workspace = workspace
+
+    def __call__(self, stream=None):
+        """Enqueue the forward on `stream` (default: torch's current stream)."""
+        _call(self.lib.gdn_fwd, "gdn_fwd", self.device, stream, ctypes.byref(self.args),
+              self.workspace.data_ptr(), self.workspace.numel())
+        return self.o, self.final_state
+
+
+def gdn_fwd(q, k, v, g, beta, scale=None, cu_seqlens=None, initial_state=None,
+            output_final_state=True, workspace=None, **prestage):
+    """Gated delta rule forward. Returns (o, final_state or None); see GdnFwdPlan for shapes and
+    the pre-stage keywords (use_qk_l2norm, use_beta_sigmoid, gate, A_log, dt_bias,
+    gate_lower_bound)."""
+    return GdnFwdPlan(q, k, v, g, beta, scale, cu_seqlens, initial_state, output_final_state,
+                      workspace, **prestage)()
+
+
+class GdnStepPlan:
+    """Validated arguments for repeated gdn_step calls on the same tensors (a serving loop that
+    writes each step's inputs in place).
+
+    q, k [B,T,H,K]; v [B,T,HV,V]; g, beta [B,T,HV]: T new tokens of B rows; state fp32
+    [slots,HV,K,V], updated in place; state_indices int32 [B] on the device, or None for slot b
+    of row b. A row whose index is negative or >= slots is padding: zeros in o, no state touched.
+    Indices of other rows must differ. o [B,T,HV,V] is allocated once and reused.
+    """
+
+    def __init__(self, q, k, v, g, beta, state, state_indices=None, scale=None, o=None,
+                 use_qk_l2norm=False, use_beta_sigmoid=False, gate=None, A_log=None,
+                 dt_bias=None, gate_lower_bound=-5.0):
+        self.lib = load()
+        a = _arguments(q, k, v, g, beta, scale, None, None, use_qk_l2norm, use_beta_sigmoid, gate,
+                       A_log, dt_bias, gate_lower_bound)
+        self.device = q.device
+        _check(state, "state", torch.float32, (state.shape[0], a.HV, a.K, a.V), q.device)
+        if state_indices is not None:
+            _check(state_indices, "state_indices", torch.int32, (a.B,), q.device)
+        elif state.shape[0] < a.B:
+            raise ValueError(f"state has {state.shape[0]} slots for {a.B} rows")
+        self.o = torch.empty_like(v) if o is None else o
+        if o is not None:
+            _check(o, "o", v.dtype, v.shape, q.device)
+        a.o = self.o.data_ptr()
+        self.args = a
+        self._call = (ctypes.byref(a), state.data_ptr(), _ptr(state_indices), state.shape[0])
+        self._keep = (q, k, v, g, beta, state, state_indices, A_log, dt_bias)
+
+    def __call__(self, stream=None):
+        """Enqueue the step on `stream` (default: torch's current stream)."""
+        _call(self.lib.gdn_step, "gdn_step", self.device, stream, *self._call)
+        return self.o
+
+
+def gdn_step(q, k, v, g, beta, state, state_indices=None, scale=None, **prestage):
+    """A serving step of the gated delta rule: returns o and updates `state` in place; see
+    GdnStepPlan."""
+    return GdnStepPlan(q, k, v, g, beta, state, state_indices, scale, **prestage)()

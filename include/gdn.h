@@ -1,0 +1,88 @@
+/*
+ * gdn.h -- C ABI of libkda_fwd: the gated delta rule with one decay per token and value head,
+ * on one AMD Instinct MI355X (gfx950).
+ *
+ * The operation: for every sequence s and value head j, with q/k head h = j / (HV / H) and a
+ * state S in R^{K x V} that starts at initial_state[s, j] (or zero), each token t does
+ *
+ *     S <- exp(g[t, j]) S;   r = v[t, j, :] - S^T k[t, h, :];
+ *     S <- S + beta[t, j] k[t, h, :] r^T;   o[t, j, :] = scale * S^T q[t, h, :]
+ *
+ * and final_state[s, j] is S after the last token. It is kda_fwd's operation with the decay of
+ * a token shared by all key dims (a KDA call with g repeated K times gives the same result).
+ *
+ * Conventions are kda_fwd.h's: device pointers, caller-owned, contiguous, 16-byte aligned;
+ * nothing is allocated, nothing synchronises, no atomics, errors only through the return value;
+ * concurrent calls use distinct workspaces and outputs. q, k and v must be finite: a NaN or an
+ * infinity makes the outputs of its sequence and heads undefined from its 64-token chunk on (in
+ * the backward, for the whole sequence); other sequences and heads never see it.
+ */
+#ifndef GDN_H
+#define GDN_H
+
+#include <stddef.h>
+#include <stdint.h>
+
+#include "kda_fwd.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+typedef struct {
+    /* Shapes as in kda_fwd_args: a dense batch has N == B sequences of T tokens; with
+       cu_seqlens B == 1 and sequence s spans [cu_seqlens[s], cu_seqlens[s + 1]).           */
+    int32_t B, T, N;
+    int32_t H, HV;            /* q/k heads and value heads, HV % H == 0                      */
+    int32_t K, V;             /* head dims, each in {64, 128}                                */
+    int32_t io;               /* kda_dtype of q, k, v, g, beta, o (and of the gradients)     */
+    const void *q;            /* [B, T, H, K]                                                */
+    const void *k;            /* [B, T, H, K]                                                */
+    const void *v;            /* [B, T, HV, V]                                               */
+    const void *g;            /* [B, T, HV]     log decay; any g <= 0 is exact to rounding,
+                                 -inf included (it clears the state)                         */
+    const void *beta;         /* [B, T, HV]                                                  */
+    float scale;              /* output scale; <= 0 or NaN selects K^-0.5                    */
+    const int64_t *cu_seqlens;/* device [N + 1] or NULL; contents as in kda_fwd_args         */
+    const float *initial_state; /* [N, HV, K, V] fp32, or NULL for zeros                     */
+    void *o;                  /* [B, T, HV, V]                                               */
+    float *final_state;       /* [N, HV, K, V] fp32, or NULL to skip; may be the same buffer
+                                 as initial_state                                            */
+    /* Pre-stage (all zero: inputs used as given), as in kda_fwd_args with one gate input a
+       token and value head:
+         qk_l2norm     q, k rows divided by sqrt(sum of squares + 1e-6)
+         beta_sigmoid  beta <- 1 / (1 + exp(-beta))
+         gate          with x = g[t, j] + dt_bias[j]: KDA_GATE_SOFTPLUS
+                       g <- -exp(A_log[j]) log(1 + exp(x)); KDA_GATE_BOUNDED
+                       g <- lower_bound / (1 + exp(-exp(A_log[j]) x))                        */
+    int32_t qk_l2norm, beta_sigmoid, gate;
+    float gate_lower_bound;   /* KDA_GATE_BOUNDED: finite and < 0                            */
+    const float *A_log;       /* [HV] fp32; required for a gate                              */
+    const float *dt_bias;     /* [HV] fp32, or NULL for zeros                                */
+} gdn_args;
+
+/* Bytes of device workspace gdn_fwd needs (only shapes, io and whether cu_seqlens is there are
+   read, and the current device's compute-unit count); 0 for arguments gdn_fwd would reject and
+   for a dense batch of at most 16 tokens a sequence, which needs none. */
+size_t gdn_fwd_workspace_bytes(const gdn_args *args);
+
+/* Enqueue the forward on `stream`: 64-token chunks (a prepare kernel, then the pass over each
+   sequence's chunks, split into segments where the batch is too small to fill the device), or,
+   for a dense batch of at most 16 tokens a sequence, the recurrence itself. Products take
+   16-bit operands in pairs (high and low part), so that the states and o carry about 17 bits
+   before their own rounding, for either io type. */
+kda_status gdn_fwd(const gdn_args *args, void *workspace, size_t ws_bytes, void *stream);
+
+/* One serving step: B rows of T new tokens each, row b on the state in slot state_indices[b]
+   of `state` [slots, HV, K, V] fp32, updated in place. state_indices: device int32 [B], or
+   NULL for slot b (slots >= B then). A row whose index is negative or >= slots is padding: its
+   o is zero and no state is touched. Two rows must not name the same slot (their updates race).
+   args: B == N, no cu_seqlens; initial_state and final_state are not read. */
+kda_status gdn_step(const gdn_args *args, float *state, const int32_t *state_indices,
+                    int32_t slots, void *stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* GDN_H */
