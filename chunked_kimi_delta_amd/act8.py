@@ -7,8 +7,7 @@ from typing import NamedTuple
 import torch
 
 from ._lib import load
-from .api import _IO
-from .gdn import _call
+from .api import _IO, _call
 
 
 class Packed8(NamedTuple):

@@ -29,6 +29,19 @@ def _check(t: torch.Tensor, name: str, dtype, shape, device):
         raise ValueError(f"{name} must be contiguous")
 
 
+def _call(fn, name, dev, stream, *args):
+    """Enqueue on `stream` (default: torch's current stream of `dev`), with `dev` current."""
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    if torch.cuda.current_device() == dev.index:
+        st = fn(*args, stream.cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, stream.cuda_stream)
+    if st != 0:
+        raise RuntimeError(f"{name} failed: {strerror(st)} ({st})")
+
+
 class KdaFwdPlan:
     """Validated arguments for repeated kda_fwd calls on the same tensors.
 

@@ -131,9 +131,163 @@ kda_status check_tensors(const gdn_args *a)
     return check_pre(a);
 }
 
+// The fields of the forward and the backward that do not depend on the workspace.
+Params params_of(const gdn_args *a, const Layout &L)
+{
+    Params p = {};
+    p.seq.cu = a->cu_seqlens;
+    p.seq.T = a->T;
+    p.seq.T_total = L.tt;
+    p.seq.N = a->N;
+    p.seq.n_slots = (int32_t)L.slots;
+    p.H = a->H;
+    p.HV = a->HV;
+    p.G = a->HV / a->H;
+    p.scale = scale_of(a);
+    p.q[0] = (const uint16_t *)a->q;
+    p.k[0] = (const uint16_t *)a->k;
+    p.v = a->v;
+    p.g = a->g;
+    p.beta = a->beta;
+    p.h0 = a->initial_state;
+    p.o = a->o;
+    p.ht = a->final_state;
+    p.pre = pre_of(a);
+    return p;
+}
+
+struct BwdLayout {
+    Layout f;
+    // bf16 io: records, kept states; fp32 io: the decay repeated over K, its gradient and
+    // kda_bwd's own workspace; with a gate, the gradient of the activated decay
+    size_t keep, dg_act, dwide, kda, kda_bytes, total;
+};
+
+size_t keep_bytes(int K, int V)
+{
+    return K == 64 ? (V == 64 ? Keep<64, 64>::BYTES : Keep<64, 128>::BYTES)
+                   : (V == 64 ? Keep<128, 64>::BYTES : Keep<128, 128>::BYTES);
+}
+
+// The KDA call that fp32 io takes: one decay per token is KDA with that decay for every key dim.
+kda_fwd_args wide_args(const gdn_args *a, const float *g)
+{
+    kda_fwd_args w = {};
+    w.B = a->B;
+    w.T = a->T;
+    w.N = a->N;
+    w.H = a->H;
+    w.HV = a->HV;
+    w.K = a->K;
+    w.V = a->V;
+    w.io = KDA_FP32;
+    w.q = a->q;
+    w.k = a->k;
+    w.v = a->v;
+    w.g = g;
+    w.beta = a->beta;
+    w.scale = a->scale;
+    w.cu_seqlens = a->cu_seqlens;
+    w.initial_state = a->initial_state;
+    w.qk_l2norm = a->qk_l2norm;
+    w.beta_sigmoid = a->beta_sigmoid;
+    return w;
+}
+
+BwdLayout bwd_layout(const gdn_args *a)
+{
+    BwdLayout L = {};
+    L.f = layout(a);
+    const size_t slots = (size_t)L.f.slots * a->HV, rows = (size_t)L.f.tt * a->HV;
+    size_t at;
+    if (a->io == KDA_BF16) {
+        L.keep = slots * RecB::BYTES;
+        at = L.keep + slots * keep_bytes(a->K, a->V);
+    } else {
+        const kda_fwd_args w = wide_args(a, nullptr);
+        L.dwide = align256(rows * a->K * 4);
+        L.kda = 2 * L.dwide;
+        L.kda_bytes = kda_bwd_workspace_bytes(&w);
+        at = L.kda + align256(L.kda_bytes);
+    }
+    L.dg_act = at;
+    L.total = at + (a->gate != KDA_GATE_NONE ? align256(rows * 4) : 0);
+    return L;
+}
+
 }  // namespace
 
 extern "C" {
+
+size_t gdn_bwd_workspace_bytes(const gdn_args *a)
+{
+    if (check_shapes(a) != KDA_OK) return 0;
+    const BwdLayout L = bwd_layout(a);
+    return a->io == KDA_FP32 && L.kda_bytes == 0 ? 0 : L.total;
+}
+
+kda_status gdn_bwd(const gdn_args *a, const void *d_o, const float *dht, void *workspace,
+                   size_t ws_bytes, void *dq, void *dk, void *dv, void *dg, void *dbeta,
+                   float *dh0, float *dA_log, float *ddt_bias, void *stream)
+{
+    kda_status st = check_shapes(a);
+    if (st != KDA_OK) return st;
+    if ((st = check_pre(a)) != KDA_OK) return st;
+    const bool gated = a->gate != KDA_GATE_NONE, f32 = a->io == KDA_FP32;
+    if (gated && (!dA_log || !aligned(dA_log, 4) || !aligned(ddt_bias, 4)))
+        return KDA_ERR_INVALID_ARG;
+    const BwdLayout L = bwd_layout(a);
+    if (L.f.tt > 0) {
+        const void *ptrs[] = {a->q, a->k, a->v, a->g, a->beta, d_o, dq, dk, dv, dg, dbeta};
+        for (const void *p : ptrs)
+            if (!p || !aligned(p, 16)) return KDA_ERR_INVALID_ARG;
+    }
+    const void *opt[] = {a->initial_state, a->cu_seqlens, dht, dh0};
+    for (const void *p : opt)
+        if (!aligned(p, 16)) return KDA_ERR_INVALID_ARG;
+    if (f32 && L.kda_bytes == 0) return KDA_ERR_UNSUPPORTED;
+    if (L.f.tt > 0 && (!workspace || ws_bytes < L.total || !aligned(workspace, 256)))
+        return KDA_ERR_WORKSPACE;
+    if (a->N == 0) return KDA_OK;
+    uint8_t *const ws = (uint8_t *)workspace;
+    hipStream_t hs = (hipStream_t)stream;
+    Params p = params_of(a, L.f);
+    p.rec = ws;
+    float *const dg_act = gated ? (float *)(ws + L.dg_act) : nullptr;
+    hipError_t e;
+    if (f32) {
+        float *const wide = (float *)ws, *const dwide = (float *)(ws + L.dwide);
+        if (launch_widen_decay(p, a->K, wide, hs) != hipSuccess) return KDA_ERR_HIP;
+        const kda_fwd_args w = wide_args(a, wide);
+        st = kda_bwd(&w, d_o, dht, ws + L.kda, L.kda_bytes, (float *)dq, (float *)dk, (float *)dv,
+                     dwide, (float *)dbeta, dh0, nullptr, nullptr, stream);
+        if (st != KDA_OK) return st;
+        e = launch_narrow_decay(p, a->K, dwide, gated ? dg_act : (float *)dg, hs);
+    } else {
+        if (L.f.tt > 0) {
+            e = a->K == 64 ? launch_prepare_bwd<64>(p, hs) : launch_prepare_bwd<128>(p, hs);
+            if (e != hipSuccess) return KDA_ERR_HIP;
+        }
+        BwdParams b = {};
+        b.f = p;
+        b.d_o = (const uint16_t *)d_o;
+        b.dht = dht;
+        b.keep = ws + L.keep;
+        b.dq = (uint16_t *)dq;
+        b.dk = (uint16_t *)dk;
+        b.dv = (uint16_t *)dv;
+        b.dbeta = (uint16_t *)dbeta;
+        b.dg = (uint16_t *)dg;
+        b.dg_act = dg_act;
+        b.dh0 = dh0;
+        e = by_dims(a->K, a->V, [&](auto k, auto v) {
+            return launch_backward<decltype(k)::value, decltype(v)::value>(b, hs);
+        });
+    }
+    if (e == hipSuccess && gated)
+        e = launch_gate_backward(p, f32, dg_act, dg, dA_log, ddt_bias, hs);
+    return e == hipSuccess ? KDA_OK : KDA_ERR_HIP;
+}
 
 size_t gdn_fwd_workspace_bytes(const gdn_args *a)
 {
@@ -156,26 +310,8 @@ kda_status gdn_fwd(const gdn_args *a, void *workspace, size_t ws_bytes, void *st
         return KDA_ERR_WORKSPACE;
     uint8_t *const ws = (uint8_t *)workspace;
     const bool f32 = a->io == KDA_FP32;
-    Params p = {};
-    p.seq.cu = a->cu_seqlens;
-    p.seq.T = a->T;
-    p.seq.T_total = L.tt;
-    p.seq.N = a->N;
-    p.seq.n_slots = (int32_t)L.slots;
-    p.H = a->H;
-    p.HV = a->HV;
-    p.G = a->HV / a->H;
-    p.scale = scale_of(a);
-    p.g = a->g;
-    p.beta = a->beta;
-    p.h0 = a->initial_state;
-    p.o = a->o;
-    p.ht = a->final_state;
+    Params p = params_of(a, L);
     p.rec = ws;
-    p.pre = pre_of(a);
-    p.v = a->v;
-    p.q[0] = (const uint16_t *)a->q;
-    p.k[0] = (const uint16_t *)a->k;
     if (f32 && L.tt > 0) {
         const int64_t n = L.tt * a->H * a->K;
         if (launch_split_planes((const float *)a->q, n, (uint16_t *)(ws + L.q), hs) != hipSuccess ||

@@ -1,0 +1,771 @@
+// gdn_backward.hip -- gradients of the gated delta rule, bf16 io (gdn_internal.h has the forward's
+// chunk formulas; matrices and row scales as there, dS' the gradient of the state at a chunk's end).
+//
+// Per chunk, newest first, the state's gradient goes through
+//     de = M^T dO + beta e^{gam-Gam} . (K dS')        dR = A^T de   (= dV)
+//     dS = e^gam dS' + Q^T (scale e^Gam . dO) - K^T (e^Gam . dR)
+// and every chunk then gives its tokens, from S at its start, dS', e and dR alone,
+//     X1 = lower(dO e^T),  X2 = -strictly_lower(dR e^T)      (gradients of M and L)
+//     dQ = (X1 . scale D beta_j) K + scale e^Gam . (dO S^T)
+//     dK = (X1 . scale D beta_j)^T Q + (W2 + W2^T) K - e^Gam . (dR S^T) + beta T,  W2 = X2 . D beta_j,
+//     T_j = e^{gam-Gam_j} dS' e_j
+//     dbeta_j = sum_i U_ij + k_j.T_j,   U = D . (X1 . scale Q K^T + X2 . K K^T)
+//     dg_t = sum_{i >= t > j} beta_j U_ij + sum_{i >= t} (q_i.dQ_i[S part] + k_i.dK_i[S part])
+//            + sum_{j < t} beta_j k_j.T_j + e^gam <S, dS'>.
+// (dg_t is what crosses t: every term holds a decay over t. As differences of row and column sums
+// the pairs on one side of t would cancel only to rounding, which a strong decay at t would show.)
+// No division by beta and no exponent above zero occurs.
+//
+// Launches: the chunk records (gdn_prepare.hip), both passes over the chunks (the forward one for
+// S and e, the reverse one for dS' and dR; they are independent, one launch), the chunks' tokens.
+// The passes carry two bf16 parts of every operand as the forward does (dh0 is an fp32 result).
+// What they leave for the chunks is scaled fp16 (2^-12 a rounding, against the 2^-8 of the bf16
+// gradients that it enters; bf16 there cost up to 5e-3 of dg, whose terms cancel), multiplied with
+// dO as fp16 (exact: a bf16 value scaled by a power of two); the 64 x 64 matrices take two bf16
+// parts against the stored q and k.
+#include <type_traits>
+
+#include "gdn_chain.h"
+
+namespace gdn {
+
+namespace {
+
+template <int K, int V>
+struct StageR {                             // LDS of one chunk of the reverse pass
+    static constexpr int MK = 64 * K * 2, MV = 64 * V * 2;
+    static constexpr int KM = 0, QM = MK, DO = 2 * MK, REC = DO + MV;
+    static constexpr int BYTES = REC + RecB::REV_KIB * 1024;
+};
+
+template <int K, int V>
+__device__ __forceinline__ void reverse_chain(const BwdParams &b, int unit, uint8_t *lds)
+{
+    using L = StageR<K, V>;
+    using R = RecB;
+    constexpr int X = R::X, NW = V / 32, NT = K / 16;
+    const Params &p = b.f;
+    const int tid = threadIdx.x, lane = tid & 63, grp = lane >> 4, r = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int s = unit / p.HV, j = unit % p.HV, h = j / p.G;
+    const int64_t bos = kda::seq_bos(p.seq, s), eos = kda::seq_eos(p.seq, s, bos);
+    const int nc = (int)((eos - bos + CT - 1) / CT);
+    const size_t slot0 = (size_t)j * p.seq.n_slots + bos / CT + s;
+    const int col0 = 32 * wave;
+
+    auto stage = [&](int c, uint8_t *buf) {
+        const int64_t t0 = bos + (int64_t)CT * c;
+        const int nv = (int)(eos - t0 < CT ? eos - t0 : CT);
+        const int64_t qk = (t0 * p.H + h) * K;
+        stage_rows<K, NW>(p.k[0] + qk, (int64_t)p.H * K, nv, buf + L::KM, wave, lane);
+        stage_rows<K, NW>(p.q[0] + qk, (int64_t)p.H * K, nv, buf + L::QM, wave, lane);
+        stage_rows<V, NW>(b.d_o + (t0 * p.HV + j) * V, (int64_t)p.HV * V, nv, buf + L::DO, wave, lane);
+        stage_block<NW>(p.rec + (slot0 + c) * R::BYTES + R::REV, R::REV_KIB, buf + L::REC, wave, lane);
+    };
+    if (nc > 0) stage(nc - 1, lds);
+
+    f32x4 S[NT][2];                         // dS, laid out as the forward's S
+    const size_t st_off = ((size_t)s * p.HV + j) * K * V + col0 + r;
+    auto state_at = [&](int t, int i, int ct) {
+        return st_off + (size_t)(32 * (t / 2) + 8 * grp + 4 * (t % 2) + i) * V + 16 * ct;
+    };
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int ct = 0; ct < 2; ++ct)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) S[t][ct][i] = b.dht ? b.dht[state_at(t, i, ct)] : 0.f;
+
+#pragma unroll 1
+    for (int c = nc - 1; c >= 0; --c) {
+        uint8_t *const buf = lds + ((nc - 1 - c) & 1) * L::BYTES;
+        uint8_t *const keep = b.keep + (slot0 + c) * Keep<K, V>::BYTES;
+        kda::vm_drain();
+        __syncthreads();
+        if (c > 0) stage(c - 1, lds + ((nc - c) & 1) * L::BYTES);
+        const uint8_t *const rec = buf + L::REC - R::REV;
+        const float *const ra = (const float *)(rec + R::RA), *const rb = (const float *)(rec + R::RB),
+                    *const rc = (const float *)(rec + R::RC);
+        const float eg = *(const float *)(rec + R::EG);
+        using KP = Keep<K, V>;
+        float *const scales = (float *)(keep + KP::SCALE) + wave;
+        keep_state<K>(S, keep + KP::DS, scales + V / 32, col0, grp, r);
+        // K dS'
+        f32x4 kS[4][2];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) kS[t][0] = kS[t][1] = zero4();
+#pragma unroll
+        for (int st = 0; st < K / 32; ++st) {
+            Parts<X> sp[2];
+#pragma unroll
+            for (int ct = 0; ct < 2; ++ct) sp[ct] = split<X>(S[2 * st][ct], S[2 * st + 1][ct]);
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                const Parts<1> kk = {lds_b128(buf + L::KM + piece_at<K>(16 * t + r, 4 * st + grp))};
+#pragma unroll
+                for (int ct = 0; ct < 2; ++ct) kS[t][ct] = mm(kk, sp[ct], kS[t][ct]);
+            }
+        }
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int ct = 0; ct < 2; ++ct) S[t][ct] *= eg;
+        // de = M^T dO + beta e^{gam-Gam} (K dS'); dO of tokens 32 st + 4 g .. + 3, + 16 per lane
+        s16x4 dv[2][2][2];
+#pragma unroll
+        for (int st = 0; st < 2; ++st)
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int ct = 0; ct < 2; ++ct)
+                    dv[st][ct][u] = lds_tr(buf + L::DO +
+                                           piece_at<V>(32 * st + 16 * u + 4 * grp + (r >> 2),
+                                                       col0 / 8 + 2 * ct + ((r & 3) >> 1)) + 8 * (r & 1));
+        Parts<X> dp[2][2];
+#pragma unroll
+        for (int st = 0; st < 2; ++st) {
+            f32x4 x[2][2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int t = 2 * st + u;
+                const f32x4 bs = *(const f32x4 *)(rb + 16 * t + 4 * grp);
+#pragma unroll
+                for (int ct = 0; ct < 2; ++ct) x[u][ct] = bs * kS[t][ct];
+#pragma unroll
+                for (int s2 = st; s2 < 2; ++s2) {
+                    const Parts<X> m = lds_parts<X>(rec + R::MT + frag_index_t(t, s2) * R::FR + lane * 16, R::MAT);
+#pragma unroll
+                    for (int ct = 0; ct < 2; ++ct)
+                        x[u][ct] = mm(m, Parts<1>{join(dv[s2][ct][0], dv[s2][ct][1])}, x[u][ct]);
+                }
+            }
+#pragma unroll
+            for (int ct = 0; ct < 2; ++ct) dp[st][ct] = split<X>(x[0][ct], x[1][ct]);
+        }
+        // dR = A^T de
+        f32x4 D[4][2];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            D[t][0] = D[t][1] = zero4();
+#pragma unroll
+            for (int st = t / 2; st < 2; ++st) {
+                const Parts<X> a = lds_parts<X>(rec + R::AT + frag_index_t(t, st) * R::FR + lane * 16, R::MAT);
+#pragma unroll
+                for (int ct = 0; ct < 2; ++ct) D[t][ct] = mm(a, dp[st][ct], D[t][ct]);
+            }
+        }
+        keep_rows(D, keep + KP::DR, scales + 3 * (V / 32), col0, grp, r);
+        // dS = e^gam dS' + Q^T (scale e^Gam dO) - K^T (e^Gam dR)
+#pragma unroll
+        for (int st = 0; st < 2; ++st) {
+            const f32x4 a0 = *(const f32x4 *)(ra + 32 * st + 4 * grp), a1 = *(const f32x4 *)(ra + 32 * st + 16 + 4 * grp);
+            const f32x4 c0 = *(const f32x4 *)(rc + 32 * st + 4 * grp), c1 = *(const f32x4 *)(rc + 32 * st + 16 + 4 * grp);
+            Parts<X> rp[2], op[2];
+#pragma unroll
+            for (int ct = 0; ct < 2; ++ct) {
+                rp[ct] = split<X>(zero4() - a0 * D[2 * st][ct], zero4() - a1 * D[2 * st + 1][ct]);
+                op[ct] = split<X>(c0 * widen(dv[st][ct][0]), c1 * widen(dv[st][ct][1]));
+            }
+            const int row = 32 * st + 4 * grp + (r >> 2);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                const int piece = 4 * (t / 2) + (r & 3), half = 8 * (t % 2);
+                const int at0 = piece_at<K>(row, piece) + half, at1 = piece_at<K>(row + 16, piece) + half;
+                const Parts<1> kt = {join(lds_tr(buf + L::KM + at0), lds_tr(buf + L::KM + at1))},
+                               qt = {join(lds_tr(buf + L::QM + at0), lds_tr(buf + L::QM + at1))};
+#pragma unroll
+                for (int ct = 0; ct < 2; ++ct) {
+                    S[t][ct] = mm(kt, rp[ct], S[t][ct]);
+                    S[t][ct] = mm(qt, op[ct], S[t][ct]);
+                }
+            }
+        }
+    }
+    if (b.dh0) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int ct = 0; ct < 2; ++ct)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) b.dh0[state_at(t, i, ct)] = S[t][ct][i];
+    }
+}
+
+}  // namespace
+
+// Both passes: workgroups 2 u and 2 u + 1 of unit u.
+template <int K, int V>
+__global__ __launch_bounds__(V * 2) void chains_kernel(BwdParams b)
+{
+    using F = Stage<K, V, 1, RecB, false>;
+    constexpr int FB = F::BYTES * F::BUFS, RB = 2 * StageR<K, V>::BYTES, BYTES = FB > RB ? FB : RB;
+    static_assert(BYTES <= 160 * 1024, "LDS of a compute unit");
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[BYTES];
+    const int unit = kda::longest_first(b.f.seq, b.f.HV, blockIdx.x >> 1);
+    if (blockIdx.x & 1)
+        reverse_chain<K, V>(b, unit, lds);
+    else
+        forward_chain<K, V, 1, RecB::X, RecB, false>(b.f, unit, lds, b.keep);
+}
+
+namespace {
+
+// LDS of the local kernel. The four 64 x 64 matrices (128-byte rows, pieces swizzled) lie where
+// the state was, once its products are done.
+template <int K, int V>
+struct Local {
+    static constexpr int MK = 64 * K * 2, MV = 64 * V * 2, MS = V * K * 2;
+    static constexpr int Q = 0, KM = MK, DO = 2 * MK, E = DO + MV, DR = E + MV, S = DR + MV, DS = S + MS;
+    static constexpr int W = S;             // P1 .. P4 [j][i], two parts each
+    static constexpr int END = DS + MS > W + 8 * 8192 ? DS + MS : W + 8 * 8192;
+};
+
+struct LocalScalars {
+    float ghi[64], glo[64], beta[64], rk[64], rq[64];
+    float rowsum[4][64], colsum[4][64];     // of beta_j U, U below the diagonal, per tile column / row
+    float diag[64];                         // of U
+    float cross[64];                        // sum_{i >= t > j} beta_j U_ij within t's own tile
+    float qs[4][64], ks[4][64], kt[4][64];  // per wave: q.dQ[S part], k.dK[S part], k.T
+    float sd[4];                            // per wave: <S, dS'>
+    float most[4];                          // per wave: the largest |dO|
+    float dot[2][4][64];                    // per wave: q.dq, k.dk (L2 norm)
+};
+
+// Within 16 lanes: the sum of the lanes before this one, and of this one and those behind it.
+__device__ __forceinline__ float row_before(float x) {
+    return __builtin_amdgcn_update_dpp(0.f, kda::row_inclusive_scan(x), 0x111, 0xf, 0xf, false);
+}
+__device__ __forceinline__ float row_from(float x) {
+    x += __builtin_amdgcn_update_dpp(0.f, x, 0x101, 0xf, 0xf, false);   // row_shl:1
+    x += __builtin_amdgcn_update_dpp(0.f, x, 0x102, 0xf, 0xf, false);
+    x += __builtin_amdgcn_update_dpp(0.f, x, 0x104, 0xf, 0xf, false);
+    x += __builtin_amdgcn_update_dpp(0.f, x, 0x108, 0xf, 0xf, false);
+    return x;
+}
+
+// rows of [64][64] bf16 with swizzled 16-byte pieces
+__device__ __forceinline__ int w_at(int row, int piece) { return (row * 8 + (piece ^ (row & 7))) * 16; }
+
+}  // namespace
+
+// One workgroup (4 waves) per (chunk slot, q/k head), over the head's value heads: dQ and dK stay
+// in registers, a wave holding K / 4 key dims of all 64 tokens, transposed (a lane: four
+// consecutive dims of one token).
+template <int K, int V>
+__global__ __launch_bounds__(256) void local_kernel(BwdParams b)
+{
+    using L = Local<K, V>;
+    using R = RecB;
+    constexpr int DW = K / 4, ND = DW / 16;     // key dims of a wave, 16-row tiles of them
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[L::END];
+    __shared__ __attribute__((aligned(16))) LocalScalars sc;
+    static_assert(L::END + sizeof(LocalScalars) <= 160 * 1024, "LDS of a compute unit");
+    const Params &p = b.f;
+    const int tid = threadIdx.x, lane = tid & 63;
+    int grp = lane >> 4, r = lane & 15;
+    // LDS addresses are cheap to form and many: without this the compiler forms those of every
+    // phase ahead of the loop over the heads and keeps them in (spilled) registers
+    auto new_phase = [&] {
+        asm volatile("" : "+v"(grp), "+v"(r));
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int slot = blockIdx.x, h = blockIdx.y;
+    int s, nv;
+    int64_t bos;
+    if (!kda::locate_slot<CT>(p.seq, slot, &s, &bos, &nv)) return;
+    const int64_t qk0 = (bos * p.H + h) * K;
+    stage_rows<K, 4>(p.q[0] + qk0, (int64_t)p.H * K, nv, lds + L::Q, wave, lane);
+    stage_rows<K, 4>(p.k[0] + qk0, (int64_t)p.H * K, nv, lds + L::KM, wave, lane);
+
+    // operand A of dims d0 + 16 n .. of this wave, k = 32 rows from `row0` of a staged matrix
+    auto dims_a = [&](int base, int row0, int n) {
+        const int row = row0 + 8 * grp + (r >> 2), piece = (DW * wave + 16 * n) / 8 + ((r & 3) >> 1);
+        const int half = 8 * (r & 1);
+        return join(lds_tr(lds + base + piece_at<K>(row, piece) + half),
+                    lds_tr(lds + base + piece_at<K>(row + 4, piece) + half));
+    };
+    auto half8 = [](bf16x8 x) { return __builtin_bit_cast(kda::f16x8, x); };
+    // operand of 16 tokens from `tok0`, k = 32 columns from `c0` of a [V][64] matrix
+    auto toks_t = [&](int base, int c0, int tok0) {
+        const int row = c0 + 8 * grp + (r >> 2), piece = tok0 / 8 + ((r & 3) >> 1), half = 8 * (r & 1);
+        return join(lds_tr(lds + base + w_at(row, piece) + half), lds_tr(lds + base + w_at(row + 4, piece) + half));
+    };
+    auto row_of = [&](int base, int n, int t) {     // four dims of token 16 t + r of q or k
+        const int d = DW * wave + 16 * n + 4 * grp;
+        f32x4 x;
+        kda::unpack_bf16x4(*(const uint2 *)(lds + base + piece_at<K>(16 * t + r, d / 8) + 2 * (d & 4)), (float *)&x);
+        return x;
+    };
+    auto dot4 = [](f32x4 a, f32x4 c) { return a[0] * c[0] + a[1] * c[1] + a[2] * c[2] + a[3] * c[3]; };
+
+    f32x4 dq[ND][4], dk[ND][4];                     // [dim tile][token tile]
+#pragma unroll
+    for (int n = 0; n < ND; ++n)
+#pragma unroll
+        for (int t = 0; t < 4; ++t) dq[n][t] = dk[n][t] = zero4();
+
+#pragma unroll 1
+    for (int m = 0; m < p.G; ++m) {
+        const int j = h * p.G + m;
+        const size_t at = (size_t)j * p.seq.n_slots + slot;
+        const uint8_t *const keep = b.keep + at * Keep<K, V>::BYTES;
+        const float *const rec = (const float *)(p.rec + at * R::BYTES);
+        if (m > 0) __syncthreads();                 // the previous head is done with the buffers
+        stage_rows<V, 4>(b.d_o + (bos * p.HV + j) * V, (int64_t)p.HV * V, nv, lds + L::DO, wave, lane);
+        // [V][64 tokens] and [V][K] records: V rows of 64 (K) values
+#pragma unroll
+        for (int q = 0; q < V / 64; ++q) {
+            stage_rows<64, 4>((const uint16_t *)(keep + Keep<K, V>::E) + q * 64 * 64, 64, 64, lds + L::E + q * 8192, wave, lane);
+            stage_rows<64, 4>((const uint16_t *)(keep + Keep<K, V>::DR) + q * 64 * 64, 64, 64, lds + L::DR + q * 8192, wave, lane);
+            stage_rows<K, 4>((const uint16_t *)(keep + Keep<K, V>::S) + q * 64 * K, K, 64, lds + L::S + q * L::MK, wave, lane);
+            stage_rows<K, 4>((const uint16_t *)(keep + Keep<K, V>::DS) + q * 64 * K, K, 64, lds + L::DS + q * L::MK, wave, lane);
+        }
+        if (wave == 0) {
+            sc.ghi[lane] = rec[R::GHI / 4 + lane];
+            sc.glo[lane] = rec[R::GLO / 4 + lane];
+            sc.beta[lane] = rec[R::BETA / 4 + lane];
+            sc.rk[lane] = rec[R::RK / 4 + lane];
+            sc.rq[lane] = rec[R::RQ / 4 + lane];
+        }
+        // factors that undo the scales of a 32-column block
+        float fs[V / 32], fds[V / 32], fe[V / 32], fdr[V / 32];
+#pragma unroll
+        for (int st = 0; st < V / 32; ++st) {
+            const float *const f = (const float *)(keep + Keep<K, V>::SCALE) + st;
+            fs[st] = f[0];
+            fds[st] = f[V / 32];
+            fe[st] = f[2 * (V / 32)];
+            fdr[st] = f[3 * (V / 32)];
+        }
+        kda::vm_drain();
+        __syncthreads();
+        const float whi = sc.ghi[63], wlo = sc.glo[63];
+        // dO as fp16, in place
+        constexpr int NP = 64 * V / 8 / 256;
+        uint4 ob[NP];
+        float most = 0.f;
+#pragma unroll
+        for (int q = 0; q < NP; ++q) {
+            ob[q] = *(const uint4 *)(lds + L::DO + (q * 256 + tid) * 16);
+            f32x4 x, y;
+            kda::unpack_bf16x4(make_uint2(ob[q].x, ob[q].y), (float *)&x);
+            kda::unpack_bf16x4(make_uint2(ob[q].z, ob[q].w), (float *)&y);
+            most = max_abs(y, max_abs(x, most));
+        }
+        most = wave_max(most);
+        if (lane == 0) sc.most[wave] = most;
+        __syncthreads();
+        const Scale so = scale_for(fmaxf(fmaxf(sc.most[0], sc.most[1]), fmaxf(sc.most[2], sc.most[3])));
+#pragma unroll
+        for (int q = 0; q < NP; ++q) {
+            f32x4 x, y;
+            kda::unpack_bf16x4(make_uint2(ob[q].x, ob[q].y), (float *)&x);
+            kda::unpack_bf16x4(make_uint2(ob[q].z, ob[q].w), (float *)&y);
+            const uint2 a = half4(x, so.f), c = half4(y, so.f);
+            *(uint4 *)(lds + L::DO + (q * 256 + tid) * 16) = make_uint4(a.x, a.y, c.x, c.y);
+        }
+        __syncthreads();
+
+        new_phase();
+        // the 64 x 64 matrices, lower tiles n = wave, wave + 4, wave + 8 of (0,0) (1,0) (1,1) ...
+        f32x4 w1[3], w2[3];
+        int tis[3], tjs[3];
+#pragma unroll
+        for (int u = 0; u < 3; ++u) {
+            const int n = wave + 4 * u;
+            const int ti = n < 1 ? 0 : n < 3 ? 1 : n < 6 ? 2 : 3, tj = n - ti * (ti + 1) / 2;
+            tis[u] = ti;
+            tjs[u] = tj;
+            if (n >= 10) continue;
+            f32x4 x1 = zero4(), x2 = zero4(), qk = zero4(), kk = zero4();
+#pragma unroll
+            for (int st = 0; st < V / 32; ++st) {
+                const kda::f16x8 e = half8(toks_t(L::E, 32 * st, 16 * tj));
+                x1 += fe[st] * mfma32(half8(lds_b128(lds + L::DO + piece_at<V>(16 * ti + r, 4 * st + grp))), e, zero4());
+                x2 += (fe[st] * fdr[st]) * mfma32(half8(toks_t(L::DR, 32 * st, 16 * ti)), e, zero4());
+            }
+#pragma unroll
+            for (int st = 0; st < K / 32; ++st) {
+                const bf16x8 kj = lds_b128(lds + L::KM + piece_at<K>(16 * tj + r, 4 * st + grp));
+                qk = mfma32(lds_b128(lds + L::Q + piece_at<K>(16 * ti + r, 4 * st + grp)), kj, qk);
+                kk = mfma32(lds_b128(lds + L::KM + piece_at<K>(16 * ti + r, 4 * st + grp)), kj, kk);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            const int jj = 16 * tj + r;
+            const float bj = sc.beta[jj], rkj = sc.rk[jj];
+            float col = 0.f;
+            f32x4 bu;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int i = 16 * ti + 4 * grp + e;
+                const float d = i >= jj && i < nv
+                                    ? __builtin_amdgcn_exp2f((sc.ghi[i] - sc.ghi[jj]) + (sc.glo[i] - sc.glo[jj]))
+                                    : 0.f;
+                const float y1 = d != 0.f ? x1[e] * so.inv * d * p.scale : 0.f;
+                const float y2 = d != 0.f && i > jj ? -x2[e] * d : 0.f;
+                const float uu = rkj * (y1 * sc.rq[i] * qk[e] + y2 * sc.rk[i] * kk[e]);
+                if (i == jj) sc.diag[i] = uu;
+                col += i > jj ? uu : 0.f;
+                float row = i > jj ? bj * uu : 0.f;
+                bu[e] = row;
+#pragma unroll
+                for (int x = 8; x >= 1; x >>= 1) row += __shfl_xor(row, x);
+                if (r == 0) sc.rowsum[tj][i] = row;
+                w1[u][e] = y1 * bj;
+                w2[u][e] = y2 * bj;
+            }
+            col = kda::sum_lane_groups(col);
+            if (grp == 0) sc.colsum[ti][jj] = col;
+            if (ti == tj) {                         // lane column r stands for t: columns j < t of rows i >= t
+                float x = 0.f;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float before = row_before(bu[e]);
+                    x += 4 * grp + e >= r ? before : 0.f;
+                }
+                x = kda::sum_lane_groups(x);
+                if (grp == 0) sc.cross[jj] = x;
+            }
+            new_phase();
+        }
+        // products with the states: dQ and dK of the S part, T
+        float sd = 0.f;
+#pragma unroll
+        for (int q = 0; q < V * K / 8 / 256; ++q) {
+            const int o = (q * 256 + tid) * 16;     // both are swizzled alike
+            const kda::f16x8 x = half8(lds_b128(lds + L::S + o)), y = half8(lds_b128(lds + L::DS + o));
+            float z = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) z += (float)x[e] * (float)y[e];
+            const int block = (q * 256 * 8) / (32 * K);     // 256 pieces lie in one block of columns
+            sd += (fs[block] * fds[block]) * z;
+        }
+        sd = kda::wave_sum(sd);
+        if (lane == 0) sc.sd[wave] = sd;
+        float qs[4] = {0.f, 0.f, 0.f, 0.f}, ks[4] = {0.f, 0.f, 0.f, 0.f}, kt[4] = {0.f, 0.f, 0.f, 0.f};
+        new_phase();
+#pragma unroll
+        for (int n = 0; n < ND; ++n) {
+            f32x4 xs[4], ys[4], zs[4];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) xs[t] = ys[t] = zs[t] = zero4();
+#pragma unroll
+            for (int st = 0; st < V / 32; ++st) {
+                const kda::f16x8 sa = half8(dims_a(L::S, 32 * st, n)), da = half8(dims_a(L::DS, 32 * st, n));
+                const float fx = fs[st], fy = fs[st] * fdr[st], fz = fds[st] * fe[st];
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    xs[t] += fx * mfma32(sa, half8(lds_b128(lds + L::DO + piece_at<V>(16 * t + r, 4 * st + grp))), zero4());
+                    ys[t] += fy * mfma32(sa, half8(toks_t(L::DR, 32 * st, 16 * t)), zero4());
+                    zs[t] += fz * mfma32(da, half8(toks_t(L::E, 32 * st, 16 * t)), zero4());
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                const int i = 16 * t + r;
+                const bool live = i < nv;
+                const float head = __builtin_amdgcn_exp2f(sc.ghi[i] + sc.glo[i]);
+                const float tail = __builtin_amdgcn_exp2f((whi - sc.ghi[i]) + (wlo - sc.glo[i]));
+                const f32x4 x = xs[t] * (live ? so.inv * p.scale * head : 0.f), y = ys[t] * (live ? -head : 0.f),
+                            z = zs[t] * (live ? tail : 0.f);
+                const f32x4 qr = row_of(L::Q, n, t), kr = row_of(L::KM, n, t);
+                qs[t] += dot4(qr, x);
+                ks[t] += dot4(kr, y);
+                kt[t] += dot4(kr, z);
+                dq[n][t] += x;
+                dk[n][t] += y + sc.beta[i] * z;
+            }
+            new_phase();
+        }
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            qs[t] = kda::sum_lane_groups(qs[t]);
+            ks[t] = kda::sum_lane_groups(ks[t]);
+            kt[t] = kda::sum_lane_groups(kt[t]);
+            if (grp == 0) {
+                const int i = 16 * t + r;
+                sc.qs[wave][i] = qs[t] * sc.rq[i];
+                sc.ks[wave][i] = ks[t] * sc.rk[i];
+                sc.kt[wave][i] = kt[t] * sc.rk[i];
+            }
+        }
+        // dv: four columns of a token per lane, from dR
+#pragma unroll
+        for (int q = 0; q < V / 16; ++q) {          // 4 token tiles x V / 16 column tiles, 4 waves
+            const int job = q * 4 + wave, t = job & 3, c0 = 16 * (job >> 2);
+            const s16x4 x = lds_tr(lds + L::DR + w_at(c0 + 4 * grp + (r >> 2), 2 * t + ((r & 3) >> 1)) + 8 * (r & 1));
+            const kda::f16x4 y = __builtin_bit_cast(kda::f16x4, x);
+            const f32x4 z = f32x4{(float)y[0], (float)y[1], (float)y[2], (float)y[3]} * fdr[q / 2];
+            if (16 * t + r < nv)
+                *(uint2 *)(b.dv + ((bos + 16 * t + r) * p.HV + j) * V + c0 + 4 * grp) =
+                    __builtin_bit_cast(uint2, kda::to_bf16x4(z));
+        }
+        __syncthreads();                            // S and dS' are read: the matrices take their place
+        new_phase();
+        uint8_t *const W = lds + L::W;
+        auto put = [&](int k, int ti, int tj, f32x4 x) {    // [j][i], a lane's four i of one j
+            const int d = 16 * ti + 4 * grp;
+            const int to = k * 16384 + w_at(16 * tj + r, d / 8) + 2 * (d & 4);
+            const kda::bf16x4 hi = kda::to_bf16x4(x);
+            kda::bf16x4 lo;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) lo[e] = (__bf16)(x[e] - (float)hi[e]);
+            *(uint2 *)(W + to) = __builtin_bit_cast(uint2, hi);
+            *(uint2 *)(W + to + 8192) = __builtin_bit_cast(uint2, lo);
+        };
+#pragma unroll
+        for (int u = 0; u < 3; ++u) {
+            if (wave + 4 * u >= 10) continue;
+            const int ti = tis[u], tj = tjs[u];
+            const float rkj = sc.rk[16 * tj + r];
+            f32x4 rqi, rki;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                rqi[e] = sc.rq[16 * ti + 4 * grp + e];
+                rki[e] = sc.rk[16 * ti + 4 * grp + e];
+            }
+            put(0, ti, tj, w1[u] * rkj);
+            put(1, ti, tj, w1[u] * rqi);
+            put(2, ti, tj, w2[u] * rki);
+            put(3, ti, tj, w2[u] * rkj);
+        }
+        if (wave >= 2) {                            // the tiles above the diagonal that are read
+            const int ti = wave == 2 ? 0 : 2;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) put(k, ti, ti + 1, zero4());
+        }
+        __syncthreads();
+        // [j][i] matrix k as operand: 16 columns i of tile t over 32 rows j, or 16 rows j over 32 i
+        auto cols = [&](int k, int t, int st) {
+            const int row = 32 * st + 8 * grp + (r >> 2), piece = 2 * t + ((r & 3) >> 1), half = 8 * (r & 1);
+            const uint8_t *const a = W + k * 16384 + w_at(row, piece) + half,
+                          *const c = W + k * 16384 + w_at(row + 4, piece) + half;
+            return Parts<2>{join(lds_tr(a), lds_tr(c)), join(lds_tr(a + 8192), lds_tr(c + 8192))};
+        };
+        auto rows = [&](int k, int t, int st) {
+            return lds_parts<2>(W + k * 16384 + w_at(16 * t + r, 4 * st + grp), 8192);
+        };
+#pragma unroll
+        for (int n = 0; n < ND; ++n)
+#pragma unroll
+            for (int st = 0; st < 2; ++st) {
+                const Parts<1> qa = {dims_a(L::Q, 32 * st, n)}, ka = {dims_a(L::KM, 32 * st, n)};
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    if (st <= t / 2) {
+                        dq[n][t] = mm(ka, cols(0, t, st), dq[n][t]);
+                        dk[n][t] = mm(ka, cols(3, t, st), dk[n][t]);
+                    }
+                    if (st >= t / 2) {
+                        dk[n][t] = mm(qa, rows(1, t, st), dk[n][t]);
+                        dk[n][t] = mm(ka, rows(2, t, st), dk[n][t]);
+                    }
+                }
+                new_phase();
+            }
+        if (wave == 0) {                            // dbeta and dg, a token per lane
+            const int i = lane;
+            const int tau = i >> 4;
+            float left = 0.f, below = 0.f, tiles = 0.f, qsum = 0.f, ksum = 0.f, tsum = 0.f, col = sc.colsum[tau][i];
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                if (w < tau) left += sc.rowsum[w][i];       // tiles left of the token's own
+                if (w > tau) below += sc.colsum[w][i];      // and below it
+                qsum += sc.qs[w][i];
+                ksum += sc.ks[w][i];
+                tsum += sc.kt[w][i];
+            }
+            // whole tiles that cross: (2,0) and (3,0) for tile 1, (3,0) and (3,1) for tile 2
+            const float c0 = row_from(sc.rowsum[0][i]), c1 = row_from(sc.rowsum[1][i < 48 ? 48 : i]);
+            const float t20 = kda::lane_read(c0, 32), t30 = kda::lane_read(c0, 48), t31 = kda::lane_read(c1, 48);
+            if (tau == 1) tiles = t20 + t30;
+            if (tau == 2) tiles = t30 + t31;
+            const bool live = i < nv;
+            const float bt = sc.beta[i], dbt = col + below + tsum + sc.diag[i];
+            const float pairs = sc.cross[i] + row_from(left) + row_before(bt * below) + tiles;
+            float x = live ? qsum + ksum : 0.f, y = live ? bt * tsum : 0.f;
+#pragma unroll
+            for (int d = 1; d < 64; d <<= 1) {
+                const float z = __shfl_down(x, d), u = __shfl_up(y, d);
+                if (lane + d < 64) x += z;
+                if (lane >= d) y += u;
+            }
+            const float before = __shfl_up(y, 1);
+            x += pairs + (lane > 0 ? before : 0.f) +
+                 __builtin_amdgcn_exp2f(whi + wlo) * (sc.sd[0] + sc.sd[1] + sc.sd[2] + sc.sd[3]);
+            if (live) {
+                const int64_t o = (bos + i) * p.HV + j;
+                const float db = p.pre.beta_sigmoid ? dbt * bt * (1.f - bt) : dbt;
+                b.dbeta[o] = __builtin_bit_cast(uint16_t, (__bf16)db);
+                if (b.dg_act)
+                    b.dg_act[o] = x;
+                else
+                    b.dg[o] = __builtin_bit_cast(uint16_t, (__bf16)x);
+            }
+        }
+    }
+    // through the L2 norm: dx = r (dy - y (y.dy)), y = r x
+    float fq[4], fk[4], gq[4] = {0.f, 0.f, 0.f, 0.f}, gk[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+        fq[t] = sc.rq[16 * t + r];
+        fk[t] = sc.rk[16 * t + r];
+    }
+    if (p.pre.qk_l2norm) {
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            float a = 0.f, c = 0.f;
+#pragma unroll
+            for (int n = 0; n < ND; ++n) {
+                a += dot4(row_of(L::Q, n, t), dq[n][t]);
+                c += dot4(row_of(L::KM, n, t), dk[n][t]);
+            }
+            a = kda::sum_lane_groups(a);
+            c = kda::sum_lane_groups(c);
+            if (grp == 0) {
+                sc.dot[0][wave][16 * t + r] = a;
+                sc.dot[1][wave][16 * t + r] = c;
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                gq[t] += sc.dot[0][w][16 * t + r];
+                gk[t] += sc.dot[1][w][16 * t + r];
+            }
+            gq[t] *= fq[t] * fq[t];
+            gk[t] *= fk[t] * fk[t];
+        }
+    }
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+        if (16 * t + r >= nv) continue;
+#pragma unroll
+        for (int n = 0; n < ND; ++n) {
+            f32x4 x = dq[n][t], y = dk[n][t];
+            if (p.pre.qk_l2norm) {
+                x = fq[t] * (x - gq[t] * row_of(L::Q, n, t));
+                y = fk[t] * (y - gk[t] * row_of(L::KM, n, t));
+            }
+            const int64_t o = ((bos + 16 * t + r) * p.H + h) * K + DW * wave + 16 * n + 4 * grp;
+            *(uint2 *)(b.dq + o) = __builtin_bit_cast(uint2, kda::to_bf16x4(x));
+            *(uint2 *)(b.dk + o) = __builtin_bit_cast(uint2, kda::to_bf16x4(y));
+        }
+    }
+}
+
+template <int K, int V>
+hipError_t launch_backward(const BwdParams &b, hipStream_t st)
+{
+    const Params &p = b.f;
+    chains_kernel<K, V><<<dim3(2 * p.seq.N * p.HV), dim3(2 * V), 0, st>>>(b);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || p.seq.T_total == 0) return e;
+    local_kernel<K, V><<<dim3(p.seq.n_slots, p.H), dim3(256), 0, st>>>(b);
+    return hipGetLastError();
+}
+
+// ------------------------------------------------------------------------------------- gate
+
+// One workgroup per value head, over all tokens in a fixed order.
+__global__ __launch_bounds__(256) void gate_backward_kernel(Params p, bool f32, const float *dg_act,
+                                                            void *dg, float *dA, float *ddt)
+{
+    __shared__ double part[2][256];
+    const int j = blockIdx.x, tid = threadIdx.x;
+    const int64_t end = kda::seq_eos(p.seq, p.seq.N - 1, 0);
+    const float a = expf(p.pre.A_log[j]), bias = p.pre.dt_bias ? p.pre.dt_bias[j] : 0.f;
+    double sa = 0.0, sb = 0.0;
+    for (int64_t t = tid; t < end; t += 256) {
+        const int64_t at = t * p.HV + j;
+        const float x = load_io(p.g, at, f32) + bias, d = dg_act[at];
+        float slope, by_a;                  // d g / d x and d g / d A_log
+        if (p.pre.gate == 1) {
+            slope = -a * exact_sigmoid(x);
+            by_a = -a * (fmaxf(x, 0.f) + log1pf(expf(-fabsf(x))));
+        } else {
+            const float y = exact_sigmoid(a * x);
+            slope = p.pre.lower_bound * y * (1.f - y) * a;
+            by_a = slope * x;
+        }
+        const float dx = d * slope;
+        if (f32)
+            ((float *)dg)[at] = dx;
+        else
+            ((uint16_t *)dg)[at] = __builtin_bit_cast(uint16_t, (__bf16)dx);
+        sb += dx;
+        sa += (double)d * by_a;
+    }
+    part[0][tid] = sa;
+    part[1][tid] = sb;
+    for (int n = 128; n >= 1; n >>= 1) {
+        __syncthreads();
+        if (tid < n) {
+            part[0][tid] += part[0][tid + n];
+            part[1][tid] += part[1][tid + n];
+        }
+    }
+    if (tid == 0) {
+        dA[j] = (float)part[0][0];
+        if (ddt) ddt[j] = (float)part[1][0];
+    }
+}
+
+hipError_t launch_gate_backward(const Params &p, bool f32, const float *dg_act, void *dg,
+                                float *dA_log, float *ddt_bias, hipStream_t st)
+{
+    gate_backward_kernel<<<dim3(p.HV), dim3(256), 0, st>>>(p, f32, dg_act, dg, dA_log, ddt_bias);
+    return hipGetLastError();
+}
+
+// --------------------------------------------------------------------------------- fp32 io
+
+__global__ __launch_bounds__(256) void widen_decay_kernel(Params p, int K, float *wide)
+{
+    const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4, row = i / K;
+    if (row >= p.seq.T_total * p.HV) return;
+    float g = activate_gate(p.pre, ((const float *)p.g)[row], (int)(row % p.HV));
+    // e^-105 is below every fp32 number, and the cumsums of the fp32 kernels stay small
+    if (g < -105.f) g = -105.f;
+    const auto rs = kda::buffer_rsrc(wide + (i - threadIdx.x * 4), 4096);
+    kda::bstore16<0>(rs, threadIdx.x * 16, 0, f32x4{g, g, g, g});
+}
+
+__global__ __launch_bounds__(256) void narrow_decay_kernel(Params p, int K, const float *wide,
+                                                           float *dg)
+{
+    const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (row >= kda::seq_eos(p.seq, p.seq.N - 1, 0) * p.HV) return;
+    const int lane = threadIdx.x & 63;
+    float s = wide[row * K + lane];
+    if (K == 128) s += wide[row * K + 64 + lane];
+    s = kda::wave_sum(s);
+    if (lane == 0) dg[row] = s;
+}
+
+hipError_t launch_widen_decay(const Params &p, int K, float *wide, hipStream_t st)
+{
+    const int64_t n = p.seq.T_total * p.HV * K / 4;
+    if (n > 0) widen_decay_kernel<<<dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st>>>(p, K, wide);
+    return hipGetLastError();
+}
+
+hipError_t launch_narrow_decay(const Params &p, int K, const float *wide, float *dg_act, hipStream_t st)
+{
+    const int64_t n = p.seq.T_total * p.HV;
+    if (n > 0) narrow_decay_kernel<<<dim3((unsigned)((n + 3) / 4)), dim3(256), 0, st>>>(p, K, wide, dg_act);
+    return hipGetLastError();
+}
+
+#define GDN_INST(K, V) template hipError_t launch_backward<K, V>(const BwdParams &, hipStream_t);
+GDN_INST(64, 64)
+GDN_INST(64, 128)
+GDN_INST(128, 64)
+GDN_INST(128, 128)
+#undef GDN_INST
+
+}  // namespace gdn

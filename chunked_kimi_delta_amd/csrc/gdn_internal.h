@@ -49,6 +49,17 @@ struct Params {
     Pre pre;
 };
 
+struct BwdParams {
+    Params f;                           // f.rec: RecB records
+    const uint16_t *d_o;                // [T_total][HV][V]
+    const float *dht;                   // or null (zero)
+    uint8_t *keep;                      // Keep records
+    uint16_t *dq, *dk, *dv;             // bf16, like q, k, v
+    uint16_t *dbeta, *dg;               // [T_total][HV] (dg: no gate)
+    float *dg_act;                      // [T_total][HV] gradient of the activated decay (gate)
+    float *dh0;                         // or null
+};
+
 // Arguments of the recurrence (gdn_step, and gdn_fwd for short dense batches).
 struct StepParams {
     int32_t B, T, H, HV, G;
@@ -79,6 +90,33 @@ struct Rec {
 };
 
 __host__ __device__ constexpr int frag_index(int t, int s) { return t < 2 ? t : 2 * t - 2 + s; }
+
+// Record of the backward (bf16 io, two parts): A as above and the row scales, then A^T and M^T,
+// upper triangular, tile t over the tokens of s >= t / 2 in the order (0,0) (0,1) (1,0) (1,1)
+// (2,1) (3,1), and more scalars per token: Gam log2(e) in two floats, beta, rk, rq.
+struct RecB {
+    static constexpr int X = 2, FR = 1024, MAT = 6 * FR;
+    static constexpr int A = 0, RA = X * MAT, RB = RA + 256, RC = RB + 256, EG = RC + 256;
+    static constexpr int AT = RA + FR, MT = AT + X * MAT;
+    static constexpr int GHI = MT + X * MAT, GLO = GHI + 256, BETA = GLO + 256, RK = BETA + 256,
+                         RQ = RK + 256;
+    static constexpr int BYTES = GHI + 2 * FR;
+    static constexpr int REV = RA, REV_KIB = 1 + 2 * X * 6;     // what the reverse pass reads
+};
+
+__host__ __device__ constexpr int frag_index_t(int t, int s) { return t < 2 ? 2 * t + s : 2 + t; }
+
+// What the backward's two passes leave for one (value head, chunk slot), fp16 with one power of
+// two for the 32 columns of a wave (16-bit values of 11 significant bits: the products that use
+// them then add little to the rounding of a bf16 gradient): the state at the chunk's start and the
+// gradient of the state at its end, both transposed [V][K]; e and the gradient of R (which is v's),
+// both [V][64 tokens]; then the factors that undo the scales, [4][V / 32] fp32 in that order.
+// Transposed, because a lane of the passes holds consecutive key dims or tokens of one column.
+template <int K, int V>
+struct Keep {
+    static constexpr int S = 0, DS = V * K * 2, E = 2 * DS, DR = E + V * 128, SCALE = DR + V * 128;
+    static constexpr int BYTES = SCALE + 256;
+};
 
 // ------------------------------------------------------------------------------- operands
 
@@ -118,6 +156,40 @@ __device__ __forceinline__ f32x4 mm(const Parts<XA> &a, const Parts<XB> &b, f32x
         for (int j = 0; j < XB; ++j)
             if (i + j < X) c = mfma32(a.p[i], b.p[j], c);
     return c;
+}
+
+// ---------------------------------------------------------------------- scaled 16-bit values
+
+// The largest of a wave's values (every lane gets it); x >= 0, NaN and infinities included.
+__device__ __forceinline__ float wave_max(float x) {
+    uint32_t u = __float_as_uint(x);
+    auto step = [&](uint32_t y) { u = u > y ? u : y; };
+    step((uint32_t)__builtin_amdgcn_update_dpp(0, (int)u, 0x111, 0xf, 0xf, false));  // row_shr:1
+    step((uint32_t)__builtin_amdgcn_update_dpp(0, (int)u, 0x112, 0xf, 0xf, false));
+    step((uint32_t)__builtin_amdgcn_update_dpp(0, (int)u, 0x114, 0xf, 0xf, false));
+    step((uint32_t)__builtin_amdgcn_update_dpp(0, (int)u, 0x118, 0xf, 0xf, false));
+    step((uint32_t)__builtin_amdgcn_update_dpp(0, (int)u, 0x142, 0xa, 0xf, false));  // row_bcast:15
+    step((uint32_t)__builtin_amdgcn_update_dpp(0, (int)u, 0x143, 0xc, 0xf, false));  // row_bcast:31
+    return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)u, 63));
+}
+
+__device__ __forceinline__ float max_abs(f32x4 x, float m) {
+    return fmaxf(fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3]))), m);
+}
+
+// The power of two that brings values of magnitude up to `most` to just below 2^14 (fp16 then has
+// 11 bits for everything down to 2^-28 of the largest), and its inverse. Below 2^-113 the inverse
+// is clamped: such values turn subnormal.
+struct Scale {
+    float f, inv;
+};
+__device__ __forceinline__ Scale scale_for(float most) {
+    const uint32_t e0 = __float_as_uint(most) >> 23, e = e0 < 14 ? 14 : e0;
+    return Scale{__uint_as_float((267u - e) << 23), __uint_as_float((e - 13u) << 23)};
+}
+
+__device__ __forceinline__ uint2 half4(f32x4 x, float f) {
+    return __builtin_bit_cast(uint2, kda::to_f16x4(x * f));
 }
 
 typedef __attribute__((address_space(3))) uint8_t lds_u8;
@@ -211,6 +283,16 @@ namespace gdn {
 // fp32 x [n] as three bf16 planes, n values apart
 hipError_t launch_split_planes(const float *x, int64_t n, uint16_t *planes, hipStream_t st);
 template <int K> hipError_t launch_prepare(const Params &p, bool f32, hipStream_t st);
+template <int K> hipError_t launch_prepare_bwd(const Params &p, hipStream_t st);    // bf16 io
+template <int K, int V> hipError_t launch_backward(const BwdParams &b, hipStream_t st);
+// The gate's share of the backward: dg and (summed over all tokens of all sequences) dA_log and
+// ddt_bias (or null) from the gradient of the activated decay.
+hipError_t launch_gate_backward(const Params &p, bool f32, const float *dg_act, void *dg,
+                                float *dA_log, float *ddt_bias, hipStream_t st);
+// fp32 io: the activated decay repeated over K, and the gradient of that summed over K
+hipError_t launch_widen_decay(const Params &p, int K, float *wide, hipStream_t st);
+hipError_t launch_narrow_decay(const Params &p, int K, const float *wide, float *dg_act,
+                               hipStream_t st);
 template <int K, int V> hipError_t launch_state(const Params &p, bool f32, hipStream_t st);
 template <int K, int V> hipError_t launch_recurrent(const StepParams &p, bool f32, hipStream_t st);
 }  // namespace gdn

@@ -8,6 +8,8 @@
 // substitution of the 16x16 diagonal blocks (four at once in one wave, a column per lane) and
 // block forward substitution between them on the fp32 matrix core: both backward stable, where
 // a product of powers of L loses digits for keys that resemble each other.
+#include <type_traits>
+
 #include "gdn_internal.h"
 
 namespace gdn {
@@ -58,11 +60,12 @@ __device__ __forceinline__ float row_factor(const uint8_t *m, int row, int part)
 }  // namespace
 
 // IN: planes of q and k (1: bf16 io, 3: fp32 io); X: parts of A and M
-template <int K, int IN, int X>
+// BWD: the backward's record (RecB).
+template <int K, int IN, int X, bool BWD>
 __global__ __launch_bounds__(256) void prepare_kernel(Params p)
 {
     constexpr int MAT = 64 * K * 2;         // bytes of one staged plane
-    using R = Rec<X>;
+    using R = std::conditional_t<BWD, RecB, Rec<X>>;
     __shared__ __attribute__((aligned(1024))) uint8_t kq[2 * IN * MAT];
     __shared__ __attribute__((aligned(16))) float Lm[64 * P], Xm[64 * P];
     __shared__ Scalars sc;
@@ -142,7 +145,7 @@ __global__ __launch_bounds__(256) void prepare_kernel(Params p)
         }
         block_put(Lm, wave, tj, grp, r, l);
     }
-    {
+    if constexpr (!BWD) {
         const int ti = 3 - wave, i = 16 * ti + r;
         for (int tj = 0; tj <= (ti | 1); ++tj) {
             f32x4 m = zero4();
@@ -151,10 +154,33 @@ __global__ __launch_bounds__(256) void prepare_kernel(Params p)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int jj = 16 * tj + 4 * grp + e;
-                    m[e] = i >= jj ? c[e] * (p.scale * sc.rq[i]) * (sc.rk[jj] * sc.beta[jj]) * decay(i, jj) : 0.f;
+                    m[e] = i >= jj && i < nv ? c[e] * (p.scale * sc.rq[i]) * (sc.rk[jj] * sc.beta[jj]) * decay(i, jj) : 0.f;
                 }
             }
             uint8_t *at = rec + R::M + frag_index(ti, tj >> 1) * R::FR + lane * 16 + (tj & 1) * 8;
+#pragma unroll
+            for (int x = 0; x < X; ++x) {
+                const kda::bf16x4 y = kda::to_bf16x4(m);
+                *(uint2 *)(at + x * R::MAT) = __builtin_bit_cast(uint2, y);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) m[e] -= (float)y[e];
+            }
+        }
+    } else {
+        // M^T of token tile tj: a lane's four values are consecutive rows i of one column
+        const int tj = wave, jj = 16 * tj + r;
+        for (int ti = tj & 2; ti < 4; ++ti) {
+            f32x4 m = zero4();
+            if (ti >= tj) {
+                const f32x4 c = gram(qm, ti, km, tj);
+                const float sj = p.scale * sc.rk[jj] * sc.beta[jj];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int i = 16 * ti + 4 * grp + e;
+                    m[e] = i >= jj && i < nv ? c[e] * sj * sc.rq[i] * decay(i, jj) : 0.f;
+                }
+            }
+            uint8_t *at = rec + R::MT + frag_index_t(tj, ti >> 1) * R::FR + lane * 16 + (ti & 1) * 8;
 #pragma unroll
             for (int x = 0; x < X; ++x) {
                 const kda::bf16x4 y = kda::to_bf16x4(m);
@@ -217,13 +243,38 @@ __global__ __launch_bounds__(256) void prepare_kernel(Params p)
         for (int k = 0; k < X; ++k)
             kda::bstore16<0>(rs, f * R::FR + lane * 16, R::A + k * R::MAT, y.p[k]);
     }
+    if constexpr (BWD) {
+        for (int f = wave; f < 6; f += 4) { // A^T's fragments
+            const int t = f < 4 ? f >> 1 : f - 2, st = f < 4 ? (f & 1) : 1, jj = 16 * t + r;
+            f32x4 x[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int i = 32 * st + 16 * u + 4 * grp + e;
+                    x[u][e] = i >= jj ? Xm[i * P + jj] : 0.f;
+                }
+            const Parts<X> y = split<X>(x[0], x[1]);
+            const auto rs = kda::buffer_rsrc(rec, R::BYTES);
+#pragma unroll
+            for (int k = 0; k < X; ++k)
+                kda::bstore16<0>(rs, f * R::FR + lane * 16, R::AT + k * R::MAT, y.p[k]);
+        }
+        if (wave == 2) {
+            ((float *)(rec + R::GHI))[lane] = sc.ghi[lane];
+            ((float *)(rec + R::GLO))[lane] = sc.glo[lane];
+            ((float *)(rec + R::BETA))[lane] = sc.beta[lane];
+            ((float *)(rec + R::RK))[lane] = sc.rk[lane];
+            ((float *)(rec + R::RQ))[lane] = sc.rq[lane];
+        }
+    }
     if (wave == 3) {
         const float whi = sc.ghi[63], wlo = sc.glo[63];
         const float head = __builtin_amdgcn_exp2f(sc.ghi[lane] + sc.glo[lane]);
         const float tail = __builtin_amdgcn_exp2f((whi - sc.ghi[lane]) + (wlo - sc.glo[lane]));
         ((float *)(rec + R::RA))[lane] = head * sc.rk[lane];
         ((float *)(rec + R::RB))[lane] = tail * sc.rk[lane] * sc.beta[lane];
-        ((float *)(rec + R::RC))[lane] = p.scale * head * sc.rq[lane];
+        ((float *)(rec + R::RC))[lane] = lane < nv ? p.scale * head * sc.rq[lane] : 0.f;
         ((float *)(rec + R::EG))[lane] = __builtin_amdgcn_exp2f(whi + wlo);
     }
 }
@@ -258,12 +309,21 @@ hipError_t launch_prepare(const Params &p, bool f32, hipStream_t st)
 {
     const dim3 grid(p.seq.n_slots, p.HV);
     if (f32)
-        prepare_kernel<K, 3, 3><<<grid, dim3(256), 0, st>>>(p);
+        prepare_kernel<K, 3, 3, false><<<grid, dim3(256), 0, st>>>(p);
     else
-        prepare_kernel<K, 1, 2><<<grid, dim3(256), 0, st>>>(p);
+        prepare_kernel<K, 1, 2, false><<<grid, dim3(256), 0, st>>>(p);
     return hipGetLastError();
 }
 
+template <int K>
+hipError_t launch_prepare_bwd(const Params &p, hipStream_t st)
+{
+    prepare_kernel<K, 1, 2, true><<<dim3(p.seq.n_slots, p.HV), dim3(256), 0, st>>>(p);
+    return hipGetLastError();
+}
+
+template hipError_t launch_prepare_bwd<64>(const Params &, hipStream_t);
+template hipError_t launch_prepare_bwd<128>(const Params &, hipStream_t);
 template hipError_t launch_prepare<64>(const Params &, bool, hipStream_t);
 template hipError_t launch_prepare<128>(const Params &, bool, hipStream_t);
 

@@ -538,7 +538,7 @@ __global__ __launch_bounds__(256) void bwd_qk_finalize_kernel(BwdParams b)
     const FwdParams &p = b.f;
     constexpr int PL = K / 64;                      // elements per lane
     const int lane = threadIdx.x & 63;
-    const int64_t rows = p.seq.T_total * p.H;
+    const int64_t rows = seq_eos(p.seq, p.seq.N - 1, 0) * p.H;  // rows behind stay as they were
     const int64_t wid = (blockIdx.x * (int64_t)blockDim.x + threadIdx.x) >> 6;
     const int64_t nw = ((int64_t)gridDim.x * blockDim.x) >> 6;
     for (int64_t row = wid; row < rows; row += nw) {

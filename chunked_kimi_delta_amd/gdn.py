@@ -6,8 +6,9 @@ import ctypes
 
 import torch
 
-from ._lib import GdnArgs, load, strerror
-from .api import _GATES, _IO, _check, _ptr
+from ._lib import GdnArgs, load
+from .act8 import Packed8, unpack8
+from .api import _GATES, _IO, _call, _check, _ptr
 
 
 def _arguments(q, k, v, g, beta, scale, cu_seqlens, initial_state, use_qk_l2norm,
@@ -59,19 +60,6 @@ def _arguments(q, k, v, g, beta, scale, cu_seqlens, initial_state, use_qk_l2norm
         a.gate_lower_bound = float(gate_lower_bound)
         a.A_log, a.dt_bias = _ptr(A_log), _ptr(dt_bias)
     return a
-
-
-def _call(fn, name, dev, stream, *args):
-    """Enqueue on `stream` (default: torch's current stream of `dev`), with `dev` current."""
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    if torch.cuda.current_device() == dev.index:
-        st = fn(*args, stream.cuda_stream)
-    else:
-        with torch.cuda.device(dev):
-            st = fn(*args, stream.cuda_stream)
-    if st != 0:
-        raise RuntimeError(f"{name} failed: {strerror(st)} ({st})")
 
 
 class GdnFwdPlan:
@@ -130,6 +118,69 @@ def gdn_fwd(q, k, v, g, beta, scale=None, cu_seqlens=None, initial_state=None,
     gate_lower_bound)."""
     return GdnFwdPlan(q, k, v, g, beta, scale, cu_seqlens, initial_state, output_final_state,
                       workspace, **prestage)()
+
+
+class GdnBwdPlan:
+    """Validated arguments for repeated gdn_bwd calls: gradients of gdn_fwd with respect to q, k, v,
+    g, beta, initial_state and (with a gate) A_log, dt_bias, from d_o (like v) and dht (fp32
+    [N,HV,K,V] or None).
+
+    Inputs and pre-stage keywords as for GdnFwdPlan. Outputs, allocated once and reused by every
+    call(): dq, dk, dv, dg, dbeta in the io dtype, dh0 fp32 [N,HV,K,V] (when want_dh0), dA_log and
+    ddt_bias fp32 [HV] (with a gate).
+    """
+
+    def __init__(self, q, k, v, g, beta, d_o, dht=None, scale=None, cu_seqlens=None,
+                 initial_state=None, want_dh0=True, workspace=None, use_qk_l2norm=False,
+                 use_beta_sigmoid=False, gate=None, A_log=None, dt_bias=None,
+                 gate_lower_bound=-5.0):
+        self.lib = load()
+        a = _arguments(q, k, v, g, beta, scale, cu_seqlens, initial_state, use_qk_l2norm,
+                       use_beta_sigmoid, gate, A_log, dt_bias, gate_lower_bound)
+        dev = self.device = q.device
+        _check(d_o, "d_o", v.dtype, v.shape, dev)
+        shape = (a.N, a.HV, a.K, a.V)
+        if dht is not None:
+            _check(dht, "dht", torch.float32, shape, dev)
+        f32 = dict(dtype=torch.float32, device=dev)
+        self.dq, self.dk, self.dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+        self.dg, self.dbeta = torch.empty_like(g), torch.empty_like(beta)
+        self.dh0 = torch.empty(shape, **f32) if want_dh0 else None
+        self.dA_log = torch.empty(a.HV, **f32) if gate is not None else None
+        self.ddt_bias = torch.empty(a.HV, **f32) if gate is not None else None
+        self.args = a
+        with torch.cuda.device(dev):
+            need = int(self.lib.gdn_bwd_workspace_bytes(ctypes.byref(a)))
+        if need == 0 and a.B * a.T > 0:
+            raise ValueError("unsupported shapes (K, V in {64, 128}; HV % H == 0)")
+        if workspace is None:
+            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+        else:
+            _check(workspace, "workspace", torch.uint8, workspace.shape, dev)
+            if workspace.numel() < need:
+                raise ValueError(f"workspace too small: {workspace.numel()} < {need} bytes")
+        self.workspace = workspace
+        outs = (self.dq, self.dk, self.dv, self.dg, self.dbeta, self.dh0, self.dA_log, self.ddt_bias)
+        self._outs = outs
+        self._ptrs = (ctypes.byref(a), _ptr(d_o), _ptr(dht), workspace.data_ptr(),
+                      workspace.numel(), *map(_ptr, outs))
+        self._keep = (q, k, v, g, beta, d_o, dht, cu_seqlens, initial_state, A_log, dt_bias)
+
+    def __call__(self, stream=None):
+        """Enqueue the backward on `stream` (default: torch's current stream); returns
+        (dq, dk, dv, dg, dbeta, dh0, dA_log, ddt_bias)."""
+        _call(self.lib.gdn_bwd, "gdn_bwd", self.device, stream, *self._ptrs)
+        return self._outs
+
+
+def gdn_bwd(q, k, v, g, beta, d_o, dht=None, scale=None, cu_seqlens=None, initial_state=None,
+            want_dh0=True, **prestage):
+    """Gated delta rule backward. Returns (dq, dk, dv, dg, dbeta in the io dtype, dh0 fp32 or None,
+    dA_log or None, ddt_bias or None); see GdnBwdPlan. q, k and v may each be a Packed8
+    checkpoint: the gradients are then those at the values that it stands for."""
+    q, k, v = (unpack8(x) if isinstance(x, Packed8) else x for x in (q, k, v))
+    return GdnBwdPlan(q, k, v, g, beta, d_o, dht, scale, cu_seqlens, initial_state, want_dh0,
+                      **prestage)()
 
 
 class GdnStepPlan:

@@ -73,6 +73,24 @@ size_t gdn_fwd_workspace_bytes(const gdn_args *args);
    before their own rounding, for either io type. */
 kda_status gdn_fwd(const gdn_args *args, void *workspace, size_t ws_bytes, void *stream);
 
+/* Gradients of gdn_fwd's inputs from the gradients of a loss with respect to o (d_o, like o) and to
+   final_state (dht, fp32 [N, HV, K, V], or NULL for zero). args as for gdn_fwd (raw inputs with
+   the pre-stage on; o and final_state are not read). Written, caller-owned, 16-byte aligned:
+     dq, dk, dv, dg, dbeta   shapes and io dtype of q, k, v, g, beta; dq, dk summed over the value
+                             heads of a q/k head, dq, dk, dg, dbeta those of the raw inputs
+     dh0                     [N, HV, K, V] fp32, or NULL to skip
+     dA_log, ddt_bias        [HV] fp32 (4-byte aligned): with a gate, dA_log required, ddt_bias or
+                             NULL; ignored without
+   bf16 io: the states and their gradients travel in two bf16 parts as in gdn_fwd (dh0 carries
+   about 17 bits); what enters the other gradients is rounded to bf16 once before its last
+   product. fp32 io: kda_bwd's fp32 arithmetic. Deterministic. Tokens behind the last sequence
+   are left as they were. `workspace`: gdn_bwd_workspace_bytes(args) bytes, 256-byte aligned. */
+size_t gdn_bwd_workspace_bytes(const gdn_args *args);
+
+kda_status gdn_bwd(const gdn_args *args, const void *d_o, const float *dht, void *workspace,
+                   size_t ws_bytes, void *dq, void *dk, void *dv, void *dg, void *dbeta,
+                   float *dh0, float *dA_log, float *ddt_bias, void *stream);
+
 /* One serving step: B rows of T new tokens each, row b on the state in slot state_indices[b]
    of `state` [slots, HV, K, V] fp32, updated in place. state_indices: device int32 [B], or
    NULL for slot b (slots >= B then). A row whose index is negative or >= slots is padding: its

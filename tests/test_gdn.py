@@ -115,6 +115,24 @@ def test_packed_arguments(lib):
     assert lib.gdn_step(ctypes.byref(args(cu_seqlens=FAKE)), FAKE, FAKE, 4, None) == _lib.KDA_ERR_INVALID_ARG
 
 
+@pytest.mark.parametrize("kw,status", BAD)
+def test_backward_refuses_bad_arguments(lib, kw, status):
+    if "o" in kw:
+        return                      # not read by the backward
+    call = lambda a, d_o=FAKE, dA=FAKE, outs=(FAKE,) * 5, ws=FAKE, n=1 << 50: lib.gdn_bwd(
+        ctypes.byref(a), d_o, FAKE, ws, n, *outs, FAKE, dA, None, None)
+    assert call(args(**kw)) == status
+    if kw == dict(K=96):            # and what the backward alone takes
+        a, bad = args(), _lib.KDA_ERR_INVALID_ARG
+        assert call(a, d_o=None) == call(a, outs=(FAKE, None, FAKE, FAKE, FAKE)) == bad
+        assert call(args(gate=1, A_log=FAKE), dA=None) == call(args(gate=1, A_log=FAKE), dA=FAKE + 2) == bad
+        for io in (0, 1):
+            a = args(io=io)
+            need = lib.gdn_bwd_workspace_bytes(ctypes.byref(a))
+            assert need > 0
+            assert call(a, ws=None) == call(a, n=need - 1) == call(a, ws=FAKE + 16) == _lib.KDA_ERR_WORKSPACE
+
+
 def test_workspace(lib):
     need = lambda **kw: lib.gdn_fwd_workspace_bytes(ctypes.byref(args(**kw)))
     assert need() > 0 and need(T=16) == 0 and need(K=96) == 0
@@ -146,6 +164,11 @@ def test_act8_refuses_bad_arguments(lib, kw, status):
 
 def test_binding_refuses_before_any_call():
     a = make(T=20, K=64, V=64)
+    with pytest.raises(ValueError, match="HIP device"):
+        kda.gdn_bwd(**a, d_o=a["v"])
+    for fn in (kda.chunk_gdn, kda.chunk_kda):
+        with pytest.raises(ValueError, match="HIP device"):
+            fn(**a)
     with pytest.raises(ValueError, match="HIP device"):
         kda.gdn_fwd(**a)
     with pytest.raises(TypeError, match="io dtype"):
