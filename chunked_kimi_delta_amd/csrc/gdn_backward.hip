@@ -38,20 +38,24 @@ struct StageR {                             // LDS of one chunk of the reverse p
     static constexpr int BYTES = REC + RecB::REV_KIB * 1024;
 };
 
+// The reverse pass over chunks c1 - 1 .. c0, from the gradient `init` of the state behind them (null:
+// zero) to the gradient `end` of the state before them (or null).
 template <int K, int V>
-__device__ __forceinline__ void reverse_chain(const BwdParams &b, int unit, uint8_t *lds)
+__device__ __forceinline__ void reverse_chain(const BwdParams &b, int s, int j, int c0, int c1,
+                                              const float *init, float *end, uint8_t *lds,
+                                              Maxima<V / 16> *mx)
 {
     using L = StageR<K, V>;
     using R = RecB;
-    constexpr int X = R::X, NW = V / 32, NT = K / 16;
+    using KP = Keep<K, V>;
+    constexpr int X = R::X, NW = V / 16, NT = K / 16;
     const Params &p = b.f;
     const int tid = threadIdx.x, lane = tid & 63, grp = lane >> 4, r = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int s = unit / p.HV, j = unit % p.HV, h = j / p.G;
+    const int h = j / p.G;
     const int64_t bos = kda::seq_bos(p.seq, s), eos = kda::seq_eos(p.seq, s, bos);
-    const int nc = (int)((eos - bos + CT - 1) / CT);
     const size_t slot0 = (size_t)j * p.seq.n_slots + bos / CT + s;
-    const int col0 = 32 * wave;
+    const int col0 = 16 * wave;
 
     auto stage = [&](int c, uint8_t *buf) {
         const int64_t t0 = bos + (int64_t)CT * c;
@@ -62,132 +66,111 @@ __device__ __forceinline__ void reverse_chain(const BwdParams &b, int unit, uint
         stage_rows<V, NW>(b.d_o + (t0 * p.HV + j) * V, (int64_t)p.HV * V, nv, buf + L::DO, wave, lane);
         stage_block<NW>(p.rec + (slot0 + c) * R::BYTES + R::REV, R::REV_KIB, buf + L::REC, wave, lane);
     };
-    if (nc > 0) stage(nc - 1, lds);
+    if (c0 < c1) stage(c1 - 1, lds);
+    auto kept = [&](int c) { return b.keep + (slot0 + c) * KP::BYTES; };
 
-    f32x4 S[NT][2];                         // dS, laid out as the forward's S
-    const size_t st_off = ((size_t)s * p.HV + j) * K * V + col0 + r;
-    auto state_at = [&](int t, int i, int ct) {
-        return st_off + (size_t)(32 * (t / 2) + 8 * grp + 4 * (t % 2) + i) * V + 16 * ct;
-    };
+    f32x4 S[NT], D[4];                      // dS, laid out as the forward's S; dR
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int ct = 0; ct < 2; ++ct)
+        for (int i = 0; i < 4; ++i) S[t][i] = init ? init[(size_t)state_row(t, i, grp) * V + col0 + r] : 0.f;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) S[t][ct][i] = b.dht ? b.dht[state_at(t, i, ct)] : 0.f;
+    for (int t = 0; t < 4; ++t) D[t] = zero4();
 
 #pragma unroll 1
-    for (int c = nc - 1; c >= 0; --c) {
-        uint8_t *const buf = lds + ((nc - 1 - c) & 1) * L::BYTES;
-        uint8_t *const keep = b.keep + (slot0 + c) * Keep<K, V>::BYTES;
+    for (int c = c1 - 1; c >= c0; --c) {
+        uint8_t *const buf = lds + ((c1 - 1 - c) & 1) * L::BYTES;
+        {
+            const float x = largest(S), y = largest(D);
+            if (lane == 0) {
+                mx->state[c & 1][wave] = x;
+                mx->rows[c & 1][wave] = y;
+            }
+        }
         kda::vm_drain();
         __syncthreads();
-        if (c > 0) stage(c - 1, lds + ((nc - c) & 1) * L::BYTES);
+        if (c > c0) stage(c - 1, lds + ((c1 - c) & 1) * L::BYTES);
+        keep_state(S, mx->scale(mx->state[c & 1]), kept(c) + KP::DS, (float *)(kept(c) + KP::SCALE) + 1, col0 + r, grp);
+        if (c < c1 - 1)
+            keep_rows(D, mx->scale(mx->rows[c & 1]), kept(c + 1) + KP::DR, (float *)(kept(c + 1) + KP::SCALE) + 3,
+                      col0 + r, grp);
         const uint8_t *const rec = buf + L::REC - R::REV;
         const float *const ra = (const float *)(rec + R::RA), *const rb = (const float *)(rec + R::RB),
                     *const rc = (const float *)(rec + R::RC);
         const float eg = *(const float *)(rec + R::EG);
-        using KP = Keep<K, V>;
-        float *const scales = (float *)(keep + KP::SCALE) + wave;
-        keep_state<K>(S, keep + KP::DS, scales + V / 32, col0, grp, r);
         // K dS'
-        f32x4 kS[4][2];
+        f32x4 kS[4];
 #pragma unroll
-        for (int t = 0; t < 4; ++t) kS[t][0] = kS[t][1] = zero4();
+        for (int t = 0; t < 4; ++t) kS[t] = zero4();
 #pragma unroll
         for (int st = 0; st < K / 32; ++st) {
-            Parts<X> sp[2];
+            const Parts<X> sp = split<X>(S[2 * st], S[2 * st + 1]);
 #pragma unroll
-            for (int ct = 0; ct < 2; ++ct) sp[ct] = split<X>(S[2 * st][ct], S[2 * st + 1][ct]);
-#pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                const Parts<1> kk = {lds_b128(buf + L::KM + piece_at<K>(16 * t + r, 4 * st + grp))};
-#pragma unroll
-                for (int ct = 0; ct < 2; ++ct) kS[t][ct] = mm(kk, sp[ct], kS[t][ct]);
-            }
+            for (int t = 0; t < 4; ++t)
+                kS[t] = mm(Parts<1>{lds_b128(buf + L::KM + piece_at<K>(16 * t + r, 4 * st + grp))}, sp, kS[t]);
         }
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int ct = 0; ct < 2; ++ct) S[t][ct] *= eg;
+        for (int t = 0; t < NT; ++t) S[t] *= eg;
         // de = M^T dO + beta e^{gam-Gam} (K dS'); dO of tokens 32 st + 4 g .. + 3, + 16 per lane
-        s16x4 dv[2][2][2];
+        s16x4 dv[2][2];
 #pragma unroll
         for (int st = 0; st < 2; ++st)
 #pragma unroll
             for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int ct = 0; ct < 2; ++ct)
-                    dv[st][ct][u] = lds_tr(buf + L::DO +
-                                           piece_at<V>(32 * st + 16 * u + 4 * grp + (r >> 2),
-                                                       col0 / 8 + 2 * ct + ((r & 3) >> 1)) + 8 * (r & 1));
-        Parts<X> dp[2][2];
+                dv[st][u] = lds_tr(buf + L::DO + piece_at<V>(32 * st + 16 * u + 4 * grp + (r >> 2),
+                                                             col0 / 8 + ((r & 3) >> 1)) + 8 * (r & 1));
+        Parts<X> dp[2];
 #pragma unroll
         for (int st = 0; st < 2; ++st) {
-            f32x4 x[2][2];
+            f32x4 x[2];
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 const int t = 2 * st + u;
-                const f32x4 bs = *(const f32x4 *)(rb + 16 * t + 4 * grp);
+                x[u] = *(const f32x4 *)(rb + 16 * t + 4 * grp) * kS[t];
 #pragma unroll
-                for (int ct = 0; ct < 2; ++ct) x[u][ct] = bs * kS[t][ct];
-#pragma unroll
-                for (int s2 = st; s2 < 2; ++s2) {
-                    const Parts<X> m = lds_parts<X>(rec + R::MT + frag_index_t(t, s2) * R::FR + lane * 16, R::MAT);
-#pragma unroll
-                    for (int ct = 0; ct < 2; ++ct)
-                        x[u][ct] = mm(m, Parts<1>{join(dv[s2][ct][0], dv[s2][ct][1])}, x[u][ct]);
-                }
+                for (int s2 = st; s2 < 2; ++s2)
+                    x[u] = mm(lds_parts<X>(rec + R::MT + frag_index_t(t, s2) * R::FR + lane * 16, R::MAT),
+                              Parts<1>{join(dv[s2][0], dv[s2][1])}, x[u]);
             }
-#pragma unroll
-            for (int ct = 0; ct < 2; ++ct) dp[st][ct] = split<X>(x[0][ct], x[1][ct]);
+            dp[st] = split<X>(x[0], x[1]);
         }
         // dR = A^T de
-        f32x4 D[4][2];
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-            D[t][0] = D[t][1] = zero4();
+            D[t] = zero4();
 #pragma unroll
-            for (int st = t / 2; st < 2; ++st) {
-                const Parts<X> a = lds_parts<X>(rec + R::AT + frag_index_t(t, st) * R::FR + lane * 16, R::MAT);
-#pragma unroll
-                for (int ct = 0; ct < 2; ++ct) D[t][ct] = mm(a, dp[st][ct], D[t][ct]);
-            }
+            for (int st = t / 2; st < 2; ++st)
+                D[t] = mm(lds_parts<X>(rec + R::AT + frag_index_t(t, st) * R::FR + lane * 16, R::MAT), dp[st], D[t]);
         }
-        keep_rows(D, keep + KP::DR, scales + 3 * (V / 32), col0, grp, r);
         // dS = e^gam dS' + Q^T (scale e^Gam dO) - K^T (e^Gam dR)
 #pragma unroll
         for (int st = 0; st < 2; ++st) {
             const f32x4 a0 = *(const f32x4 *)(ra + 32 * st + 4 * grp), a1 = *(const f32x4 *)(ra + 32 * st + 16 + 4 * grp);
-            const f32x4 c0 = *(const f32x4 *)(rc + 32 * st + 4 * grp), c1 = *(const f32x4 *)(rc + 32 * st + 16 + 4 * grp);
-            Parts<X> rp[2], op[2];
-#pragma unroll
-            for (int ct = 0; ct < 2; ++ct) {
-                rp[ct] = split<X>(zero4() - a0 * D[2 * st][ct], zero4() - a1 * D[2 * st + 1][ct]);
-                op[ct] = split<X>(c0 * widen(dv[st][ct][0]), c1 * widen(dv[st][ct][1]));
-            }
+            const f32x4 c0v = *(const f32x4 *)(rc + 32 * st + 4 * grp), c1v = *(const f32x4 *)(rc + 32 * st + 16 + 4 * grp);
+            const Parts<X> rp = split<X>(zero4() - a0 * D[2 * st], zero4() - a1 * D[2 * st + 1]),
+                           op = split<X>(c0v * widen(dv[st][0]), c1v * widen(dv[st][1]));
             const int row = 32 * st + 4 * grp + (r >> 2);
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
                 const int piece = 4 * (t / 2) + (r & 3), half = 8 * (t % 2);
                 const int at0 = piece_at<K>(row, piece) + half, at1 = piece_at<K>(row + 16, piece) + half;
-                const Parts<1> kt = {join(lds_tr(buf + L::KM + at0), lds_tr(buf + L::KM + at1))},
-                               qt = {join(lds_tr(buf + L::QM + at0), lds_tr(buf + L::QM + at1))};
-#pragma unroll
-                for (int ct = 0; ct < 2; ++ct) {
-                    S[t][ct] = mm(kt, rp[ct], S[t][ct]);
-                    S[t][ct] = mm(qt, op[ct], S[t][ct]);
-                }
+                S[t] = mm(Parts<1>{join(lds_tr(buf + L::KM + at0), lds_tr(buf + L::KM + at1))}, rp, S[t]);
+                S[t] = mm(Parts<1>{join(lds_tr(buf + L::QM + at0), lds_tr(buf + L::QM + at1))}, op, S[t]);
             }
         }
     }
-    if (b.dh0) {
+    if (c0 < c1) {
+        const float y = largest(D);
+        if (lane == 0) mx->rows[(c0 - 1) & 1][wave] = y;
+        __syncthreads();
+        keep_rows(D, mx->scale(mx->rows[(c0 - 1) & 1]), kept(c0) + KP::DR, (float *)(kept(c0) + KP::SCALE) + 3,
+                  col0 + r, grp);
+    }
+    if (end) {
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int ct = 0; ct < 2; ++ct)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) b.dh0[state_at(t, i, ct)] = S[t][ct][i];
+            for (int i = 0; i < 4; ++i) end[(size_t)state_row(t, i, grp) * V + col0 + r] = S[t][i];
     }
 }
 
@@ -195,17 +178,24 @@ __device__ __forceinline__ void reverse_chain(const BwdParams &b, int unit, uint
 
 // Both passes: workgroups 2 u and 2 u + 1 of unit u.
 template <int K, int V>
-__global__ __launch_bounds__(V * 2) void chains_kernel(BwdParams b)
+__global__ __launch_bounds__(V * 4) void chains_kernel(BwdParams b)
 {
-    using F = Stage<K, V, 1, RecB, false>;
+    using F = Stage<K, V, 1, RecB, KEEP>;
     constexpr int FB = F::BYTES * F::BUFS, RB = 2 * StageR<K, V>::BYTES, BYTES = FB > RB ? FB : RB;
-    static_assert(BYTES <= 160 * 1024, "LDS of a compute unit");
     __shared__ __attribute__((aligned(1024))) uint8_t lds[BYTES];
-    const int unit = kda::longest_first(b.f.seq, b.f.HV, blockIdx.x >> 1);
+    __shared__ Maxima<V / 16> mx;
+    static_assert(BYTES + sizeof(mx) <= 160 * 1024, "LDS of a compute unit");
+    const Params &p = b.f;
+    const int unit = kda::longest_first(p.seq, p.HV, blockIdx.x >> 1);
+    const int s = unit / p.HV, j = unit % p.HV;
+    const int64_t bos = kda::seq_bos(p.seq, s), eos = kda::seq_eos(p.seq, s, bos);
+    const int nc = (int)((eos - bos + CT - 1) / CT);
+    const size_t at = ((size_t)s * p.HV + j) * K * V;
     if (blockIdx.x & 1)
-        reverse_chain<K, V>(b, unit, lds);
+        reverse_chain<K, V>(b, s, j, 0, nc, b.dht ? b.dht + at : nullptr, b.dh0 ? b.dh0 + at : nullptr, lds, &mx);
     else
-        forward_chain<K, V, 1, RecB::X, RecB, false>(b.f, unit, lds, b.keep);
+        forward_chain<K, V, V, 1, RecB::X, RecB, KEEP>(p, s, j, 0, nc, 0, p.h0 ? p.h0 + at : nullptr, nullptr, lds,
+                                                       b.keep, &mx);
 }
 
 namespace {
@@ -220,15 +210,15 @@ struct Local {
     static constexpr int END = DS + MS > W + 8 * 8192 ? DS + MS : W + 8 * 8192;
 };
 
+template <int NW>
 struct LocalScalars {
     float ghi[64], glo[64], beta[64], rk[64], rq[64];
     float rowsum[4][64], colsum[4][64];     // of beta_j U, U below the diagonal, per tile column / row
     float diag[64];                         // of U
     float cross[64];                        // sum_{i >= t > j} beta_j U_ij within t's own tile
-    float qs[4][64], ks[4][64], kt[4][64];  // per wave: q.dQ[S part], k.dK[S part], k.T
-    float sd[4];                            // per wave: <S, dS'>
-    float most[4];                          // per wave: the largest |dO|
-    float dot[2][4][64];                    // per wave: q.dq, k.dk (L2 norm)
+    float qs[NW][64], ks[NW][64], kt[NW][64];   // per wave: q.dQ[S part], k.dK[S part], k.T
+    float sd[NW], most[NW];                 // per wave: <S, dS'>, the largest |dO|
+    float dot[2][NW][64];                   // per wave: q.dq, k.dk (L2 norm)
 };
 
 // Within 16 lanes: the sum of the lanes before this one, and of this one and those behind it.
@@ -248,18 +238,17 @@ __device__ __forceinline__ int w_at(int row, int piece) { return (row * 8 + (pie
 
 }  // namespace
 
-// One workgroup (4 waves) per (chunk slot, q/k head), over the head's value heads: dQ and dK stay
-// in registers, a wave holding K / 4 key dims of all 64 tokens, transposed (a lane: four
-// consecutive dims of one token).
+// One workgroup per (chunk slot, q/k head), over the head's value heads, one wave per 16 key dims:
+// dQ and dK stay in registers, transposed (a lane: four consecutive dims of one token).
 template <int K, int V>
-__global__ __launch_bounds__(256) void local_kernel(BwdParams b)
+__global__ __launch_bounds__(K * 4) void local_kernel(BwdParams b)
 {
     using L = Local<K, V>;
     using R = RecB;
-    constexpr int DW = K / 4, ND = DW / 16;     // key dims of a wave, 16-row tiles of them
+    constexpr int NW = K / 16, NTH = 64 * NW;
     __shared__ __attribute__((aligned(1024))) uint8_t lds[L::END];
-    __shared__ __attribute__((aligned(16))) LocalScalars sc;
-    static_assert(L::END + sizeof(LocalScalars) <= 160 * 1024, "LDS of a compute unit");
+    __shared__ __attribute__((aligned(16))) LocalScalars<NW> sc;
+    static_assert(L::END + sizeof(sc) <= 160 * 1024, "LDS of a compute unit");
     const Params &p = b.f;
     const int tid = threadIdx.x, lane = tid & 63;
     int grp = lane >> 4, r = lane & 15;
@@ -275,12 +264,12 @@ __global__ __launch_bounds__(256) void local_kernel(BwdParams b)
     int64_t bos;
     if (!kda::locate_slot<CT>(p.seq, slot, &s, &bos, &nv)) return;
     const int64_t qk0 = (bos * p.H + h) * K;
-    stage_rows<K, 4>(p.q[0] + qk0, (int64_t)p.H * K, nv, lds + L::Q, wave, lane);
-    stage_rows<K, 4>(p.k[0] + qk0, (int64_t)p.H * K, nv, lds + L::KM, wave, lane);
+    stage_rows<K, NW>(p.q[0] + qk0, (int64_t)p.H * K, nv, lds + L::Q, wave, lane);
+    stage_rows<K, NW>(p.k[0] + qk0, (int64_t)p.H * K, nv, lds + L::KM, wave, lane);
 
-    // operand A of dims d0 + 16 n .. of this wave, k = 32 rows from `row0` of a staged matrix
-    auto dims_a = [&](int base, int row0, int n) {
-        const int row = row0 + 8 * grp + (r >> 2), piece = (DW * wave + 16 * n) / 8 + ((r & 3) >> 1);
+    // operand A of this wave's 16 key dims, k = 32 rows from `row0` of a staged matrix
+    auto dims_a = [&](int base, int row0) {
+        const int row = row0 + 8 * grp + (r >> 2), piece = 2 * wave + ((r & 3) >> 1);
         const int half = 8 * (r & 1);
         return join(lds_tr(lds + base + piece_at<K>(row, piece) + half),
                     lds_tr(lds + base + piece_at<K>(row + 4, piece) + half));
@@ -291,19 +280,17 @@ __global__ __launch_bounds__(256) void local_kernel(BwdParams b)
         const int row = c0 + 8 * grp + (r >> 2), piece = tok0 / 8 + ((r & 3) >> 1), half = 8 * (r & 1);
         return join(lds_tr(lds + base + w_at(row, piece) + half), lds_tr(lds + base + w_at(row + 4, piece) + half));
     };
-    auto row_of = [&](int base, int n, int t) {     // four dims of token 16 t + r of q or k
-        const int d = DW * wave + 16 * n + 4 * grp;
+    auto row_of = [&](int base, int t) {            // four dims of token 16 t + r of q or k
+        const int d = 16 * wave + 4 * grp;
         f32x4 x;
         kda::unpack_bf16x4(*(const uint2 *)(lds + base + piece_at<K>(16 * t + r, d / 8) + 2 * (d & 4)), (float *)&x);
         return x;
     };
     auto dot4 = [](f32x4 a, f32x4 c) { return a[0] * c[0] + a[1] * c[1] + a[2] * c[2] + a[3] * c[3]; };
 
-    f32x4 dq[ND][4], dk[ND][4];                     // [dim tile][token tile]
+    f32x4 dq[4], dk[4];                             // [token tile]
 #pragma unroll
-    for (int n = 0; n < ND; ++n)
-#pragma unroll
-        for (int t = 0; t < 4; ++t) dq[n][t] = dk[n][t] = zero4();
+    for (int t = 0; t < 4; ++t) dq[t] = dk[t] = zero4();
 
 #pragma unroll 1
     for (int m = 0; m < p.G; ++m) {
@@ -312,14 +299,14 @@ __global__ __launch_bounds__(256) void local_kernel(BwdParams b)
         const uint8_t *const keep = b.keep + at * Keep<K, V>::BYTES;
         const float *const rec = (const float *)(p.rec + at * R::BYTES);
         if (m > 0) __syncthreads();                 // the previous head is done with the buffers
-        stage_rows<V, 4>(b.d_o + (bos * p.HV + j) * V, (int64_t)p.HV * V, nv, lds + L::DO, wave, lane);
+        stage_rows<V, NW>(b.d_o + (bos * p.HV + j) * V, (int64_t)p.HV * V, nv, lds + L::DO, wave, lane);
         // [V][64 tokens] and [V][K] records: V rows of 64 (K) values
 #pragma unroll
         for (int q = 0; q < V / 64; ++q) {
-            stage_rows<64, 4>((const uint16_t *)(keep + Keep<K, V>::E) + q * 64 * 64, 64, 64, lds + L::E + q * 8192, wave, lane);
-            stage_rows<64, 4>((const uint16_t *)(keep + Keep<K, V>::DR) + q * 64 * 64, 64, 64, lds + L::DR + q * 8192, wave, lane);
-            stage_rows<K, 4>((const uint16_t *)(keep + Keep<K, V>::S) + q * 64 * K, K, 64, lds + L::S + q * L::MK, wave, lane);
-            stage_rows<K, 4>((const uint16_t *)(keep + Keep<K, V>::DS) + q * 64 * K, K, 64, lds + L::DS + q * L::MK, wave, lane);
+            stage_rows<64, NW>((const uint16_t *)(keep + Keep<K, V>::E) + q * 64 * 64, 64, 64, lds + L::E + q * 8192, wave, lane);
+            stage_rows<64, NW>((const uint16_t *)(keep + Keep<K, V>::DR) + q * 64 * 64, 64, 64, lds + L::DR + q * 8192, wave, lane);
+            stage_rows<K, NW>((const uint16_t *)(keep + Keep<K, V>::S) + q * 64 * K, K, 64, lds + L::S + q * L::MK, wave, lane);
+            stage_rows<K, NW>((const uint16_t *)(keep + Keep<K, V>::DS) + q * 64 * K, K, 64, lds + L::DS + q * L::MK, wave, lane);
         }
         if (wave == 0) {
             sc.ghi[lane] = rec[R::GHI / 4 + lane];
@@ -328,26 +315,18 @@ __global__ __launch_bounds__(256) void local_kernel(BwdParams b)
             sc.rk[lane] = rec[R::RK / 4 + lane];
             sc.rq[lane] = rec[R::RQ / 4 + lane];
         }
-        // factors that undo the scales of a 32-column block
-        float fs[V / 32], fds[V / 32], fe[V / 32], fdr[V / 32];
-#pragma unroll
-        for (int st = 0; st < V / 32; ++st) {
-            const float *const f = (const float *)(keep + Keep<K, V>::SCALE) + st;
-            fs[st] = f[0];
-            fds[st] = f[V / 32];
-            fe[st] = f[2 * (V / 32)];
-            fdr[st] = f[3 * (V / 32)];
-        }
+        const float *const inv = (const float *)(keep + Keep<K, V>::SCALE);
+        const float fs = inv[0], fds = inv[1], fe = inv[2], fdr = inv[3];
         kda::vm_drain();
         __syncthreads();
         const float whi = sc.ghi[63], wlo = sc.glo[63];
         // dO as fp16, in place
-        constexpr int NP = 64 * V / 8 / 256;
+        constexpr int NP = 64 * V / 8 / NTH;
         uint4 ob[NP];
         float most = 0.f;
 #pragma unroll
         for (int q = 0; q < NP; ++q) {
-            ob[q] = *(const uint4 *)(lds + L::DO + (q * 256 + tid) * 16);
+            ob[q] = *(const uint4 *)(lds + L::DO + (q * NTH + tid) * 16);
             f32x4 x, y;
             kda::unpack_bf16x4(make_uint2(ob[q].x, ob[q].y), (float *)&x);
             kda::unpack_bf16x4(make_uint2(ob[q].z, ob[q].w), (float *)&y);
@@ -356,24 +335,25 @@ __global__ __launch_bounds__(256) void local_kernel(BwdParams b)
         most = wave_max(most);
         if (lane == 0) sc.most[wave] = most;
         __syncthreads();
-        const Scale so = scale_for(fmaxf(fmaxf(sc.most[0], sc.most[1]), fmaxf(sc.most[2], sc.most[3])));
+        const Scale so = Maxima<NW>::scale(sc.most);
 #pragma unroll
         for (int q = 0; q < NP; ++q) {
             f32x4 x, y;
             kda::unpack_bf16x4(make_uint2(ob[q].x, ob[q].y), (float *)&x);
             kda::unpack_bf16x4(make_uint2(ob[q].z, ob[q].w), (float *)&y);
             const uint2 a = half4(x, so.f), c = half4(y, so.f);
-            *(uint4 *)(lds + L::DO + (q * 256 + tid) * 16) = make_uint4(a.x, a.y, c.x, c.y);
+            *(uint4 *)(lds + L::DO + (q * NTH + tid) * 16) = make_uint4(a.x, a.y, c.x, c.y);
         }
         __syncthreads();
 
         new_phase();
-        // the 64 x 64 matrices, lower tiles n = wave, wave + 4, wave + 8 of (0,0) (1,0) (1,1) ...
-        f32x4 w1[3], w2[3];
-        int tis[3], tjs[3];
+        // the 64 x 64 matrices, lower tiles n = wave, wave + NW, .. of (0,0) (1,0) (1,1) ...
+        constexpr int NU = (10 + NW - 1) / NW;
+        f32x4 w1[NU], w2[NU];
+        int tis[NU], tjs[NU];
 #pragma unroll
-        for (int u = 0; u < 3; ++u) {
-            const int n = wave + 4 * u;
+        for (int u = 0; u < NU; ++u) {
+            const int n = wave + NW * u;
             const int ti = n < 1 ? 0 : n < 3 ? 1 : n < 6 ? 2 : 3, tj = n - ti * (ti + 1) / 2;
             tis[u] = ti;
             tjs[u] = tj;
@@ -382,8 +362,8 @@ __global__ __launch_bounds__(256) void local_kernel(BwdParams b)
 #pragma unroll
             for (int st = 0; st < V / 32; ++st) {
                 const kda::f16x8 e = half8(toks_t(L::E, 32 * st, 16 * tj));
-                x1 += fe[st] * mfma32(half8(lds_b128(lds + L::DO + piece_at<V>(16 * ti + r, 4 * st + grp))), e, zero4());
-                x2 += (fe[st] * fdr[st]) * mfma32(half8(toks_t(L::DR, 32 * st, 16 * ti)), e, zero4());
+                x1 = mfma32(half8(lds_b128(lds + L::DO + piece_at<V>(16 * ti + r, 4 * st + grp))), e, x1);
+                x2 = mfma32(half8(toks_t(L::DR, 32 * st, 16 * ti)), e, x2);
             }
 #pragma unroll
             for (int st = 0; st < K / 32; ++st) {
@@ -393,7 +373,7 @@ __global__ __launch_bounds__(256) void local_kernel(BwdParams b)
             }
             __builtin_amdgcn_sched_barrier(0);
             const int jj = 16 * tj + r;
-            const float bj = sc.beta[jj], rkj = sc.rk[jj];
+            const float bj = sc.beta[jj], rkj = sc.rk[jj], f1 = so.inv * fe * p.scale, f2 = -fdr * fe;
             float col = 0.f;
             f32x4 bu;
 #pragma unroll
@@ -402,8 +382,8 @@ __global__ __launch_bounds__(256) void local_kernel(BwdParams b)
                 const float d = i >= jj && i < nv
                                     ? __builtin_amdgcn_exp2f((sc.ghi[i] - sc.ghi[jj]) + (sc.glo[i] - sc.glo[jj]))
                                     : 0.f;
-                const float y1 = d != 0.f ? x1[e] * so.inv * d * p.scale : 0.f;
-                const float y2 = d != 0.f && i > jj ? -x2[e] * d : 0.f;
+                const float y1 = d != 0.f ? x1[e] * d * f1 : 0.f;
+                const float y2 = d != 0.f && i > jj ? x2[e] * d * f2 : 0.f;
                 const float uu = rkj * (y1 * sc.rq[i] * qk[e] + y2 * sc.rk[i] * kk[e]);
                 if (i == jj) sc.diag[i] = uu;
                 col += i > jj ? uu : 0.f;
@@ -432,52 +412,45 @@ __global__ __launch_bounds__(256) void local_kernel(BwdParams b)
         // products with the states: dQ and dK of the S part, T
         float sd = 0.f;
 #pragma unroll
-        for (int q = 0; q < V * K / 8 / 256; ++q) {
-            const int o = (q * 256 + tid) * 16;     // both are swizzled alike
+        for (int q = 0; q < V * K / 8 / NTH; ++q) {
+            const int o = (q * NTH + tid) * 16;     // both are swizzled alike
             const kda::f16x8 x = half8(lds_b128(lds + L::S + o)), y = half8(lds_b128(lds + L::DS + o));
-            float z = 0.f;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) z += (float)x[e] * (float)y[e];
-            const int block = (q * 256 * 8) / (32 * K);     // 256 pieces lie in one block of columns
-            sd += (fs[block] * fds[block]) * z;
+            for (int e = 0; e < 8; ++e) sd += (float)x[e] * (float)y[e];
         }
+        sd *= fs * fds;
         sd = kda::wave_sum(sd);
         if (lane == 0) sc.sd[wave] = sd;
         float qs[4] = {0.f, 0.f, 0.f, 0.f}, ks[4] = {0.f, 0.f, 0.f, 0.f}, kt[4] = {0.f, 0.f, 0.f, 0.f};
         new_phase();
+        f32x4 xs[4], ys[4], zs[4];
 #pragma unroll
-        for (int n = 0; n < ND; ++n) {
-            f32x4 xs[4], ys[4], zs[4];
+        for (int t = 0; t < 4; ++t) xs[t] = ys[t] = zs[t] = zero4();
 #pragma unroll
-            for (int t = 0; t < 4; ++t) xs[t] = ys[t] = zs[t] = zero4();
-#pragma unroll
-            for (int st = 0; st < V / 32; ++st) {
-                const kda::f16x8 sa = half8(dims_a(L::S, 32 * st, n)), da = half8(dims_a(L::DS, 32 * st, n));
-                const float fx = fs[st], fy = fs[st] * fdr[st], fz = fds[st] * fe[st];
-#pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    xs[t] += fx * mfma32(sa, half8(lds_b128(lds + L::DO + piece_at<V>(16 * t + r, 4 * st + grp))), zero4());
-                    ys[t] += fy * mfma32(sa, half8(toks_t(L::DR, 32 * st, 16 * t)), zero4());
-                    zs[t] += fz * mfma32(da, half8(toks_t(L::E, 32 * st, 16 * t)), zero4());
-                }
-                __builtin_amdgcn_sched_barrier(0);
-            }
+        for (int st = 0; st < V / 32; ++st) {
+            const kda::f16x8 sa = half8(dims_a(L::S, 32 * st)), da = half8(dims_a(L::DS, 32 * st));
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
-                const int i = 16 * t + r;
-                const bool live = i < nv;
-                const float head = __builtin_amdgcn_exp2f(sc.ghi[i] + sc.glo[i]);
-                const float tail = __builtin_amdgcn_exp2f((whi - sc.ghi[i]) + (wlo - sc.glo[i]));
-                const f32x4 x = xs[t] * (live ? so.inv * p.scale * head : 0.f), y = ys[t] * (live ? -head : 0.f),
-                            z = zs[t] * (live ? tail : 0.f);
-                const f32x4 qr = row_of(L::Q, n, t), kr = row_of(L::KM, n, t);
-                qs[t] += dot4(qr, x);
-                ks[t] += dot4(kr, y);
-                kt[t] += dot4(kr, z);
-                dq[n][t] += x;
-                dk[n][t] += y + sc.beta[i] * z;
+                xs[t] = mfma32(sa, half8(lds_b128(lds + L::DO + piece_at<V>(16 * t + r, 4 * st + grp))), xs[t]);
+                ys[t] = mfma32(sa, half8(toks_t(L::DR, 32 * st, 16 * t)), ys[t]);
+                zs[t] = mfma32(da, half8(toks_t(L::E, 32 * st, 16 * t)), zs[t]);
             }
-            new_phase();
+        }
+        new_phase();
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            const int i = 16 * t + r;
+            const bool live = i < nv;
+            const float head = __builtin_amdgcn_exp2f(sc.ghi[i] + sc.glo[i]);
+            const float tail = __builtin_amdgcn_exp2f((whi - sc.ghi[i]) + (wlo - sc.glo[i]));
+            const f32x4 x = xs[t] * (live ? fs * so.inv * p.scale * head : 0.f),
+                        y = ys[t] * (live ? -fs * fdr * head : 0.f), z = zs[t] * (live ? fds * fe * tail : 0.f);
+            const f32x4 qr = row_of(L::Q, t), kr = row_of(L::KM, t);
+            qs[t] += dot4(qr, x);
+            ks[t] += dot4(kr, y);
+            kt[t] += dot4(kr, z);
+            dq[t] += x;
+            dk[t] += y + sc.beta[i] * z;
         }
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
@@ -493,11 +466,11 @@ __global__ __launch_bounds__(256) void local_kernel(BwdParams b)
         }
         // dv: four columns of a token per lane, from dR
 #pragma unroll
-        for (int q = 0; q < V / 16; ++q) {          // 4 token tiles x V / 16 column tiles, 4 waves
-            const int job = q * 4 + wave, t = job & 3, c0 = 16 * (job >> 2);
+        for (int q = 0; q < V / 4 / NW; ++q) {      // 4 token tiles x V / 16 column tiles
+            const int job = q * NW + wave, t = job & 3, c0 = 16 * (job >> 2);
             const s16x4 x = lds_tr(lds + L::DR + w_at(c0 + 4 * grp + (r >> 2), 2 * t + ((r & 3) >> 1)) + 8 * (r & 1));
             const kda::f16x4 y = __builtin_bit_cast(kda::f16x4, x);
-            const f32x4 z = f32x4{(float)y[0], (float)y[1], (float)y[2], (float)y[3]} * fdr[q / 2];
+            const f32x4 z = f32x4{(float)y[0], (float)y[1], (float)y[2], (float)y[3]} * fdr;
             if (16 * t + r < nv)
                 *(uint2 *)(b.dv + ((bos + 16 * t + r) * p.HV + j) * V + c0 + 4 * grp) =
                     __builtin_bit_cast(uint2, kda::to_bf16x4(z));
@@ -516,8 +489,8 @@ __global__ __launch_bounds__(256) void local_kernel(BwdParams b)
             *(uint2 *)(W + to + 8192) = __builtin_bit_cast(uint2, lo);
         };
 #pragma unroll
-        for (int u = 0; u < 3; ++u) {
-            if (wave + 4 * u >= 10) continue;
+        for (int u = 0; u < NU; ++u) {
+            if (wave + NW * u >= 10) continue;
             const int ti = tis[u], tj = tjs[u];
             const float rkj = sc.rk[16 * tj + r];
             f32x4 rqi, rki;
@@ -531,8 +504,8 @@ __global__ __launch_bounds__(256) void local_kernel(BwdParams b)
             put(2, ti, tj, w2[u] * rki);
             put(3, ti, tj, w2[u] * rkj);
         }
-        if (wave >= 2) {                            // the tiles above the diagonal that are read
-            const int ti = wave == 2 ? 0 : 2;
+        if (wave >= NW - 2) {                       // the tiles above the diagonal that are read
+            const int ti = wave == NW - 2 ? 0 : 2;
 #pragma unroll
             for (int k = 0; k < 4; ++k) put(k, ti, ti + 1, zero4());
         }
@@ -548,23 +521,21 @@ __global__ __launch_bounds__(256) void local_kernel(BwdParams b)
             return lds_parts<2>(W + k * 16384 + w_at(16 * t + r, 4 * st + grp), 8192);
         };
 #pragma unroll
-        for (int n = 0; n < ND; ++n)
+        for (int st = 0; st < 2; ++st) {
+            const Parts<1> qa = {dims_a(L::Q, 32 * st)}, ka = {dims_a(L::KM, 32 * st)};
 #pragma unroll
-            for (int st = 0; st < 2; ++st) {
-                const Parts<1> qa = {dims_a(L::Q, 32 * st, n)}, ka = {dims_a(L::KM, 32 * st, n)};
-#pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    if (st <= t / 2) {
-                        dq[n][t] = mm(ka, cols(0, t, st), dq[n][t]);
-                        dk[n][t] = mm(ka, cols(3, t, st), dk[n][t]);
-                    }
-                    if (st >= t / 2) {
-                        dk[n][t] = mm(qa, rows(1, t, st), dk[n][t]);
-                        dk[n][t] = mm(ka, rows(2, t, st), dk[n][t]);
-                    }
+            for (int t = 0; t < 4; ++t) {
+                if (st <= t / 2) {
+                    dq[t] = mm(ka, cols(0, t, st), dq[t]);
+                    dk[t] = mm(ka, cols(3, t, st), dk[t]);
                 }
-                new_phase();
+                if (st >= t / 2) {
+                    dk[t] = mm(qa, rows(1, t, st), dk[t]);
+                    dk[t] = mm(ka, rows(2, t, st), dk[t]);
+                }
             }
+            new_phase();
+        }
         if (wave == 0) {                            // dbeta and dg, a token per lane
             const int i = lane;
             const int tau = i >> 4;
@@ -573,9 +544,14 @@ __global__ __launch_bounds__(256) void local_kernel(BwdParams b)
             for (int w = 0; w < 4; ++w) {
                 if (w < tau) left += sc.rowsum[w][i];       // tiles left of the token's own
                 if (w > tau) below += sc.colsum[w][i];      // and below it
+            }
+            float sd = 0.f;
+#pragma unroll
+            for (int w = 0; w < NW; ++w) {
                 qsum += sc.qs[w][i];
                 ksum += sc.ks[w][i];
                 tsum += sc.kt[w][i];
+                sd += sc.sd[w];
             }
             // whole tiles that cross: (2,0) and (3,0) for tile 1, (3,0) and (3,1) for tile 2
             const float c0 = row_from(sc.rowsum[0][i]), c1 = row_from(sc.rowsum[1][i < 48 ? 48 : i]);
@@ -594,7 +570,7 @@ __global__ __launch_bounds__(256) void local_kernel(BwdParams b)
             }
             const float before = __shfl_up(y, 1);
             x += pairs + (lane > 0 ? before : 0.f) +
-                 __builtin_amdgcn_exp2f(whi + wlo) * (sc.sd[0] + sc.sd[1] + sc.sd[2] + sc.sd[3]);
+                 __builtin_amdgcn_exp2f(whi + wlo) * sd;
             if (live) {
                 const int64_t o = (bos + i) * p.HV + j;
                 const float db = p.pre.beta_sigmoid ? dbt * bt * (1.f - bt) : dbt;
@@ -616,14 +592,8 @@ __global__ __launch_bounds__(256) void local_kernel(BwdParams b)
     if (p.pre.qk_l2norm) {
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-            float a = 0.f, c = 0.f;
-#pragma unroll
-            for (int n = 0; n < ND; ++n) {
-                a += dot4(row_of(L::Q, n, t), dq[n][t]);
-                c += dot4(row_of(L::KM, n, t), dk[n][t]);
-            }
-            a = kda::sum_lane_groups(a);
-            c = kda::sum_lane_groups(c);
+            const float a = kda::sum_lane_groups(dot4(row_of(L::Q, t), dq[t]));
+            const float c = kda::sum_lane_groups(dot4(row_of(L::KM, t), dk[t]));
             if (grp == 0) {
                 sc.dot[0][wave][16 * t + r] = a;
                 sc.dot[1][wave][16 * t + r] = c;
@@ -633,7 +603,7 @@ __global__ __launch_bounds__(256) void local_kernel(BwdParams b)
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {
+            for (int w = 0; w < NW; ++w) {
                 gq[t] += sc.dot[0][w][16 * t + r];
                 gk[t] += sc.dot[1][w][16 * t + r];
             }
@@ -644,17 +614,14 @@ __global__ __launch_bounds__(256) void local_kernel(BwdParams b)
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
         if (16 * t + r >= nv) continue;
-#pragma unroll
-        for (int n = 0; n < ND; ++n) {
-            f32x4 x = dq[n][t], y = dk[n][t];
-            if (p.pre.qk_l2norm) {
-                x = fq[t] * (x - gq[t] * row_of(L::Q, n, t));
-                y = fk[t] * (y - gk[t] * row_of(L::KM, n, t));
-            }
-            const int64_t o = ((bos + 16 * t + r) * p.H + h) * K + DW * wave + 16 * n + 4 * grp;
-            *(uint2 *)(b.dq + o) = __builtin_bit_cast(uint2, kda::to_bf16x4(x));
-            *(uint2 *)(b.dk + o) = __builtin_bit_cast(uint2, kda::to_bf16x4(y));
+        f32x4 x = dq[t], y = dk[t];
+        if (p.pre.qk_l2norm) {
+            x = fq[t] * (x - gq[t] * row_of(L::Q, t));
+            y = fk[t] * (y - gk[t] * row_of(L::KM, t));
         }
+        const int64_t o = ((bos + 16 * t + r) * p.H + h) * K + 16 * wave + 4 * grp;
+        *(uint2 *)(b.dq + o) = __builtin_bit_cast(uint2, kda::to_bf16x4(x));
+        *(uint2 *)(b.dk + o) = __builtin_bit_cast(uint2, kda::to_bf16x4(y));
     }
 }
 
@@ -662,10 +629,10 @@ template <int K, int V>
 hipError_t launch_backward(const BwdParams &b, hipStream_t st)
 {
     const Params &p = b.f;
-    chains_kernel<K, V><<<dim3(2 * p.seq.N * p.HV), dim3(2 * V), 0, st>>>(b);
+    chains_kernel<K, V><<<dim3(2 * p.seq.N * p.HV), dim3(4 * V), 0, st>>>(b);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.seq.T_total == 0) return e;
-    local_kernel<K, V><<<dim3(p.seq.n_slots, p.H), dim3(256), 0, st>>>(b);
+    local_kernel<K, V><<<dim3(p.seq.n_slots, p.H), dim3(4 * K), 0, st>>>(b);
     return hipGetLastError();
 }
 

@@ -78,15 +78,16 @@ struct StepParams {
 // the order (0,0) (1,0) (2,0) (2,1) (3,0) (3,1): lane (g, m) holds row 16 t + m, elements e < 4
 // token 32 s + 4 g + e and e >= 4 token 32 s + 16 + 4 g + e - 4 (so that two C-layout tiles are
 // the other operand, as they are).
-//   A and M, each [parts][6][64 lanes][8] bf16; then fp32 row scales of the chunk's 64 tokens:
+//   A and M, each [parts][6][64 lanes][8] bf16; between them fp32 row scales of the 64 tokens:
 //   RA = e^Gam rk, RB = beta e^{gam - Gam} rk, RC = scale e^Gam rq (rk, rq the L2-norm factors),
-//   and EG [1] = e^gam (one KiB-aligned block, so it is copied to LDS in 1 KiB steps).
+//   and EG [1] = e^gam. Copied to LDS in 1 KiB steps, without M where there is no output.
 template <int X>
 struct Rec {
     static constexpr int FR = 1024, MAT = 6 * FR;       // one fragment, one part of a matrix
-    static constexpr int A = 0, M = X * MAT;
-    static constexpr int RA = 2 * X * MAT, RB = RA + 256, RC = RB + 256, EG = RC + 256;
-    static constexpr int BYTES = RA + FR;
+    static constexpr int A = 0;
+    static constexpr int RA = X * MAT, RB = RA + 256, RC = RB + 256, EG = RC + 256;
+    static constexpr int M = RA + FR;
+    static constexpr int BYTES = M + X * MAT;
 };
 
 __host__ __device__ constexpr int frag_index(int t, int s) { return t < 2 ? t : 2 * t - 2 + s; }
@@ -106,12 +107,12 @@ struct RecB {
 
 __host__ __device__ constexpr int frag_index_t(int t, int s) { return t < 2 ? 2 * t + s : 2 + t; }
 
-// What the backward's two passes leave for one (value head, chunk slot), fp16 with one power of
-// two for the 32 columns of a wave (16-bit values of 11 significant bits: the products that use
-// them then add little to the rounding of a bf16 gradient): the state at the chunk's start and the
-// gradient of the state at its end, both transposed [V][K]; e and the gradient of R (which is v's),
-// both [V][64 tokens]; then the factors that undo the scales, [4][V / 32] fp32 in that order.
-// Transposed, because a lane of the passes holds consecutive key dims or tokens of one column.
+// What the backward's two passes leave for one (value head, chunk slot), fp16 with a power of two
+// for each of four matrices (16-bit values of 11 significant bits: the products that use them then
+// add little to the rounding of a bf16 gradient): the state at the chunk's start and the gradient of
+// the state at its end, both transposed [V][K]; e and the gradient of R (which is v's), both
+// [V][64 tokens]; then the factors that undo the scales, fp32, in that order. Transposed, because a
+// lane of the passes holds consecutive key dims or tokens of one column.
 template <int K, int V>
 struct Keep {
     static constexpr int S = 0, DS = V * K * 2, E = 2 * DS, DR = E + V * 128, SCALE = DR + V * 128;
@@ -125,24 +126,25 @@ struct Parts {
     bf16x8 p[X];
 };
 
-// Eight values (two C-layout tiles) as X bf16 parts.
+// Eight values (two C-layout tiles) as X bf16 parts. Two values are rounded by one instruction and
+// their rounded parts taken back from the packed pair: three instructions a value for two parts.
 template <int X>
 __device__ __forceinline__ Parts<X> split(f32x4 x, f32x4 y) {
+    typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2;
     Parts<X> r;
+    float v[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
 #pragma unroll
     for (int k = 0; k < X; ++k) {
+        uint32_t w[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            r.p[k][i] = (__bf16)x[i];
-            r.p[k][4 + i] = (__bf16)y[i];
-        }
-        if (k + 1 < X) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                x[i] -= (float)r.p[k][i];
-                y[i] -= (float)r.p[k][4 + i];
+            w[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(kda::f32v2{v[2 * i], v[2 * i + 1]}, bf16x2));
+            if (k + 1 < X) {
+                v[2 * i] -= kda::bf16lo(w[i]);
+                v[2 * i + 1] -= kda::bf16hi(w[i]);
             }
         }
+        r.p[k] = __builtin_bit_cast(bf16x8, kda::u32x4{w[0], w[1], w[2], w[3]});
     }
     return r;
 }
@@ -229,10 +231,14 @@ __device__ __forceinline__ int piece_at(int row, int piece) {
     return (row * NP + (piece ^ (row & (NP - 1)))) * 16;
 }
 
+// 16 bytes per lane from memory to LDS at dst + 16 lane. Written out, because behind the builtin
+// the compiler waits for every copy in flight before the next transposing read of LDS, also where
+// the copies go to the other buffer. The kernels wait themselves (vm_drain) before the barrier
+// behind which the data is read. M0 takes its value one cycle before the copy reads it (s_nop).
 __device__ __forceinline__ void copy16_to_lds(const void *src, uint8_t *dst) {
-    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)src,
-                                     (__attribute__((address_space(3))) void *)(lds_u8 *)dst, 16,
-                                     0, 0);
+    const uint32_t at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_u8 *)dst);
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
+                 :: "s"(at), "v"(src) : "memory", "m0");
 }
 
 // Stage rows 0 .. 63 of a [tokens][stride] matrix into LDS (W columns, layout piece_at); rows
