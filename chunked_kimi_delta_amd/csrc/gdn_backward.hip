@@ -57,25 +57,27 @@ __device__ __forceinline__ void reverse_chain(const BwdParams &b, int s, int j, 
     const size_t slot0 = (size_t)j * p.seq.n_slots + bos / CT + s;
     const int col0 = 16 * wave;
 
+    const RowStage<K, NW> qk_rows((int64_t)p.H * K, wave, lane);
+    const RowStage<V, NW> v_rows((int64_t)p.HV * V, wave, lane);
     auto stage = [&](int c, uint8_t *buf) {
         const int64_t t0 = bos + (int64_t)CT * c;
         const int nv = (int)(eos - t0 < CT ? eos - t0 : CT);
         const int64_t qk = (t0 * p.H + h) * K;
-        stage_rows<K, NW>(p.k[0] + qk, (int64_t)p.H * K, nv, buf + L::KM, wave, lane);
-        stage_rows<K, NW>(p.q[0] + qk, (int64_t)p.H * K, nv, buf + L::QM, wave, lane);
-        stage_rows<V, NW>(b.d_o + (t0 * p.HV + j) * V, (int64_t)p.HV * V, nv, buf + L::DO, wave, lane);
-        stage_block<NW>(p.rec + (slot0 + c) * R::BYTES + R::REV, R::REV_KIB, buf + L::REC, wave, lane);
+        qk_rows(p.k[0] + qk, nv, buf + L::KM, wave);
+        qk_rows(p.q[0] + qk, nv, buf + L::QM, wave);
+        v_rows(b.d_o + (t0 * p.HV + j) * V, nv, buf + L::DO, wave);
+        stage_block<R::REV_KIB, NW>(p.rec + (slot0 + c) * R::BYTES + R::REV, buf + L::REC, wave, lane);
     };
     if (c0 < c1) stage(c1 - 1, lds);
     auto kept = [&](int c) { return b.keep + (slot0 + c) * KP::BYTES; };
 
-    f32x4 S[NT], D[4];                      // dS, laid out as the forward's S; dR
+    f32x4 S[NT][1], D[4][1];                // dS, laid out as the forward's S; dR
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) S[t][i] = init ? init[(size_t)state_row(t, i, grp) * V + col0 + r] : 0.f;
+        for (int i = 0; i < 4; ++i) S[t][0][i] = init ? init[(size_t)state_row(t, i, grp) * V + col0 + r] : 0.f;
 #pragma unroll
-    for (int t = 0; t < 4; ++t) D[t] = zero4();
+    for (int t = 0; t < 4; ++t) D[t][0] = zero4();
 
 #pragma unroll 1
     for (int c = c1 - 1; c >= c0; --c) {
@@ -104,13 +106,13 @@ __device__ __forceinline__ void reverse_chain(const BwdParams &b, int s, int j, 
         for (int t = 0; t < 4; ++t) kS[t] = zero4();
 #pragma unroll
         for (int st = 0; st < K / 32; ++st) {
-            const Parts<X> sp = split<X>(S[2 * st], S[2 * st + 1]);
+            const Parts<X> sp = split<X>(S[2 * st][0], S[2 * st + 1][0]);
 #pragma unroll
             for (int t = 0; t < 4; ++t)
                 kS[t] = mm(Parts<1>{lds_b128(buf + L::KM + piece_at<K>(16 * t + r, 4 * st + grp))}, sp, kS[t]);
         }
 #pragma unroll
-        for (int t = 0; t < NT; ++t) S[t] *= eg;
+        for (int t = 0; t < NT; ++t) S[t][0] *= eg;
         // de = M^T dO + beta e^{gam-Gam} (K dS'); dO of tokens 32 st + 4 g .. + 3, + 16 per lane
         s16x4 dv[2][2];
 #pragma unroll
@@ -137,25 +139,25 @@ __device__ __forceinline__ void reverse_chain(const BwdParams &b, int s, int j, 
         // dR = A^T de
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-            D[t] = zero4();
+            D[t][0] = zero4();
 #pragma unroll
             for (int st = t / 2; st < 2; ++st)
-                D[t] = mm(lds_parts<X>(rec + R::AT + frag_index_t(t, st) * R::FR + lane * 16, R::MAT), dp[st], D[t]);
+                D[t][0] = mm(lds_parts<X>(rec + R::AT + frag_index_t(t, st) * R::FR + lane * 16, R::MAT), dp[st], D[t][0]);
         }
         // dS = e^gam dS' + Q^T (scale e^Gam dO) - K^T (e^Gam dR)
 #pragma unroll
         for (int st = 0; st < 2; ++st) {
             const f32x4 a0 = *(const f32x4 *)(ra + 32 * st + 4 * grp), a1 = *(const f32x4 *)(ra + 32 * st + 16 + 4 * grp);
             const f32x4 c0v = *(const f32x4 *)(rc + 32 * st + 4 * grp), c1v = *(const f32x4 *)(rc + 32 * st + 16 + 4 * grp);
-            const Parts<X> rp = split<X>(zero4() - a0 * D[2 * st], zero4() - a1 * D[2 * st + 1]),
+            const Parts<X> rp = split<X>(zero4() - a0 * D[2 * st][0], zero4() - a1 * D[2 * st + 1][0]),
                            op = split<X>(c0v * widen(dv[st][0]), c1v * widen(dv[st][1]));
             const int row = 32 * st + 4 * grp + (r >> 2);
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
                 const int piece = 4 * (t / 2) + (r & 3), half = 8 * (t % 2);
                 const int at0 = piece_at<K>(row, piece) + half, at1 = piece_at<K>(row + 16, piece) + half;
-                S[t] = mm(Parts<1>{join(lds_tr(buf + L::KM + at0), lds_tr(buf + L::KM + at1))}, rp, S[t]);
-                S[t] = mm(Parts<1>{join(lds_tr(buf + L::QM + at0), lds_tr(buf + L::QM + at1))}, op, S[t]);
+                S[t][0] = mm(Parts<1>{join(lds_tr(buf + L::KM + at0), lds_tr(buf + L::KM + at1))}, rp, S[t][0]);
+                S[t][0] = mm(Parts<1>{join(lds_tr(buf + L::QM + at0), lds_tr(buf + L::QM + at1))}, op, S[t][0]);
             }
         }
     }
@@ -170,7 +172,7 @@ __device__ __forceinline__ void reverse_chain(const BwdParams &b, int s, int j, 
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) end[(size_t)state_row(t, i, grp) * V + col0 + r] = S[t][i];
+            for (int i = 0; i < 4; ++i) end[(size_t)state_row(t, i, grp) * V + col0 + r] = S[t][0][i];
     }
 }
 
@@ -194,7 +196,7 @@ __global__ __launch_bounds__(V * 4) void chains_kernel(BwdParams b)
     if (blockIdx.x & 1)
         reverse_chain<K, V>(b, s, j, 0, nc, b.dht ? b.dht + at : nullptr, b.dh0 ? b.dh0 + at : nullptr, lds, &mx);
     else
-        forward_chain<K, V, V, 1, RecB::X, RecB, KEEP>(p, s, j, 0, nc, 0, p.h0 ? p.h0 + at : nullptr, nullptr, lds,
+        forward_chain<K, V, V, 1, 1, RecB::X, RecB, KEEP>(p, s, j, 0, nc, 0, p.h0 ? p.h0 + at : nullptr, nullptr, lds,
                                                        b.keep, &mx);
 }
 
@@ -233,8 +235,7 @@ __device__ __forceinline__ float row_from(float x) {
     return x;
 }
 
-// rows of [64][64] bf16 with swizzled 16-byte pieces
-__device__ __forceinline__ int w_at(int row, int piece) { return (row * 8 + (piece ^ (row & 7))) * 16; }
+__device__ __forceinline__ int w_at(int row, int piece) { return piece_at<64>(row, piece); }
 
 }  // namespace
 

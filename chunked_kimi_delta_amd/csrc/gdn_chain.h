@@ -1,5 +1,5 @@
 // gdn_chain.h -- the pass over a sequence's 64-token chunks (gdn_internal.h has the formulas): one
-// wave per 16 value columns of a (sequence, value head).
+// wave per 16 or 32 value columns of a (sequence, value head).
 //
 // The columns of S are independent, so a wave keeps its K x 16 slice of S in fp32 registers for
 // the whole pass and needs nothing from the other waves: S, R and e leave one product in the very
@@ -48,96 +48,109 @@ template <int NW>
 struct Maxima {
     float state[2][NW], rows[2][NW];
     static __device__ __forceinline__ Scale scale(const float (&m)[NW]) {
-        float x = m[0];
+        uint32_t x = __float_as_uint(m[0]);
 #pragma unroll
-        for (int w = 1; w < NW; ++w) x = __uint_as_float(max(__float_as_uint(x), __float_as_uint(m[w])));
-        return scale_for(x);
+        for (int w = 1; w < NW; ++w) x = max(x, __float_as_uint(m[w]));
+        return scale_for(__uint_as_float(x));
     }
 };
 
-template <int N>
-__device__ __forceinline__ float largest(const f32x4 (&x)[N]) {
+template <int N, int CTW>
+__device__ __forceinline__ float largest(const f32x4 (&x)[N][CTW]) {
     uint32_t m = 0;
 #pragma unroll
     for (int t = 0; t < N; ++t)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) m = max(m, __float_as_uint(x[t][i]) & 0x7fffffffu);   // NaN counts as the largest
+        for (int ct = 0; ct < CTW; ++ct)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) m = max(m, __float_as_uint(x[t][ct][i]) & 0x7fffffffu);     // NaN counts
     return wave_max(__uint_as_float(m));
 }
 
-// A wave's columns of the state to the workspace, [V][K] fp16 (column `col` of this lane).
-template <int NT>
-__device__ __forceinline__ void keep_state(const f32x4 (&S)[NT], Scale f, uint8_t *base, float *inv, int col,
+// A wave's columns of the state to the workspace, [V][K] fp16 (col: this lane's first column).
+template <int NT, int CTW>
+__device__ __forceinline__ void keep_state(const f32x4 (&S)[NT][CTW], Scale f, uint8_t *base, float *inv, int col,
                                            int grp)
 {
     const auto rs = kda::buffer_rsrc(base, 1u << 20);
 #pragma unroll
     for (int t = 0; t < NT; ++t)
-        kda::bstore8<0>(rs, col * NT * 32 + 16 * grp, 64 * (t / 2) + 8 * (t % 2), half4(S[t], f.f));
+#pragma unroll
+        for (int ct = 0; ct < CTW; ++ct)
+            kda::bstore8<0>(rs, (col + 16 * ct) * NT * 32 + 16 * grp, 64 * (t / 2) + 8 * (t % 2), half4(S[t][ct], f.f));
     if (threadIdx.x == 0) *inv = f.inv;
 }
 
 // A wave's columns of a [64 tokens][V] matrix in C-layout to the workspace, [V][64] fp16.
-__device__ __forceinline__ void keep_rows(const f32x4 (&E)[4], Scale f, uint8_t *base, float *inv, int col, int grp)
+template <int CTW>
+__device__ __forceinline__ void keep_rows(const f32x4 (&E)[4][CTW], Scale f, uint8_t *base, float *inv, int col, int grp)
 {
     const auto rs = kda::buffer_rsrc(base, 1u << 20);
 #pragma unroll
-    for (int t = 0; t < 4; ++t) kda::bstore8<0>(rs, col * 128 + 8 * grp, 32 * t, half4(E[t], f.f));
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int ct = 0; ct < CTW; ++ct)
+            kda::bstore8<0>(rs, (col + 16 * ct) * 128 + 8 * grp, 32 * t, half4(E[t][ct], f.f));
     if (threadIdx.x == 0) *inv = f.inv;
 }
 
-// The chunks [c0, c1) of one (sequence, value head) for the C columns from `cbase` of `ld` columns.
+// The chunks [c0, c1) of one (sequence, value head) for the C columns from `cbase` of `ld` columns,
+// CTW 16-column tiles a wave (one wave per 16 CTW columns of C).
 // init: the state's first element at c0 (row-major, `ld` columns), null for zeros (PHI: ignored);
 // end: where to put the end state, or null.
-template <int K, int V, int C, int IN, int X, class R, Mode M>
+template <int K, int V, int C, int CTW, int IN, int X, class R, Mode M>
 __device__ __forceinline__ void forward_chain(const Params &p, int s, int j, int c0, int c1, int cbase,
                                               const float *init, float *end, uint8_t *lds,
-                                              uint8_t *keep = nullptr, Maxima<C / 16> *mx = nullptr)
+                                              uint8_t *keep = nullptr, Maxima<C / 16 / CTW> *mx = nullptr)
 {
     using L = Stage<K, C, IN, R, M>;
     static_assert(L::BYTES * L::BUFS <= 160 * 1024, "LDS of a compute unit");
-    constexpr int NW = C / 16, NT = K / 16, LD = M == PHI ? K : V;
+    constexpr int NW = C / 16 / CTW, NT = K / 16, LD = M == PHI ? K : V, NS = K / 32;
     const int tid = threadIdx.x, lane = tid & 63, grp = lane >> 4, r = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int h = j / p.G;
     const int64_t bos = kda::seq_bos(p.seq, s), eos = kda::seq_eos(p.seq, s, bos);
     const size_t slot0 = (size_t)j * p.seq.n_slots + bos / CT + s;
-    const int col0 = 16 * wave;             // within the workgroup's columns
+    const int col0 = 16 * CTW * wave;       // within the workgroup's columns
 
+    const RowStage<K, NW> qk_rows((int64_t)p.H * K, wave, lane);
+    const RowStage<C, NW> v_rows((int64_t)p.HV * V, wave, lane);
     auto stage = [&](int c, uint8_t *buf) {
         const int64_t t0 = bos + (int64_t)CT * c;
         const int nv = (int)(eos - t0 < CT ? eos - t0 : CT);
         const int64_t qk = (t0 * p.H + h) * K;
 #pragma unroll
         for (int i = 0; i < IN; ++i) {
-            stage_rows<K, NW>(p.k[i] + qk, (int64_t)p.H * K, nv, buf + L::KM + i * L::MK, wave, lane);
-            if constexpr (M == OUT)
-                stage_rows<K, NW>(p.q[i] + qk, (int64_t)p.H * K, nv, buf + L::QM + i * L::MK, wave, lane);
+            qk_rows(p.k[i] + qk, nv, buf + L::KM + i * L::MK, wave);
+            if constexpr (M == OUT) qk_rows(p.q[i] + qk, nv, buf + L::QM + i * L::MK, wave);
         }
         if constexpr (IN == 1 && M != PHI)
-            stage_rows<C, NW>((const uint16_t *)p.v + (t0 * p.HV + j) * V + cbase, (int64_t)p.HV * V, nv,
-                              buf + L::VM, wave, lane);
-        stage_block<NW>(p.rec + (slot0 + c) * R::BYTES, L::KIB, buf + L::REC, wave, lane);
+            v_rows((const uint16_t *)p.v + (t0 * p.HV + j) * V + cbase, nv, buf + L::VM, wave);
+        stage_block<L::KIB, NW>(p.rec + (slot0 + c) * R::BYTES, buf + L::REC, wave, lane);
     };
     if (c0 < c1) stage(c0, lds);
 
-    f32x4 S[NT];
+    f32x4 S[NT][CTW];
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int row = state_row(t, i, grp), col = cbase + col0 + r;
-            if constexpr (M == PHI)
-                S[t][i] = row == col ? 1.f : 0.f;
-            else
-                S[t][i] = init ? init[(size_t)row * LD + col] : 0.f;
-        }
+        for (int ct = 0; ct < CTW; ++ct)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int row = state_row(t, i, grp), col = cbase + col0 + 16 * ct + r;
+                if constexpr (M == PHI)
+                    S[t][ct][i] = row == col ? 1.f : 0.f;
+                else
+                    S[t][ct][i] = init ? init[(size_t)row * LD + col] : 0.f;
+            }
 
     using KP = Keep<K, V>;
     auto kept = [&](int c) { return keep + (slot0 + c) * KP::BYTES; };
-    f32x4 E[4];
+    f32x4 E[4][CTW];
 #pragma unroll
-    for (int t = 0; t < 4; ++t) E[t] = zero4();
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int ct = 0; ct < CTW; ++ct) E[t][ct] = zero4();
 #pragma unroll 1
     for (int c = c0; c < c1; ++c) {
         uint8_t *const buf = lds + ((c - c0) % L::BUFS) * L::BYTES;
@@ -163,97 +176,176 @@ __device__ __forceinline__ void forward_chain(const Params &p, int s, int j, int
         const uint8_t *const rec = buf + L::REC;
         const float *const ra = (const float *)(rec + R::RA), *const rb = (const float *)(rec + R::RB);
         const float eg = *(const float *)(rec + R::EG);
-        f32x4 kS[4], O[4];
-#pragma unroll
-        for (int t = 0; t < 4; ++t) kS[t] = O[t] = zero4();
-        // K S and (Q S)^T
-#pragma unroll
-        for (int st = 0; st < K / 32; ++st) {
-            const Parts<X> sp = split<X>(S[2 * st], S[2 * st + 1]);
+        // Operands are read from LDS a phase ahead of the products that take them (AHEAD; the reads of
+        // a phase fit the registers for one plane only): the compiler by itself reads each operand
+        // right before its product and waits.
+        constexpr bool AHEAD = IN == 1;
+        auto phase = [] { __builtin_amdgcn_sched_barrier(0); };
+        Parts<IN> kf[AHEAD ? NS : 1][4], qf[AHEAD && M == OUT ? NS : 1][4];
+        auto read_kq = [&](int st, Parts<IN> (&kk)[4], Parts<IN> (&qq)[4]) {
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
                 const int at = piece_at<K>(16 * t + r, 4 * st + grp);
-                kS[t] = mm(lds_parts<IN>(buf + L::KM + at, L::MK), sp, kS[t]);
-                if constexpr (M == OUT) O[t] = mm(sp, lds_parts<IN>(buf + L::QM + at, L::MK), O[t]);
+                kk[t] = lds_parts<IN>(buf + L::KM + at, L::MK);
+                if constexpr (M == OUT) qq[t] = lds_parts<IN>(buf + L::QM + at, L::MK);
             }
-        }
+        };
+        Parts<X> af[6];
+        f32x4 a4[4], v4[4][CTW];
+        auto read_av = [&] {
 #pragma unroll
-        for (int t = 0; t < NT; ++t) S[t] *= eg;
-        // R = V - e^Gam (K S), as operands
-        Parts<X> rp[2];
+            for (int t = 0; t < 4; ++t) {
+                a4[t] = *(const f32x4 *)(ra + 16 * t + 4 * grp);
 #pragma unroll
-        for (int st = 0; st < 2; ++st) {
-            f32x4 x[2];
+                for (int ct = 0; ct < CTW; ++ct) {
+                    v4[t][ct] = zero4();
+                    if constexpr (M == PHI) {
+                    } else if constexpr (IN == 1) {
+                        v4[t][ct] = widen(lds_tr(buf + L::VM + piece_at<C>(16 * t + 4 * grp + (r >> 2),
+                                                                           (col0 + 16 * ct) / 8 + ((r & 3) >> 1)) +
+                                                 8 * (r & 1)));
+                    } else {
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const int t = 2 * st + u;
-                const f32x4 a = *(const f32x4 *)(ra + 16 * t + 4 * grp);
-                f32x4 v = zero4();
-                if constexpr (M == PHI) {
-                } else if constexpr (IN == 1) {
-                    v = widen(lds_tr(buf + L::VM + piece_at<C>(16 * t + 4 * grp + (r >> 2),
-                                                               col0 / 8 + ((r & 3) >> 1)) + 8 * (r & 1)));
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int row = 16 * t + 4 * grp + i;
-                        v[i] = ((const float *)p.v)[((t0 + (row < nv ? row : nv - 1)) * p.HV + j) * V +
-                                                    cbase + col0 + r];
+                        for (int i = 0; i < 4; ++i) {
+                            const int row = 16 * t + 4 * grp + i;
+                            v4[t][ct][i] = ((const float *)p.v)[((t0 + (row < nv ? row : nv - 1)) * p.HV + j) * V +
+                                                                cbase + col0 + 16 * ct + r];
+                        }
                     }
                 }
-                x[u] = v - a * kS[t];
             }
-            rp[st] = split<X>(x[0], x[1]);
+#pragma unroll
+            for (int f = 0; f < 6; ++f) af[f] = lds_parts<X>(rec + R::A + f * R::FR + lane * 16, R::MAT);
+        };
+        Parts<IN> ktf[AHEAD ? 2 : 1][AHEAD ? NT : 1];
+        f32x4 b4[4];
+        auto read_kt = [&](int st, int t) {
+            const int row = 32 * st + 4 * grp + (r >> 2), piece = 4 * (t / 2) + (r & 3), half = 8 * (t % 2);
+            const int at0 = piece_at<K>(row, piece) + half, at1 = piece_at<K>(row + 16, piece) + half;
+            Parts<IN> kt;
+#pragma unroll
+            for (int i = 0; i < IN; ++i)
+                kt.p[i] = join(lds_tr(buf + L::KM + i * L::MK + at0), lds_tr(buf + L::KM + i * L::MK + at1));
+            return kt;
+        };
+        auto read_kts = [&](int st) {
+            if constexpr (AHEAD) {
+#pragma unroll
+                for (int t = 0; t < NT; ++t) ktf[st][t] = read_kt(st, t);
+            }
+            b4[2 * st] = *(const f32x4 *)(rb + 32 * st + 4 * grp);
+            b4[2 * st + 1] = *(const f32x4 *)(rb + 32 * st + 16 + 4 * grp);
+        };
+
+        f32x4 kS[4][CTW], O[4][CTW];
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int ct = 0; ct < CTW; ++ct) kS[t][ct] = O[t][ct] = zero4();
+        if constexpr (AHEAD) {
+#pragma unroll
+            for (int st = 0; st < NS; ++st) read_kq(st, kf[st], qf[M == OUT ? st : 0]);
+            phase();
         }
-        // e = A R
+        // K S and (Q S)^T
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            E[t] = zero4();
+        for (int st = 0; st < NS; ++st) {
+            if constexpr (!AHEAD) read_kq(st, kf[0], qf[0]);
+            if (AHEAD && st == NS - 1) {
+                phase();
+                read_av();
+                phase();
+            }
+            Parts<X> sp[CTW];
 #pragma unroll
-            for (int st = 0; st <= t / 2; ++st)
-                E[t] = mm(lds_parts<X>(rec + R::A + frag_index(t, st) * R::FR + lane * 16, R::MAT), rp[st], E[t]);
+            for (int ct = 0; ct < CTW; ++ct) sp[ct] = split<X>(S[2 * st][ct], S[2 * st + 1][ct]);
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int ct = 0; ct < CTW; ++ct) {
+                    kS[t][ct] = mm(kf[AHEAD ? st : 0][t], sp[ct], kS[t][ct]);
+                    if constexpr (M == OUT) O[t][ct] = mm(sp[ct], qf[AHEAD ? st : 0][t], O[t][ct]);
+                }
+        }
+        if constexpr (!AHEAD) read_av();
+        phase();
+        read_kts(0);
+        phase();
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int ct = 0; ct < CTW; ++ct) S[t][ct] *= eg;
+        // R = V - e^Gam (K S), as operands; e = A R
+        Parts<X> rp[2][CTW];
+#pragma unroll
+        for (int st = 0; st < 2; ++st)
+#pragma unroll
+            for (int ct = 0; ct < CTW; ++ct)
+                rp[st][ct] = split<X>(v4[2 * st][ct] - a4[2 * st] * kS[2 * st][ct],
+                                      v4[2 * st + 1][ct] - a4[2 * st + 1] * kS[2 * st + 1][ct]);
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int ct = 0; ct < CTW; ++ct) {
+                E[t][ct] = mm(af[frag_index(t, 0)], rp[0][ct], zero4());
+                if (t >= 2) E[t][ct] = mm(af[frag_index(t, 1)], rp[1][ct], E[t][ct]);
+            }
+        phase();
+        read_kts(1);
+        phase();
+        Parts<X> mf[6];
+        if constexpr (M == OUT && AHEAD) {
+#pragma unroll
+            for (int f = 0; f < 6; ++f) mf[f] = lds_parts<X>(rec + R::M + f * R::FR + lane * 16, R::MAT);
+            phase();
         }
         // S += K^T (beta e^{gam - Gam} e)
 #pragma unroll
         for (int st = 0; st < 2; ++st) {
-            const f32x4 b0 = *(const f32x4 *)(rb + 32 * st + 4 * grp),
-                        b1 = *(const f32x4 *)(rb + 32 * st + 16 + 4 * grp);
-            const Parts<X> dp = split<X>(b0 * E[2 * st], b1 * E[2 * st + 1]);
-            const int row = 32 * st + 4 * grp + (r >> 2);
+            Parts<X> dp[CTW];
+#pragma unroll
+            for (int ct = 0; ct < CTW; ++ct)
+                dp[ct] = split<X>(b4[2 * st] * E[2 * st][ct], b4[2 * st + 1] * E[2 * st + 1][ct]);
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-                const int piece = 4 * (t / 2) + (r & 3), half = 8 * (t % 2);
-                const int at0 = piece_at<K>(row, piece) + half, at1 = piece_at<K>(row + 16, piece) + half;
-                Parts<IN> kt;
+                const Parts<IN> kt = AHEAD ? ktf[AHEAD ? st : 0][AHEAD ? t : 0] : read_kt(st, t);
 #pragma unroll
-                for (int i = 0; i < IN; ++i)
-                    kt.p[i] = join(lds_tr(buf + L::KM + i * L::MK + at0), lds_tr(buf + L::KM + i * L::MK + at1));
-                S[t] = mm(kt, dp, S[t]);
+                for (int ct = 0; ct < CTW; ++ct) S[t][ct] = mm(kt, dp[ct], S[t][ct]);
             }
         }
         if constexpr (M == OUT) {           // o = scale e^Gam (Q S) + M e
             const float *const rc = (const float *)(rec + R::RC);
 #pragma unroll
-            for (int t = 0; t < 4; ++t) O[t] *= rc[16 * t + r];
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int ct = 0; ct < CTW; ++ct) O[t][ct] *= rc[16 * t + r];
 #pragma unroll
             for (int st = 0; st < 2; ++st) {
-                const Parts<X> ep = split<X>(E[2 * st], E[2 * st + 1]);
+                Parts<X> ep[CTW];
 #pragma unroll
-                for (int t = 2 * st; t < 4; ++t)
-                    O[t] = mm(ep, lds_parts<X>(rec + R::M + frag_index(t, st) * R::FR + lane * 16, R::MAT), O[t]);
+                for (int ct = 0; ct < CTW; ++ct) ep[ct] = split<X>(E[2 * st][ct], E[2 * st + 1][ct]);
+#pragma unroll
+                for (int t = 2 * st; t < 4; ++t) {
+                    const int f = frag_index(t, st);
+                    const Parts<X> m = AHEAD ? mf[f] : lds_parts<X>(rec + R::M + f * R::FR + lane * 16, R::MAT);
+#pragma unroll
+                    for (int ct = 0; ct < CTW; ++ct) O[t][ct] = mm(ep[ct], m, O[t][ct]);
+                }
             }
             constexpr int SZ = IN == 1 ? 2 : 4;
             // rows past the sequence end lie outside the resource: their stores are dropped
             const auto ob = kda::rows_in((uint8_t *)p.o + (t0 * p.HV + j) * (int64_t)V * SZ, nv,
                                          (int64_t)p.HV * V * SZ, V * SZ);
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                const int at = ((16 * t + r) * p.HV * V + cbase + col0 + 4 * grp) * SZ;
-                if constexpr (IN == 1)
-                    kda::bstore8<0>(ob, at, 0, kda::to_bf16x4(O[t]));
-                else
-                    kda::bstore16<0>(ob, at, 0, O[t]);
-            }
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int ct = 0; ct < CTW; ++ct) {
+                    const int at = ((16 * t + r) * p.HV * V + cbase + col0 + 16 * ct + 4 * grp) * SZ;
+                    if constexpr (IN == 1)
+                        kda::bstore8<0>(ob, at, 0, kda::to_bf16x4(O[t][ct]));
+                    else
+                        kda::bstore16<0>(ob, at, 0, O[t][ct]);
+                }
         }
         if (L::BUFS == 1 && c + 1 < c1) {
             __syncthreads();                // every wave is done with the buffer
@@ -273,8 +365,10 @@ __device__ __forceinline__ void forward_chain(const Params &p, int s, int j, int
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                end[(size_t)state_row(t, i, grp) * LD + cbase + col0 + r] = S[t][i];
+            for (int ct = 0; ct < CTW; ++ct)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    end[(size_t)state_row(t, i, grp) * LD + cbase + col0 + 16 * ct + r] = S[t][ct][i];
     }
 }
 

@@ -223,46 +223,78 @@ __device__ __forceinline__ f32x4 widen(s16x4 a) {
     return r;
 }
 
-// A staged matrix has 64 rows of W bf16 in 16-byte pieces; piece p of row r lies at place
-// p ^ (r % pieces) of its row, so that sixteen rows at one piece touch all banks.
+// A staged matrix has rows of W 16-bit values in 16-byte pieces; piece p of row r lies at place
+// p ^ swizzle(r) of its row. Sixteen lanes of a transposing read take four neighbouring rows of two
+// or four pieces, sixteen lanes of a 16-byte read one piece of sixteen rows: the two low bits of the
+// row spread the former over the banks (a row of 64 values fills only half of them, so there the
+// lowest bit does without), the next two the latter. With p ^ (r % 16) the transposing reads of
+// K met four to a bank (36% of the LDS cycles of the state pass).
+template <int W>
+__device__ __forceinline__ int swizzle(int row) {
+    return W == 128 ? (row & 3) << 2 | (row >> 2 & 3) : (row & 2) << 1 | (row >> 2 & 3);
+}
 template <int W>
 __device__ __forceinline__ int piece_at(int row, int piece) {
     constexpr int NP = W / 8;
-    return (row * NP + (piece ^ (row & (NP - 1)))) * 16;
+    return (row * NP + (piece ^ swizzle<W>(row))) * 16;
 }
 
-// 16 bytes per lane from memory to LDS at dst + 16 lane. Written out, because behind the builtin
-// the compiler waits for every copy in flight before the next transposing read of LDS, also where
-// the copies go to the other buffer. The kernels wait themselves (vm_drain) before the barrier
-// behind which the data is read. M0 takes its value one cycle before the copy reads it (s_nop).
-__device__ __forceinline__ void copy16_to_lds(const void *src, uint8_t *dst) {
+// 16 bytes per lane, from base + off, to LDS at dst + 16 lane (base and dst uniform). Written out,
+// because behind the builtin the compiler waits for every copy in flight before the next transposing
+// read of LDS, also where the copies go to the other buffer. The kernels wait themselves (vm_drain)
+// before the barrier behind which the data is read. M0 takes its value one cycle before the copy
+// reads it (s_nop).
+__device__ __forceinline__ void copy16_to_lds(const void *base, uint32_t off, uint8_t *dst) {
     const uint32_t at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_u8 *)dst);
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
-                 :: "s"(at), "v"(src) : "memory", "m0");
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+                 :: "s"(at), "v"(off), "s"(base) : "memory", "m0");
 }
 
-// Stage rows 0 .. 63 of a [tokens][stride] matrix into LDS (W columns, layout piece_at); rows
-// from nv on repeat row nv - 1, so that every read lies inside the sequence (the row scales and
-// operands that meet them are zero). NW waves share the work; no wait.
+// Stages 64 rows of W 16-bit values (rows `stride` values apart) into LDS, layout piece_at, NW waves
+// sharing the work. A wave's steps are NW * (64 / pieces) rows apart, a multiple of the rows after
+// which the swizzle repeats, so one offset per lane serves them all. Rows from nv on repeat row
+// nv - 1: every read lies inside the sequence, and the row scales and operands that meet such rows are
+// zero. No wait.
 template <int W, int NW>
-__device__ __forceinline__ void stage_rows(const uint16_t *src, int64_t stride, int nv,
-                                           uint8_t *dst, int wave, int lane) {
-    constexpr int NP = W / 8, STEPS = 64 * NP / 64;
-#pragma unroll
-    for (int q = 0; q < STEPS / NW; ++q) {
-        const int step = q * NW + wave;
-        const int at = step * 64 + lane, row = at / NP, piece = (at % NP) ^ (row & (NP - 1));
-        const int rr = row < nv ? row : nv - 1;
-        copy16_to_lds(src + rr * stride + piece * 8, dst + step * 1024);
+struct RowStage {
+    static constexpr int NP = W / 8, ROWS = 64 / NP, STEPS = NP / NW;
+    static_assert(STEPS >= 1 && (STEPS == 1 || NW * ROWS % (W == 128 ? 16 : 8) == 0), "one offset per lane");
+    int row, piece;
+    uint32_t off;                           // bytes
+    int64_t stride;
+    __device__ __forceinline__ RowStage(int64_t stride_, int wave, int lane) : stride(stride_) {
+        row = wave * ROWS + lane / NP;
+        piece = (lane % NP) ^ swizzle<W>(row);
+        off = (uint32_t)((row * stride + piece * 8) * 2);
     }
+    __device__ __forceinline__ void operator()(const uint16_t *src, int nv, uint8_t *dst, int wave) const {
+#pragma unroll
+        for (int q = 0; q < STEPS; ++q) {
+            uint8_t *const to = dst + (q * NW + wave) * 1024;
+            if (nv == 64) {
+                copy16_to_lds(src + q * NW * ROWS * stride, off, to);
+            } else {
+                const int r = row + q * NW * ROWS;
+                copy16_to_lds(src, (uint32_t)(((r < nv ? r : nv - 1) * stride + piece * 8) * 2), to);
+            }
+        }
+    }
+};
+
+template <int W, int NW>
+__device__ __forceinline__ void stage_rows(const uint16_t *src, int64_t stride, int nv, uint8_t *dst, int wave,
+                                           int lane) {
+    RowStage<W, NW>(stride, wave, lane)(src, nv, dst, wave);
 }
 
-// Stage `kib` KiB of consecutive memory.
-template <int NW>
-__device__ __forceinline__ void stage_block(const uint8_t *src, int kib, uint8_t *dst, int wave,
-                                            int lane) {
-    for (int step = wave; step < kib; step += NW)
-        copy16_to_lds(src + step * 1024 + lane * 16, dst + step * 1024);
+// Stage `KIB` KiB of consecutive memory.
+template <int KIB, int NW>
+__device__ __forceinline__ void stage_block(const uint8_t *src, uint8_t *dst, int wave, int lane) {
+#pragma unroll
+    for (int q = 0; q < (KIB + NW - 1) / NW; ++q) {
+        const int step = q * NW + wave;
+        if (step < KIB) copy16_to_lds(src + step * 1024, lane * 16, dst + step * 1024);
+    }
 }
 
 // ------------------------------------------------------------------------------- pre-stage
