@@ -66,9 +66,12 @@ __global__ __launch_bounds__(256) void prepare_kernel(Params p)
 {
     constexpr int MAT = 64 * K * 2;         // bytes of one staged plane
     using R = std::conditional_t<BWD, RecB, Rec<X>>;
-    __shared__ __attribute__((aligned(1024))) uint8_t kq[2 * IN * MAT];
-    __shared__ __attribute__((aligned(16))) float Lm[64 * P], Xm[64 * P];
+    // L and X take the place of K and Q once the Gram products are done: with less LDS more
+    // workgroups share a compute unit, which is what hides the phases' latencies
+    constexpr int LX = 2 * 64 * P * 4, AREA = 2 * IN * MAT > LX ? 2 * IN * MAT : LX;
+    __shared__ __attribute__((aligned(1024))) uint8_t kq[AREA];
     __shared__ Scalars sc;
+    float *const Lm = (float *)kq, *const Xm = Lm + 64 * P;
     uint8_t *const km = kq, *const qm = kq + IN * MAT;
     const int tid = threadIdx.x, lane = tid & 63, grp = lane >> 4, r = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -133,17 +136,19 @@ __global__ __launch_bounds__(256) void prepare_kernel(Params p)
     };
     // L row tile `wave` (rows in C-layout), and M of query tile 3 - wave, transposed, so that
     // a lane's four values are consecutive tokens of one query row: five tiles a wave
-    for (int tj = 0; tj <= wave; ++tj) {
+    f32x4 lt[4];
+#pragma unroll
+    for (int tj = 0; tj < 4; ++tj) {
+        lt[tj] = zero4();
+        if (tj > wave) continue;
         const f32x4 c = gram(km, wave, km, tj);
         const int jj = 16 * tj + r;
         const float sj = sc.rk[jj] * sc.beta[jj];
-        f32x4 l;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const int i = 16 * wave + 4 * grp + e;
-            l[e] = i > jj ? c[e] * sj * sc.rk[i] * decay(i, jj) : 0.f;
+            lt[tj][e] = i > jj ? c[e] * sj * sc.rk[i] * decay(i, jj) : 0.f;
         }
-        block_put(Lm, wave, tj, grp, r, l);
     }
     if constexpr (!BWD) {
         const int ti = 3 - wave, i = 16 * ti + r;
@@ -190,6 +195,10 @@ __global__ __launch_bounds__(256) void prepare_kernel(Params p)
             }
         }
     }
+    __syncthreads();
+#pragma unroll
+    for (int tj = 0; tj < 4; ++tj)
+        if (tj <= wave) block_put(Lm, wave, tj, grp, r, lt[tj]);
     __syncthreads();
     if (wave == 0) {                        // the four diagonal blocks, column r of block grp
         float x[16];

@@ -26,14 +26,10 @@ void run(const Params &p, hipStream_t st)
 template <int K, int V>
 hipError_t launch_state(const Params &p, bool f32, hipStream_t st)
 {
-    const int64_t units = (int64_t)p.seq.N * p.HV;
-    const bool halves = 2 * units <= kda::current_device_cus();
     if (f32)
         run<K, V, 64, 1, 3, 3>(p, st);
-    else if (halves || V == 64)
-        run<K, V, 64, 1, 1, 2>(p, st);
     else
-        run<K, V, V, V / 64, 1, 2>(p, st);
+        run<K, V, 64, 1, 1, 2>(p, st);
     return hipGetLastError();
 }
 
