@@ -57,9 +57,37 @@ float scale_of(const gdn_args *a)
 // A dense batch of short sequences takes the recurrence: a chunk has a fixed cost of 64 tokens.
 bool recurrent(const gdn_args *a) { return !a->cu_seqlens && a->T <= 16; }
 
+// Segments: the split with the shortest expected time, from the number of (sequence, value head)
+// units and the mean length (the lengths of packed sequences lie on the device). A workgroup's chunk
+// takes `last` us with outputs (one workgroup a compute unit at a time) and 3 us in the first pass (two at
+// a time), joining a segment 0.7 us, and the two more launches about 6 us.
+//   16 heads x 4096: 204 us whole, 62 us in 8 segments
+Segments plan_segments(int64_t tt, int64_t N, int64_t HV, int K, int V, int ends_parts, int last_parts, double last)
+{
+    Segments g = {};
+    if (N == 0 || tt == 0) return g;
+    const int64_t n = (tt / N + CT - 1) / CT, units = N * HV, cus = kda::current_device_cus();
+    auto rounds = [](int64_t x, int64_t y) { return (double)((x + y - 1) / y); };
+    double best = rounds(units * last_parts, cus) * n * last;
+    for (int64_t count = 2; count <= 64 && n / count >= 4; count *= 2) {
+        const int64_t len = (n + count - 1) / count;
+        const int64_t first = units * ((count - 1) * ends_parts + (count - 2) * (K / 64));
+        const double t = rounds(first, 2 * cus) * len * 3.0 + (count - 2) * 0.7 + 6.0 +
+                         rounds(units * count * last_parts, cus) * len * last;
+        if (t < 0.9 * best) {
+            best = t;
+            g.chunks = (int32_t)len;
+        }
+    }
+    if (g.chunks) g.slots = (int32_t)(tt / (CT * (int64_t)g.chunks) + N);
+    return g;
+}
+
 struct Layout {                     // byte offsets in the workspace
     int64_t tt, slots;
     size_t q, k, total;             // three bf16 planes each of q and k (fp32 io)
+    Segments seg;
+    size_t E, PHI;
 };
 
 Layout layout(const gdn_args *a)
@@ -71,7 +99,11 @@ Layout layout(const gdn_args *a)
     L.q = (size_t)L.slots * a->HV * (f32 ? Rec<3>::BYTES : Rec<2>::BYTES);
     const size_t planes = f32 ? align256((size_t)L.tt * a->H * a->K * 6) : 0;
     L.k = L.q + planes;
-    L.total = L.k + planes;
+    L.E = L.k + planes;
+    L.seg = plan_segments(L.tt, a->N, a->HV, a->K, a->V, a->V / 64, a->V / 64, f32 ? 9.0 : 3.2);
+    const size_t ends = (size_t)L.seg.slots * a->HV * a->K * 4;
+    L.PHI = L.E + ends * a->V;
+    L.total = L.PHI + 2 * ends * a->K;
     return L;
 }
 
@@ -312,6 +344,9 @@ kda_status gdn_fwd(const gdn_args *a, void *workspace, size_t ws_bytes, void *st
     const bool f32 = a->io == KDA_FP32;
     Params p = params_of(a, L);
     p.rec = ws;
+    p.seg = L.seg;
+    p.seg.E = (float *)(ws + L.E);
+    p.seg.PHI = (float *)(ws + L.PHI);
     if (f32 && L.tt > 0) {
         const int64_t n = L.tt * a->H * a->K;
         if (launch_split_planes((const float *)a->q, n, (uint16_t *)(ws + L.q), hs) != hipSuccess ||

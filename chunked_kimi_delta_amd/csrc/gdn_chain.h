@@ -94,6 +94,35 @@ __device__ __forceinline__ void keep_rows(const f32x4 (&E)[4][CTW], Scale f, uin
     if (threadIdx.x == 0) *inv = f.inv;
 }
 
+// One segment: its sequence, its place in it, and its chunks [c0, c1).
+struct Segment {
+    int s, i, count, c0, c1;
+    __device__ __forceinline__ bool last() const { return i == count - 1; }
+};
+
+// Slot -> segment; false where the slot holds none (a sequence without tokens has one, empty segment, so
+// that its state is passed on). Binary search as in locate_slot.
+__device__ __forceinline__ bool locate_segment(const SeqGeom &sg, int chunks, int slot, Segment *out) {
+    const int64_t len = (int64_t)CT * chunks;
+    int lo = 0, hi = sg.N - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (kda::seq_bos(sg, mid) / len + mid <= slot) lo = mid; else hi = mid - 1;
+    }
+    const int64_t bos = kda::seq_bos(sg, lo), n = (kda::seq_eos(sg, lo, bos) - bos + CT - 1) / CT;
+    const int64_t i = slot - (bos / len + lo), count = n > 0 ? (n + chunks - 1) / chunks : 1;
+    if (i < 0 || i >= count) return false;
+    const int64_t c1 = (i + 1) * chunks;
+    *out = Segment{lo, (int)i, (int)count, (int)(i * chunks), (int)(c1 < n ? c1 : n)};
+    return true;
+}
+
+// The whole sequence as one segment.
+__device__ __forceinline__ Segment whole_sequence(const SeqGeom &sg, int s) {
+    const int64_t bos = kda::seq_bos(sg, s);
+    return Segment{s, 0, 1, 0, (int)((kda::seq_eos(sg, s, bos) - bos + CT - 1) / CT)};
+}
+
 // The chunks [c0, c1) of one (sequence, value head) for the C columns from `cbase` of `ld` columns,
 // CTW 16-column tiles a wave (one wave per 16 CTW columns of C).
 // init: the state's first element at c0 (row-major, `ld` columns), null for zeros (PHI: ignored);
@@ -369,6 +398,12 @@ __device__ __forceinline__ void forward_chain(const Params &p, int s, int j, int
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     end[(size_t)state_row(t, i, grp) * LD + cbase + col0 + 16 * ct + r] = S[t][ct][i];
+        if constexpr (M == PHI) {           // and the transpose behind it
+            const auto rs = kda::buffer_rsrc(end + K * K, K * K * 4);
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+                kda::bstore16<0>(rs, ((cbase + col0 + r) * K + state_row(t, 0, grp)) * 4, 0, S[t][0]);
+        }
     }
 }
 

@@ -30,6 +30,20 @@ using kda::zero4;
 
 constexpr int CT = 64;                  // tokens per chunk
 
+// Segments of `chunks` chunks each, where a batch is too small to fill the device (chunks > 0). Segment
+// i of sequence s lies in slot floor(bos_s / (64 chunks)) + s + i. A chunk step is affine in the state,
+// so with PHI_i the transition of segment i (its end state from the identity, without v) and E_i its end
+// state from zero (segment 0: from the initial state), the true end states are
+//     E_i <- PHI_i E_{i-1} + E_i,
+// and in reverse the gradients before the segments G_i <- PHI_i^T G_{i+1} + G_i, G_i from zero (the last
+// segment: from dht). First pass: E, G and PHI of all segments side by side; the few products above; then
+// every segment from its true start. The last segment's slot of E and the first one's of G are not
+// needed for that and hold copies of the initial state (which final_state may overwrite).
+struct Segments {
+    int32_t chunks, slots;
+    float *E, *G, *PHI;                 // [slots][HV][K][V], the same, [slots][HV][2][K][K] (and transposed)
+};
+
 struct Pre {
     int32_t qk_l2norm, beta_sigmoid, gate;
     float lower_bound;
@@ -47,6 +61,7 @@ struct Params {
     float *ht;
     uint8_t *rec;                       // chunk records
     Pre pre;
+    Segments seg;
 };
 
 struct BwdParams {
@@ -243,11 +258,11 @@ __device__ __forceinline__ int piece_at(int row, int piece) {
 // because behind the builtin the compiler waits for every copy in flight before the next transposing
 // read of LDS, also where the copies go to the other buffer. The kernels wait themselves (vm_drain)
 // before the barrier behind which the data is read. M0 takes its value one cycle before the copy
-// reads it (s_nop).
+// reads it (s_nop); nothing else in these kernels uses M0.
 __device__ __forceinline__ void copy16_to_lds(const void *base, uint32_t off, uint8_t *dst) {
     const uint32_t at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_u8 *)dst);
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
-                 :: "s"(at), "v"(off), "s"(base) : "memory", "m0");
+                 :: "s"(at), "v"(off), "s"(base) : "memory");
 }
 
 // Stages 64 rows of W 16-bit values (rows `stride` values apart) into LDS, layout piece_at, NW waves

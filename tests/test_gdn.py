@@ -137,6 +137,10 @@ def test_workspace(lib):
     need = lambda **kw: lib.gdn_fwd_workspace_bytes(ctypes.byref(args(**kw)))
     assert need() > 0 and need(T=16) == 0 and need(K=96) == 0
     assert need(T=16, cu_seqlens=FAKE) > 0
+    # few heads and long sequences: room for the segments' ends behind the chunks' records
+    records = lambda T, HV, N=1: (T // 64 + N) * HV * 25 * 1024
+    assert need() == records(100, 4) and need(T=4096, H=64, HV=256) == records(4096, 256)
+    assert need(T=4096, H=2, HV=2) > records(4096, 2)
     n = need()
     call = lambda ws, size: lib.gdn_fwd(ctypes.byref(args()), ws, size, None)
     assert call(None, n) == call(FAKE, n - 1) == call(FAKE + 16, n) == _lib.KDA_ERR_WORKSPACE

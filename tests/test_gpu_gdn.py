@@ -45,6 +45,25 @@ def test_packed(lens, dtype):
     check(make(H=1, G=3, K=64, V=128, lens=lens, dtype=dtype, h0=True, seed=len(lens)))
 
 
+# long sequences of few heads run in segments that are joined: dense and ragged, with sequences of one
+# segment and of none next to long ones
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("kw", [
+    dict(T=1030, K=128, V=128), dict(T=2100, K=64, V=128), dict(T=1500, K=128, V=64, raw=True, gate="softplus"),
+    dict(lens=[900, 0, 64, 1300, 1], K=64, V=64), dict(lens=[3000, 5], K=64, V=64), dict(B=2, T=700, K=64, V=64)])
+def test_segments(kw, dtype):
+    for h0 in (False, True):
+        check(make(H=1, G=2, dtype=dtype, h0=h0, **kw))
+
+
+def test_segments_update_the_state_in_place():
+    a = to(make(T=2000, H=1, G=2, K=64, V=128, h0=True), DEV)
+    o, fin = kda.gdn_fwd(**a)
+    h = a["initial_state"].clone()
+    o2, _ = kda.GdnFwdPlan(**(a | {"initial_state": h}), final_state=h)()
+    assert torch.equal(o, o2) and torch.equal(h, fin)
+
+
 @pytest.mark.parametrize("dtype", [BF, FP])
 @pytest.mark.parametrize("gate,dt_bias", [(None, True), ("softplus", True), ("softplus", False), ("bounded", True)])
 @pytest.mark.parametrize("T", [3, 90])
@@ -214,8 +233,9 @@ def test_many_rows_of_a_step():
 
 # ------------------------------------------------------------------------- streams and graphs
 
-def test_replays_of_a_graph():
-    a = to(make(B=1, T=300, H=2, K=128, V=128, h0=True), DEV)
+@pytest.mark.parametrize("T", [300, 1200])
+def test_replays_of_a_graph(T):
+    a = to(make(B=1, T=T, H=2, K=128, V=128, h0=True), DEV)
     st = to(make(B=2, T=1, H=2, K=128, V=128), DEV)
     pool = torch.zeros(2, 2, 128, 128, device=DEV)
     plan, step = kda.GdnFwdPlan(**a), kda.GdnStepPlan(**st, state=pool)
@@ -226,7 +246,7 @@ def test_replays_of_a_graph():
         plan()
         step()
     for seed in range(3):
-        for d, n in ((a, dict(B=1, T=300, h0=True)), (st, dict(B=2, T=1))):
+        for d, n in ((a, dict(B=1, T=T, h0=True)), (st, dict(B=2, T=1))):
             new = to(make(H=2, K=128, V=128, seed=seed + 20, **n), DEV)
             for x in d:
                 d[x].copy_(new[x])
