@@ -57,24 +57,31 @@ float scale_of(const gdn_args *a)
 // A dense batch of short sequences takes the recurrence: a chunk has a fixed cost of 64 tokens.
 bool recurrent(const gdn_args *a) { return !a->cu_seqlens && a->T <= 16; }
 
-// Segments: the split with the shortest expected time, from the number of (sequence, value head)
-// units and the mean length (the lengths of packed sequences lie on the device). A workgroup's chunk
-// takes `last` us with outputs (one workgroup a compute unit at a time) and 3 us in the first pass (two at
-// a time), joining a segment 0.7 us, and the two more launches about 6 us.
-//   16 heads x 4096: 204 us whole, 62 us in 8 segments
-Segments plan_segments(int64_t tt, int64_t N, int64_t HV, int K, int V, int ends_parts, int last_parts, double last)
+// What a chunk takes, us, by kernel: a workgroup of the whole-sequence pass alone, of the last pass over
+// segments with every compute unit busy, and of the first pass (two workgroups a compute unit).
+struct ChunkTimes {
+    double whole, last, first;
+};
+
+// The number of segments with the shortest expected time, from the number of (sequence, value head) units
+// and the mean length (the lengths of packed sequences lie on the device). Joining takes 2.1 us a segment,
+// two more launches about 6 us. Measured, 16 heads x 4096, bf16 io, state pass of the forward: whole 206
+// us; 4 segments 97, 6: 87, 8: 77, 11: 103, 16: 97 us. 8 packed sequences x 32 heads: whole 465 us, two or
+// more segments 660 us and up (512 workgroups fill the device already).
+Segments plan_segments(int64_t tt, int64_t N, int64_t HV, int K, int ends_parts, int last_parts, ChunkTimes us)
 {
     Segments g = {};
     if (N == 0 || tt == 0) return g;
     const int64_t n = (tt / N + CT - 1) / CT, units = N * HV, cus = kda::current_device_cus();
     auto rounds = [](int64_t x, int64_t y) { return (double)((x + y - 1) / y); };
-    double best = rounds(units * last_parts, cus) * n * last;
-    for (int64_t count = 2; count <= 64 && n / count >= 4; count *= 2) {
+    double best = rounds(units * last_parts, cus) * n * us.whole;
+    for (int64_t count = 2; count <= 64; ++count) {
         const int64_t len = (n + count - 1) / count;
+        if (len < 2) break;
         const int64_t first = units * ((count - 1) * ends_parts + (count - 2) * (K / 64));
-        const double t = rounds(first, 2 * cus) * len * 3.0 + (count - 2) * 0.7 + 6.0 +
-                         rounds(units * count * last_parts, cus) * len * last;
-        if (t < 0.9 * best) {
+        const double t = rounds(first, 2 * cus) * len * us.first + (count - 2) * 2.1 + 6.0 +
+                         rounds(units * count * last_parts, cus) * len * us.last;
+        if (t < 0.95 * best) {
             best = t;
             g.chunks = (int32_t)len;
         }
@@ -100,7 +107,8 @@ Layout layout(const gdn_args *a)
     const size_t planes = f32 ? align256((size_t)L.tt * a->H * a->K * 6) : 0;
     L.k = L.q + planes;
     L.E = L.k + planes;
-    L.seg = plan_segments(L.tt, a->N, a->HV, a->K, a->V, a->V / 64, a->V / 64, f32 ? 9.0 : 3.2);
+    L.seg = plan_segments(L.tt, a->N, a->HV, a->K, a->V / 64, a->V / 64,
+                          f32 ? ChunkTimes{7.8, 8.7, 5.2} : ChunkTimes{3.2, 4.1, 3.8});
     const size_t ends = (size_t)L.seg.slots * a->HV * a->K * 4;
     L.PHI = L.E + ends * a->V;
     L.total = L.PHI + 2 * ends * a->K;
@@ -192,7 +200,8 @@ struct BwdLayout {
     Layout f;
     // bf16 io: records, kept states; fp32 io: the decay repeated over K, its gradient and
     // kda_bwd's own workspace; with a gate, the gradient of the activated decay
-    size_t keep, dg_act, dwide, kda, kda_bytes, total;
+    size_t keep, dg_act, dwide, kda, kda_bytes, E, G, PHI, total;
+    Segments seg;
 };
 
 size_t keep_bytes(int K, int V)
@@ -234,7 +243,12 @@ BwdLayout bwd_layout(const gdn_args *a)
     size_t at;
     if (a->io == KDA_BF16) {
         L.keep = slots * RecB::BYTES;
-        at = L.keep + slots * keep_bytes(a->K, a->V);
+        L.E = L.keep + slots * keep_bytes(a->K, a->V);
+        L.seg = plan_segments(L.f.tt, a->N, a->HV, a->K, 2 * (a->V / 64), 2, ChunkTimes{6.0, 7.0, 4.0});
+        const size_t ends = (size_t)L.seg.slots * a->HV * a->K * 4;
+        L.G = L.E + ends * a->V;
+        L.PHI = L.G + ends * a->V;
+        at = L.PHI + 2 * ends * a->K;
     } else {
         const kda_fwd_args w = wide_args(a, nullptr);
         L.dwide = align256(rows * a->K * 4);
@@ -302,6 +316,10 @@ kda_status gdn_bwd(const gdn_args *a, const void *d_o, const float *dht, void *w
         }
         BwdParams b = {};
         b.f = p;
+        b.f.seg = L.seg;
+        b.f.seg.E = (float *)(ws + L.E);
+        b.f.seg.G = (float *)(ws + L.G);
+        b.f.seg.PHI = (float *)(ws + L.PHI);
         b.d_o = (const uint16_t *)d_o;
         b.dht = dht;
         b.keep = ws + L.keep;

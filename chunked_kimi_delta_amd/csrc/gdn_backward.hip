@@ -25,30 +25,31 @@
 // parts against the stored q and k.
 #include <type_traits>
 
-#include "gdn_chain.h"
+#include "gdn_segments.h"
 
 namespace gdn {
 
 namespace {
 
-template <int K, int V>
+template <int K, int C>
 struct StageR {                             // LDS of one chunk of the reverse pass
-    static constexpr int MK = 64 * K * 2, MV = 64 * V * 2;
+    static constexpr int MK = 64 * K * 2, MV = 64 * C * 2;
     static constexpr int KM = 0, QM = MK, DO = 2 * MK, REC = DO + MV;
     static constexpr int BYTES = REC + RecB::REV_KIB * 1024;
 };
 
-// The reverse pass over chunks c1 - 1 .. c0, from the gradient `init` of the state behind them (null:
-// zero) to the gradient `end` of the state before them (or null).
-template <int K, int V>
-__device__ __forceinline__ void reverse_chain(const BwdParams &b, int s, int j, int c0, int c1,
+// The reverse pass over chunks c1 - 1 .. c0 for the C columns from `cbase`, from the gradient `init` of the
+// state behind them (null: zero) to the gradient `end` of the state before them (or null). KEPT: leaves dS'
+// and dR for the local kernel (all columns in one workgroup then, for the scales); else a segment's end only.
+template <int K, int V, int C, int BUFS, bool KEPT>
+__device__ __forceinline__ void reverse_chain(const BwdParams &b, int s, int j, int c0, int c1, int cbase,
                                               const float *init, float *end, uint8_t *lds,
-                                              Maxima<V / 16> *mx)
+                                              Maxima<C / 16> *mx = nullptr)
 {
-    using L = StageR<K, V>;
+    using L = StageR<K, C>;
     using R = RecB;
     using KP = Keep<K, V>;
-    constexpr int X = R::X, NW = V / 16, NT = K / 16;
+    constexpr int X = R::X, NW = C / 16, NT = K / 16;
     const Params &p = b.f;
     const int tid = threadIdx.x, lane = tid & 63, grp = lane >> 4, r = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -58,14 +59,14 @@ __device__ __forceinline__ void reverse_chain(const BwdParams &b, int s, int j, 
     const int col0 = 16 * wave;
 
     const RowStage<K, NW> qk_rows((int64_t)p.H * K, wave, lane);
-    const RowStage<V, NW> v_rows((int64_t)p.HV * V, wave, lane);
+    const RowStage<C, NW> v_rows((int64_t)p.HV * V, wave, lane);
     auto stage = [&](int c, uint8_t *buf) {
         const int64_t t0 = bos + (int64_t)CT * c;
         const int nv = (int)(eos - t0 < CT ? eos - t0 : CT);
         const int64_t qk = (t0 * p.H + h) * K;
         qk_rows(p.k[0] + qk, nv, buf + L::KM, wave);
         qk_rows(p.q[0] + qk, nv, buf + L::QM, wave);
-        v_rows(b.d_o + (t0 * p.HV + j) * V, nv, buf + L::DO, wave);
+        v_rows(b.d_o + (t0 * p.HV + j) * V + cbase, nv, buf + L::DO, wave);
         stage_block<R::REV_KIB, NW>(p.rec + (slot0 + c) * R::BYTES + R::REV, buf + L::REC, wave, lane);
     };
     if (c0 < c1) stage(c1 - 1, lds);
@@ -75,14 +76,14 @@ __device__ __forceinline__ void reverse_chain(const BwdParams &b, int s, int j, 
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) S[t][0][i] = init ? init[(size_t)state_row(t, i, grp) * V + col0 + r] : 0.f;
+        for (int i = 0; i < 4; ++i) S[t][0][i] = init ? init[(size_t)state_row(t, i, grp) * V + cbase + col0 + r] : 0.f;
 #pragma unroll
     for (int t = 0; t < 4; ++t) D[t][0] = zero4();
 
 #pragma unroll 1
     for (int c = c1 - 1; c >= c0; --c) {
-        uint8_t *const buf = lds + ((c1 - 1 - c) & 1) * L::BYTES;
-        {
+        uint8_t *const buf = lds + (c1 - 1 - c) % BUFS * L::BYTES;
+        if constexpr (KEPT) {
             const float x = largest(S), y = largest(D);
             if (lane == 0) {
                 mx->state[c & 1][wave] = x;
@@ -91,11 +92,13 @@ __device__ __forceinline__ void reverse_chain(const BwdParams &b, int s, int j, 
         }
         kda::vm_drain();
         __syncthreads();
-        if (c > c0) stage(c - 1, lds + ((c1 - c) & 1) * L::BYTES);
+        if (BUFS == 2 && c > c0) stage(c - 1, lds + (c1 - c) % BUFS * L::BYTES);
+        if constexpr (KEPT) {
         keep_state(S, mx->scale(mx->state[c & 1]), kept(c) + KP::DS, (float *)(kept(c) + KP::SCALE) + 1, col0 + r, grp);
         if (c < c1 - 1)
             keep_rows(D, mx->scale(mx->rows[c & 1]), kept(c + 1) + KP::DR, (float *)(kept(c + 1) + KP::SCALE) + 3,
                       col0 + r, grp);
+        }
         const uint8_t *const rec = buf + L::REC - R::REV;
         const float *const ra = (const float *)(rec + R::RA), *const rb = (const float *)(rec + R::RB),
                     *const rc = (const float *)(rec + R::RC);
@@ -119,7 +122,7 @@ __device__ __forceinline__ void reverse_chain(const BwdParams &b, int s, int j, 
         for (int st = 0; st < 2; ++st)
 #pragma unroll
             for (int u = 0; u < 2; ++u)
-                dv[st][u] = lds_tr(buf + L::DO + piece_at<V>(32 * st + 16 * u + 4 * grp + (r >> 2),
+                dv[st][u] = lds_tr(buf + L::DO + piece_at<C>(32 * st + 16 * u + 4 * grp + (r >> 2),
                                                              col0 / 8 + ((r & 3) >> 1)) + 8 * (r & 1));
         Parts<X> dp[2];
 #pragma unroll
@@ -160,8 +163,12 @@ __device__ __forceinline__ void reverse_chain(const BwdParams &b, int s, int j, 
                 S[t][0] = mm(Parts<1>{join(lds_tr(buf + L::QM + at0), lds_tr(buf + L::QM + at1))}, op, S[t][0]);
             }
         }
+        if (BUFS == 1 && c > c0) {
+            __syncthreads();                // every wave is done with the buffer
+            stage(c - 1, lds);
+        }
     }
-    if (c0 < c1) {
+    if (KEPT && c0 < c1) {
         const float y = largest(D);
         if (lane == 0) mx->rows[(c0 - 1) & 1][wave] = y;
         __syncthreads();
@@ -172,14 +179,14 @@ __device__ __forceinline__ void reverse_chain(const BwdParams &b, int s, int j, 
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) end[(size_t)state_row(t, i, grp) * V + col0 + r] = S[t][0][i];
+            for (int i = 0; i < 4; ++i) end[(size_t)state_row(t, i, grp) * V + cbase + col0 + r] = S[t][0][i];
     }
 }
 
 }  // namespace
 
-// Both passes: workgroups 2 u and 2 u + 1 of unit u.
-template <int K, int V>
+// Both passes: parts 0 and 1 of a unit (SEG: of a segment).
+template <int K, int V, bool SEG>
 __global__ __launch_bounds__(V * 4) void chains_kernel(BwdParams b)
 {
     using F = Stage<K, V, 1, RecB, KEEP>;
@@ -188,16 +195,61 @@ __global__ __launch_bounds__(V * 4) void chains_kernel(BwdParams b)
     __shared__ Maxima<V / 16> mx;
     static_assert(BYTES + sizeof(mx) <= 160 * 1024, "LDS of a compute unit");
     const Params &p = b.f;
-    const int unit = kda::longest_first(p.seq, p.HV, blockIdx.x >> 1);
+    constexpr size_t KV = (size_t)K * V;
+    int unit, part;
+    if (!unit_of(blockIdx.x, 2, (SEG ? p.seg.slots : p.seq.N) * p.HV, &unit, &part)) return;
+    Segment g;
+    if constexpr (SEG) {
+        if (!locate_segment(p.seq, p.seg.chunks, unit / p.HV, &g)) return;
+    } else {
+        unit = kda::longest_first(p.seq, p.HV, unit);
+        g = whole_sequence(p.seq, unit / p.HV);
+    }
+    const int j = unit % p.HV;
+    const size_t at = ((size_t)g.s * p.HV + j) * KV;
+    if (part == 0) {
+        const float *const init = SEG ? segment_start<K, V>(p, g, unit / p.HV, j) : p.h0 ? p.h0 + at : nullptr;
+        forward_chain<K, V, V, 1, 1, RecB::X, RecB, KEEP>(p, g.s, j, g.c0, g.c1, 0, init, nullptr, lds, b.keep, &mx);
+    } else {
+        const float *const init = !g.last() ? p.seg.G + ((size_t)unit + p.HV) * KV : b.dht ? b.dht + at : nullptr;
+        reverse_chain<K, V, V, 2, true>(b, g.s, j, g.c0, g.c1, 0, init, g.i == 0 && b.dh0 ? b.dh0 + at : nullptr, lds, &mx);
+    }
+}
+
+// The first pass over segments: E and PHI (gdn_segments.h), and G of every segment but the first.
+template <int K, int V>
+__global__ __launch_bounds__(256, 2) void bwd_ends_kernel(BwdParams b)
+{
+    using LE = Stage<K, 64, 1, RecB, END>;
+    using LP = Stage<K, 64, 1, RecB, PHI>;
+    constexpr int A = LE::BYTES * LE::BUFS, B = LP::BYTES * LP::BUFS, G = StageR<K, 64>::BYTES;
+    constexpr int AB = A > B ? A : B, NF = V / 64 + K / 64, NP = NF + V / 64;
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[AB > G ? AB : G];
+    const Params &p = b.f;
+    int unit, part;
+    if (!unit_of(blockIdx.x, NP, p.seg.slots * p.HV, &unit, &part)) return;
+    const int j = unit % p.HV;
+    if (part < NF) {
+        forward_ends<K, V, 1, RecB::X, RecB>(p, unit / p.HV, j, part, lds);
+        return;
+    }
+    Segment g;
+    if (!locate_segment(p.seq, p.seg.chunks, unit / p.HV, &g) || g.i == 0) return;
+    const float *const init = g.last() && b.dht ? b.dht + ((size_t)g.s * p.HV + j) * K * V : nullptr;
+    reverse_chain<K, V, 64, 1, false>(b, g.s, j, g.c0, g.c1, 64 * (part - NF), init, p.seg.G + (size_t)unit * K * V, lds);
+}
+
+template <int K, int V>
+__global__ __launch_bounds__(256) void bwd_join_kernel(Params p)
+{
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[Join<K, RecB::X>::BYTES];
+    int unit, part;
+    if (!unit_of(blockIdx.x, V / 8, p.seq.N * p.HV, &unit, &part)) return;
     const int s = unit / p.HV, j = unit % p.HV;
-    const int64_t bos = kda::seq_bos(p.seq, s), eos = kda::seq_eos(p.seq, s, bos);
-    const int nc = (int)((eos - bos + CT - 1) / CT);
-    const size_t at = ((size_t)s * p.HV + j) * K * V;
-    if (blockIdx.x & 1)
-        reverse_chain<K, V>(b, s, j, 0, nc, b.dht ? b.dht + at : nullptr, b.dh0 ? b.dh0 + at : nullptr, lds, &mx);
+    if (part & 1)
+        join_ends<K, V, RecB::X, true>(p, p.seg.G, s, j, part / 2 * 16, lds);
     else
-        forward_chain<K, V, V, 1, 1, RecB::X, RecB, KEEP>(p, s, j, 0, nc, 0, p.h0 ? p.h0 + at : nullptr, nullptr, lds,
-                                                       b.keep, &mx);
+        join_ends<K, V, RecB::X, false>(p, p.seg.E, s, j, part / 2 * 16, lds);
 }
 
 namespace {
@@ -630,8 +682,15 @@ template <int K, int V>
 hipError_t launch_backward(const BwdParams &b, hipStream_t st)
 {
     const Params &p = b.f;
-    chains_kernel<K, V><<<dim3(2 * p.seq.N * p.HV), dim3(4 * V), 0, st>>>(b);
-    hipError_t e = hipGetLastError();
+    const int64_t units = (int64_t)p.seq.N * p.HV, segs = (int64_t)p.seg.slots * p.HV;
+    if (p.seg.chunks == 0) {
+        chains_kernel<K, V, false><<<dim3(grid_for(units, 2)), dim3(4 * V), 0, st>>>(b);
+    } else {
+        bwd_ends_kernel<K, V><<<dim3(grid_for(segs, 2 * (V / 64) + K / 64)), dim3(256), 0, st>>>(b);
+        bwd_join_kernel<K, V><<<dim3(grid_for(units, V / 8)), dim3(256), 0, st>>>(p);
+        chains_kernel<K, V, true><<<dim3(grid_for(segs, 2)), dim3(4 * V), 0, st>>>(b);
+    }
+    const hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.seq.T_total == 0) return e;
     local_kernel<K, V><<<dim3(p.seq.n_slots, p.H), dim3(4 * K), 0, st>>>(b);
     return hipGetLastError();

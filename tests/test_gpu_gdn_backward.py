@@ -89,6 +89,15 @@ def test_packed(lens, dtype):
     check(make(H=1, G=3, K=64, V=128, lens=lens, dtype=dtype, h0=True, seed=len(lens)))
 
 
+# segments (dense and ragged, with sequences of one segment and of none next to long ones)
+@pytest.mark.parametrize("kw", [
+    dict(T=1030, G=1, K=128, V=128), dict(T=900, G=2, K=64, V=128), dict(T=770, G=2, K=128, V=64, raw=True, gate="softplus"),
+    dict(lens=[900, 0, 64, 600, 1], G=1, K=64, V=64), dict(B=2, T=700, G=2, K=64, V=64)])
+@pytest.mark.parametrize("h0", [False, True])
+def test_segments(kw, h0):
+    check(make(H=1, h0=h0, **kw), dht=h0)
+
+
 @pytest.mark.parametrize("dtype", [BF, FP])
 @pytest.mark.parametrize("gate,dt_bias", [(None, True), ("softplus", True), ("softplus", False), ("bounded", True)])
 @pytest.mark.parametrize("T", [3, 90])
@@ -180,9 +189,9 @@ def test_runs_are_equal_and_streams_do_not_matter():
             assert torch.equal(x, y)
 
 
-@pytest.mark.parametrize("dtype", [BF, FP])
-def test_replays_of_a_graph(dtype):
-    kw = dict(B=1, T=200, H=2, K=64, V=64, dtype=dtype, raw=True, gate="softplus", h0=True)
+@pytest.mark.parametrize("dtype,T", [(BF, 200), (FP, 200), (BF, 1000)])
+def test_replays_of_a_graph(dtype, T):
+    kw = dict(B=1, T=T, H=2, K=64, V=64, dtype=dtype, raw=True, gate="softplus", h0=True)
     a = to(make(**kw), DEV)
     d_o = torch.randn_like(a["v"])
     plan = kda.GdnBwdPlan(**a, d_o=d_o)
