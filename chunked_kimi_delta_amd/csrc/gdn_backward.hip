@@ -254,19 +254,19 @@ __global__ __launch_bounds__(256) void bwd_join_kernel(Params p)
 
 namespace {
 
-// LDS of the local kernel. The four 64 x 64 matrices (128-byte rows, pieces swizzled) lie where
-// the state was, once its products are done.
+// LDS of the local kernel. The two 64 x 64 matrices (128-byte rows, pieces swizzled) lie where the state
+// was, once its products are done.
 template <int K, int V>
 struct Local {
     static constexpr int MK = 64 * K * 2, MV = 64 * V * 2, MS = V * K * 2;
     static constexpr int Q = 0, KM = MK, DO = 2 * MK, E = DO + MV, DR = E + MV, S = DR + MV, DS = S + MS;
-    static constexpr int W = S;             // P1 .. P4 [j][i], two parts each
-    static constexpr int END = DS + MS > W + 8 * 8192 ? DS + MS : W + 8 * 8192;
+    static constexpr int W = S;             // P1, P2 [j][i], two parts each
+    static constexpr int SCAL = DS + MS > W + 4 * 8192 ? DS + MS : W + 4 * 8192;
+    static constexpr int INV = SCAL + 2048, END = INV + 1024;   // RecB's scalars, Keep's scales
 };
 
 template <int NW>
 struct LocalScalars {
-    float ghi[64], glo[64], beta[64], rk[64], rq[64];
     float rowsum[4][64], colsum[4][64];     // of beta_j U, U below the diagonal, per tile column / row
     float diag[64];                         // of U
     float cross[64];                        // sum_{i >= t > j} beta_j U_ij within t's own tile
@@ -316,6 +316,9 @@ __global__ __launch_bounds__(K * 4) void local_kernel(BwdParams b)
     int s, nv;
     int64_t bos;
     if (!kda::locate_slot<CT>(p.seq, slot, &s, &bos, &nv)) return;
+    const float *const scal = (const float *)(lds + L::SCAL);
+    const float *const ghi = scal, *const glo = scal + 64, *const beta = scal + 128, *const rk = scal + 192,
+                *const rq = scal + 256;
     const int64_t qk0 = (bos * p.H + h) * K;
     stage_rows<K, NW>(p.q[0] + qk0, (int64_t)p.H * K, nv, lds + L::Q, wave, lane);
     stage_rows<K, NW>(p.k[0] + qk0, (int64_t)p.H * K, nv, lds + L::KM, wave, lane);
@@ -350,29 +353,27 @@ __global__ __launch_bounds__(K * 4) void local_kernel(BwdParams b)
         const int j = h * p.G + m;
         const size_t at = (size_t)j * p.seq.n_slots + slot;
         const uint8_t *const keep = b.keep + at * Keep<K, V>::BYTES;
-        const float *const rec = (const float *)(p.rec + at * R::BYTES);
         if (m > 0) __syncthreads();                 // the previous head is done with the buffers
+        stage_block<2, NW>(p.rec + at * R::BYTES + R::GHI, lds + L::SCAL, wave, lane);
+        if (wave == NW - 1) copy16_to_lds(keep + Keep<K, V>::SCALE, lane * 16, lds + L::INV);
         stage_rows<V, NW>(b.d_o + (bos * p.HV + j) * V, (int64_t)p.HV * V, nv, lds + L::DO, wave, lane);
-        // [V][64 tokens] and [V][K] records: V rows of 64 (K) values
+        // [V][64 tokens] and [V][K] records: V rows of 64 (K) values; the states last, as they are used last
 #pragma unroll
         for (int q = 0; q < V / 64; ++q) {
             stage_rows<64, NW>((const uint16_t *)(keep + Keep<K, V>::E) + q * 64 * 64, 64, 64, lds + L::E + q * 8192, wave, lane);
             stage_rows<64, NW>((const uint16_t *)(keep + Keep<K, V>::DR) + q * 64 * 64, 64, 64, lds + L::DR + q * 8192, wave, lane);
+        }
+#pragma unroll
+        for (int q = 0; q < V / 64; ++q) {
             stage_rows<K, NW>((const uint16_t *)(keep + Keep<K, V>::S) + q * 64 * K, K, 64, lds + L::S + q * L::MK, wave, lane);
             stage_rows<K, NW>((const uint16_t *)(keep + Keep<K, V>::DS) + q * 64 * K, K, 64, lds + L::DS + q * L::MK, wave, lane);
         }
-        if (wave == 0) {
-            sc.ghi[lane] = rec[R::GHI / 4 + lane];
-            sc.glo[lane] = rec[R::GLO / 4 + lane];
-            sc.beta[lane] = rec[R::BETA / 4 + lane];
-            sc.rk[lane] = rec[R::RK / 4 + lane];
-            sc.rq[lane] = rec[R::RQ / 4 + lane];
-        }
-        const float *const inv = (const float *)(keep + Keep<K, V>::SCALE);
-        const float fs = inv[0], fds = inv[1], fe = inv[2], fdr = inv[3];
-        kda::vm_drain();
+        constexpr int LATE = V / 64 * 2 * RowStage<K, NW>::STEPS;  // copies of the states
+        asm volatile("s_waitcnt vmcnt(%0)" :: "n"(LATE) : "memory");
         __syncthreads();
-        const float whi = sc.ghi[63], wlo = sc.glo[63];
+        const float *const inv = (const float *)(lds + L::INV);
+        const float fs = inv[0], fds = inv[1], fe = inv[2], fdr = inv[3];
+        const float whi = ghi[63], wlo = glo[63];
         // dO as fp16, in place
         constexpr int NP = 64 * V / 8 / NTH;
         uint4 ob[NP];
@@ -426,29 +427,28 @@ __global__ __launch_bounds__(K * 4) void local_kernel(BwdParams b)
             }
             __builtin_amdgcn_sched_barrier(0);
             const int jj = 16 * tj + r;
-            const float bj = sc.beta[jj], rkj = sc.rk[jj], f1 = so.inv * fe * p.scale, f2 = -fdr * fe;
+            const float bj = beta[jj], rkj = rk[jj], f1 = so.inv * fe * p.scale, f2 = -fdr * fe;
             float col = 0.f;
             f32x4 bu;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int i = 16 * ti + 4 * grp + e;
                 const float d = i >= jj && i < nv
-                                    ? __builtin_amdgcn_exp2f((sc.ghi[i] - sc.ghi[jj]) + (sc.glo[i] - sc.glo[jj]))
+                                    ? __builtin_amdgcn_exp2f((ghi[i] - ghi[jj]) + (glo[i] - glo[jj]))
                                     : 0.f;
                 const float y1 = d != 0.f ? x1[e] * d * f1 : 0.f;
                 const float y2 = d != 0.f && i > jj ? x2[e] * d * f2 : 0.f;
-                const float uu = rkj * (y1 * sc.rq[i] * qk[e] + y2 * sc.rk[i] * kk[e]);
+                const float uu = rkj * (y1 * rq[i] * qk[e] + y2 * rk[i] * kk[e]);
                 if (i == jj) sc.diag[i] = uu;
                 col += i > jj ? uu : 0.f;
                 float row = i > jj ? bj * uu : 0.f;
                 bu[e] = row;
-#pragma unroll
-                for (int x = 8; x >= 1; x >>= 1) row += __shfl_xor(row, x);
-                if (r == 0) sc.rowsum[tj][i] = row;
-                w1[u][e] = y1 * bj;
-                w2[u][e] = y2 * bj;
+                row = kda::row_inclusive_scan(row);
+                if (r == 15) sc.rowsum[tj][i] = row;
+                w1[u][e] = y1 * bj * rkj * rq[i];
+                w2[u][e] = y2 * bj * rkj * rk[i];
             }
-            col = kda::sum_lane_groups(col);
+            col = sum_groups(col);
             if (grp == 0) sc.colsum[ti][jj] = col;
             if (ti == tj) {                         // lane column r stands for t: columns j < t of rows i >= t
                 float x = 0.f;
@@ -457,12 +457,14 @@ __global__ __launch_bounds__(K * 4) void local_kernel(BwdParams b)
                     const float before = row_before(bu[e]);
                     x += 4 * grp + e >= r ? before : 0.f;
                 }
-                x = kda::sum_lane_groups(x);
+                x = sum_groups(x);
                 if (grp == 0) sc.cross[jj] = x;
             }
             new_phase();
         }
-        // products with the states: dQ and dK of the S part, T
+        // products with the states: dQ and dK of the S part, T; dq and dk are times rq and rk
+        kda::vm_drain();
+        __syncthreads();
         float sd = 0.f;
 #pragma unroll
         for (int q = 0; q < V * K / 8 / NTH; ++q) {
@@ -494,27 +496,28 @@ __global__ __launch_bounds__(K * 4) void local_kernel(BwdParams b)
         for (int t = 0; t < 4; ++t) {
             const int i = 16 * t + r;
             const bool live = i < nv;
-            const float head = __builtin_amdgcn_exp2f(sc.ghi[i] + sc.glo[i]);
-            const float tail = __builtin_amdgcn_exp2f((whi - sc.ghi[i]) + (wlo - sc.glo[i]));
-            const f32x4 x = xs[t] * (live ? fs * so.inv * p.scale * head : 0.f),
-                        y = ys[t] * (live ? -fs * fdr * head : 0.f), z = zs[t] * (live ? fds * fe * tail : 0.f);
+            const float head = __builtin_amdgcn_exp2f(ghi[i] + glo[i]);
+            const float tail = __builtin_amdgcn_exp2f((whi - ghi[i]) + (wlo - glo[i]));
+            const f32x4 x = xs[t] * (live ? fs * so.inv * p.scale * head * rq[i] : 0.f),
+                        y = ys[t] * (live ? -fs * fdr * head * rk[i] : 0.f),
+                        z = zs[t] * (live ? fds * fe * tail * rk[i] : 0.f);
             const f32x4 qr = row_of(L::Q, t), kr = row_of(L::KM, t);
             qs[t] += dot4(qr, x);
             ks[t] += dot4(kr, y);
             kt[t] += dot4(kr, z);
             dq[t] += x;
-            dk[t] += y + sc.beta[i] * z;
+            dk[t] += y + beta[i] * z;
         }
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-            qs[t] = kda::sum_lane_groups(qs[t]);
-            ks[t] = kda::sum_lane_groups(ks[t]);
-            kt[t] = kda::sum_lane_groups(kt[t]);
+            qs[t] = sum_groups(qs[t]);
+            ks[t] = sum_groups(ks[t]);
+            kt[t] = sum_groups(kt[t]);
             if (grp == 0) {
                 const int i = 16 * t + r;
-                sc.qs[wave][i] = qs[t] * sc.rq[i];
-                sc.ks[wave][i] = ks[t] * sc.rk[i];
-                sc.kt[wave][i] = kt[t] * sc.rk[i];
+                sc.qs[wave][i] = qs[t];
+                sc.ks[wave][i] = ks[t];
+                sc.kt[wave][i] = kt[t];
             }
         }
         // dv: four columns of a token per lane, from dR
@@ -545,22 +548,13 @@ __global__ __launch_bounds__(K * 4) void local_kernel(BwdParams b)
         for (int u = 0; u < NU; ++u) {
             if (wave + NW * u >= 10) continue;
             const int ti = tis[u], tj = tjs[u];
-            const float rkj = sc.rk[16 * tj + r];
-            f32x4 rqi, rki;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                rqi[e] = sc.rq[16 * ti + 4 * grp + e];
-                rki[e] = sc.rk[16 * ti + 4 * grp + e];
-            }
-            put(0, ti, tj, w1[u] * rkj);
-            put(1, ti, tj, w1[u] * rqi);
-            put(2, ti, tj, w2[u] * rki);
-            put(3, ti, tj, w2[u] * rkj);
+            put(0, ti, tj, w1[u]);
+            put(1, ti, tj, w2[u]);
         }
         if (wave >= NW - 2) {                       // the tiles above the diagonal that are read
             const int ti = wave == NW - 2 ? 0 : 2;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) put(k, ti, ti + 1, zero4());
+            for (int k = 0; k < 2; ++k) put(k, ti, ti + 1, zero4());
         }
         __syncthreads();
         // [j][i] matrix k as operand: 16 columns i of tile t over 32 rows j, or 16 rows j over 32 i
@@ -580,11 +574,11 @@ __global__ __launch_bounds__(K * 4) void local_kernel(BwdParams b)
             for (int t = 0; t < 4; ++t) {
                 if (st <= t / 2) {
                     dq[t] = mm(ka, cols(0, t, st), dq[t]);
-                    dk[t] = mm(ka, cols(3, t, st), dk[t]);
+                    dk[t] = mm(ka, cols(1, t, st), dk[t]);
                 }
                 if (st >= t / 2) {
-                    dk[t] = mm(qa, rows(1, t, st), dk[t]);
-                    dk[t] = mm(ka, rows(2, t, st), dk[t]);
+                    dk[t] = mm(qa, rows(0, t, st), dk[t]);
+                    dk[t] = mm(ka, rows(1, t, st), dk[t]);
                 }
             }
             new_phase();
@@ -612,7 +606,7 @@ __global__ __launch_bounds__(K * 4) void local_kernel(BwdParams b)
             if (tau == 1) tiles = t20 + t30;
             if (tau == 2) tiles = t30 + t31;
             const bool live = i < nv;
-            const float bt = sc.beta[i], dbt = col + below + tsum + sc.diag[i];
+            const float bt = beta[i], dbt = col + below + tsum + sc.diag[i];
             const float pairs = sc.cross[i] + row_from(left) + row_before(bt * below) + tiles;
             float x = live ? qsum + ksum : 0.f, y = live ? bt * tsum : 0.f;
 #pragma unroll
@@ -635,18 +629,13 @@ __global__ __launch_bounds__(K * 4) void local_kernel(BwdParams b)
             }
         }
     }
-    // through the L2 norm: dx = r (dy - y (y.dy)), y = r x
-    float fq[4], fk[4], gq[4] = {0.f, 0.f, 0.f, 0.f}, gk[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-        fq[t] = sc.rq[16 * t + r];
-        fk[t] = sc.rk[16 * t + r];
-    }
+    // through the L2 norm: dx = r dy - r^2 x (x . r dy), y = r x
+    float gq[4] = {0.f, 0.f, 0.f, 0.f}, gk[4] = {0.f, 0.f, 0.f, 0.f};
     if (p.pre.qk_l2norm) {
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-            const float a = kda::sum_lane_groups(dot4(row_of(L::Q, t), dq[t]));
-            const float c = kda::sum_lane_groups(dot4(row_of(L::KM, t), dk[t]));
+            const float a = sum_groups(dot4(row_of(L::Q, t), dq[t]));
+            const float c = sum_groups(dot4(row_of(L::KM, t), dk[t]));
             if (grp == 0) {
                 sc.dot[0][wave][16 * t + r] = a;
                 sc.dot[1][wave][16 * t + r] = c;
@@ -660,8 +649,8 @@ __global__ __launch_bounds__(K * 4) void local_kernel(BwdParams b)
                 gq[t] += sc.dot[0][w][16 * t + r];
                 gk[t] += sc.dot[1][w][16 * t + r];
             }
-            gq[t] *= fq[t] * fq[t];
-            gk[t] *= fk[t] * fk[t];
+            gq[t] *= rq[16 * t + r] * rq[16 * t + r];
+            gk[t] *= rk[16 * t + r] * rk[16 * t + r];
         }
     }
 #pragma unroll
@@ -669,8 +658,8 @@ __global__ __launch_bounds__(K * 4) void local_kernel(BwdParams b)
         if (16 * t + r >= nv) continue;
         f32x4 x = dq[t], y = dk[t];
         if (p.pre.qk_l2norm) {
-            x = fq[t] * (x - gq[t] * row_of(L::Q, t));
-            y = fk[t] * (y - gk[t] * row_of(L::KM, t));
+            x -= gq[t] * row_of(L::Q, t);
+            y -= gk[t] * row_of(L::KM, t);
         }
         const int64_t o = ((bos + 16 * t + r) * p.H + h) * K + 16 * wave + 4 * grp;
         *(uint2 *)(b.dq + o) = __builtin_bit_cast(uint2, kda::to_bf16x4(x));

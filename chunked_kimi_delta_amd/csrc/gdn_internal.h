@@ -131,7 +131,7 @@ __host__ __device__ constexpr int frag_index_t(int t, int s) { return t < 2 ? 2 
 template <int K, int V>
 struct Keep {
     static constexpr int S = 0, DS = V * K * 2, E = 2 * DS, DR = E + V * 128, SCALE = DR + V * 128;
-    static constexpr int BYTES = SCALE + 256;
+    static constexpr int BYTES = SCALE + 1024;          // (copied to LDS as one KiB)
 };
 
 // ------------------------------------------------------------------------------- operands
@@ -188,6 +188,15 @@ __device__ __forceinline__ float wave_max(float x) {
     step((uint32_t)__builtin_amdgcn_update_dpp(0, (int)u, 0x142, 0xa, 0xf, false));  // row_bcast:15
     step((uint32_t)__builtin_amdgcn_update_dpp(0, (int)u, 0x143, 0xc, 0xf, false));  // row_bcast:31
     return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)u, 63));
+}
+
+// Sum over the four lanes that share lane % 16 (every one gets it): two exchanges of half a wave and of
+// neighbouring rows of 16 lanes, without LDS.
+__device__ __forceinline__ float sum_groups(float x) {
+    const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+    const auto c = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return __uint_as_float(c[0]) + __uint_as_float(c[1]);
 }
 
 __device__ __forceinline__ float max_abs(f32x4 x, float m) {
