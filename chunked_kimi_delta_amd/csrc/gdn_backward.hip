@@ -94,9 +94,9 @@ __device__ __forceinline__ void reverse_chain(const BwdParams &b, int s, int j, 
         __syncthreads();
         if (BUFS == 2 && c > c0) stage(c - 1, lds + (c1 - c) % BUFS * L::BYTES);
         if constexpr (KEPT) {
-        keep_state(S, mx->scale(mx->state[c & 1]), kept(c) + KP::DS, (float *)(kept(c) + KP::SCALE) + 1, col0 + r, grp);
+        keep_state<KP>(S, mx->scale(mx->state[c & 1]), kept(c) + KP::DS, (float *)(kept(c) + KP::SCALE) + 1, col0 + r, grp);
         if (c < c1 - 1)
-            keep_rows(D, mx->scale(mx->rows[c & 1]), kept(c + 1) + KP::DR, (float *)(kept(c + 1) + KP::SCALE) + 3,
+            keep_rows<KP>(D, mx->scale(mx->rows[c & 1]), kept(c + 1) + KP::DR, (float *)(kept(c + 1) + KP::SCALE) + 3,
                       col0 + r, grp);
         }
         const uint8_t *const rec = buf + L::REC - R::REV;
@@ -172,7 +172,7 @@ __device__ __forceinline__ void reverse_chain(const BwdParams &b, int s, int j, 
         const float y = largest(D);
         if (lane == 0) mx->rows[(c0 - 1) & 1][wave] = y;
         __syncthreads();
-        keep_rows(D, mx->scale(mx->rows[(c0 - 1) & 1]), kept(c0) + KP::DR, (float *)(kept(c0) + KP::SCALE) + 3,
+        keep_rows<KP>(D, mx->scale(mx->rows[(c0 - 1) & 1]), kept(c0) + KP::DR, (float *)(kept(c0) + KP::SCALE) + 3,
                   col0 + r, grp);
     }
     if (end) {
@@ -276,8 +276,12 @@ struct LocalScalars {
 };
 
 // Within 16 lanes: the sum of the lanes before this one, and of this one and those behind it.
-__device__ __forceinline__ float row_before(float x) {
-    return __builtin_amdgcn_update_dpp(0.f, kda::row_inclusive_scan(x), 0x111, 0xf, 0xf, false);
+__device__ __forceinline__ float row_shift(float x) {      // the value of the lane before, or zero
+    return __builtin_amdgcn_update_dpp(0.f, x, 0x111, 0xf, 0xf, false);
+}
+__device__ __forceinline__ float row_before(float x) { return row_shift(kda::row_inclusive_scan(x)); }
+__device__ __forceinline__ float lane_of(float x, int lane) {
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), lane));
 }
 __device__ __forceinline__ float row_from(float x) {
     x += __builtin_amdgcn_update_dpp(0.f, x, 0x101, 0xf, 0xf, false);   // row_shl:1
@@ -323,7 +327,13 @@ __global__ __launch_bounds__(K * 4) void local_kernel(BwdParams b)
     stage_rows<K, NW>(p.q[0] + qk0, (int64_t)p.H * K, nv, lds + L::Q, wave, lane);
     stage_rows<K, NW>(p.k[0] + qk0, (int64_t)p.H * K, nv, lds + L::KM, wave, lane);
 
-    // operand A of this wave's 16 key dims, k = 32 rows from `row0` of a staged matrix
+    using KP = Keep<K, V>;
+    // operand of this wave's 16 key dims, k = 32 columns from `c0` of a kept state
+    auto state_a = [&](int base, int c0) {
+        const int col = c0 + 8 * grp + (r >> 2), dim = 16 * wave + 4 * (r & 3);
+        return join(lds_tr(lds + base + KP::state_at(col, dim)), lds_tr(lds + base + KP::state_at(col + 4, dim)));
+    };
+    // and k = 32 rows from `row0` of q or k
     auto dims_a = [&](int base, int row0) {
         const int row = row0 + 8 * grp + (r >> 2), piece = 2 * wave + ((r & 3) >> 1);
         const int half = 8 * (r & 1);
@@ -331,10 +341,10 @@ __global__ __launch_bounds__(K * 4) void local_kernel(BwdParams b)
                     lds_tr(lds + base + piece_at<K>(row + 4, piece) + half));
     };
     auto half8 = [](bf16x8 x) { return __builtin_bit_cast(kda::f16x8, x); };
-    // operand of 16 tokens from `tok0`, k = 32 columns from `c0` of a [V][64] matrix
+    // operand of 16 tokens from `tok0`, k = 32 columns from `c0` of e or dR
     auto toks_t = [&](int base, int c0, int tok0) {
-        const int row = c0 + 8 * grp + (r >> 2), piece = tok0 / 8 + ((r & 3) >> 1), half = 8 * (r & 1);
-        return join(lds_tr(lds + base + w_at(row, piece) + half), lds_tr(lds + base + w_at(row + 4, piece) + half));
+        const int col = c0 + 8 * grp + (r >> 2), tok = tok0 + 4 * (r & 3);
+        return join(lds_tr(lds + base + KP::row_at(col, tok)), lds_tr(lds + base + KP::row_at(col + 4, tok)));
     };
     auto row_of = [&](int base, int t) {            // four dims of token 16 t + r of q or k
         const int d = 16 * wave + 4 * grp;
@@ -352,23 +362,16 @@ __global__ __launch_bounds__(K * 4) void local_kernel(BwdParams b)
     for (int m = 0; m < p.G; ++m) {
         const int j = h * p.G + m;
         const size_t at = (size_t)j * p.seq.n_slots + slot;
-        const uint8_t *const keep = b.keep + at * Keep<K, V>::BYTES;
+        const uint8_t *const keep = b.keep + at * KP::BYTES;
         if (m > 0) __syncthreads();                 // the previous head is done with the buffers
         stage_block<2, NW>(p.rec + at * R::BYTES + R::GHI, lds + L::SCAL, wave, lane);
-        if (wave == NW - 1) copy16_to_lds(keep + Keep<K, V>::SCALE, lane * 16, lds + L::INV);
         stage_rows<V, NW>(b.d_o + (bos * p.HV + j) * V, (int64_t)p.HV * V, nv, lds + L::DO, wave, lane);
-        // [V][64 tokens] and [V][K] records: V rows of 64 (K) values; the states last, as they are used last
-#pragma unroll
-        for (int q = 0; q < V / 64; ++q) {
-            stage_rows<64, NW>((const uint16_t *)(keep + Keep<K, V>::E) + q * 64 * 64, 64, 64, lds + L::E + q * 8192, wave, lane);
-            stage_rows<64, NW>((const uint16_t *)(keep + Keep<K, V>::DR) + q * 64 * 64, 64, 64, lds + L::DR + q * 8192, wave, lane);
-        }
-#pragma unroll
-        for (int q = 0; q < V / 64; ++q) {
-            stage_rows<K, NW>((const uint16_t *)(keep + Keep<K, V>::S) + q * 64 * K, K, 64, lds + L::S + q * L::MK, wave, lane);
-            stage_rows<K, NW>((const uint16_t *)(keep + Keep<K, V>::DS) + q * 64 * K, K, 64, lds + L::DS + q * L::MK, wave, lane);
-        }
-        constexpr int LATE = V / 64 * 2 * RowStage<K, NW>::STEPS;  // copies of the states
+        // e, dR and the scales; the states last, as they are used last
+        static_assert(L::DR == L::E + L::MV && L::DS == L::S + L::MS, "copied as they are stored");
+        stage_block<2 * L::MV / 1024, NW>(keep + KP::E, lds + L::E, wave, lane);
+        if (wave == NW - 1) copy16_to_lds(keep + KP::SCALE, lane * 16, lds + L::INV);
+        stage_block<2 * L::MS / 1024, NW>(keep + KP::S, lds + L::S, wave, lane);
+        constexpr int LATE = 2 * L::MS / 1024 / NW;     // copies of the states
         asm volatile("s_waitcnt vmcnt(%0)" :: "n"(LATE) : "memory");
         __syncthreads();
         const float *const inv = (const float *)(lds + L::INV);
@@ -468,7 +471,7 @@ __global__ __launch_bounds__(K * 4) void local_kernel(BwdParams b)
         float sd = 0.f;
 #pragma unroll
         for (int q = 0; q < V * K / 8 / NTH; ++q) {
-            const int o = (q * NTH + tid) * 16;     // both are swizzled alike
+            const int o = (q * NTH + tid) * 16;
             const kda::f16x8 x = half8(lds_b128(lds + L::S + o)), y = half8(lds_b128(lds + L::DS + o));
 #pragma unroll
             for (int e = 0; e < 8; ++e) sd += (float)x[e] * (float)y[e];
@@ -483,7 +486,7 @@ __global__ __launch_bounds__(K * 4) void local_kernel(BwdParams b)
         for (int t = 0; t < 4; ++t) xs[t] = ys[t] = zs[t] = zero4();
 #pragma unroll
         for (int st = 0; st < V / 32; ++st) {
-            const kda::f16x8 sa = half8(dims_a(L::S, 32 * st)), da = half8(dims_a(L::DS, 32 * st));
+            const kda::f16x8 sa = half8(state_a(L::S, 32 * st)), da = half8(state_a(L::DS, 32 * st));
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
                 xs[t] = mfma32(sa, half8(lds_b128(lds + L::DO + piece_at<V>(16 * t + r, 4 * st + grp))), xs[t]);
@@ -524,7 +527,7 @@ __global__ __launch_bounds__(K * 4) void local_kernel(BwdParams b)
 #pragma unroll
         for (int q = 0; q < V / 4 / NW; ++q) {      // 4 token tiles x V / 16 column tiles
             const int job = q * NW + wave, t = job & 3, c0 = 16 * (job >> 2);
-            const s16x4 x = lds_tr(lds + L::DR + w_at(c0 + 4 * grp + (r >> 2), 2 * t + ((r & 3) >> 1)) + 8 * (r & 1));
+            const s16x4 x = lds_tr(lds + L::DR + KP::row_at(c0 + 4 * grp + (r >> 2), 16 * t + 4 * (r & 3)));
             const kda::f16x4 y = __builtin_bit_cast(kda::f16x4, x);
             const f32x4 z = f32x4{(float)y[0], (float)y[1], (float)y[2], (float)y[3]} * fdr;
             if (16 * t + r < nv)
@@ -602,22 +605,21 @@ __global__ __launch_bounds__(K * 4) void local_kernel(BwdParams b)
             }
             // whole tiles that cross: (2,0) and (3,0) for tile 1, (3,0) and (3,1) for tile 2
             const float c0 = row_from(sc.rowsum[0][i]), c1 = row_from(sc.rowsum[1][i < 48 ? 48 : i]);
-            const float t20 = kda::lane_read(c0, 32), t30 = kda::lane_read(c0, 48), t31 = kda::lane_read(c1, 48);
+            const float t20 = lane_of(c0, 32), t30 = lane_of(c0, 48), t31 = lane_of(c1, 48);
             if (tau == 1) tiles = t20 + t30;
             if (tau == 2) tiles = t30 + t31;
             const bool live = i < nv;
             const float bt = beta[i], dbt = col + below + tsum + sc.diag[i];
             const float pairs = sc.cross[i] + row_from(left) + row_before(bt * below) + tiles;
-            float x = live ? qsum + ksum : 0.f, y = live ? bt * tsum : 0.f;
+            // the suffix sums of the states' parts and the prefix sums of beta k.T: within 16 lanes, then the
+            // other tiles' sums
+            const float from = row_from(live ? qsum + ksum : 0.f), upto = kda::row_inclusive_scan(live ? bt * tsum : 0.f);
+            float x = pairs + from + row_shift(upto) + __builtin_amdgcn_exp2f(whi + wlo) * sd;
 #pragma unroll
-            for (int d = 1; d < 64; d <<= 1) {
-                const float z = __shfl_down(x, d), u = __shfl_up(y, d);
-                if (lane + d < 64) x += z;
-                if (lane >= d) y += u;
+            for (int w = 0; w < 4; ++w) {
+                if (w > tau) x += lane_of(from, 16 * w);
+                if (w < tau) x += lane_of(upto, 16 * w + 15);
             }
-            const float before = __shfl_up(y, 1);
-            x += pairs + (lane > 0 ? before : 0.f) +
-                 __builtin_amdgcn_exp2f(whi + wlo) * sd;
             if (live) {
                 const int64_t o = (bos + i) * p.HV + j;
                 const float db = p.pre.beta_sigmoid ? dbt * bt * (1.f - bt) : dbt;

@@ -67,30 +67,30 @@ __device__ __forceinline__ float largest(const f32x4 (&x)[N][CTW]) {
     return wave_max(__uint_as_float(m));
 }
 
-// A wave's columns of the state to the workspace, [V][K] fp16 (col: this lane's first column).
-template <int NT, int CTW>
+// A wave's columns of the state, or of a [64 tokens][V] matrix in C-layout, to the workspace (`col`: this
+// lane's first column).
+template <class KP, int NT, int CTW>
 __device__ __forceinline__ void keep_state(const f32x4 (&S)[NT][CTW], Scale f, uint8_t *base, float *inv, int col,
                                            int grp)
 {
-    const auto rs = kda::buffer_rsrc(base, 1u << 20);
+    const auto rs = kda::buffer_rsrc(base, KP::BYTES);
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int ct = 0; ct < CTW; ++ct)
-            kda::bstore8<0>(rs, (col + 16 * ct) * NT * 32 + 16 * grp, 64 * (t / 2) + 8 * (t % 2), half4(S[t][ct], f.f));
+            kda::bstore8<0>(rs, KP::state_at(col + 16 * ct, state_row(t, 0, grp)), 0, half4(S[t][ct], f.f));
     if (threadIdx.x == 0) *inv = f.inv;
 }
 
-// A wave's columns of a [64 tokens][V] matrix in C-layout to the workspace, [V][64] fp16.
-template <int CTW>
+template <class KP, int CTW>
 __device__ __forceinline__ void keep_rows(const f32x4 (&E)[4][CTW], Scale f, uint8_t *base, float *inv, int col, int grp)
 {
-    const auto rs = kda::buffer_rsrc(base, 1u << 20);
+    const auto rs = kda::buffer_rsrc(base, KP::BYTES);
 #pragma unroll
     for (int t = 0; t < 4; ++t)
 #pragma unroll
         for (int ct = 0; ct < CTW; ++ct)
-            kda::bstore8<0>(rs, (col + 16 * ct) * 128 + 8 * grp, 32 * t, half4(E[t][ct], f.f));
+            kda::bstore8<0>(rs, KP::row_at(col + 16 * ct, 16 * t + 4 * grp), 0, half4(E[t][ct], f.f));
     if (threadIdx.x == 0) *inv = f.inv;
 }
 
@@ -197,9 +197,9 @@ __device__ __forceinline__ void forward_chain(const Params &p, int s, int j, int
         if (L::BUFS == 2 && c + 1 < c1) stage(c + 1, lds + ((c + 1 - c0) % L::BUFS) * L::BYTES);
         if constexpr (M == KEEP) {          // S of this chunk, e of the one before
             float *const inv = (float *)(kept(c) + KP::SCALE);
-            keep_state(S, mx->scale(mx->state[c & 1]), kept(c) + KP::S, inv, cbase + col0 + r, grp);
+            keep_state<KP>(S, mx->scale(mx->state[c & 1]), kept(c) + KP::S, inv, cbase + col0 + r, grp);
             if (c > c0)
-                keep_rows(E, mx->scale(mx->rows[c & 1]), kept(c - 1) + KP::E, (float *)(kept(c - 1) + KP::SCALE) + 2,
+                keep_rows<KP>(E, mx->scale(mx->rows[c & 1]), kept(c - 1) + KP::E, (float *)(kept(c - 1) + KP::SCALE) + 2,
                           cbase + col0 + r, grp);
         }
         const uint8_t *const rec = buf + L::REC;
@@ -386,7 +386,7 @@ __device__ __forceinline__ void forward_chain(const Params &p, int s, int j, int
             const float b = largest(E);
             if (lane == 0) mx->rows[c1 & 1][wave] = b;
             __syncthreads();
-            keep_rows(E, mx->scale(mx->rows[c1 & 1]), kept(c1 - 1) + KP::E, (float *)(kept(c1 - 1) + KP::SCALE) + 2,
+            keep_rows<KP>(E, mx->scale(mx->rows[c1 & 1]), kept(c1 - 1) + KP::E, (float *)(kept(c1 - 1) + KP::SCALE) + 2,
                       cbase + col0 + r, grp);
         }
     }
