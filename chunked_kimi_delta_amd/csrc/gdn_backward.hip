@@ -265,14 +265,14 @@ struct Local {
     static constexpr int INV = SCAL + 2048, END = INV + 1024;   // RecB's scalars, Keep's scales
 };
 
-template <int NW>
+template <int ND, int NW>
 struct LocalScalars {
     float rowsum[4][64], colsum[4][64];     // of beta_j U, U below the diagonal, per tile column / row
     float diag[64];                         // of U
     float cross[64];                        // sum_{i >= t > j} beta_j U_ij within t's own tile
-    float qs[NW][64], ks[NW][64], kt[NW][64];   // per wave: q.dQ[S part], k.dK[S part], k.T
+    float qs[ND][64], ks[ND][64], kt[ND][64];   // per 16 key dims: q.dQ[S part], k.dK[S part], k.T
     float sd[NW], most[NW];                 // per wave: <S, dS'>, the largest |dO|
-    float dot[2][NW][64];                   // per wave: q.dq, k.dk (L2 norm)
+    float dot[2][ND][64];                   // per 16 key dims: q.dq, k.dk (L2 norm)
 };
 
 // Within 16 lanes: the sum of the lanes before this one, and of this one and those behind it.
@@ -295,16 +295,18 @@ __device__ __forceinline__ int w_at(int row, int piece) { return piece_at<64>(ro
 
 }  // namespace
 
-// One workgroup per (chunk slot, q/k head), over the head's value heads, one wave per 16 key dims:
-// dQ and dK stay in registers, transposed (a lane: four consecutive dims of one token).
+// One workgroup per (chunk slot, q/k head), over the head's value heads, one wave per 16 key dims and half
+// of the tokens: dQ and dK stay in registers, transposed (a lane: four consecutive dims of one token). A
+// chunk fills the LDS of a compute unit, so the waves of one workgroup are all there is to hide latencies:
+// 16 waves took 78 us for 16 heads x 4096 tokens, eight waves with all tokens each 81 us.
 template <int K, int V>
-__global__ __launch_bounds__(K * 4) void local_kernel(BwdParams b)
+__global__ __launch_bounds__(K * 8) void local_kernel(BwdParams b)
 {
     using L = Local<K, V>;
     using R = RecB;
-    constexpr int NW = K / 16, NTH = 64 * NW;
+    constexpr int ND = K / 16, NW = 2 * ND, NTH = 64 * NW, NL = 8;  // NL: waves that copy to LDS
     __shared__ __attribute__((aligned(1024))) uint8_t lds[L::END];
-    __shared__ __attribute__((aligned(16))) LocalScalars<NW> sc;
+    __shared__ __attribute__((aligned(16))) LocalScalars<ND, NW> sc;
     static_assert(L::END + sizeof(sc) <= 160 * 1024, "LDS of a compute unit");
     const Params &p = b.f;
     const int tid = threadIdx.x, lane = tid & 63;
@@ -316,6 +318,7 @@ __global__ __launch_bounds__(K * 4) void local_kernel(BwdParams b)
         __builtin_amdgcn_sched_barrier(0);
     };
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int dims = wave % ND, half = wave / ND;   // this wave's key dims 16 dims .., token tiles 2 half ..
     const int slot = blockIdx.x, h = blockIdx.y;
     int s, nv;
     int64_t bos;
@@ -324,21 +327,22 @@ __global__ __launch_bounds__(K * 4) void local_kernel(BwdParams b)
     const float *const ghi = scal, *const glo = scal + 64, *const beta = scal + 128, *const rk = scal + 192,
                 *const rq = scal + 256;
     const int64_t qk0 = (bos * p.H + h) * K;
-    stage_rows<K, NW>(p.q[0] + qk0, (int64_t)p.H * K, nv, lds + L::Q, wave, lane);
-    stage_rows<K, NW>(p.k[0] + qk0, (int64_t)p.H * K, nv, lds + L::KM, wave, lane);
+    if (wave < NL) {
+        stage_rows<K, NL>(p.q[0] + qk0, (int64_t)p.H * K, nv, lds + L::Q, wave, lane);
+        stage_rows<K, NL>(p.k[0] + qk0, (int64_t)p.H * K, nv, lds + L::KM, wave, lane);
+    }
 
     using KP = Keep<K, V>;
     // operand of this wave's 16 key dims, k = 32 columns from `c0` of a kept state
     auto state_a = [&](int base, int c0) {
-        const int col = c0 + 8 * grp + (r >> 2), dim = 16 * wave + 4 * (r & 3);
+        const int col = c0 + 8 * grp + (r >> 2), dim = 16 * dims + 4 * (r & 3);
         return join(lds_tr(lds + base + KP::state_at(col, dim)), lds_tr(lds + base + KP::state_at(col + 4, dim)));
     };
     // and k = 32 rows from `row0` of q or k
     auto dims_a = [&](int base, int row0) {
-        const int row = row0 + 8 * grp + (r >> 2), piece = 2 * wave + ((r & 3) >> 1);
-        const int half = 8 * (r & 1);
-        return join(lds_tr(lds + base + piece_at<K>(row, piece) + half),
-                    lds_tr(lds + base + piece_at<K>(row + 4, piece) + half));
+        const int row = row0 + 8 * grp + (r >> 2), piece = 2 * dims + ((r & 3) >> 1);
+        return join(lds_tr(lds + base + piece_at<K>(row, piece) + 8 * (r & 1)),
+                    lds_tr(lds + base + piece_at<K>(row + 4, piece) + 8 * (r & 1)));
     };
     auto half8 = [](bf16x8 x) { return __builtin_bit_cast(kda::f16x8, x); };
     // operand of 16 tokens from `tok0`, k = 32 columns from `c0` of e or dR
@@ -347,16 +351,16 @@ __global__ __launch_bounds__(K * 4) void local_kernel(BwdParams b)
         return join(lds_tr(lds + base + KP::row_at(col, tok)), lds_tr(lds + base + KP::row_at(col + 4, tok)));
     };
     auto row_of = [&](int base, int t) {            // four dims of token 16 t + r of q or k
-        const int d = 16 * wave + 4 * grp;
+        const int d = 16 * dims + 4 * grp;
         f32x4 x;
         kda::unpack_bf16x4(*(const uint2 *)(lds + base + piece_at<K>(16 * t + r, d / 8) + 2 * (d & 4)), (float *)&x);
         return x;
     };
     auto dot4 = [](f32x4 a, f32x4 c) { return a[0] * c[0] + a[1] * c[1] + a[2] * c[2] + a[3] * c[3]; };
 
-    f32x4 dq[4], dk[4];                             // [token tile]
+    f32x4 dq[2], dk[2];                             // [token tile]
 #pragma unroll
-    for (int t = 0; t < 4; ++t) dq[t] = dk[t] = zero4();
+    for (int u = 0; u < 2; ++u) dq[u] = dk[u] = zero4();
 
 #pragma unroll 1
     for (int m = 0; m < p.G; ++m) {
@@ -364,26 +368,29 @@ __global__ __launch_bounds__(K * 4) void local_kernel(BwdParams b)
         const size_t at = (size_t)j * p.seq.n_slots + slot;
         const uint8_t *const keep = b.keep + at * KP::BYTES;
         if (m > 0) __syncthreads();                 // the previous head is done with the buffers
-        stage_block<2, NW>(p.rec + at * R::BYTES + R::GHI, lds + L::SCAL, wave, lane);
-        stage_rows<V, NW>(b.d_o + (bos * p.HV + j) * V, (int64_t)p.HV * V, nv, lds + L::DO, wave, lane);
-        // e, dR and the scales; the states last, as they are used last
         static_assert(L::DR == L::E + L::MV && L::DS == L::S + L::MS, "copied as they are stored");
-        stage_block<2 * L::MV / 1024, NW>(keep + KP::E, lds + L::E, wave, lane);
-        if (wave == NW - 1) copy16_to_lds(keep + KP::SCALE, lane * 16, lds + L::INV);
-        stage_block<2 * L::MS / 1024, NW>(keep + KP::S, lds + L::S, wave, lane);
-        constexpr int LATE = 2 * L::MS / 1024 / NW;     // copies of the states
+        constexpr int LATE = 2 * L::MS / 1024 / NL;     // copies of the states, a wave
+        if (wave < NL) {
+            stage_block<2, NL>(p.rec + at * R::BYTES + R::GHI, lds + L::SCAL, wave, lane);
+            stage_rows<V, NL>(b.d_o + (bos * p.HV + j) * V, (int64_t)p.HV * V, nv, lds + L::DO, wave, lane);
+            // e, dR and the scales; the states last, as they are used last
+            stage_block<2 * L::MV / 1024, NL>(keep + KP::E, lds + L::E, wave, lane);
+            if (wave == NL - 1) copy16_to_lds(keep + KP::SCALE, lane * 16, lds + L::INV);
+            stage_block<2 * L::MS / 1024, NL>(keep + KP::S, lds + L::S, wave, lane);
+        }
         asm volatile("s_waitcnt vmcnt(%0)" :: "n"(LATE) : "memory");
         __syncthreads();
         const float *const inv = (const float *)(lds + L::INV);
         const float fs = inv[0], fds = inv[1], fe = inv[2], fdr = inv[3];
         const float whi = ghi[63], wlo = glo[63];
         // dO as fp16, in place
-        constexpr int NP = 64 * V / 8 / NTH;
+        constexpr int NP = (64 * V / 8 + NTH - 1) / NTH;
         uint4 ob[NP];
         float most = 0.f;
 #pragma unroll
         for (int q = 0; q < NP; ++q) {
-            ob[q] = *(const uint4 *)(lds + L::DO + (q * NTH + tid) * 16);
+            const int at = (q * NTH + tid) * 16;
+            ob[q] = at < L::MV ? *(const uint4 *)(lds + L::DO + at) : make_uint4(0, 0, 0, 0);
             f32x4 x, y;
             kda::unpack_bf16x4(make_uint2(ob[q].x, ob[q].y), (float *)&x);
             kda::unpack_bf16x4(make_uint2(ob[q].z, ob[q].w), (float *)&y);
@@ -395,11 +402,12 @@ __global__ __launch_bounds__(K * 4) void local_kernel(BwdParams b)
         const Scale so = Maxima<NW>::scale(sc.most);
 #pragma unroll
         for (int q = 0; q < NP; ++q) {
+            const int at = (q * NTH + tid) * 16;
             f32x4 x, y;
             kda::unpack_bf16x4(make_uint2(ob[q].x, ob[q].y), (float *)&x);
             kda::unpack_bf16x4(make_uint2(ob[q].z, ob[q].w), (float *)&y);
             const uint2 a = half4(x, so.f), c = half4(y, so.f);
-            *(uint4 *)(lds + L::DO + (q * NTH + tid) * 16) = make_uint4(a.x, a.y, c.x, c.y);
+            if (at < L::MV) *(uint4 *)(lds + L::DO + at) = make_uint4(a.x, a.y, c.x, c.y);
         }
         __syncthreads();
 
@@ -479,49 +487,40 @@ __global__ __launch_bounds__(K * 4) void local_kernel(BwdParams b)
         sd *= fs * fds;
         sd = kda::wave_sum(sd);
         if (lane == 0) sc.sd[wave] = sd;
-        float qs[4] = {0.f, 0.f, 0.f, 0.f}, ks[4] = {0.f, 0.f, 0.f, 0.f}, kt[4] = {0.f, 0.f, 0.f, 0.f};
         new_phase();
-        f32x4 xs[4], ys[4], zs[4];
+        f32x4 xs[2], ys[2], zs[2];
 #pragma unroll
-        for (int t = 0; t < 4; ++t) xs[t] = ys[t] = zs[t] = zero4();
+        for (int u = 0; u < 2; ++u) xs[u] = ys[u] = zs[u] = zero4();
 #pragma unroll
         for (int st = 0; st < V / 32; ++st) {
             const kda::f16x8 sa = half8(state_a(L::S, 32 * st)), da = half8(state_a(L::DS, 32 * st));
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                xs[t] = mfma32(sa, half8(lds_b128(lds + L::DO + piece_at<V>(16 * t + r, 4 * st + grp))), xs[t]);
-                ys[t] = mfma32(sa, half8(toks_t(L::DR, 32 * st, 16 * t)), ys[t]);
-                zs[t] = mfma32(da, half8(toks_t(L::E, 32 * st, 16 * t)), zs[t]);
+            for (int u = 0; u < 2; ++u) {
+                const int t = 2 * half + u;
+                xs[u] = mfma32(sa, half8(lds_b128(lds + L::DO + piece_at<V>(16 * t + r, 4 * st + grp))), xs[u]);
+                ys[u] = mfma32(sa, half8(toks_t(L::DR, 32 * st, 16 * t)), ys[u]);
+                zs[u] = mfma32(da, half8(toks_t(L::E, 32 * st, 16 * t)), zs[u]);
             }
         }
         new_phase();
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            const int i = 16 * t + r;
+        for (int u = 0; u < 2; ++u) {
+            const int t = 2 * half + u, i = 16 * t + r;
             const bool live = i < nv;
             const float head = __builtin_amdgcn_exp2f(ghi[i] + glo[i]);
             const float tail = __builtin_amdgcn_exp2f((whi - ghi[i]) + (wlo - glo[i]));
-            const f32x4 x = xs[t] * (live ? fs * so.inv * p.scale * head * rq[i] : 0.f),
-                        y = ys[t] * (live ? -fs * fdr * head * rk[i] : 0.f),
-                        z = zs[t] * (live ? fds * fe * tail * rk[i] : 0.f);
+            const f32x4 x = xs[u] * (live ? fs * so.inv * p.scale * head * rq[i] : 0.f),
+                        y = ys[u] * (live ? -fs * fdr * head * rk[i] : 0.f),
+                        z = zs[u] * (live ? fds * fe * tail * rk[i] : 0.f);
             const f32x4 qr = row_of(L::Q, t), kr = row_of(L::KM, t);
-            qs[t] += dot4(qr, x);
-            ks[t] += dot4(kr, y);
-            kt[t] += dot4(kr, z);
-            dq[t] += x;
-            dk[t] += y + beta[i] * z;
-        }
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            qs[t] = sum_groups(qs[t]);
-            ks[t] = sum_groups(ks[t]);
-            kt[t] = sum_groups(kt[t]);
+            const float qs = sum_groups(dot4(qr, x)), ks = sum_groups(dot4(kr, y)), kt = sum_groups(dot4(kr, z));
             if (grp == 0) {
-                const int i = 16 * t + r;
-                sc.qs[wave][i] = qs[t];
-                sc.ks[wave][i] = ks[t];
-                sc.kt[wave][i] = kt[t];
+                sc.qs[dims][i] = qs;
+                sc.ks[dims][i] = ks;
+                sc.kt[dims][i] = kt;
             }
+            dq[u] += x;
+            dk[u] += y + beta[i] * z;
         }
         // dv: four columns of a token per lane, from dR
 #pragma unroll
@@ -574,14 +573,15 @@ __global__ __launch_bounds__(K * 4) void local_kernel(BwdParams b)
         for (int st = 0; st < 2; ++st) {
             const Parts<1> qa = {dims_a(L::Q, 32 * st)}, ka = {dims_a(L::KM, 32 * st)};
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                if (st <= t / 2) {
-                    dq[t] = mm(ka, cols(0, t, st), dq[t]);
-                    dk[t] = mm(ka, cols(1, t, st), dk[t]);
+            for (int u = 0; u < 2; ++u) {
+                const int t = 2 * half + u;
+                if (st <= half) {
+                    dq[u] = mm(ka, cols(0, t, st), dq[u]);
+                    dk[u] = mm(ka, cols(1, t, st), dk[u]);
                 }
-                if (st >= t / 2) {
-                    dk[t] = mm(qa, rows(0, t, st), dk[t]);
-                    dk[t] = mm(ka, rows(1, t, st), dk[t]);
+                if (st >= half) {
+                    dk[u] = mm(qa, rows(0, t, st), dk[u]);
+                    dk[u] = mm(ka, rows(1, t, st), dk[u]);
                 }
             }
             new_phase();
@@ -597,12 +597,13 @@ __global__ __launch_bounds__(K * 4) void local_kernel(BwdParams b)
             }
             float sd = 0.f;
 #pragma unroll
-            for (int w = 0; w < NW; ++w) {
+            for (int w = 0; w < ND; ++w) {
                 qsum += sc.qs[w][i];
                 ksum += sc.ks[w][i];
                 tsum += sc.kt[w][i];
-                sd += sc.sd[w];
             }
+#pragma unroll
+            for (int w = 0; w < NW; ++w) sd += sc.sd[w];
             // whole tiles that cross: (2,0) and (3,0) for tile 1, (3,0) and (3,1) for tile 2
             const float c0 = row_from(sc.rowsum[0][i]), c1 = row_from(sc.rowsum[1][i < 48 ? 48 : i]);
             const float t20 = lane_of(c0, 32), t30 = lane_of(c0, 48), t31 = lane_of(c1, 48);
@@ -632,38 +633,40 @@ __global__ __launch_bounds__(K * 4) void local_kernel(BwdParams b)
         }
     }
     // through the L2 norm: dx = r dy - r^2 x (x . r dy), y = r x
-    float gq[4] = {0.f, 0.f, 0.f, 0.f}, gk[4] = {0.f, 0.f, 0.f, 0.f};
+    float gq[2] = {0.f, 0.f}, gk[2] = {0.f, 0.f};
     if (p.pre.qk_l2norm) {
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            const float a = sum_groups(dot4(row_of(L::Q, t), dq[t]));
-            const float c = sum_groups(dot4(row_of(L::KM, t), dk[t]));
+        for (int u = 0; u < 2; ++u) {
+            const int t = 2 * half + u;
+            const float a = sum_groups(dot4(row_of(L::Q, t), dq[u])), c = sum_groups(dot4(row_of(L::KM, t), dk[u]));
             if (grp == 0) {
-                sc.dot[0][wave][16 * t + r] = a;
-                sc.dot[1][wave][16 * t + r] = c;
+                sc.dot[0][dims][16 * t + r] = a;
+                sc.dot[1][dims][16 * t + r] = c;
             }
         }
         __syncthreads();
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
+        for (int u = 0; u < 2; ++u) {
+            const int i = 16 * (2 * half + u) + r;
 #pragma unroll
-            for (int w = 0; w < NW; ++w) {
-                gq[t] += sc.dot[0][w][16 * t + r];
-                gk[t] += sc.dot[1][w][16 * t + r];
+            for (int w = 0; w < ND; ++w) {
+                gq[u] += sc.dot[0][w][i];
+                gk[u] += sc.dot[1][w][i];
             }
-            gq[t] *= rq[16 * t + r] * rq[16 * t + r];
-            gk[t] *= rk[16 * t + r] * rk[16 * t + r];
+            gq[u] *= rq[i] * rq[i];
+            gk[u] *= rk[i] * rk[i];
         }
     }
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
+    for (int u = 0; u < 2; ++u) {
+        const int t = 2 * half + u;
         if (16 * t + r >= nv) continue;
-        f32x4 x = dq[t], y = dk[t];
+        f32x4 x = dq[u], y = dk[u];
         if (p.pre.qk_l2norm) {
-            x -= gq[t] * row_of(L::Q, t);
-            y -= gk[t] * row_of(L::KM, t);
+            x -= gq[u] * row_of(L::Q, t);
+            y -= gk[u] * row_of(L::KM, t);
         }
-        const int64_t o = ((bos + 16 * t + r) * p.H + h) * K + 16 * wave + 4 * grp;
+        const int64_t o = ((bos + 16 * t + r) * p.H + h) * K + 16 * dims + 4 * grp;
         *(uint2 *)(b.dq + o) = __builtin_bit_cast(uint2, kda::to_bf16x4(x));
         *(uint2 *)(b.dk + o) = __builtin_bit_cast(uint2, kda::to_bf16x4(y));
     }
@@ -683,7 +686,7 @@ hipError_t launch_backward(const BwdParams &b, hipStream_t st)
     }
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.seq.T_total == 0) return e;
-    local_kernel<K, V><<<dim3(p.seq.n_slots, p.H), dim3(4 * K), 0, st>>>(b);
+    local_kernel<K, V><<<dim3(p.seq.n_slots, p.H), dim3(8 * K), 0, st>>>(b);
     return hipGetLastError();
 }
 
