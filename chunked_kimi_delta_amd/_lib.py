@@ -92,6 +92,10 @@ def load():
     lib.gdn_bwd_workspace_bytes.restype = ctypes.c_size_t
     lib.gdn_bwd.argtypes = [gdn, ptr, ptr, ptr, ctypes.c_size_t] + [ptr] * 9
     lib.gdn_bwd.restype = ctypes.c_int
+    lib.gdn_bwd_packed_workspace_bytes.argtypes = [gdn]
+    lib.gdn_bwd_packed_workspace_bytes.restype = ctypes.c_size_t
+    lib.gdn_bwd_packed.argtypes = [gdn] + [ptr] * 6 + [ctypes.c_size_t] + [ptr] * 9
+    lib.gdn_bwd_packed.restype = ctypes.c_int
     lib.gdn_step.argtypes = [gdn, ptr, ptr, ctypes.c_int32, ptr]
     lib.gdn_step.restype = ctypes.c_int
     lib.act8_pack.argtypes = [ptr, ctypes.c_int32, ctypes.c_int64, ctypes.c_int32, ptr, ptr, ptr]

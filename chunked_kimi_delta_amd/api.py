@@ -21,7 +21,7 @@ def _ptr(t: Optional[torch.Tensor]):
 def _check(t: torch.Tensor, name: str, dtype, shape, device):
     if t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != tuple(shape):
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.device != device:
         raise ValueError(f"{name}: expected device {device}, got {t.device}")
@@ -31,15 +31,22 @@ def _check(t: torch.Tensor, name: str, dtype, shape, device):
 
 def _call(fn, name, dev, stream, *args):
     """Enqueue on `stream` (default: torch's current stream of `dev`), with `dev` current."""
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    if torch.cuda.current_device() == dev.index:
-        st = fn(*args, stream.cuda_stream)
+    raw = torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream.cuda_stream
+    if torch._C._cuda_getDevice() == dev.index:
+        st = fn(*args, raw)
     else:
         with torch.cuda.device(dev):
-            st = fn(*args, stream.cuda_stream)
+            st = fn(*args, raw)
     if st != 0:
         raise RuntimeError(f"{name} failed: {strerror(st)} ({st})")
+
+
+def _on(dev, fn, *args):
+    """fn(*args) with `dev` current (workspace sizes depend on the device)."""
+    if torch._C._cuda_getDevice() == dev.index:
+        return fn(*args)
+    with torch.cuda.device(dev):
+        return fn(*args)
 
 
 class KdaFwdPlan:

@@ -54,6 +54,17 @@ float scale_of(const gdn_args *a)
     return a->scale > 0.f && !isnan(a->scale) ? a->scale : 1.0f / sqrtf((float)a->K);
 }
 
+// What the chunked kernels take: a launch has less than 2^32 threads along a dimension (up to 1024 a chunk,
+// four workgroups of 512 a unit, fp32 io: 64 a row of the decay's gradient).
+kda_status check_chunks(const gdn_args *a)
+{
+    const kda_status st = check_shapes(a);
+    if (st != KDA_OK) return st;
+    const int64_t tt = (int64_t)a->B * a->T;
+    if (tt / CT + a->N >= 1 << 22 || (int64_t)a->N * a->HV >= (1 << 21) - 8) return KDA_ERR_UNSUPPORTED;
+    return a->io == KDA_FP32 && tt * a->HV >= 1 << 26 ? KDA_ERR_UNSUPPORTED : KDA_OK;
+}
+
 // A dense batch of short sequences takes the recurrence: a chunk has a fixed cost of 64 tokens.
 bool recurrent(const gdn_args *a) { return !a->cu_seqlens && a->T <= 16; }
 
@@ -261,13 +272,32 @@ BwdLayout bwd_layout(const gdn_args *a)
     return L;
 }
 
+// gdn_bwd's arguments but q, k, v and the workspace.
+kda_status check_bwd(const gdn_args *a, const void *d_o, const float *dht, const void *dq, const void *dk,
+                     const void *dv, const void *dg, const void *dbeta, const float *dh0,
+                     const float *dA_log, const float *ddt_bias)
+{
+    kda_status st = check_chunks(a);
+    if (st != KDA_OK || (st = check_pre(a)) != KDA_OK) return st;
+    if (a->gate != KDA_GATE_NONE && (!dA_log || !aligned(dA_log, 4) || !aligned(ddt_bias, 4)))
+        return KDA_ERR_INVALID_ARG;
+    const void *ptrs[] = {a->g, a->beta, d_o, dq, dk, dv, dg, dbeta};
+    if ((int64_t)a->B * a->T > 0)
+        for (const void *p : ptrs)
+            if (!p || !aligned(p, 16)) return KDA_ERR_INVALID_ARG;
+    const void *opt[] = {a->initial_state, a->cu_seqlens, dht, dh0};
+    for (const void *p : opt)
+        if (!aligned(p, 16)) return KDA_ERR_INVALID_ARG;
+    return KDA_OK;
+}
+
 }  // namespace
 
 extern "C" {
 
 size_t gdn_bwd_workspace_bytes(const gdn_args *a)
 {
-    if (check_shapes(a) != KDA_OK) return 0;
+    if (check_chunks(a) != KDA_OK) return 0;
     const BwdLayout L = bwd_layout(a);
     return a->io == KDA_FP32 && L.kda_bytes == 0 ? 0 : L.total;
 }
@@ -276,21 +306,14 @@ kda_status gdn_bwd(const gdn_args *a, const void *d_o, const float *dht, void *w
                    size_t ws_bytes, void *dq, void *dk, void *dv, void *dg, void *dbeta,
                    float *dh0, float *dA_log, float *ddt_bias, void *stream)
 {
-    kda_status st = check_shapes(a);
+    kda_status st = check_bwd(a, d_o, dht, dq, dk, dv, dg, dbeta, dh0, dA_log, ddt_bias);
     if (st != KDA_OK) return st;
-    if ((st = check_pre(a)) != KDA_OK) return st;
     const bool gated = a->gate != KDA_GATE_NONE, f32 = a->io == KDA_FP32;
-    if (gated && (!dA_log || !aligned(dA_log, 4) || !aligned(ddt_bias, 4)))
-        return KDA_ERR_INVALID_ARG;
     const BwdLayout L = bwd_layout(a);
-    if (L.f.tt > 0) {
-        const void *ptrs[] = {a->q, a->k, a->v, a->g, a->beta, d_o, dq, dk, dv, dg, dbeta};
-        for (const void *p : ptrs)
+    const void *qkv[] = {a->q, a->k, a->v};
+    if (L.f.tt > 0)
+        for (const void *p : qkv)
             if (!p || !aligned(p, 16)) return KDA_ERR_INVALID_ARG;
-    }
-    const void *opt[] = {a->initial_state, a->cu_seqlens, dht, dh0};
-    for (const void *p : opt)
-        if (!aligned(p, 16)) return KDA_ERR_INVALID_ARG;
     if (f32 && L.kda_bytes == 0) return KDA_ERR_UNSUPPORTED;
     if (L.f.tt > 0 && (!workspace || ws_bytes < L.total || !aligned(workspace, 256)))
         return KDA_ERR_WORKSPACE;
@@ -339,9 +362,49 @@ kda_status gdn_bwd(const gdn_args *a, const void *d_o, const float *dht, void *w
     return e == hipSuccess ? KDA_OK : KDA_ERR_HIP;
 }
 
+size_t gdn_bwd_packed_workspace_bytes(const gdn_args *a)
+{
+    const size_t need = gdn_bwd_workspace_bytes(a);
+    if (need == 0) return 0;
+    const size_t e = a->io == KDA_FP32 ? 4 : 2, tt = (size_t)a->B * a->T;
+    return align256(need) + 2 * align256(tt * a->H * a->K * e) + align256(tt * a->HV * a->V * e);
+}
+
+kda_status gdn_bwd_packed(const gdn_args *a, const float *q_scale, const float *k_scale,
+                          const float *v_scale, const void *d_o, const float *dht, void *workspace,
+                          size_t ws_bytes, void *dq, void *dk, void *dv, void *dg, void *dbeta,
+                          float *dh0, float *dA_log, float *ddt_bias, void *stream)
+{
+    const kda_status st = check_bwd(a, d_o, dht, dq, dk, dv, dg, dbeta, dh0, dA_log, ddt_bias);
+    if (st != KDA_OK) return st;
+    const size_t need = align256(gdn_bwd_workspace_bytes(a)), total = gdn_bwd_packed_workspace_bytes(a);
+    const int64_t tt = (int64_t)a->B * a->T;
+    gdn_args b = *a;
+    if (tt > 0) {
+        const float *const scale[3] = {q_scale, k_scale, v_scale};
+        const int8_t *const data[3] = {(const int8_t *)a->q, (const int8_t *)a->k, (const int8_t *)a->v};
+        for (int i = 0; i < 3; ++i)
+            if (!data[i] || !scale[i] || !aligned(data[i], 16) || !aligned(scale[i], 4)) return KDA_ERR_INVALID_ARG;
+        // four values a lane, less than 2^32 lanes
+        if (total == 0 || tt * (2 * a->H * a->K + a->HV * a->V) >= (int64_t)1 << 33) return KDA_ERR_UNSUPPORTED;
+        if (!workspace || ws_bytes < total || !aligned(workspace, 256)) return KDA_ERR_WORKSPACE;
+        const size_t e = a->io == KDA_FP32 ? 4 : 2, qk = align256((size_t)tt * a->H * a->K * e);
+        uint8_t *const at = (uint8_t *)workspace + need;
+        void *const x[3] = {at, at + qk, at + 2 * qk};
+        b.q = x[0];
+        b.k = x[1];
+        b.v = x[2];
+        const int64_t rows[3] = {tt * a->H, tt * a->H, tt * a->HV};
+        const int32_t D[3] = {a->K, a->K, a->V};
+        if (launch_unpack3(data, scale, rows, D, x, a->io == KDA_FP32, (hipStream_t)stream) != hipSuccess)
+            return KDA_ERR_HIP;
+    }
+    return gdn_bwd(&b, d_o, dht, workspace, need, dq, dk, dv, dg, dbeta, dh0, dA_log, ddt_bias, stream);
+}
+
 size_t gdn_fwd_workspace_bytes(const gdn_args *a)
 {
-    if (check_shapes(a) != KDA_OK || recurrent(a)) return 0;
+    if (check_chunks(a) != KDA_OK || recurrent(a)) return 0;
     return layout(a).total;
 }
 
@@ -355,6 +418,7 @@ kda_status gdn_fwd(const gdn_args *a, void *workspace, size_t ws_bytes, void *st
         if (a->N == 0) return KDA_OK;
         return run_recurrent(a, a->initial_state, a->final_state, nullptr, 0, hs);
     }
+    if ((st = check_chunks(a)) != KDA_OK) return st;
     const Layout L = layout(a);
     if (L.tt > 0 && (!workspace || ws_bytes < L.total || !aligned(workspace, 256)))
         return KDA_ERR_WORKSPACE;

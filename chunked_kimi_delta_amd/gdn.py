@@ -7,14 +7,15 @@ import ctypes
 import torch
 
 from ._lib import GdnArgs, load
-from .act8 import Packed8, unpack8
-from .api import _GATES, _IO, _call, _check, _ptr
+from .act8 import Packed8, _check_packed, unpack8
+from .api import _GATES, _IO, _call, _check, _on, _ptr
 
 
 def _arguments(q, k, v, g, beta, scale, cu_seqlens, initial_state, use_qk_l2norm,
-               use_beta_sigmoid, gate, A_log, dt_bias, gate_lower_bound):
-    """Checked gdn_args of the inputs; o and the final state are the caller's to set."""
-    dt, dev = q.dtype, q.device
+               use_beta_sigmoid, gate, A_log, dt_bias, gate_lower_bound, io=None):
+    """Checked gdn_args of the inputs; o and the final state are the caller's to set. io: the io dtype
+    where q, k and v are the int8 rows of checkpoints."""
+    dt, dev = io or q.dtype, q.device
     if dt not in _IO:
         raise TypeError(f"unsupported io dtype {dt} (bf16 or fp32)")
     if dev.type != "cuda":
@@ -23,43 +24,37 @@ def _arguments(q, k, v, g, beta, scale, cu_seqlens, initial_state, use_qk_l2norm
         raise ValueError("q must be [B, T, H, K] and v [B, T, HV, V]")
     B, T, H, K = q.shape
     HV, V = v.shape[2], v.shape[3]
-    _check(q, "q", dt, (B, T, H, K), dev)
-    _check(k, "k", dt, (B, T, H, K), dev)
-    _check(v, "v", dt, (B, T, HV, V), dev)
+    rows = q.dtype
+    _check(q, "q", rows, (B, T, H, K), dev)
+    _check(k, "k", rows, (B, T, H, K), dev)
+    _check(v, "v", rows, (B, T, HV, V), dev)
     _check(g, "g", dt, (B, T, HV), dev)
     _check(beta, "beta", dt, (B, T, HV), dev)
-    N = B
+    N, cu, h0 = B, None, None
     if cu_seqlens is not None:
         if cu_seqlens.dtype != torch.int64 or cu_seqlens.device != dev or cu_seqlens.dim() != 1:
             raise ValueError("cu_seqlens must be a 1-D int64 tensor on the inputs' device")
         if not cu_seqlens.is_contiguous():
             raise ValueError("cu_seqlens must be contiguous")
-        N = cu_seqlens.numel() - 1
+        N, cu = cu_seqlens.numel() - 1, cu_seqlens.data_ptr()
     if initial_state is not None:
         _check(initial_state, "initial_state", torch.float32, (N, HV, K, V), dev)
+        h0 = initial_state.data_ptr()
     if gate not in _GATES:
         raise ValueError(f"gate must be None, 'softplus' or 'bounded' (got {gate!r})")
-    a = GdnArgs()
-    a.B, a.T, a.N, a.H, a.HV, a.K, a.V, a.io = B, T, N, H, HV, K, V, _IO[dt]
-    a.q, a.k, a.v, a.g, a.beta = (q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
-                                  beta.data_ptr())
-    a.scale = float("nan") if scale is None else float(scale)
-    if cu_seqlens is not None:
-        a.cu_seqlens = cu_seqlens.data_ptr()
-    if initial_state is not None:
-        a.initial_state = initial_state.data_ptr()
-    a.qk_l2norm = int(bool(use_qk_l2norm))
-    a.beta_sigmoid = int(bool(use_beta_sigmoid))
+    A = bias = None
     if gate is not None:
         if A_log is None:
             raise ValueError("a gate needs A_log")
         _check(A_log, "A_log", torch.float32, (HV,), dev)
+        A = A_log.data_ptr()
         if dt_bias is not None:
             _check(dt_bias, "dt_bias", torch.float32, (HV,), dev)
-        a.gate = _GATES[gate]
-        a.gate_lower_bound = float(gate_lower_bound)
-        a.A_log, a.dt_bias = _ptr(A_log), _ptr(dt_bias)
-    return a
+            bias = dt_bias.data_ptr()
+    return GdnArgs(B, T, N, H, HV, K, V, _IO[dt], q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                   g.data_ptr(), beta.data_ptr(), float("nan") if scale is None else float(scale),
+                   cu, h0, None, None, int(bool(use_qk_l2norm)), int(bool(use_beta_sigmoid)),
+                   _GATES[gate], float(gate_lower_bound), A, bias)
 
 
 class GdnFwdPlan:
@@ -94,8 +89,7 @@ class GdnFwdPlan:
         self.args = a
         self._keep = (q, k, v, g, beta, cu_seqlens, initial_state, A_log, dt_bias)
         # 0: refused (the call says why), or the recurrence, which needs none
-        with torch.cuda.device(dev):
-            need = int(self.lib.gdn_fwd_workspace_bytes(ctypes.byref(a)))
+        need = _on(dev, self.lib.gdn_fwd_workspace_bytes, ctypes.byref(a))
         if workspace is None:
             workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
         else:
@@ -125,7 +119,8 @@ class GdnBwdPlan:
     g, beta, initial_state and (with a gate) A_log, dt_bias, from d_o (like v) and dht (fp32
     [N,HV,K,V] or None).
 
-    Inputs and pre-stage keywords as for GdnFwdPlan. Outputs, allocated once and reused by every
+    Inputs and pre-stage keywords as for GdnFwdPlan; q, k and v may be Packed8 checkpoints (of one dtype, the
+    io dtype), which the call unpacks. Outputs, allocated once and reused by every
     call(): dq, dk, dv, dg, dbeta in the io dtype, dh0 fp32 [N,HV,K,V] (when want_dh0), dA_log and
     ddt_bias fp32 [HV] (with a gate).
     """
@@ -135,22 +130,37 @@ class GdnBwdPlan:
                  use_beta_sigmoid=False, gate=None, A_log=None, dt_bias=None,
                  gate_lower_bound=-5.0):
         self.lib = load()
+        packed = [isinstance(x, Packed8) for x in (q, k, v)]
+        io, scales = None, ()
+        if all(packed):
+            io = q.dtype
+            if k.dtype != io or v.dtype != io:
+                raise TypeError("checkpoints of q, k and v must stand for one dtype")
+            for x, name in ((q, "q"), (k, "k"), (v, "v")):
+                _check_packed(x, name, q.data.device)
+            scales = tuple(x.scale.data_ptr() for x in (q, k, v))
+            self._packed = (q, k, v)
+            q, k, v = q.data, k.data, v.data
+        elif any(packed):
+            q, k, v = (unpack8(x) if p else x for x, p in zip((q, k, v), packed))
         a = _arguments(q, k, v, g, beta, scale, cu_seqlens, initial_state, use_qk_l2norm,
-                       use_beta_sigmoid, gate, A_log, dt_bias, gate_lower_bound)
+                       use_beta_sigmoid, gate, A_log, dt_bias, gate_lower_bound, io)
         dev = self.device = q.device
-        _check(d_o, "d_o", v.dtype, v.shape, dev)
+        io = io or q.dtype
+        self._fn, name = ((self.lib.gdn_bwd_packed, self.lib.gdn_bwd_packed_workspace_bytes) if scales else
+                          (self.lib.gdn_bwd, self.lib.gdn_bwd_workspace_bytes))
+        _check(d_o, "d_o", io, v.shape, dev)
         shape = (a.N, a.HV, a.K, a.V)
         if dht is not None:
             _check(dht, "dht", torch.float32, shape, dev)
         f32 = dict(dtype=torch.float32, device=dev)
-        self.dq, self.dk, self.dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+        self.dq, self.dk, self.dv = (torch.empty_like(x, dtype=io) for x in (q, k, v))
         self.dg, self.dbeta = torch.empty_like(g), torch.empty_like(beta)
         self.dh0 = torch.empty(shape, **f32) if want_dh0 else None
         self.dA_log = torch.empty(a.HV, **f32) if gate is not None else None
         self.ddt_bias = torch.empty(a.HV, **f32) if gate is not None else None
         self.args = a
-        with torch.cuda.device(dev):
-            need = int(self.lib.gdn_bwd_workspace_bytes(ctypes.byref(a)))
+        need = _on(dev, name, ctypes.byref(a))
         if need == 0 and a.B * a.T > 0:
             raise ValueError("unsupported shapes (K, V in {64, 128}; HV % H == 0)")
         if workspace is None:
@@ -162,14 +172,14 @@ class GdnBwdPlan:
         self.workspace = workspace
         outs = (self.dq, self.dk, self.dv, self.dg, self.dbeta, self.dh0, self.dA_log, self.ddt_bias)
         self._outs = outs
-        self._ptrs = (ctypes.byref(a), _ptr(d_o), _ptr(dht), workspace.data_ptr(),
+        self._ptrs = (ctypes.byref(a), *scales, _ptr(d_o), _ptr(dht), workspace.data_ptr(),
                       workspace.numel(), *map(_ptr, outs))
         self._keep = (q, k, v, g, beta, d_o, dht, cu_seqlens, initial_state, A_log, dt_bias)
 
     def __call__(self, stream=None):
         """Enqueue the backward on `stream` (default: torch's current stream); returns
         (dq, dk, dv, dg, dbeta, dh0, dA_log, ddt_bias)."""
-        _call(self.lib.gdn_bwd, "gdn_bwd", self.device, stream, *self._ptrs)
+        _call(self._fn, "gdn_bwd", self.device, stream, *self._ptrs)
         return self._outs
 
 
@@ -178,7 +188,6 @@ def gdn_bwd(q, k, v, g, beta, d_o, dht=None, scale=None, cu_seqlens=None, initia
     """Gated delta rule backward. Returns (dq, dk, dv, dg, dbeta in the io dtype, dh0 fp32 or None,
     dA_log or None, ddt_bias or None); see GdnBwdPlan. q, k and v may each be a Packed8
     checkpoint: the gradients are then those at the values that it stands for."""
-    q, k, v = (unpack8(x) if isinstance(x, Packed8) else x for x in (q, k, v))
     return GdnBwdPlan(q, k, v, g, beta, d_o, dht, scale, cu_seqlens, initial_state, want_dh0,
                       **prestage)()
 

@@ -17,8 +17,8 @@
 extern "C" {
 #endif
 
-/* x [rows, D] (io dtype) -> data [rows, D] int8, scale [rows] fp32. D: a multiple of 8, 8 .. 512.
-   x and data 16- and 8-byte aligned, scale 4-byte aligned. */
+/* x [rows, D] (io dtype) -> data [rows, D] int8, scale [rows] fp32. D: a multiple of 8, 8 .. 512;
+   rows * D below 2^33. x and data 16- and 8-byte aligned, scale 4-byte aligned. */
 kda_status act8_pack(const void *x, int32_t io, int64_t rows, int32_t D, int8_t *data,
                      float *scale, void *stream);
 

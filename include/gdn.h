@@ -91,6 +91,16 @@ kda_status gdn_bwd(const gdn_args *args, const void *d_o, const float *dht, void
                    size_t ws_bytes, void *dq, void *dk, void *dv, void *dg, void *dbeta,
                    float *dh0, float *dA_log, float *ddt_bias, void *stream);
 
+/* gdn_bwd with q, k and v kept as 8-bit checkpoints (act8.h): args->q, k, v are their int8 rows, q_scale,
+   k_scale [B, T, H] and v_scale [B, T, HV] fp32 (4-byte aligned) the rows' scales. They are unpacked to
+   the io type into the workspace; the gradients are those at these values. */
+size_t gdn_bwd_packed_workspace_bytes(const gdn_args *args);
+
+kda_status gdn_bwd_packed(const gdn_args *args, const float *q_scale, const float *k_scale,
+                          const float *v_scale, const void *d_o, const float *dht, void *workspace,
+                          size_t ws_bytes, void *dq, void *dk, void *dv, void *dg, void *dbeta,
+                          float *dh0, float *dA_log, float *ddt_bias, void *stream);
+
 /* One serving step: B rows of T new tokens each, row b on the state in slot state_indices[b]
    of `state` [slots, HV, K, V] fp32, updated in place. state_indices: device int32 [B], or
    NULL for slot b (slots >= B then). A row whose index is negative or >= slots is padding: its

@@ -133,6 +133,33 @@ def test_backward_refuses_bad_arguments(lib, kw, status):
             assert call(a, ws=None) == call(a, n=need - 1) == call(a, ws=FAKE + 16) == _lib.KDA_ERR_WORKSPACE
 
 
+@pytest.mark.parametrize("kw,status", BAD)
+def test_backward_from_checkpoints_refuses_bad_arguments(lib, kw, status):
+    if "o" in kw:
+        return
+    call = lambda a, scale=FAKE, d_o=FAKE, ws=FAKE, n=1 << 50: lib.gdn_bwd_packed(
+        ctypes.byref(a), FAKE, scale, FAKE, d_o, FAKE, ws, n, *(FAKE,) * 5, FAKE, FAKE, None, None)
+    assert call(args(**kw)) == status
+    if kw == dict(K=96):
+        bad = _lib.KDA_ERR_INVALID_ARG
+        assert call(args(), scale=None) == call(args(), scale=FAKE + 2) == call(args(), d_o=None) == bad
+        for io in (0, 1):
+            a = args(io=io)
+            need, plain = (f(ctypes.byref(a)) for f in (lib.gdn_bwd_packed_workspace_bytes, lib.gdn_bwd_workspace_bytes))
+            assert need >= plain + 100 * (2 * 2 * 128 + 4 * 64) * (4 if io else 2)
+            assert call(a, ws=None) == call(a, n=need - 1) == call(a, ws=FAKE + 16) == _lib.KDA_ERR_WORKSPACE
+
+
+@pytest.mark.parametrize("kw", [
+    dict(T=1 << 28), dict(N=1 << 22, cu_seqlens=FAKE), dict(N=1 << 16, H=32, HV=32, cu_seqlens=FAKE),
+    dict(io=1, T=1 << 21, H=32, HV=32), dict(B=1 << 21, N=1 << 21, T=17, H=1, HV=1)])
+def test_launches_that_do_not_fit_are_refused(lib, kw):
+    a = args(**kw)
+    bwd = lib.gdn_bwd(ctypes.byref(a), FAKE, FAKE, FAKE, 1 << 62, *(FAKE,) * 6, None, None, None)
+    assert lib.gdn_fwd(ctypes.byref(a), FAKE, 1 << 62, None) == bwd == _lib.KDA_ERR_UNSUPPORTED
+    assert lib.gdn_fwd_workspace_bytes(ctypes.byref(a)) == lib.gdn_bwd_workspace_bytes(ctypes.byref(a)) == 0
+
+
 def test_workspace(lib):
     need = lambda **kw: lib.gdn_fwd_workspace_bytes(ctypes.byref(args(**kw)))
     assert need() > 0 and need(T=16) == 0 and need(K=96) == 0
@@ -157,6 +184,7 @@ def test_step_refuses_bad_pools(lib):
     (dict(rows=-1), _lib.KDA_ERR_INVALID_ARG), (dict(D=12), _lib.KDA_ERR_INVALID_ARG),
     (dict(D=0), _lib.KDA_ERR_INVALID_ARG), (dict(D=520), _lib.KDA_ERR_UNSUPPORTED),
     (dict(io=7), _lib.KDA_ERR_UNSUPPORTED), (dict(rows=1 << 36), _lib.KDA_ERR_UNSUPPORTED),
+    (dict(rows=1 << 30, D=8), _lib.KDA_ERR_UNSUPPORTED),
     (dict(x=None), _lib.KDA_ERR_INVALID_ARG), (dict(x=FAKE + 8), _lib.KDA_ERR_INVALID_ARG),
     (dict(data=FAKE + 4), _lib.KDA_ERR_INVALID_ARG), (dict(scale=None), _lib.KDA_ERR_INVALID_ARG),
 ])
@@ -190,3 +218,8 @@ def test_binding_refuses_before_any_call():
         kda.unpack8(p._replace(scale=torch.zeros(3)))
     with pytest.raises(TypeError, match="int8"):
         kda.unpack8(p._replace(data=torch.zeros(4, 64)))
+    p = {n: kda.Packed8(a[n].to(torch.int8), a[n][..., 0].float(), torch.bfloat16) for n in ("q", "k", "v")}
+    with pytest.raises(ValueError, match="HIP device"):
+        kda.gdn_bwd(**(a | p), d_o=a["v"])
+    with pytest.raises(TypeError, match="one dtype"):
+        kda.gdn_bwd(**(a | p | {"k": p["k"]._replace(dtype=torch.float32)}), d_o=a["v"])

@@ -264,6 +264,42 @@ def test_packed_inputs_are_their_values():
         assert torch.equal(x, y)
 
 
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_some_or_all_inputs_packed(dtype):
+    a = to(make(B=2, T=77, H=2, G=2, K=64, V=128, dtype=dtype, raw=True, gate="softplus", h0=True), DEV)
+    d_o, dh = (x.to(DEV) for x in cotangents(a))
+    p = {n: kda.pack8(a[n]) for n in ("q", "k", "v")}
+    for names in ("qkv", "qk", "v"):
+        b = {n: p[n] for n in names}
+        got = kda.gdn_bwd(**(a | b), d_o=d_o, dht=dh)
+        want = kda.gdn_bwd(**(a | {n: kda.unpack8(x) for n, x in b.items()}), d_o=d_o, dht=dh)
+        for x, y in zip(got, want):
+            assert torch.equal(x, y), names
+
+
+def test_replays_of_a_graph_from_checkpoints():
+    a = to(make(T=150, H=2, K=64, V=64), DEV)
+    d_o = torch.randn_like(a["v"])
+    p = {n: kda.pack8(a[n]) for n in ("q", "k", "v")}
+    plan = kda.GdnBwdPlan(**(a | p), d_o=d_o)
+    plan()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        plan()
+    for seed in range(3):
+        torch.manual_seed(seed)
+        for n in p:
+            q = kda.pack8(torch.randn_like(a[n].float()).bfloat16() * 0.1)
+            p[n].data.copy_(q.data)
+            p[n].scale.copy_(q.scale)
+        want = kda.gdn_bwd(**(a | p), d_o=d_o)
+        graph.replay()
+        torch.cuda.synchronize()
+        for x, y in zip(plan._outs[:6], want[:6]):
+            assert torch.equal(x, y)
+
+
 def test_gradient_is_the_forwards_difference():
     # the GPU's own forward (fp32 io) along a direction: (f(x + e d) - f(x - e d)) / 2 e
     a = to(make(T=100, H=1, K=64, V=64, dtype=FP, h0=True, seed=9), DEV)
