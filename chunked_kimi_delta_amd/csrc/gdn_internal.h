@@ -333,13 +333,29 @@ __device__ __forceinline__ void stage_block(const uint8_t *src, uint8_t *dst, in
 
 __device__ __forceinline__ float exact_sigmoid(float x) { return 1.f / (1.f + expf(-x)); }
 
+// A head's gate parameters, loaded ahead of their use.
+struct GateHead {
+    float A_log, bias;
+};
+__device__ __forceinline__ GateHead gate_head(const Pre &pre, int j) {
+    GateHead h = {0.f, 0.f};
+    if (pre.gate) {
+        h.A_log = pre.A_log[j];
+        if (pre.dt_bias) h.bias = pre.dt_bias[j];
+    }
+    return h;
+}
+
 // The log decay of raw input x (bias not added yet).
-__device__ __forceinline__ float activate_gate(const Pre &pre, float x, int j) {
+__device__ __forceinline__ float activate_gate(const Pre &pre, float x, GateHead h) {
     if (pre.gate == 0) return x;
-    if (pre.dt_bias) x += pre.dt_bias[j];
-    const float a = expf(pre.A_log[j]);
+    x += h.bias;
+    const float a = expf(h.A_log);
     if (pre.gate == 1) return -a * (fmaxf(x, 0.f) + log1pf(expf(-fabsf(x))));
     return pre.lower_bound * exact_sigmoid(a * x);
+}
+__device__ __forceinline__ float activate_gate(const Pre &pre, float x, int j) {
+    return activate_gate(pre, x, gate_head(pre, j));
 }
 
 __device__ __forceinline__ float load_io(const void *p, int64_t i, bool f32) {

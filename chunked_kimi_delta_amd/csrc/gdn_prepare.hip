@@ -6,8 +6,14 @@
 // results take the decays afterwards, each one e^{Gam_i - Gam_j} of a difference held in two
 // floats (from a 64-bit cumsum), so no decay is too strong. The inverse is the forward
 // substitution of the 16x16 diagonal blocks (four at once in one wave, a column per lane) and
-// block forward substitution between them on the fp32 matrix core: both backward stable, where
-// a product of powers of L loses digits for keys that resemble each other.
+// block forward substitution between them on the fp32 matrix core: both backward stable,
+// where a product of powers of L loses digits for keys that resemble each other.
+//
+// Measured (K = V = 128, bf16 io): 32 heads of 21412 packed tokens 150 us for 620 MB, 16 heads x 4096 tokens
+// 17 us for 58 MB: about 80% and 65% of what a large copy reaches; a workgroup alone takes 6 us (two to
+// three of them in the loads, one in the diagonal blocks' substitution). With Q staged next to K (four
+// workgroups a compute unit instead of five) 184 and 18 us; 19.9 us where the gate's parameters were loaded
+// behind the decays and the decays formed before the barrier that the other waves wait at.
 #include <type_traits>
 
 #include "gdn_internal.h"
@@ -16,20 +22,24 @@ namespace gdn {
 
 namespace {
 
-constexpr int P = 68;                       // floats per row of a 64 x 64 matrix in LDS
+// L and the inverse X in LDS: 16x16 blocks of the lower triangle, rows of 20 floats. X's diagonal blocks
+// take the place of L's (the one wave that inverts them reads all of a block first).
+constexpr int BP = 20, BLK = 16 * BP, BLOCKS = 16;
 
-__device__ __forceinline__ f32x4 block_a(const float *m, int bi, int bj, int grp, int r) {
-    return *(const f32x4 *)(m + (16 * bi + r) * P + 16 * bj + 4 * grp);
+__device__ __forceinline__ float *block_l(float *m, int i, int j) { return m + (i * (i + 1) / 2 + j) * BLK; }
+__device__ __forceinline__ float *block_x(float *m, int i, int j) {
+    return i == j ? block_l(m, i, i) : m + (10 + i * (i - 1) / 2 + j) * BLK;
 }
-__device__ __forceinline__ f32x4 block_b(const float *m, int bi, int bj, int grp, int r) {
+__device__ __forceinline__ f32x4 block_a(const float *b, int grp, int r) { return *(const f32x4 *)(b + r * BP + 4 * grp); }
+__device__ __forceinline__ f32x4 block_b(const float *b, int grp, int r) {
     f32x4 x;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = m[(16 * bi + 4 * grp + i) * P + 16 * bj + r];
+    for (int i = 0; i < 4; ++i) x[i] = b[(4 * grp + i) * BP + r];
     return x;
 }
-__device__ __forceinline__ void block_put(float *m, int bi, int bj, int grp, int r, f32x4 x) {
+__device__ __forceinline__ void block_put(float *b, int grp, int r, f32x4 x) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) m[(16 * bi + 4 * grp + i) * P + 16 * bj + r] = x[i];
+    for (int i = 0; i < 4; ++i) b[(4 * grp + i) * BP + r] = x[i];
 }
 
 struct Scalars {                            // per token of the chunk
@@ -37,24 +47,17 @@ struct Scalars {                            // per token of the chunk
     float beta[64], rk[64], rq[64];
 };
 
-// 1 / sqrt(sum of squares + 1e-6) of a staged row, its quarter `part` per thread (four threads
-// of a row are neighbours)
-template <int K, int IN>
-__device__ __forceinline__ float row_factor(const uint8_t *m, int row, int part) {
+// sum of the squares of eight values
+template <int IN>
+__device__ __forceinline__ float squares(const Parts<IN> &x) {
     float s = 0.f;
 #pragma unroll
-    for (int c = 0; c < K / 32; ++c) {
-        const Parts<IN> x = lds_parts<IN>(m + piece_at<K>(row, part * (K / 32) + c), 64 * K * 2);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            float v = (float)x.p[0][e];
-            if constexpr (IN == 3) v += (float)x.p[1][e] + (float)x.p[2][e];
-            s += v * v;
-        }
+    for (int e = 0; e < 8; ++e) {
+        float v = (float)x.p[0][e];
+        if constexpr (IN == 3) v += (float)x.p[1][e] + (float)x.p[2][e];
+        s += v * v;
     }
-    s += __shfl_xor(s, 1);
-    s += __shfl_xor(s, 2);
-    return 1.f / sqrtf(s + kda::L2NORM_EPS);
+    return s;
 }
 
 }  // namespace
@@ -62,17 +65,17 @@ __device__ __forceinline__ float row_factor(const uint8_t *m, int row, int part)
 // IN: planes of q and k (1: bf16 io, 3: fp32 io); X: parts of A and M
 // BWD: the backward's record (RecB).
 template <int K, int IN, int X, bool BWD>
-__global__ __launch_bounds__(256) void prepare_kernel(Params p)
+__global__ __launch_bounds__(256, IN == 3 ? 1 : 4) void prepare_kernel(Params p)
 {
     constexpr int MAT = 64 * K * 2;         // bytes of one staged plane
     using R = std::conditional_t<BWD, RecB, Rec<X>>;
-    // L and X take the place of K and Q once the Gram products are done: with less LDS more
-    // workgroups share a compute unit, which is what hides the phases' latencies
-    constexpr int LX = 2 * 64 * P * 4, AREA = 2 * IN * MAT > LX ? 2 * IN * MAT : LX;
-    __shared__ __attribute__((aligned(1024))) uint8_t kq[AREA];
+    constexpr int R_M = [] { if constexpr (BWD) return RecB::MT; else return Rec<X>::M; }();
+    // L and X take the place of K once the Gram products are done, and each wave holds its tile of Q in
+    // registers: with less LDS more workgroups share a compute unit, which hides the phases' latencies
+    constexpr int LX = BLOCKS * BLK * 4, AREA = IN * MAT > LX ? IN * MAT : LX;
+    __shared__ __attribute__((aligned(1024))) uint8_t km[AREA];
     __shared__ Scalars sc;
-    float *const Lm = (float *)kq, *const Xm = Lm + 64 * P;
-    uint8_t *const km = kq, *const qm = kq + IN * MAT;
+    float *const lx = (float *)km;
     const int tid = threadIdx.x, lane = tid & 63, grp = lane >> 4, r = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int slot = blockIdx.x, j = blockIdx.y, h = j / p.G;
@@ -80,17 +83,29 @@ __global__ __launch_bounds__(256) void prepare_kernel(Params p)
     int64_t bos;
     if (!kda::locate_slot<CT>(p.seq, slot, &s, &bos, &nv)) return;
 
+    // every load at once: what one wave needs for the scalars first (loads complete in order)
+    const bool live = lane < nv;
+    float g = 0.f, b = 0.f;
+    const GateHead gate = gate_head(p.pre, j);
+    if (wave == 0) {
+        const int64_t at = (bos + (live ? lane : nv - 1)) * p.HV + j;
+        g = load_io(p.g, at, IN == 3);
+        b = load_io(p.beta, at, IN == 3);
+    }
     const int64_t stride = (int64_t)p.H * K, off = (bos * p.H + h) * K;
+    const int ti = 3 - wave, qi = 16 * ti + r;          // the wave's query tile, the lane's row of it
+    Parts<IN> qt[K / 32];
 #pragma unroll
     for (int i = 0; i < IN; ++i) {
+        const uint16_t *const q = p.q[i] + off + (qi < nv ? qi : nv - 1) * stride + 8 * grp;
+#pragma unroll
+        for (int st = 0; st < K / 32; ++st) qt[st].p[i] = *(const bf16x8 *)(q + 32 * st);
         stage_rows<K, 4>(p.k[i] + off, stride, nv, km + i * MAT, wave, lane);
-        stage_rows<K, 4>(p.q[i] + off, stride, nv, qm + i * MAT, wave, lane);
     }
+    kda::vm_drain();
+    __syncthreads();
     if (wave == 0) {
-        const bool live = lane < nv;
-        const int64_t at = (bos + (live ? lane : nv - 1)) * p.HV + j;
-        float g = activate_gate(p.pre, load_io(p.g, at, IN == 3), j);
-        float b = load_io(p.beta, at, IN == 3);
+        g = activate_gate(p.pre, g, gate);
         if (p.pre.beta_sigmoid) b = exact_sigmoid(b);
         // a decay below e^-100000 is zero whatever its size; -inf would make differences NaN
         if (g < -1e5f) g = -1e5f;
@@ -104,147 +119,146 @@ __global__ __launch_bounds__(256) void prepare_kernel(Params p)
         sc.ghi[lane] = hi;
         sc.glo[lane] = (float)(x - (double)hi);
         sc.beta[lane] = live ? b : 0.f;
-    }
-    kda::vm_drain();
-    __syncthreads();
-    {
-        const int row = tid >> 2, part = tid & 3;
-        float fk = 1.f, fq = 1.f;
+    } else if (wave < 3) {                  // meanwhile: two neighbouring threads a row of K
+        const int row = (tid - 64) >> 1, part = tid & 1;
+        float f = 1.f;
         if (p.pre.qk_l2norm) {
-            fk = row_factor<K, IN>(km, row, part);
-            fq = row_factor<K, IN>(qm, row, part);
+            f = 0.f;
+#pragma unroll
+            for (int c = 0; c < K / 16; ++c) f += squares(lds_parts<IN>(km + piece_at<K>(row, part * (K / 16) + c), MAT));
+            f += __shfl_xor(f, 1);
+            f = 1.f / sqrtf(f + kda::L2NORM_EPS);
         }
-        if (part == 0) {
-            sc.rk[row] = fk;
-            sc.rq[row] = fq;
+        if (part == 0) sc.rk[row] = f;
+    }
+    {
+        float f = 1.f;
+        if (p.pre.qk_l2norm) {
+            f = 0.f;
+#pragma unroll
+            for (int c = 0; c < K / 32; ++c) f += squares(qt[c]);
+            f = 1.f / sqrtf(sum_groups(f) + kda::L2NORM_EPS);
         }
+        if (grp == 0) sc.rq[qi] = f;
     }
     __syncthreads();
 
     uint8_t *const rec = p.rec + ((size_t)j * p.seq.n_slots + slot) * R::BYTES;
-    auto decay = [&](int i, int jj) {       // e^{Gam_i - Gam_jj}
-        return __builtin_amdgcn_exp2f((sc.ghi[i] - sc.ghi[jj]) + (sc.glo[i] - sc.glo[jj]));
-    };
-    // products of row tile a of X and row tile b of Y over the K columns
-    auto gram = [&](const uint8_t *x, int a, const uint8_t *y, int b) {
-        f32x4 c = zero4();
+    auto k_tile = [&](int t, int st) { return lds_parts<IN>(km + piece_at<K>(16 * t + r, 4 * st + grp), MAT); };
+    auto four = [&](const float *x, int t) { return *(const f32x4 *)(x + 16 * t + 4 * grp); };
+    // e^{Gam_i - Gam_j}, the exponents held in two floats each
+    auto decay = [&](float hi, float lo) { return __builtin_amdgcn_exp2f(hi + lo); };
+    // L's row tile `wave` and M's query tile 3 - wave, five tiles a wave. A lane's four values are
+    // consecutive columns j of a row i (in the backward's M, which is stored transposed, consecutive rows
+    // of a column); a key tile serves both.
+    const int li = 16 * wave + r;
+    Parts<IN> kt[K / 32];
 #pragma unroll
-        for (int st = 0; st < K / 32; ++st)
-            c = mm(lds_parts<IN>(x + piece_at<K>(16 * a + r, 4 * st + grp), MAT),
-                   lds_parts<IN>(y + piece_at<K>(16 * b + r, 4 * st + grp), MAT), c);
-        return c;
-    };
-    // L row tile `wave` (rows in C-layout), and M of query tile 3 - wave, transposed, so that
-    // a lane's four values are consecutive tokens of one query row: five tiles a wave
+    for (int st = 0; st < K / 32; ++st) kt[st] = k_tile(wave, st);
+    const float lhi = sc.ghi[li], llo = sc.glo[li], lrk = sc.rk[li];
+    const f32x4 mhi = BWD ? four(sc.ghi, ti) : f32x4{sc.ghi[qi]}, mlo = BWD ? four(sc.glo, ti) : f32x4{sc.glo[qi]};
+    f32x4 mrq = BWD ? four(sc.rq, ti) : f32x4{sc.rq[qi]};
+    mrq *= p.scale;
     f32x4 lt[4];
 #pragma unroll
     for (int tj = 0; tj < 4; ++tj) {
         lt[tj] = zero4();
-        if (tj > wave) continue;
-        const f32x4 c = gram(km, wave, km, tj);
-        const int jj = 16 * tj + r;
-        const float sj = sc.rk[jj] * sc.beta[jj];
+        if (tj > wave && tj > (ti | 1)) continue;
+        Parts<IN> x[K / 32];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int i = 16 * wave + 4 * grp + e;
-            lt[tj][e] = i > jj ? c[e] * sj * sc.rk[i] * decay(i, jj) : 0.f;
+        for (int st = 0; st < K / 32; ++st) x[st] = k_tile(tj, st);
+        const f32x4 hi = four(sc.ghi, tj), lo = four(sc.glo, tj), s = four(sc.rk, tj) * four(sc.beta, tj);
+        const int j0 = 16 * tj + 4 * grp;
+        if (tj <= wave) {
+            f32x4 c = zero4();
+#pragma unroll
+            for (int st = 0; st < K / 32; ++st) c = mm(x[st], kt[st], c);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) lt[tj][e] = li > j0 + e ? c[e] * (lrk * s[e]) * decay(lhi - hi[e], llo - lo[e]) : 0.f;
         }
-    }
-    if constexpr (!BWD) {
-        const int ti = 3 - wave, i = 16 * ti + r;
-        for (int tj = 0; tj <= (ti | 1); ++tj) {
-            f32x4 m = zero4();
-            if (tj <= ti) {
-                const f32x4 c = gram(km, tj, qm, ti);
+        if (tj > (ti | 1)) continue;
+        f32x4 m = zero4();
+        if (tj <= ti) {
+            f32x4 c = zero4();
+            if constexpr (BWD) {
+                const int jj = 16 * tj + r;
+                const float ch = sc.ghi[jj], cl = sc.glo[jj], cs = sc.rk[jj] * sc.beta[jj];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int jj = 16 * tj + 4 * grp + e;
-                    m[e] = i >= jj && i < nv ? c[e] * (p.scale * sc.rq[i]) * (sc.rk[jj] * sc.beta[jj]) * decay(i, jj) : 0.f;
-                }
-            }
-            uint8_t *at = rec + R::M + frag_index(ti, tj >> 1) * R::FR + lane * 16 + (tj & 1) * 8;
-#pragma unroll
-            for (int x = 0; x < X; ++x) {
-                const kda::bf16x4 y = kda::to_bf16x4(m);
-                *(uint2 *)(at + x * R::MAT) = __builtin_bit_cast(uint2, y);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) m[e] -= (float)y[e];
-            }
-        }
-    } else {
-        // M^T of token tile tj: a lane's four values are consecutive rows i of one column
-        const int tj = wave, jj = 16 * tj + r;
-        for (int ti = tj & 2; ti < 4; ++ti) {
-            f32x4 m = zero4();
-            if (ti >= tj) {
-                const f32x4 c = gram(qm, ti, km, tj);
-                const float sj = p.scale * sc.rk[jj] * sc.beta[jj];
+                for (int st = 0; st < K / 32; ++st) c = mm(qt[st], x[st], c);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int i = 16 * ti + 4 * grp + e;
-                    m[e] = i >= jj && i < nv ? c[e] * sj * sc.rq[i] * decay(i, jj) : 0.f;
+                    m[e] = i >= jj && i < nv ? c[e] * (mrq[e] * cs) * decay(mhi[e] - ch, mlo[e] - cl) : 0.f;
                 }
-            }
-            uint8_t *at = rec + R::MT + frag_index_t(tj, ti >> 1) * R::FR + lane * 16 + (ti & 1) * 8;
+            } else {
 #pragma unroll
-            for (int x = 0; x < X; ++x) {
-                const kda::bf16x4 y = kda::to_bf16x4(m);
-                *(uint2 *)(at + x * R::MAT) = __builtin_bit_cast(uint2, y);
+                for (int st = 0; st < K / 32; ++st) c = mm(x[st], qt[st], c);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) m[e] -= (float)y[e];
+                for (int e = 0; e < 4; ++e)
+                    m[e] = qi >= j0 + e && qi < nv ? c[e] * (mrq[0] * s[e]) * decay(mhi[0] - hi[e], mlo[0] - lo[e]) : 0.f;
             }
+        }
+        uint8_t *at = rec + lane * 16 + (BWD ? R_M + frag_index_t(tj, ti >> 1) * R::FR + (ti & 1) * 8
+                                             : R_M + frag_index(ti, tj >> 1) * R::FR + (tj & 1) * 8);
+#pragma unroll
+        for (int k = 0; k < X; ++k) {
+            const kda::bf16x4 y = kda::to_bf16x4(m);
+            *(uint2 *)(at + k * R::MAT) = __builtin_bit_cast(uint2, y);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) m[e] -= (float)y[e];
         }
     }
     __syncthreads();
 #pragma unroll
     for (int tj = 0; tj < 4; ++tj)
-        if (tj <= wave) block_put(Lm, wave, tj, grp, r, lt[tj]);
+        if (tj <= wave) *(f32x4 *)(block_l(lx, wave, tj) + r * BP + 4 * grp) = lt[tj];
     __syncthreads();
     if (wave == 0) {                        // the four diagonal blocks, column r of block grp
         float x[16];
-        const float *m = Lm + 16 * grp * P + 16 * grp;
+        float *const m = block_l(lx, grp, grp);
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
             float acc = i == r ? 1.f : 0.f;
 #pragma unroll
-            for (int jj = 0; jj < i; ++jj) acc -= m[i * P + jj] * x[jj];
+            for (int jj = 0; jj < i; ++jj) acc -= m[i * BP + jj] * x[jj];
             x[i] = acc;
         }
 #pragma unroll
-        for (int i = 0; i < 16; ++i) Xm[(16 * grp + i) * P + 16 * grp + r] = x[i];
+        for (int i = 0; i < 16; ++i) m[i * BP + r] = x[i];
     }
     __syncthreads();
-    auto a_of = [&](const float *m, int bi, int bj) { return block_a(m, bi, bj, grp, r); };
-    auto b_of = [&](const float *m, int bi, int bj) { return block_b(m, bi, bj, grp, r); };
+    auto l_a = [&](int bi, int bj) { return block_a(block_l(lx, bi, bj), grp, r); };
+    auto x_a = [&](int bi, int bj) { return block_a(block_x(lx, bi, bj), grp, r); };
+    auto x_b = [&](int bi, int bj) { return block_b(block_x(lx, bi, bj), grp, r); };
     auto neg = [](f32x4 x) { return f32x4{-x[0], -x[1], -x[2], -x[3]}; };
     if (wave < 2) {                         // X_10 = -X_11 L_10 X_00, X_32 = -X_33 L_32 X_22
         const int lo = 2 * wave, hi = lo + 1;
-        const f32x4 t = kda::mm16_f32(a_of(Lm, hi, lo), b_of(Xm, lo, lo), zero4());
-        block_put(Xm, hi, lo, grp, r, neg(kda::mm16_f32(a_of(Xm, hi, hi), t, zero4())));
+        const f32x4 t = kda::mm16_f32(l_a(hi, lo), x_b(lo, lo), zero4());
+        block_put(block_x(lx, hi, lo), grp, r, neg(kda::mm16_f32(x_a(hi, hi), t, zero4())));
     }
     __syncthreads();
     {                                       // X_ij = -sum_k X_ik (L X)_kj, i = 2, 3, j = 0, 1
         const int i = 2 + (wave >> 1), c = wave & 1;
-        auto lx = [&](int row) {
-            f32x4 t = kda::mm16_f32(a_of(Lm, row, c), b_of(Xm, c, c), zero4());
-            return c == 0 ? kda::mm16_f32(a_of(Lm, row, 1), b_of(Xm, 1, 0), t) : t;
+        auto row_of = [&](int row) {        // (L X) of block row `row`, block column c
+            f32x4 t = kda::mm16_f32(l_a(row, c), x_b(c, c), zero4());
+            return c == 0 ? kda::mm16_f32(l_a(row, 1), x_b(1, 0), t) : t;
         };
-        const f32x4 t2 = lx(2);
-        f32x4 x = kda::mm16_f32(a_of(Xm, i, 2), t2, zero4());
-        if (i == 3) x = kda::mm16_f32(a_of(Xm, 3, 3), lx(3), x);
-        block_put(Xm, i, c, grp, r, neg(x));
+        const f32x4 t2 = row_of(2);
+        f32x4 x = kda::mm16_f32(x_a(i, 2), t2, zero4());
+        if (i == 3) x = kda::mm16_f32(x_a(3, 3), row_of(3), x);
+        block_put(block_x(lx, i, c), grp, r, neg(x));
     }
     __syncthreads();
     for (int f = wave; f < 6; f += 4) {     // A's fragments
         const int t = f < 2 ? f : 2 + ((f - 2) >> 1), st = f < 2 ? 0 : (f & 1);
-        const int i = 16 * t + r;
         f32x4 x[2];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            const int c0 = 32 * st + 16 * u + 4 * grp;
-            const f32x4 y = *(const f32x4 *)(Xm + i * P + c0);
+            const int bj = 2 * st + u;
+            x[u] = bj <= t ? x_a(t, bj) : zero4();
+            if (bj == t)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[u][e] = c0 + e <= i ? y[e] : 0.f;
+                for (int e = 0; e < 4; ++e) x[u][e] = 4 * grp + e <= r ? x[u][e] : 0.f;
         }
         const Parts<X> y = split<X>(x[0], x[1]);
         const auto rs = kda::buffer_rsrc(rec, R::BYTES);
@@ -254,15 +268,16 @@ __global__ __launch_bounds__(256) void prepare_kernel(Params p)
     }
     if constexpr (BWD) {
         for (int f = wave; f < 6; f += 4) { // A^T's fragments
-            const int t = f < 4 ? f >> 1 : f - 2, st = f < 4 ? (f & 1) : 1, jj = 16 * t + r;
+            const int t = f < 4 ? f >> 1 : f - 2, st = f < 4 ? (f & 1) : 1;
             f32x4 x[2];
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
+            for (int u = 0; u < 2; ++u) {
+                const int bi = 2 * st + u;
+                x[u] = bi >= t ? x_b(bi, t) : zero4();
+                if (bi == t)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int i = 32 * st + 16 * u + 4 * grp + e;
-                    x[u][e] = i >= jj ? Xm[i * P + jj] : 0.f;
-                }
+                    for (int e = 0; e < 4; ++e) x[u][e] = 4 * grp + e >= r ? x[u][e] : 0.f;
+            }
             const Parts<X> y = split<X>(x[0], x[1]);
             const auto rs = kda::buffer_rsrc(rec, R::BYTES);
 #pragma unroll
