@@ -79,7 +79,14 @@ struct ChunkTimes {
 // two more launches about 6 us. Measured, 16 heads x 4096, bf16 io, state pass of the forward: whole 206
 // us; 4 segments 97, 6: 87, 8: 77, 11: 103, 16: 97 us. 8 packed sequences x 32 heads: whole 465 us, two or
 // more segments 660 us and up (512 workgroups fill the device already).
-Segments plan_segments(int64_t tt, int64_t N, int64_t HV, int K, int ends_parts, int last_parts, ChunkTimes us)
+//
+// Packed sequences that would go whole, and leave no compute unit two workgroups, are cut at one and a half
+// times the mean length: even batches hardly notice, a long sequence no longer sets the time alone. Forward
+// (backward) us, 16 heads, K = V = 128: 8 x 2048 tokens 194 -> 202 (637 -> 641), 7 x 512 + 16384 tokens 867 ->
+// 452 (1946 -> 1177), 3 .. 8192 tokens 482 -> 469 (1262 -> 1228). The last with 32 heads 586 -> 768 (1750 ->
+// 2064): there the last pass fills the device either way, and the first one only adds to it.
+Segments plan_segments(int64_t tt, int64_t N, bool packed, int64_t HV, int K, int ends_parts, int last_parts,
+                       ChunkTimes us)
 {
     Segments g = {};
     if (N == 0 || tt == 0) return g;
@@ -97,6 +104,8 @@ Segments plan_segments(int64_t tt, int64_t N, int64_t HV, int K, int ends_parts,
             g.chunks = (int32_t)len;
         }
     }
+    if (g.chunks == 0 && packed && N > 1 && n >= 16 && units * last_parts <= cus)
+        g.chunks = (int32_t)(n + n / 2);
     if (g.chunks) g.slots = (int32_t)(tt / (CT * (int64_t)g.chunks) + N);
     return g;
 }
@@ -118,7 +127,7 @@ Layout layout(const gdn_args *a)
     const size_t planes = f32 ? align256((size_t)L.tt * a->H * a->K * 6) : 0;
     L.k = L.q + planes;
     L.E = L.k + planes;
-    L.seg = plan_segments(L.tt, a->N, a->HV, a->K, a->V / 64, a->V / 64,
+    L.seg = plan_segments(L.tt, a->N, a->cu_seqlens != nullptr, a->HV, a->K, a->V / 64, a->V / 64,
                           f32 ? ChunkTimes{7.8, 8.7, 5.2} : ChunkTimes{3.2, 4.1, 3.8});
     const size_t ends = (size_t)L.seg.slots * a->HV * a->K * 4;
     L.PHI = L.E + ends * a->V;
@@ -255,7 +264,8 @@ BwdLayout bwd_layout(const gdn_args *a)
     if (a->io == KDA_BF16) {
         L.keep = slots * RecB::BYTES;
         L.E = L.keep + slots * keep_bytes(a->K, a->V);
-        L.seg = plan_segments(L.f.tt, a->N, a->HV, a->K, 2 * (a->V / 64), 2, ChunkTimes{6.0, 7.0, 4.0});
+        L.seg = plan_segments(L.f.tt, a->N, a->cu_seqlens != nullptr, a->HV, a->K, 2 * (a->V / 64), 2,
+                              ChunkTimes{6.0, 7.0, 4.0});
         const size_t ends = (size_t)L.seg.slots * a->HV * a->K * 4;
         L.G = L.E + ends * a->V;
         L.PHI = L.G + ends * a->V;

@@ -56,6 +56,12 @@ def test_segments(kw, dtype):
         check(make(H=1, G=2, dtype=dtype, h0=h0, **kw))
 
 
+# many heads, so that only the length beyond the mean is cut
+@pytest.mark.parametrize("lens", [[100, 4000, 1, 700, 64, 0, 2500, 1000], [1200, 1000, 1100, 1024, 1088, 1, 1500, 1600]])
+def test_long_and_short_sequences_of_many_heads(lens):
+    check(make(lens=lens, H=32, K=64, V=64, h0=True))
+
+
 def test_segments_update_the_state_in_place():
     a = to(make(T=2000, H=1, G=2, K=64, V=128, h0=True), DEV)
     o, fin = kda.gdn_fwd(**a)

@@ -264,6 +264,24 @@ def test_packed_inputs_are_their_values():
         assert torch.equal(x, y)
 
 
+def test_long_and_short_sequences_of_many_heads():
+    # each sequence by a call of its own: two results, each within its bar
+    lens = [100, 4000, 1, 700, 64, 2500, 1000]
+    a = to(make(lens=lens + [0], H=16, G=2, K=64, V=64, h0=True), DEV)
+    d_o, dh = (x.to(DEV) for x in cotangents(a))
+    got = kda.gdn_bwd(**a, d_o=d_o, dht=dh)
+    at = 0
+    for s, n in enumerate(lens):
+        part = {m: a[m][:, at:at + n].contiguous() for m in ("q", "k", "v", "g", "beta")}
+        want = kda.gdn_bwd(**part, initial_state=a["initial_state"][s:s + 1], d_o=d_o[:, at:at + n].contiguous(),
+                           dht=dh[s:s + 1])
+        for m, x, y in zip(OUTS[:6], got, want):
+            x = x[s:s + 1] if m == "initial_state" else x[:, at:at + n]
+            assert (x.double() - y.double()).norm() <= 2 * tol(m, BF) * y.double().norm(), (s, m)
+        at += n
+    assert torch.equal(got[5][7], dh[7])
+
+
 @pytest.mark.parametrize("dtype", [BF, FP])
 def test_some_or_all_inputs_packed(dtype):
     a = to(make(B=2, T=77, H=2, G=2, K=64, V=128, dtype=dtype, raw=True, gate="softplus", h0=True), DEV)
