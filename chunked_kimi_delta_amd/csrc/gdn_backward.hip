@@ -72,13 +72,13 @@ __device__ __forceinline__ void reverse_chain(const BwdParams &b, int s, int j, 
     if (c0 < c1) stage(c1 - 1, lds);
     auto kept = [&](int c) { return b.keep + (slot0 + c) * KP::BYTES; };
 
-    f32x4 S[NT][1], D[4][1];                // dS, laid out as the forward's S; dR
+    f32x4 S[NT], D[4];                      // dS, laid out as the forward's S; dR
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) S[t][0][i] = init ? init[(size_t)state_row(t, i, grp) * V + cbase + col0 + r] : 0.f;
+        for (int i = 0; i < 4; ++i) S[t][i] = init ? init[(size_t)state_row(t, i, grp) * V + cbase + col0 + r] : 0.f;
 #pragma unroll
-    for (int t = 0; t < 4; ++t) D[t][0] = zero4();
+    for (int t = 0; t < 4; ++t) D[t] = zero4();
 
 #pragma unroll 1
     for (int c = c1 - 1; c >= c0; --c) {
@@ -109,13 +109,13 @@ __device__ __forceinline__ void reverse_chain(const BwdParams &b, int s, int j, 
         for (int t = 0; t < 4; ++t) kS[t] = zero4();
 #pragma unroll
         for (int st = 0; st < K / 32; ++st) {
-            const Parts<X> sp = split<X>(S[2 * st][0], S[2 * st + 1][0]);
+            const Parts<X> sp = split<X>(S[2 * st], S[2 * st + 1]);
 #pragma unroll
             for (int t = 0; t < 4; ++t)
                 kS[t] = mm(Parts<1>{lds_b128(buf + L::KM + piece_at<K>(16 * t + r, 4 * st + grp))}, sp, kS[t]);
         }
 #pragma unroll
-        for (int t = 0; t < NT; ++t) S[t][0] *= eg;
+        for (int t = 0; t < NT; ++t) S[t] *= eg;
         // de = M^T dO + beta e^{gam-Gam} (K dS'); dO of tokens 32 st + 4 g .. + 3, + 16 per lane
         s16x4 dv[2][2];
 #pragma unroll
@@ -142,25 +142,25 @@ __device__ __forceinline__ void reverse_chain(const BwdParams &b, int s, int j, 
         // dR = A^T de
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-            D[t][0] = zero4();
+            D[t] = zero4();
 #pragma unroll
             for (int st = t / 2; st < 2; ++st)
-                D[t][0] = mm(lds_parts<X>(rec + R::AT + frag_index_t(t, st) * R::FR + lane * 16, R::MAT), dp[st], D[t][0]);
+                D[t] = mm(lds_parts<X>(rec + R::AT + frag_index_t(t, st) * R::FR + lane * 16, R::MAT), dp[st], D[t]);
         }
         // dS = e^gam dS' + Q^T (scale e^Gam dO) - K^T (e^Gam dR)
 #pragma unroll
         for (int st = 0; st < 2; ++st) {
             const f32x4 a0 = *(const f32x4 *)(ra + 32 * st + 4 * grp), a1 = *(const f32x4 *)(ra + 32 * st + 16 + 4 * grp);
             const f32x4 c0v = *(const f32x4 *)(rc + 32 * st + 4 * grp), c1v = *(const f32x4 *)(rc + 32 * st + 16 + 4 * grp);
-            const Parts<X> rp = split<X>(zero4() - a0 * D[2 * st][0], zero4() - a1 * D[2 * st + 1][0]),
+            const Parts<X> rp = split<X>(zero4() - a0 * D[2 * st], zero4() - a1 * D[2 * st + 1]),
                            op = split<X>(c0v * widen(dv[st][0]), c1v * widen(dv[st][1]));
             const int row = 32 * st + 4 * grp + (r >> 2);
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
                 const int piece = 4 * (t / 2) + (r & 3), half = 8 * (t % 2);
                 const int at0 = piece_at<K>(row, piece) + half, at1 = piece_at<K>(row + 16, piece) + half;
-                S[t][0] = mm(Parts<1>{join(lds_tr(buf + L::KM + at0), lds_tr(buf + L::KM + at1))}, rp, S[t][0]);
-                S[t][0] = mm(Parts<1>{join(lds_tr(buf + L::QM + at0), lds_tr(buf + L::QM + at1))}, op, S[t][0]);
+                S[t] = mm(Parts<1>{join(lds_tr(buf + L::KM + at0), lds_tr(buf + L::KM + at1))}, rp, S[t]);
+                S[t] = mm(Parts<1>{join(lds_tr(buf + L::QM + at0), lds_tr(buf + L::QM + at1))}, op, S[t]);
             }
         }
         if (BUFS == 1 && c > c0) {
@@ -179,7 +179,7 @@ __device__ __forceinline__ void reverse_chain(const BwdParams &b, int s, int j, 
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) end[(size_t)state_row(t, i, grp) * V + cbase + col0 + r] = S[t][0][i];
+            for (int i = 0; i < 4; ++i) end[(size_t)state_row(t, i, grp) * V + cbase + col0 + r] = S[t][i];
     }
 }
 
@@ -209,7 +209,7 @@ __global__ __launch_bounds__(V * 4) void chains_kernel(BwdParams b)
     const size_t at = ((size_t)g.s * p.HV + j) * KV;
     if (part == 0) {
         const float *const init = SEG ? segment_start<K, V>(p, g, unit / p.HV, j) : p.h0 ? p.h0 + at : nullptr;
-        forward_chain<K, V, V, 1, 1, RecB::X, RecB, KEEP>(p, g.s, j, g.c0, g.c1, 0, init, nullptr, lds, b.keep, &mx);
+        forward_chain<K, V, V, 1, RecB::X, RecB, KEEP>(p, g.s, j, g.c0, g.c1, 0, init, nullptr, lds, b.keep, &mx);
     } else {
         const float *const init = !g.last() ? p.seg.G + ((size_t)unit + p.HV) * KV : b.dht ? b.dht + at : nullptr;
         reverse_chain<K, V, V, 2, true>(b, g.s, j, g.c0, g.c1, 0, init, g.i == 0 && b.dh0 ? b.dh0 + at : nullptr, lds, &mx);

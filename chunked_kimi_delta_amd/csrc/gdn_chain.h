@@ -1,5 +1,5 @@
 // gdn_chain.h -- the pass over a sequence's 64-token chunks (gdn_internal.h has the formulas): one
-// wave per 16 or 32 value columns of a (sequence, value head).
+// wave per 16 value columns of a (sequence, value head).
 //
 // The columns of S are independent, so a wave keeps its K x 16 slice of S in fp32 registers for
 // the whole pass and needs nothing from the other waves: S, R and e leave one product in the very
@@ -55,42 +55,36 @@ struct Maxima {
     }
 };
 
-template <int N, int CTW>
-__device__ __forceinline__ float largest(const f32x4 (&x)[N][CTW]) {
+template <int N>
+__device__ __forceinline__ float largest(const f32x4 (&x)[N]) {
     uint32_t m = 0;
 #pragma unroll
     for (int t = 0; t < N; ++t)
 #pragma unroll
-        for (int ct = 0; ct < CTW; ++ct)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) m = max(m, __float_as_uint(x[t][ct][i]) & 0x7fffffffu);     // NaN counts
+        for (int i = 0; i < 4; ++i) m = max(m, __float_as_uint(x[t][i]) & 0x7fffffffu);     // NaN counts
     return wave_max(__uint_as_float(m));
 }
 
 // A wave's columns of the state, or of a [64 tokens][V] matrix in C-layout, to the workspace (`col`: this
-// lane's first column).
-template <class KP, int NT, int CTW>
-__device__ __forceinline__ void keep_state(const f32x4 (&S)[NT][CTW], Scale f, uint8_t *base, float *inv, int col,
+// lane's column).
+template <class KP, int NT>
+__device__ __forceinline__ void keep_state(const f32x4 (&S)[NT], Scale f, uint8_t *base, float *inv, int col,
                                            int grp)
 {
     const auto rs = kda::buffer_rsrc(base, KP::BYTES);
 #pragma unroll
     for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int ct = 0; ct < CTW; ++ct)
-            kda::bstore8<0>(rs, KP::state_at(col + 16 * ct, state_row(t, 0, grp)), 0, half4(S[t][ct], f.f));
+        kda::bstore8<0>(rs, KP::state_at(col, state_row(t, 0, grp)), 0, half4(S[t], f.f));
     if (threadIdx.x == 0) *inv = f.inv;
 }
 
-template <class KP, int CTW>
-__device__ __forceinline__ void keep_rows(const f32x4 (&E)[4][CTW], Scale f, uint8_t *base, float *inv, int col, int grp)
+template <class KP>
+__device__ __forceinline__ void keep_rows(const f32x4 (&E)[4], Scale f, uint8_t *base, float *inv, int col, int grp)
 {
     const auto rs = kda::buffer_rsrc(base, KP::BYTES);
 #pragma unroll
     for (int t = 0; t < 4; ++t)
-#pragma unroll
-        for (int ct = 0; ct < CTW; ++ct)
-            kda::bstore8<0>(rs, KP::row_at(col + 16 * ct, 16 * t + 4 * grp), 0, half4(E[t][ct], f.f));
+        kda::bstore8<0>(rs, KP::row_at(col, 16 * t + 4 * grp), 0, half4(E[t], f.f));
     if (threadIdx.x == 0) *inv = f.inv;
 }
 
@@ -124,23 +118,23 @@ __device__ __forceinline__ Segment whole_sequence(const SeqGeom &sg, int s) {
 }
 
 // The chunks [c0, c1) of one (sequence, value head) for the C columns from `cbase` of `ld` columns,
-// CTW 16-column tiles a wave (one wave per 16 CTW columns of C).
+// one wave per 16 columns of C.
 // init: the state's first element at c0 (row-major, `ld` columns), null for zeros (PHI: ignored);
 // end: where to put the end state, or null.
-template <int K, int V, int C, int CTW, int IN, int X, class R, Mode M>
+template <int K, int V, int C, int IN, int X, class R, Mode M>
 __device__ __forceinline__ void forward_chain(const Params &p, int s, int j, int c0, int c1, int cbase,
                                               const float *init, float *end, uint8_t *lds,
-                                              uint8_t *keep = nullptr, Maxima<C / 16 / CTW> *mx = nullptr)
+                                              uint8_t *keep = nullptr, Maxima<C / 16> *mx = nullptr)
 {
     using L = Stage<K, C, IN, R, M>;
     static_assert(L::BYTES * L::BUFS <= 160 * 1024, "LDS of a compute unit");
-    constexpr int NW = C / 16 / CTW, NT = K / 16, LD = M == PHI ? K : V, NS = K / 32;
+    constexpr int NW = C / 16, NT = K / 16, LD = M == PHI ? K : V, NS = K / 32;
     const int tid = threadIdx.x, lane = tid & 63, grp = lane >> 4, r = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int h = j / p.G;
     const int64_t bos = kda::seq_bos(p.seq, s), eos = kda::seq_eos(p.seq, s, bos);
     const size_t slot0 = (size_t)j * p.seq.n_slots + bos / CT + s;
-    const int col0 = 16 * CTW * wave;       // within the workgroup's columns
+    const int col0 = 16 * wave;             // within the workgroup's columns
 
     const RowStage<K, NW> qk_rows((int64_t)p.H * K, wave, lane);
     const RowStage<C, NW> v_rows((int64_t)p.HV * V, wave, lane);
@@ -159,27 +153,24 @@ __device__ __forceinline__ void forward_chain(const Params &p, int s, int j, int
     };
     if (c0 < c1) stage(c0, lds);
 
-    f32x4 S[NT][CTW];
+    f32x4 S[NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int ct = 0; ct < CTW; ++ct)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int row = state_row(t, i, grp), col = cbase + col0 + 16 * ct + r;
-                if constexpr (M == PHI)
-                    S[t][ct][i] = row == col ? 1.f : 0.f;
-                else
-                    S[t][ct][i] = init ? init[(size_t)row * LD + col] : 0.f;
-            }
+        for (int i = 0; i < 4; ++i) {
+            const int row = state_row(t, i, grp), col = cbase + col0 + r;
+            if constexpr (M == PHI)
+                S[t][i] = row == col ? 1.f : 0.f;
+            else
+                S[t][i] = init ? init[(size_t)row * LD + col] : 0.f;
+        }
 
     using KP = Keep<K, V>;
     auto kept = [&](int c) { return keep + (slot0 + c) * KP::BYTES; };
-    f32x4 E[4][CTW];
+    f32x4 E[4];
 #pragma unroll
     for (int t = 0; t < 4; ++t)
-#pragma unroll
-        for (int ct = 0; ct < CTW; ++ct) E[t][ct] = zero4();
+        E[t] = zero4();
 #pragma unroll 1
     for (int c = c0; c < c1; ++c) {
         uint8_t *const buf = lds + ((c - c0) % L::BUFS) * L::BYTES;
@@ -220,26 +211,21 @@ __device__ __forceinline__ void forward_chain(const Params &p, int s, int j, int
             }
         };
         Parts<X> af[6];
-        f32x4 a4[4], v4[4][CTW];
+        f32x4 a4[4], v4[4];
         auto read_av = [&] {
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
                 a4[t] = *(const f32x4 *)(ra + 16 * t + 4 * grp);
+                v4[t] = zero4();
+                if constexpr (M == PHI) {
+                } else if constexpr (IN == 1) {
+                    v4[t] = widen(lds_tr(buf + L::VM + piece_at<C>(16 * t + 4 * grp + (r >> 2), col0 / 8 + ((r & 3) >> 1)) +
+                                         8 * (r & 1)));
+                } else {
 #pragma unroll
-                for (int ct = 0; ct < CTW; ++ct) {
-                    v4[t][ct] = zero4();
-                    if constexpr (M == PHI) {
-                    } else if constexpr (IN == 1) {
-                        v4[t][ct] = widen(lds_tr(buf + L::VM + piece_at<C>(16 * t + 4 * grp + (r >> 2),
-                                                                           (col0 + 16 * ct) / 8 + ((r & 3) >> 1)) +
-                                                 8 * (r & 1)));
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int row = 16 * t + 4 * grp + i;
-                            v4[t][ct][i] = ((const float *)p.v)[((t0 + (row < nv ? row : nv - 1)) * p.HV + j) * V +
-                                                                cbase + col0 + 16 * ct + r];
-                        }
+                    for (int i = 0; i < 4; ++i) {
+                        const int row = 16 * t + 4 * grp + i;
+                        v4[t][i] = ((const float *)p.v)[((t0 + (row < nv ? row : nv - 1)) * p.HV + j) * V + cbase + col0 + r];
                     }
                 }
             }
@@ -266,11 +252,10 @@ __device__ __forceinline__ void forward_chain(const Params &p, int s, int j, int
             b4[2 * st + 1] = *(const f32x4 *)(rb + 32 * st + 16 + 4 * grp);
         };
 
-        f32x4 kS[4][CTW], O[4][CTW];
+        f32x4 kS[4], O[4];
 #pragma unroll
         for (int t = 0; t < 4; ++t)
-#pragma unroll
-            for (int ct = 0; ct < CTW; ++ct) kS[t][ct] = O[t][ct] = zero4();
+            kS[t] = O[t] = zero4();
         if constexpr (AHEAD) {
 #pragma unroll
             for (int st = 0; st < NS; ++st) read_kq(st, kf[st], qf[M == OUT ? st : 0]);
@@ -285,16 +270,12 @@ __device__ __forceinline__ void forward_chain(const Params &p, int s, int j, int
                 read_av();
                 phase();
             }
-            Parts<X> sp[CTW];
+            const Parts<X> sp = split<X>(S[2 * st], S[2 * st + 1]);
 #pragma unroll
-            for (int ct = 0; ct < CTW; ++ct) sp[ct] = split<X>(S[2 * st][ct], S[2 * st + 1][ct]);
-#pragma unroll
-            for (int t = 0; t < 4; ++t)
-#pragma unroll
-                for (int ct = 0; ct < CTW; ++ct) {
-                    kS[t][ct] = mm(kf[AHEAD ? st : 0][t], sp[ct], kS[t][ct]);
-                    if constexpr (M == OUT) O[t][ct] = mm(sp[ct], qf[AHEAD ? st : 0][t], O[t][ct]);
-                }
+            for (int t = 0; t < 4; ++t) {
+                kS[t] = mm(kf[AHEAD ? st : 0][t], sp, kS[t]);
+                if constexpr (M == OUT) O[t] = mm(sp, qf[AHEAD ? st : 0][t], O[t]);
+            }
         }
         if constexpr (!AHEAD) read_av();
         phase();
@@ -302,23 +283,18 @@ __device__ __forceinline__ void forward_chain(const Params &p, int s, int j, int
         phase();
 #pragma unroll
         for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int ct = 0; ct < CTW; ++ct) S[t][ct] *= eg;
+            S[t] *= eg;
         // R = V - e^Gam (K S), as operands; e = A R
-        Parts<X> rp[2][CTW];
+        Parts<X> rp[2];
 #pragma unroll
         for (int st = 0; st < 2; ++st)
+            rp[st] = split<X>(v4[2 * st] - a4[2 * st] * kS[2 * st],
+                              v4[2 * st + 1] - a4[2 * st + 1] * kS[2 * st + 1]);
 #pragma unroll
-            for (int ct = 0; ct < CTW; ++ct)
-                rp[st][ct] = split<X>(v4[2 * st][ct] - a4[2 * st] * kS[2 * st][ct],
-                                      v4[2 * st + 1][ct] - a4[2 * st + 1] * kS[2 * st + 1][ct]);
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-#pragma unroll
-            for (int ct = 0; ct < CTW; ++ct) {
-                E[t][ct] = mm(af[frag_index(t, 0)], rp[0][ct], zero4());
-                if (t >= 2) E[t][ct] = mm(af[frag_index(t, 1)], rp[1][ct], E[t][ct]);
-            }
+        for (int t = 0; t < 4; ++t) {
+            E[t] = mm(af[frag_index(t, 0)], rp[0], zero4());
+            if (t >= 2) E[t] = mm(af[frag_index(t, 1)], rp[1], E[t]);
+        }
         phase();
         read_kts(1);
         phase();
@@ -331,34 +307,26 @@ __device__ __forceinline__ void forward_chain(const Params &p, int s, int j, int
         // S += K^T (beta e^{gam - Gam} e)
 #pragma unroll
         for (int st = 0; st < 2; ++st) {
-            Parts<X> dp[CTW];
-#pragma unroll
-            for (int ct = 0; ct < CTW; ++ct)
-                dp[ct] = split<X>(b4[2 * st] * E[2 * st][ct], b4[2 * st + 1] * E[2 * st + 1][ct]);
+            const Parts<X> dp = split<X>(b4[2 * st] * E[2 * st], b4[2 * st + 1] * E[2 * st + 1]);
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
                 const Parts<IN> kt = AHEAD ? ktf[AHEAD ? st : 0][AHEAD ? t : 0] : read_kt(st, t);
-#pragma unroll
-                for (int ct = 0; ct < CTW; ++ct) S[t][ct] = mm(kt, dp[ct], S[t][ct]);
+                S[t] = mm(kt, dp, S[t]);
             }
         }
         if constexpr (M == OUT) {           // o = scale e^Gam (Q S) + M e
             const float *const rc = (const float *)(rec + R::RC);
 #pragma unroll
             for (int t = 0; t < 4; ++t)
-#pragma unroll
-                for (int ct = 0; ct < CTW; ++ct) O[t][ct] *= rc[16 * t + r];
+                O[t] *= rc[16 * t + r];
 #pragma unroll
             for (int st = 0; st < 2; ++st) {
-                Parts<X> ep[CTW];
-#pragma unroll
-                for (int ct = 0; ct < CTW; ++ct) ep[ct] = split<X>(E[2 * st][ct], E[2 * st + 1][ct]);
+                const Parts<X> ep = split<X>(E[2 * st], E[2 * st + 1]);
 #pragma unroll
                 for (int t = 2 * st; t < 4; ++t) {
                     const int f = frag_index(t, st);
                     const Parts<X> m = AHEAD ? mf[f] : lds_parts<X>(rec + R::M + f * R::FR + lane * 16, R::MAT);
-#pragma unroll
-                    for (int ct = 0; ct < CTW; ++ct) O[t][ct] = mm(ep[ct], m, O[t][ct]);
+                    O[t] = mm(ep, m, O[t]);
                 }
             }
             constexpr int SZ = IN == 1 ? 2 : 4;
@@ -366,15 +334,13 @@ __device__ __forceinline__ void forward_chain(const Params &p, int s, int j, int
             const auto ob = kda::rows_in((uint8_t *)p.o + (t0 * p.HV + j) * (int64_t)V * SZ, nv,
                                          (int64_t)p.HV * V * SZ, V * SZ);
 #pragma unroll
-            for (int t = 0; t < 4; ++t)
-#pragma unroll
-                for (int ct = 0; ct < CTW; ++ct) {
-                    const int at = ((16 * t + r) * p.HV * V + cbase + col0 + 16 * ct + 4 * grp) * SZ;
-                    if constexpr (IN == 1)
-                        kda::bstore8<0>(ob, at, 0, kda::to_bf16x4(O[t][ct]));
-                    else
-                        kda::bstore16<0>(ob, at, 0, O[t][ct]);
-                }
+            for (int t = 0; t < 4; ++t) {
+                const int at = ((16 * t + r) * p.HV * V + cbase + col0 + 4 * grp) * SZ;
+                if constexpr (IN == 1)
+                    kda::bstore8<0>(ob, at, 0, kda::to_bf16x4(O[t]));
+                else
+                    kda::bstore16<0>(ob, at, 0, O[t]);
+            }
         }
         if (L::BUFS == 1 && c + 1 < c1) {
             __syncthreads();                // every wave is done with the buffer
@@ -394,15 +360,13 @@ __device__ __forceinline__ void forward_chain(const Params &p, int s, int j, int
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int ct = 0; ct < CTW; ++ct)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    end[(size_t)state_row(t, i, grp) * LD + cbase + col0 + 16 * ct + r] = S[t][ct][i];
+            for (int i = 0; i < 4; ++i)
+                end[(size_t)state_row(t, i, grp) * LD + cbase + col0 + r] = S[t][i];
         if constexpr (M == PHI) {           // and the transpose behind it
             const auto rs = kda::buffer_rsrc(end + K * K, K * K * 4);
 #pragma unroll
             for (int t = 0; t < NT; ++t)
-                kda::bstore16<0>(rs, ((cbase + col0 + r) * K + state_row(t, 0, grp)) * 4, 0, S[t][0]);
+                kda::bstore16<0>(rs, ((cbase + col0 + r) * K + state_row(t, 0, grp)) * 4, 0, S[t]);
         }
     }
 }

@@ -24,9 +24,9 @@ __device__ __forceinline__ void forward_ends(const Params &p, int slot, int j, i
                 *(float2 *)(copy + to) = *(const float2 *)(h0 + to);
             }
         }
-        forward_chain<K, V, 64, 1, IN, X, R, END>(p, g.s, j, g.c0, g.c1, 64 * part, h0, p.seg.E + at * K * V, lds);
+        forward_chain<K, V, 64, IN, X, R, END>(p, g.s, j, g.c0, g.c1, 64 * part, h0, p.seg.E + at * K * V, lds);
     } else if (g.i > 0) {
-        forward_chain<K, V, 64, 1, IN, X, R, PHI>(p, g.s, j, g.c0, g.c1, 64 * (part - V / 64), nullptr,
+        forward_chain<K, V, 64, IN, X, R, PHI>(p, g.s, j, g.c0, g.c1, 64 * (part - V / 64), nullptr,
                                                   p.seg.PHI + at * 2 * K * K, lds);
     }
 }

@@ -29,7 +29,7 @@ __global__ __launch_bounds__(256) void state_kernel(Params p)
         init = p.h0 ? p.h0 + (size_t)unit * K * V : nullptr;
     }
     float *const end = p.ht && g.last() ? p.ht + ((size_t)g.s * p.HV + j) * K * V : nullptr;
-    forward_chain<K, V, 64, 1, IN, X, Rec<X>, OUT>(p, g.s, j, g.c0, g.c1, 64 * part, init, end, lds);
+    forward_chain<K, V, 64, IN, X, Rec<X>, OUT>(p, g.s, j, g.c0, g.c1, 64 * part, init, end, lds);
 }
 
 template <int K, int V, int IN, int X>
