@@ -441,8 +441,8 @@ kda_status gdn_fwd(const gdn_args *a, void *workspace, size_t ws_bytes, void *st
     p.seg.PHI = (float *)(ws + L.PHI);
     if (f32 && L.tt > 0) {
         const int64_t n = L.tt * a->H * a->K;
-        if (launch_split_planes((const float *)a->q, n, (uint16_t *)(ws + L.q), hs) != hipSuccess ||
-            launch_split_planes((const float *)a->k, n, (uint16_t *)(ws + L.k), hs) != hipSuccess)
+        if (launch_split_planes((const float *)a->q, (const float *)a->k, n, (uint16_t *)(ws + L.q),
+                                (uint16_t *)(ws + L.k), hs) != hipSuccess)
             return KDA_ERR_HIP;
         for (int i = 0; i < 3; ++i) {
             p.q[i] = (const uint16_t *)(ws + L.q) + i * n;

@@ -366,8 +366,9 @@ __device__ __forceinline__ float load_io(const void *p, int64_t i, bool f32) {
 
 // Host-side launchers (defined next to their kernels).
 namespace gdn {
-// fp32 x [n] as three bf16 planes, n values apart
-hipError_t launch_split_planes(const float *x, int64_t n, uint16_t *planes, hipStream_t st);
+// fp32 q and k [n] as three bf16 planes each, n values apart
+hipError_t launch_split_planes(const float *q, const float *k, int64_t n, uint16_t *q_planes, uint16_t *k_planes,
+                               hipStream_t st);
 template <int K> hipError_t launch_prepare(const Params &p, bool f32, hipStream_t st);
 template <int K> hipError_t launch_prepare_bwd(const Params &p, hipStream_t st);    // bf16 io
 template <int K, int V> hipError_t launch_backward(const BwdParams &b, hipStream_t st);

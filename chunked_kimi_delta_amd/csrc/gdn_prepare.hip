@@ -303,28 +303,31 @@ __global__ __launch_bounds__(256, IN == 3 ? 1 : 4) void prepare_kernel(Params p)
     }
 }
 
-// fp32 x as three bf16 planes: their sum is x to 2^-24 or better
-__global__ __launch_bounds__(256) void split_planes_kernel(const float *x, int64_t n4,
-                                                           uint2 *planes)
+// fp32 q and k (blockIdx.y) as three bf16 planes each: their sum is x to 2^-24 or better
+__global__ __launch_bounds__(256) void split_planes_kernel(const float *q, const float *k, int64_t n4,
+                                                           uint2 *q_planes, uint2 *k_planes)
 {
+    const float *const x = blockIdx.y ? k : q;
+    uint2 *const planes = blockIdx.y ? k_planes : q_planes;
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (i >= n4) return;
     f32x4 v = ((const f32x4 *)x)[i];
 #pragma unroll
-    for (int k = 0; k < 3; ++k) {
+    for (int j = 0; j < 3; ++j) {
         const kda::bf16x4 y = kda::to_bf16x4(v);
-        planes[k * n4 + i] = __builtin_bit_cast(uint2, y);
+        planes[j * n4 + i] = __builtin_bit_cast(uint2, y);
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e] -= (float)y[e];
     }
 }
 
-hipError_t launch_split_planes(const float *x, int64_t n, uint16_t *planes, hipStream_t st)
+hipError_t launch_split_planes(const float *q, const float *k, int64_t n, uint16_t *q_planes, uint16_t *k_planes,
+                               hipStream_t st)
 {
     const int64_t n4 = n / 4;               // rows are 64 or 128 wide
     if (n4 == 0) return hipSuccess;
-    split_planes_kernel<<<dim3((unsigned)((n4 + 255) / 256)), dim3(256), 0, st>>>(x, n4,
-                                                                                  (uint2 *)planes);
+    split_planes_kernel<<<dim3((unsigned)((n4 + 255) / 256), 2), dim3(256), 0, st>>>(q, k, n4, (uint2 *)q_planes,
+                                                                                     (uint2 *)k_planes);
     return hipGetLastError();
 }
 
