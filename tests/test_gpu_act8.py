@@ -79,3 +79,23 @@ def test_replays_of_a_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(y, want)
+
+
+def test_offsets_beyond_32_bits():
+    rows, D = (1 << 25) + 5, 128                # 4.3e9 values: the last rows against a call of their own
+    x = torch.empty(rows, D, dtype=torch.bfloat16, device=DEV).normal_()
+    p = kda.pack8(x)
+    tail = kda.pack8(x[-1000:].clone())
+    assert torch.equal(p.data[-1000:], tail.data) and torch.equal(p.scale[-1000:], tail.scale)
+    assert torch.equal(kda.unpack8(p)[-1000:], kda.unpack8(tail))
+
+
+def test_other_streams():
+    x = torch.randn(3000, 64, device=DEV).bfloat16()
+    want = kda.unpack8(kda.pack8(x))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        y = kda.unpack8(kda.pack8(x))
+    side.synchronize()
+    assert torch.equal(y, want)

@@ -282,6 +282,31 @@ def test_long_and_short_sequences_of_many_heads():
     assert torch.equal(got[5][7], dh[7])
 
 
+def test_offsets_beyond_32_bits():
+    # 2.2e9 elements a tensor; the last sequence by calls of its own, each result within its bar
+    n, N, H, D = 33000, 8, 64, 128
+    gen = torch.Generator(device=DEV).manual_seed(1)
+    big = lambda *s: torch.empty(*s, dtype=BF, device=DEV).normal_(generator=gen)
+    a = {m: big(1, n * N, H, D) for m in ("q", "k", "v")}
+    a["g"] = -big(1, n * N, H).abs() * 0.1
+    a["beta"] = big(1, n * N, H)
+    d_o = big(1, n * N, H, D)
+    assert d_o.numel() > 2 ** 31
+    pre = dict(use_qk_l2norm=True, use_beta_sigmoid=True)
+    cu = torch.arange(0, n * N + 1, n, device=DEV)
+    part = {m: x[:, -n:].contiguous() for m, x in a.items()}
+    far = lambda x, y: float((x.double() - y.double()).norm() / y.double().norm())
+    o, fin = kda.gdn_fwd(**a, cu_seqlens=cu, **pre)
+    want_o, want_fin = kda.gdn_fwd(**part, **pre)
+    assert far(o[:, -n:], want_o) <= 2.0 ** -7 and far(fin[-1:], want_fin) <= 2 * 2.0 ** -13
+    del o, want_o
+    got = kda.gdn_bwd(**a, d_o=d_o, cu_seqlens=cu, **pre)
+    want = kda.gdn_bwd(**part, d_o=d_o[:, -n:].contiguous(), **pre)
+    for m, x, y in zip(OUTS[:5], got, want):
+        assert far(x[:, -n:], y) <= 2 * tol(m, BF), m
+    assert far(got[5][-1:], want[5]) <= 2 * tol("initial_state", BF)
+
+
 @pytest.mark.parametrize("dtype", [BF, FP])
 def test_some_or_all_inputs_packed(dtype):
     a = to(make(B=2, T=77, H=2, G=2, K=64, V=128, dtype=dtype, raw=True, gate="softplus", h0=True), DEV)
