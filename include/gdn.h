@@ -68,9 +68,11 @@ size_t gdn_fwd_workspace_bytes(const gdn_args *args);
 
 /* Enqueue the forward on `stream`: 64-token chunks (a prepare kernel, then the pass over each
    sequence's chunks, split into segments where the batch is too small to fill the device), or,
-   for a dense batch of at most 16 tokens a sequence, the recurrence itself. Products take
-   16-bit operands in pairs (high and low part), so that the states and o carry about 17 bits
-   before their own rounding, for either io type. */
+   for a dense batch of at most 16 tokens a sequence, the recurrence itself. Products take bf16
+   operands in parts: two for bf16 io (the states and o carry about 17 bits before their own
+   rounding), three for fp32 io (24 bits). Tokens behind the last sequence are left as they were.
+   The chunked form takes less than 2^28 tokens, 2^21 (sequence, value head) pairs and, with fp32
+   io, 2^26 (token, value head) pairs a call; so does gdn_bwd, for any length. */
 kda_status gdn_fwd(const gdn_args *args, void *workspace, size_t ws_bytes, void *stream);
 
 /* Gradients of gdn_fwd's inputs from the gradients of a loss with respect to o (d_o, like o) and to
@@ -82,8 +84,8 @@ kda_status gdn_fwd(const gdn_args *args, void *workspace, size_t ws_bytes, void 
      dA_log, ddt_bias        [HV] fp32 (4-byte aligned): with a gate, dA_log required, ddt_bias or
                              NULL; ignored without
    bf16 io: the states and their gradients travel in two bf16 parts as in gdn_fwd (dh0 carries
-   about 17 bits); what enters the other gradients is rounded to bf16 once before its last
-   product. fp32 io: kda_bwd's fp32 arithmetic. Deterministic. Tokens behind the last sequence
+   about 17 bits); for the other gradients the states, their gradients, e and v's gradient are kept
+   with 11 bits (scaled fp16), and so is d_o in the products. fp32 io: kda_bwd's fp32 arithmetic. Deterministic. Tokens behind the last sequence
    are left as they were. `workspace`: gdn_bwd_workspace_bytes(args) bytes, 256-byte aligned. */
 size_t gdn_bwd_workspace_bytes(const gdn_args *args);
 
