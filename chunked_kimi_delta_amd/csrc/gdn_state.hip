@@ -3,16 +3,20 @@
 
 namespace gdn {
 
-// 64 columns of V a workgroup (four waves, one to a SIMD), two buffers of LDS: of the shapes tried, the
-// one with the shortest chunk. 16 heads x 4096 tokens without segments: 203 us, against 251 us for all
-// 128 columns in eight waves, 330 us for four waves of 32 columns, 225 us for one buffer and two
-// workgroups a compute unit.
-template <int K, int V, int IN, int X, bool SEG>
-__global__ __launch_bounds__(256) void state_kernel(Params p)
+// C columns of V a workgroup, 16 a wave, two buffers of LDS (one for three planes). 64 columns (a wave on each
+// SIMD) have the shortest chunk: 16 heads x 4096 tokens without segments 203 us, against 251 us for 128
+// columns in eight waves, 330 us for four waves of 32 columns, 225 us for one buffer and two workgroups a
+// compute unit. 128 columns share what is copied to LDS, and their waves hide each other's latencies: bf16
+// io with more 64-column workgroups than compute units, all of one length, takes those (whole forward, K = V
+// = 128: 5 x 1024 tokens of 32 heads 156 -> 127 us, 8 x 2048 of 32 403 -> 344, 16 x 512 of 32 213 -> 196, K =
+// 64: 8 x 1024 of 32 145 -> 121 us). Among packed lengths the longest sequence's chunks count (8 sequences of 3
+// .. 8192 tokens, 32 heads: 471 us with 64 columns, 588 us with 128).
+template <int K, int V, int C, int IN, int X, bool SEG>
+__global__ __launch_bounds__(4 * C) void state_kernel(Params p)
 {
-    using L = Stage<K, 64, IN, Rec<X>, OUT>;
+    using L = Stage<K, C, IN, Rec<X>, OUT>;
     __shared__ __attribute__((aligned(1024))) uint8_t lds[L::BYTES * L::BUFS];
-    constexpr int NV = V / 64;
+    constexpr int NV = V / C;
     int unit, part;
     if (!unit_of(blockIdx.x, NV, (SEG ? p.seg.slots : p.seq.N) * p.HV, &unit, &part)) return;
     int j = unit % p.HV;
@@ -29,7 +33,7 @@ __global__ __launch_bounds__(256) void state_kernel(Params p)
         init = p.h0 ? p.h0 + (size_t)unit * K * V : nullptr;
     }
     float *const end = p.ht && g.last() ? p.ht + ((size_t)g.s * p.HV + j) * K * V : nullptr;
-    forward_chain<K, V, 64, IN, X, Rec<X>, OUT>(p, g.s, j, g.c0, g.c1, 64 * part, init, end, lds);
+    forward_chain<K, V, C, IN, X, Rec<X>, OUT>(p, g.s, j, g.c0, g.c1, C * part, init, end, lds);
 }
 
 template <int K, int V, int IN, int X>
@@ -58,12 +62,18 @@ hipError_t run(const Params &p, hipStream_t st)
 {
     const int64_t units = (int64_t)p.seq.N * p.HV, segs = (int64_t)p.seg.slots * p.HV;
     if (p.seg.chunks == 0) {
-        state_kernel<K, V, IN, X, false><<<dim3(grid_for(units, V / 64)), dim3(256), 0, st>>>(p);
+        if constexpr (V == 128 && IN == 1) {
+            if (!p.seq.cu && 2 * units > kda::current_device_cus()) {
+                state_kernel<K, V, 128, IN, X, false><<<dim3(grid_for(units, 1)), dim3(512), 0, st>>>(p);
+                return hipGetLastError();
+            }
+        }
+        state_kernel<K, V, 64, IN, X, false><<<dim3(grid_for(units, V / 64)), dim3(256), 0, st>>>(p);
         return hipGetLastError();
     }
     ends_kernel<K, V, IN, X><<<dim3(grid_for(segs, V / 64 + K / 64)), dim3(256), 0, st>>>(p);
     join_kernel<K, V, X><<<dim3(grid_for(units, V / 16)), dim3(256), 0, st>>>(p);
-    state_kernel<K, V, IN, X, true><<<dim3(grid_for(segs, V / 64)), dim3(256), 0, st>>>(p);
+    state_kernel<K, V, 64, IN, X, true><<<dim3(grid_for(segs, V / 64)), dim3(256), 0, st>>>(p);
     return hipGetLastError();
 }
 

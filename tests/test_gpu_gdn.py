@@ -163,6 +163,18 @@ def test_grouped_heads_are_repeated_heads_and_packed_is_dense():
     assert torch.equal(o.reshape(o3.shape), o3) and torch.equal(fin, fin3)
 
 
+@pytest.mark.parametrize("K", [64, 128])
+def test_many_dense_sequences(K):
+    # enough of them for 128 columns a workgroup: the same sums, so what packing gives, and the oracle's
+    a = make(B=5, T=150, H=32, K=K, V=128, h0=True, raw=True, gate="softplus")
+    check(a)
+    a = to(a, DEV)
+    o, fin = kda.gdn_fwd(**a)
+    flat = {n: a[n].flatten(0, 1)[None] for n in ("q", "k", "v", "g", "beta")}
+    o2, fin2 = kda.gdn_fwd(**(a | flat), cu_seqlens=torch.arange(0, 751, 150, device=DEV))
+    assert torch.equal(o.flatten(0, 1), o2[0]) and torch.equal(fin, fin2)
+
+
 def test_equals_kda_with_the_decay_repeated():
     a = make(B=1, T=100, H=2, K=64, V=64, dtype=FP, h0=True)
     o, fin = run(a)
