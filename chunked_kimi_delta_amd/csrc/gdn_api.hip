@@ -76,9 +76,11 @@ struct ChunkTimes {
 
 // The number of segments with the shortest expected time, from the number of (sequence, value head) units
 // and the mean length (the lengths of packed sequences lie on the device). Joining takes 2.1 us a segment,
-// two more launches about 6 us. Measured, 16 heads x 4096, bf16 io, state pass of the forward: whole 206
-// us; 4 segments 97, 6: 87, 8: 77, 11: 103, 16: 97 us. 8 packed sequences x 32 heads: whole 465 us, two or
-// more segments 660 us and up (512 workgroups fill the device already).
+// two more launches about 6 us. The first pass's workgroups share compute units two by two and take 15% longer
+// once a third waits. Measured, 16 heads x 4096, bf16 io, state pass of the forward: whole 206 us; 4 segments
+// 97, 6: 87, 8: 77, 11: 103, 16: 97 us. Whole backward in segments of 32 chunks 374 us, 16: 262, 11: 224, 8:
+// 216, 4: 234, 2: 284; 8 heads x 16384: 32: 532, 16: 422, 8: 441. 8 packed sequences x 32 heads: whole 465 us,
+// two or more segments 660 us and up (512 workgroups fill the device already).
 //
 // Packed sequences that would go whole, and leave no compute unit two workgroups, are cut at one and a half
 // times the mean length: even batches hardly notice, a long sequence no longer sets the time alone. Forward
@@ -92,14 +94,14 @@ Segments plan_segments(int64_t tt, int64_t N, bool packed, int64_t HV, int K, in
     if (N == 0 || tt == 0) return g;
     const int64_t n = (tt / N + CT - 1) / CT, units = N * HV, cus = kda::current_device_cus();
     auto rounds = [](int64_t x, int64_t y) { return (double)((x + y - 1) / y); };
-    double best = rounds(units * last_parts, cus) * n * us.whole;
+    double best = 0.95 * rounds(units * last_parts, cus) * n * us.whole;
     for (int64_t count = 2; count <= 64; ++count) {
         const int64_t len = (n + count - 1) / count;
         if (len < 2) break;
-        const int64_t first = units * ((count - 1) * ends_parts + (count - 2) * (K / 64));
-        const double t = rounds(first, 2 * cus) * len * us.first + (count - 2) * 2.1 + 6.0 +
+        const double first = (double)(units * ((count - 1) * ends_parts + (count - 2) * (K / 64))) / (2 * cus);
+        const double t = (first > 1.0 ? 1.15 * first : 1.0) * len * us.first + (count - 2) * 2.1 + 6.0 +
                          rounds(units * count * last_parts, cus) * len * us.last;
-        if (t < 0.95 * best) {
+        if (t < best) {
             best = t;
             g.chunks = (int32_t)len;
         }
