@@ -6,7 +6,7 @@ import torch
 
 from .act8 import Packed8, pack8, unpack8
 from .api import kda_bwd, kda_fwd
-from .gdn import gdn_bwd, gdn_fwd
+from .gdn import GdnBwdPlan, GdnFwdPlan
 
 
 def _save(ctx, checkpoint, q, k, v, *rest):
@@ -85,8 +85,11 @@ class ChunkGDNFunction(torch.autograd.Function):
                 use_qk_l2norm, use_beta_sigmoid, gate, gate_lower_bound, checkpoint=None):
         ctx.pre = dict(use_qk_l2norm=use_qk_l2norm, use_beta_sigmoid=use_beta_sigmoid, gate=gate,
                        gate_lower_bound=gate_lower_bound)
-        o, fin = gdn_fwd(q, k, v, g, beta, scale=scale, cu_seqlens=cu_seqlens,
-                         initial_state=initial_state, A_log=A_log, dt_bias=dt_bias, **ctx.pre)
+        plan = GdnFwdPlan(q, k, v, g, beta, scale=scale, cu_seqlens=cu_seqlens,
+                          initial_state=initial_state, A_log=A_log, dt_bias=dt_bias, **ctx.pre)
+        if cu_seqlens is not None:
+            plan.o.zero_()                  # the kernels leave rows behind the last sequence alone
+        o, fin = plan()
         _save(ctx, checkpoint, q, k, v, g, beta, initial_state, A_log, dt_bias, cu_seqlens)
         ctx.scale = scale
         return o, fin
@@ -95,9 +98,13 @@ class ChunkGDNFunction(torch.autograd.Function):
     def backward(ctx, d_o, d_fin):
         q, k, v, g, beta, h0, A_log, dt_bias, cu = _saved(ctx)
         d_o = d_o.to(g.dtype).contiguous()
-        dq, dk, dv, dg, db, dh0, dA, ddt = gdn_bwd(
+        plan = GdnBwdPlan(
             q, k, v, g, beta, d_o, d_fin.float().contiguous(), scale=ctx.scale, cu_seqlens=cu,
             initial_state=h0, want_dh0=h0 is not None, A_log=A_log, dt_bias=dt_bias, **ctx.pre)
+        if cu is not None:
+            for x in (plan.dq, plan.dk, plan.dv, plan.dg, plan.dbeta):
+                x.zero_()
+        dq, dk, dv, dg, db, dh0, dA, ddt = plan()
         return (dq, dk, dv, dg, db, dh0, dA, None if dt_bias is None else ddt,
                 None, None, None, None, None, None, None)
 
@@ -108,7 +115,8 @@ def chunk_gdn(q, k, v, g, beta, scale=None, initial_state=None, cu_seqlens=None,
     """Differentiable gated delta rule (one decay per token and value head); returns (o,
     final_state). Shapes as GdnFwdPlan; every tensor argument may require grad (cu_seqlens
     excepted). checkpoint="int8" keeps q, k and v for the backward in 8 bits (pack8), which then
-    gives the gradients at those values."""
+    gives the gradients at those values. Rows behind the last packed sequence are zero in o and in
+    the gradients."""
     return ChunkGDNFunction.apply(q, k, v, g, beta, initial_state, A_log, dt_bias, scale,
                                   cu_seqlens, use_qk_l2norm, use_beta_sigmoid, gate,
                                   gate_lower_bound, checkpoint)

@@ -54,8 +54,8 @@ float scale_of(const gdn_args *a)
     return a->scale > 0.f && !isnan(a->scale) ? a->scale : 1.0f / sqrtf((float)a->K);
 }
 
-// What the chunked kernels take: a launch has less than 2^32 threads along a dimension (up to 1024 a chunk,
-// four workgroups of 512 a unit, fp32 io: 64 a row of the decay's gradient).
+// What the chunked kernels take: a launch has less than 2^32 threads along a dimension (up to 1024 a chunk or a
+// pair of sequence and value head, fp32 io: 64 a row of the decay's gradient).
 kda_status check_chunks(const gdn_args *a)
 {
     const kda_status st = check_shapes(a);

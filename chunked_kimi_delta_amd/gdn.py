@@ -107,9 +107,9 @@ class GdnFwdPlan:
 
 def gdn_fwd(q, k, v, g, beta, scale=None, cu_seqlens=None, initial_state=None,
             output_final_state=True, workspace=None, **prestage):
-    """Gated delta rule forward. Returns (o, final_state or None); see GdnFwdPlan for shapes and
-    the pre-stage keywords (use_qk_l2norm, use_beta_sigmoid, gate, A_log, dt_bias,
-    gate_lower_bound)."""
+    """Gated delta rule forward. Returns (o, final_state or None; rows of o behind the last packed
+    sequence hold anything); see GdnFwdPlan for shapes and the pre-stage keywords (use_qk_l2norm,
+    use_beta_sigmoid, gate, A_log, dt_bias, gate_lower_bound)."""
     return GdnFwdPlan(q, k, v, g, beta, scale, cu_seqlens, initial_state, output_final_state,
                       workspace, **prestage)()
 
@@ -119,10 +119,10 @@ class GdnBwdPlan:
     g, beta, initial_state and (with a gate) A_log, dt_bias, from d_o (like v) and dht (fp32
     [N,HV,K,V] or None).
 
-    Inputs and pre-stage keywords as for GdnFwdPlan; q, k and v may be Packed8 checkpoints (of one dtype, the
-    io dtype), which the call unpacks. Outputs, allocated once and reused by every
-    call(): dq, dk, dv, dg, dbeta in the io dtype, dh0 fp32 [N,HV,K,V] (when want_dh0), dA_log and
-    ddt_bias fp32 [HV] (with a gate).
+    Inputs and pre-stage keywords as for GdnFwdPlan; q, k and v may be Packed8 checkpoints (of one
+    dtype, the io dtype), which the call unpacks (single ones when the plan is made). Outputs,
+    allocated once and reused by every call(): dq, dk, dv, dg, dbeta in the io dtype, dh0 fp32
+    [N,HV,K,V] (when want_dh0), dA_log and ddt_bias fp32 [HV] (with a gate).
     """
 
     def __init__(self, q, k, v, g, beta, d_o, dht=None, scale=None, cu_seqlens=None,
@@ -186,7 +186,8 @@ class GdnBwdPlan:
 def gdn_bwd(q, k, v, g, beta, d_o, dht=None, scale=None, cu_seqlens=None, initial_state=None,
             want_dh0=True, **prestage):
     """Gated delta rule backward. Returns (dq, dk, dv, dg, dbeta in the io dtype, dh0 fp32 or None,
-    dA_log or None, ddt_bias or None); see GdnBwdPlan. q, k and v may each be a Packed8
+    dA_log or None, ddt_bias or None; rows behind the last packed sequence hold anything); see
+    GdnBwdPlan. q, k and v may each be a Packed8
     checkpoint: the gradients are then those at the values that it stands for."""
     return GdnBwdPlan(q, k, v, g, beta, d_o, dht, scale, cu_seqlens, initial_state, want_dh0,
                       **prestage)()

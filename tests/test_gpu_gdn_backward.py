@@ -363,6 +363,21 @@ def test_gradient_is_the_forwards_difference():
         assert abs(diff - slope) <= 0.02 + 1e-3 * got[n].double().norm(), n
 
 
+@pytest.mark.parametrize("checkpoint", [None, "int8"])
+def test_chunk_gdn_rows_behind_the_last_sequence_are_zero(checkpoint):
+    a = to(make(lens=[70, 0, 100], H=2, K=64, V=64, tail=30), DEV)
+    a["v"][:, 170:] = float("nan")              # read by nothing
+    d_o = torch.randn_like(a["v"].float()).bfloat16()
+    poison = [torch.full_like(a[n], float("nan")) for n in ("q", "k", "v", "g", "beta") for _ in range(3)]
+    del poison                                  # new tensors may well start as these
+    leaves = {n: a[n].clone().requires_grad_() for n in ("q", "k", "v", "g", "beta")}
+    o, _ = kda.chunk_gdn(**leaves, cu_seqlens=a["cu_seqlens"], checkpoint=checkpoint)
+    o.backward(d_o)
+    assert (o[:, 170:] == 0).all() and torch.isfinite(o).all()
+    for n, x in leaves.items():
+        assert (x.grad[:, 170:] == 0).all() and torch.isfinite(x.grad).all() and x.grad.norm() > 0, n
+
+
 def test_training_step_runs():
     torch.manual_seed(0)
     a = to(make(B=2, T=70, H=2, K=64, V=64, raw=True), DEV)
