@@ -119,9 +119,9 @@ class GdnBwdPlan:
     g, beta, initial_state and (with a gate) A_log, dt_bias, from d_o (like v) and dht (fp32
     [N,HV,K,V] or None).
 
-    Inputs and pre-stage keywords as for GdnFwdPlan; q, k and v may be Packed8 checkpoints (of one
-    dtype, the io dtype), which the call unpacks (single ones when the plan is made). Outputs,
-    allocated once and reused by every call(): dq, dk, dv, dg, dbeta in the io dtype, dh0 fp32
+    Inputs and pre-stage keywords as for GdnFwdPlan; q, k and v may all be Packed8 checkpoints (of
+    one dtype, the io dtype), which every call unpacks into the workspace. Outputs, allocated once
+    and reused by every call(): dq, dk, dv, dg, dbeta in the io dtype, dh0 fp32
     [N,HV,K,V] (when want_dh0), dA_log and ddt_bias fp32 [HV] (with a gate).
     """
 
@@ -142,7 +142,7 @@ class GdnBwdPlan:
             self._packed = (q, k, v)
             q, k, v = q.data, k.data, v.data
         elif any(packed):
-            q, k, v = (unpack8(x) if p else x for x, p in zip((q, k, v), packed))
+            raise TypeError("q, k and v must all be checkpoints or none (unpack8 gives a tensor)")
         a = _arguments(q, k, v, g, beta, scale, cu_seqlens, initial_state, use_qk_l2norm,
                        use_beta_sigmoid, gate, A_log, dt_bias, gate_lower_bound, io)
         dev = self.device = q.device
@@ -189,6 +189,9 @@ def gdn_bwd(q, k, v, g, beta, d_o, dht=None, scale=None, cu_seqlens=None, initia
     dA_log or None, ddt_bias or None; rows behind the last packed sequence hold anything); see
     GdnBwdPlan. q, k and v may each be a Packed8
     checkpoint: the gradients are then those at the values that it stands for."""
+    packed = [isinstance(x, Packed8) for x in (q, k, v)]
+    if not all(packed):
+        q, k, v = (unpack8(x) if p else x for x, p in zip((q, k, v), packed))
     return GdnBwdPlan(q, k, v, g, beta, d_o, dht, scale, cu_seqlens, initial_state, want_dh0,
                       **prestage)()
 

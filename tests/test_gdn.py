@@ -221,5 +221,7 @@ def test_binding_refuses_before_any_call():
     p = {n: kda.Packed8(a[n].to(torch.int8), a[n][..., 0].float(), torch.bfloat16) for n in ("q", "k", "v")}
     with pytest.raises(ValueError, match="HIP device"):
         kda.gdn_bwd(**(a | p), d_o=a["v"])
+    with pytest.raises(TypeError, match="all be checkpoints"):
+        kda.GdnBwdPlan(**(a | {"q": p["q"]}), d_o=a["v"])
     with pytest.raises(TypeError, match="one dtype"):
         kda.gdn_bwd(**(a | p | {"k": p["k"]._replace(dtype=torch.float32)}), d_o=a["v"])
