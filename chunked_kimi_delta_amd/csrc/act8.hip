@@ -5,7 +5,9 @@
 // of 127 x tells which: d = 127 x - n m is exact for bf16 rows (15 bits each), and n stands where
 // |2 d| < m. Where a wave holds a value that may not, it divides (correctly rounded, which decides every
 // case of bf16 exactly); fp32 rows divide in 64 bits. A lane takes eight values of a row, and a row's
-// maximum is a butterfly over its lanes. Unpacking writes eight bytes a lane, whole lines a store.
+// maximum is a butterfly over its lanes. Unpacking writes eight bytes a lane, whole lines a store. 4096 x 48 rows
+// of 128 bf16: packing 19.4 us (4.0 TB/s, its vector instructions; two rows a lane 21, four 24 us: loads in
+// flight are not what it lacks), unpacking 15.0 us (5.1 TB/s, what a copy reaches).
 #include "act8.h"
 #include "kda_internal.h"
 
