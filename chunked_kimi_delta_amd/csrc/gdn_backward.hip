@@ -23,6 +23,12 @@
 // gradients that it enters; bf16 there cost up to 5e-3 of dg, whose terms cancel), multiplied with
 // dO as fp16 (exact: a bf16 value scaled by a power of two); the 64 x 64 matrices take two bf16
 // parts against the stored q and k.
+//
+// Measured, 16 heads x 4096 tokens, K = V = 128: records 18 us, segments' ends 62, their joining 16, both
+// passes 62, tokens 78 (227 for the call; without segments and with four 64 x 64 matrices 519). The passes are
+// bound by a chunk's dependent products with two waves a SIMD (7 us a chunk with every compute unit busy), the
+// tokens' kernel by LDS: of a workgroup's 36 thousand cycles 8 load, 6 form the matrices, 9 multiply with the
+// states (520 KB of LDS reads), 5 do the other products.
 #include <type_traits>
 
 #include "gdn_segments.h"

@@ -8,6 +8,8 @@
 // a token, both products of a token come from the state before it,
 //     r = v - a (S^T k),   o = scale (a (S^T q) + (q.k) beta r),
 // so the waves' partial sums meet once per token (in LDS, double buffered: one barrier).
+// Measured: 64 rows (8 padding) of 32 heads, K = V = 128, 237 MB: 38.6 us where the states fit the last-level
+// cache from step to step, 46 us (5.1 TB/s, what a copy reaches) where they do not.
 #include "gdn_internal.h"
 
 namespace gdn {
