@@ -11,8 +11,8 @@
 // four consecutive columns of one token and stores eight bytes.
 //
 // What bounds it: a chunk is a chain of dependent products and splits, 3.2 us for 64 columns alone (K = 128,
-// bf16 io) of which the matrix core works 0.9, LDS reads of K, Q and the record (290 KB) take 1.2 and the
-// splits 0.7; with every compute unit busy 4.1 us. Reading operands a phase ahead took 16 heads x 4096 tokens
+// bf16 io); by count the matrix core works 0.9 of them, LDS reads of K, Q and the record (290 KB) 1.2 and the
+// splits 0.7. With every compute unit busy 4.1 us. Reading operands a phase ahead took 16 heads x 4096 tokens
 // without segments from 205 to 196 us; interleaving the two kinds of instructions by hand 209.
 #pragma once
 
