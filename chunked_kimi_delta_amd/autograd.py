@@ -3,6 +3,7 @@ marshalling only; both directions are the library's kernels)."""
 from __future__ import annotations
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from .act8 import Packed8, pack8, unpack8
 from .api import kda_bwd, kda_fwd
@@ -77,7 +78,7 @@ def chunk_kda(q, k, v, g, beta, scale=None, initial_state=None, cu_seqlens=None,
 
 
 class ChunkGDNFunction(torch.autograd.Function):
-    """o, final_state = gated delta rule(q, k, v, g, beta; initial_state), differentiable as
+    """o, final_state = gated delta rule(q, k, v, g, beta; initial_state), differentiable (once) as
     ChunkKDAFunction is."""
 
     @staticmethod
@@ -95,6 +96,7 @@ class ChunkGDNFunction(torch.autograd.Function):
         return o, fin
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, d_o, d_fin):
         q, k, v, g, beta, h0, A_log, dt_bias, cu = _saved(ctx)
         d_o = d_o.to(g.dtype).contiguous()

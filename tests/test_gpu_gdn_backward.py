@@ -378,6 +378,15 @@ def test_chunk_gdn_rows_behind_the_last_sequence_are_zero(checkpoint):
         assert (x.grad[:, 170:] == 0).all() and torch.isfinite(x.grad).all() and x.grad.norm() > 0, n
 
 
+def test_second_derivatives_are_refused():
+    a = to(make(T=20, H=1, K=64, V=64, dtype=FP), DEV)
+    q = a["q"].clone().requires_grad_()
+    o, _ = kda.chunk_gdn(**(a | {"q": q}))
+    dq, = torch.autograd.grad(o.square().sum(), q, create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        dq.sum().backward()
+
+
 def test_training_step_runs():
     torch.manual_seed(0)
     a = to(make(B=2, T=70, H=2, K=64, V=64, raw=True), DEV)
