@@ -11,9 +11,10 @@
 //
 // Measured (K = V = 128, bf16 io): 32 heads of 21412 packed tokens 150 us for 620 MB, 16 heads x 4096 tokens
 // 17 us for 58 MB: about 80% and 65% of what a large copy reaches; a workgroup alone takes 6 us (two to
-// three of them in the loads, one in the diagonal blocks' substitution). With Q staged next to K (four
-// workgroups a compute unit instead of five) 184 and 18 us; 19.9 us where the gate's parameters were loaded
-// behind the decays and the decays formed before the barrier that the other waves wait at.
+// three of them in the loads, one in the diagonal blocks' substitution), and four share a compute unit (102
+// registers). With Q staged in LDS next to K, also four, 184 and 18 us; with Q in registers, the gate's parameters
+// loaded behind the decays, every key tile read twice and seven workgroups a compute unit (72 registers) 151
+// and 19.9 us: fewer waits did as much as more waves.
 #include <type_traits>
 
 #include "gdn_internal.h"
@@ -71,7 +72,7 @@ __global__ __launch_bounds__(256, IN == 3 ? 1 : 4) void prepare_kernel(Params p)
     using R = std::conditional_t<BWD, RecB, Rec<X>>;
     constexpr int R_M = [] { if constexpr (BWD) return RecB::MT; else return Rec<X>::M; }();
     // L and X take the place of K once the Gram products are done, and each wave holds its tile of Q in
-    // registers: with less LDS more workgroups share a compute unit, which hides the phases' latencies
+    // registers: LDS does not limit the workgroups of a compute unit (but for three planes of K = 128)
     constexpr int LX = BLOCKS * BLK * 4, AREA = IN * MAT > LX ? IN * MAT : LX;
     __shared__ __attribute__((aligned(1024))) uint8_t km[AREA];
     __shared__ Scalars sc;
