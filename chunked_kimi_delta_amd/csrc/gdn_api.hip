@@ -55,7 +55,7 @@ float scale_of(const gdn_args *a)
 }
 
 // What the chunked kernels take: a launch has less than 2^32 threads along a dimension (up to 1024 a chunk or a
-// pair of sequence and value head, fp32 io: 64 a row of the decay's gradient).
+// pair of sequence and value head, fp32 io: 32 a row of q or k that is split).
 kda_status check_chunks(const gdn_args *a)
 {
     const kda_status st = check_shapes(a);
@@ -220,9 +220,9 @@ Params params_of(const gdn_args *a, const Layout &L)
 
 struct BwdLayout {
     Layout f;
-    // bf16 io: records, kept states; fp32 io: the decay repeated over K, its gradient and
-    // kda_bwd's own workspace; with a gate, the gradient of the activated decay
-    size_t keep, dg_act, dwide, kda, kda_bytes, E, G, PHI, total;
+    // bf16 io: records, kept states; fp32 io: the fp32 backward's own workspace and, with a gate, the
+    // activated decay; with a gate, the gradient of the activated decay
+    size_t keep, dg_act, act, kda_bytes, E, G, PHI, total;
     Segments seg;
 };
 
@@ -232,8 +232,8 @@ size_t keep_bytes(int K, int V)
                    : (V == 64 ? Keep<128, 64>::BYTES : Keep<128, 128>::BYTES);
 }
 
-// The KDA call that fp32 io takes: one decay per token is KDA with that decay for every key dim.
-kda_fwd_args wide_args(const gdn_args *a, const float *g)
+// fp32 io: the arguments of kda::run_backward (g: the activated decay).
+kda_fwd_args f32_args(const gdn_args *a, const float *g)
 {
     kda_fwd_args w = {};
     w.B = a->B;
@@ -273,11 +273,10 @@ BwdLayout bwd_layout(const gdn_args *a)
         L.PHI = L.G + ends * a->V;
         at = L.PHI + 2 * ends * a->K;
     } else {
-        const kda_fwd_args w = wide_args(a, nullptr);
-        L.dwide = align256(rows * a->K * 4);
-        L.kda = 2 * L.dwide;
+        const kda_fwd_args w = f32_args(a, nullptr);
         L.kda_bytes = kda_bwd_workspace_bytes(&w);
-        at = L.kda + align256(L.kda_bytes);
+        L.act = align256(L.kda_bytes);
+        at = L.act + (a->gate != KDA_GATE_NONE ? align256(rows * 4) : 0);
     }
     L.dg_act = at;
     L.total = at + (a->gate != KDA_GATE_NONE ? align256(rows * 4) : 0);
@@ -337,13 +336,13 @@ kda_status gdn_bwd(const gdn_args *a, const void *d_o, const float *dht, void *w
     float *const dg_act = gated ? (float *)(ws + L.dg_act) : nullptr;
     hipError_t e;
     if (f32) {
-        float *const wide = (float *)ws, *const dwide = (float *)(ws + L.dwide);
-        if (launch_widen_decay(p, a->K, wide, hs) != hipSuccess) return KDA_ERR_HIP;
-        const kda_fwd_args w = wide_args(a, wide);
-        st = kda_bwd(&w, d_o, dht, ws + L.kda, L.kda_bytes, (float *)dq, (float *)dk, (float *)dv,
-                     dwide, (float *)dbeta, dh0, nullptr, nullptr, stream);
+        float *const act = gated ? (float *)(ws + L.act) : nullptr;
+        if (gated && launch_activate_decay(p, act, hs) != hipSuccess) return KDA_ERR_HIP;
+        const kda_fwd_args w = f32_args(a, gated ? act : (const float *)a->g);
+        st = kda::run_backward(&w, true, d_o, dht, ws, L.kda_bytes, (float *)dq, (float *)dk, (float *)dv,
+                               gated ? dg_act : (float *)dg, (float *)dbeta, dh0, nullptr, nullptr, stream);
         if (st != KDA_OK) return st;
-        e = launch_narrow_decay(p, a->K, dwide, gated ? dg_act : (float *)dg, hs);
+        e = hipSuccess;
     } else {
         if (L.f.tt > 0) {
             e = a->K == 64 ? launch_prepare_bwd<64>(p, hs) : launch_prepare_bwd<128>(p, hs);

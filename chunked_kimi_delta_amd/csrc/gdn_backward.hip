@@ -751,40 +751,16 @@ hipError_t launch_gate_backward(const Params &p, bool f32, const float *dg_act, 
 
 // --------------------------------------------------------------------------------- fp32 io
 
-__global__ __launch_bounds__(256) void widen_decay_kernel(Params p, int K, float *wide)
+__global__ __launch_bounds__(256) void activate_decay_kernel(Params p, float *act)
 {
-    const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4, row = i / K;
-    if (row >= p.seq.T_total * p.HV) return;
-    float g = activate_gate(p.pre, ((const float *)p.g)[row], (int)(row % p.HV));
-    // e^-105 is below every fp32 number, and the cumsums of the fp32 kernels stay small
-    if (g < -105.f) g = -105.f;
-    const auto rs = kda::buffer_rsrc(wide + (i - threadIdx.x * 4), 4096);
-    kda::bstore16<0>(rs, threadIdx.x * 16, 0, f32x4{g, g, g, g});
+    const int64_t row = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (row < p.seq.T_total * p.HV) act[row] = activate_gate(p.pre, ((const float *)p.g)[row], (int)(row % p.HV));
 }
 
-__global__ __launch_bounds__(256) void narrow_decay_kernel(Params p, int K, const float *wide,
-                                                           float *dg)
-{
-    const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (row >= kda::seq_eos(p.seq, p.seq.N - 1, 0) * p.HV) return;
-    const int lane = threadIdx.x & 63;
-    float s = wide[row * K + lane];
-    if (K == 128) s += wide[row * K + 64 + lane];
-    s = kda::wave_sum(s);
-    if (lane == 0) dg[row] = s;
-}
-
-hipError_t launch_widen_decay(const Params &p, int K, float *wide, hipStream_t st)
-{
-    const int64_t n = p.seq.T_total * p.HV * K / 4;
-    if (n > 0) widen_decay_kernel<<<dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st>>>(p, K, wide);
-    return hipGetLastError();
-}
-
-hipError_t launch_narrow_decay(const Params &p, int K, const float *wide, float *dg_act, hipStream_t st)
+hipError_t launch_activate_decay(const Params &p, float *act, hipStream_t st)
 {
     const int64_t n = p.seq.T_total * p.HV;
-    if (n > 0) narrow_decay_kernel<<<dim3((unsigned)((n + 3) / 4)), dim3(256), 0, st>>>(p, K, wide, dg_act);
+    if (n > 0) activate_decay_kernel<<<dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st>>>(p, act);
     return hipGetLastError();
 }
 

@@ -379,10 +379,8 @@ hipError_t launch_gate_backward(const Params &p, bool f32, const float *dg_act, 
 // Rows of 8-bit checkpoints (include/act8.h) back in the io type: three tensors, one launch.
 hipError_t launch_unpack3(const int8_t *const data[3], const float *const scale[3], const int64_t rows[3],
                           const int32_t D[3], void *const x[3], bool f32, hipStream_t st);
-// fp32 io: the activated decay repeated over K, and the gradient of that summed over K
-hipError_t launch_widen_decay(const Params &p, int K, float *wide, hipStream_t st);
-hipError_t launch_narrow_decay(const Params &p, int K, const float *wide, float *dg_act,
-                               hipStream_t st);
+// fp32 io: the activated decay [T_total][HV]
+hipError_t launch_activate_decay(const Params &p, float *act, hipStream_t st);
 template <int K, int V> hipError_t launch_state(const Params &p, bool f32, hipStream_t st);
 template <int K, int V> hipError_t launch_recurrent(const StepParams &p, bool f32, hipStream_t st);
 }  // namespace gdn

@@ -284,27 +284,13 @@ kda_status check_bwd(const kda_fwd_args *a, int64_t *T_total, int64_t *n_slots, 
     return KDA_OK;
 }
 
-template <int K, int V>
-hipError_t dispatch_bwd(const BwdParams &b, int io, hipStream_t st)
-{
-    return launch_backward<K, V>(b, io == KDA_BF16, st);
-}
-
 }  // namespace
 
-extern "C" {
+namespace kda {
 
-size_t kda_bwd_workspace_bytes(const kda_fwd_args *a)
-{
-    int64_t tt, ns;
-    BwdLayout L;
-    if (check_bwd(a, &tt, &ns, &L) != KDA_OK) return 0;
-    return L.total;
-}
-
-kda_status kda_bwd(const kda_fwd_args *a, const void *d_o, const float *dht, void *workspace,
-                   size_t ws_bytes, float *dq, float *dk, float *dv, float *dg, float *dbeta,
-                   float *dh0, float *dA_log, float *ddt_bias, void *stream)
+kda_status run_backward(const kda_fwd_args *a, bool scalar, const void *d_o, const float *dht, void *workspace,
+                        size_t ws_bytes, float *dq, float *dk, float *dv, float *dg, float *dbeta,
+                        float *dh0, float *dA_log, float *ddt_bias, void *stream)
 {
     int64_t tt, ns;
     BwdLayout L;
@@ -374,12 +360,32 @@ kda_status kda_bwd(const kda_fwd_args *a, const void *d_o, const float *dht, voi
 
     hipStream_t s = (hipStream_t)stream;
     hipError_t e;
+    const bool bf16 = a->io == KDA_BF16;
     if (a->K == 64)
-        e = a->V == 64 ? dispatch_bwd<64, 64>(b, a->io, s) : dispatch_bwd<64, 128>(b, a->io, s);
+        e = a->V == 64 ? launch_backward<64, 64>(b, bf16, scalar, s) : launch_backward<64, 128>(b, bf16, scalar, s);
     else
-        e = a->V == 64 ? dispatch_bwd<128, 64>(b, a->io, s)
-                       : dispatch_bwd<128, 128>(b, a->io, s);
+        e = a->V == 64 ? launch_backward<128, 64>(b, bf16, scalar, s) : launch_backward<128, 128>(b, bf16, scalar, s);
     return e == hipSuccess ? KDA_OK : KDA_ERR_HIP;
+}
+
+}  // namespace kda
+
+extern "C" {
+
+size_t kda_bwd_workspace_bytes(const kda_fwd_args *a)
+{
+    int64_t tt, ns;
+    BwdLayout L;
+    if (check_bwd(a, &tt, &ns, &L) != KDA_OK) return 0;
+    return L.total;
+}
+
+kda_status kda_bwd(const kda_fwd_args *a, const void *d_o, const float *dht, void *workspace,
+                   size_t ws_bytes, float *dq, float *dk, float *dv, float *dg, float *dbeta,
+                   float *dh0, float *dA_log, float *ddt_bias, void *stream)
+{
+    return run_backward(a, false, d_o, dht, workspace, ws_bytes, dq, dk, dv, dg, dbeta, dh0, dA_log, ddt_bias,
+                        stream);
 }
 
 size_t kda_fwd_workspace_bytes(const kda_fwd_args *a)

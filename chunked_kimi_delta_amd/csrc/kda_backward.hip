@@ -66,9 +66,9 @@ __global__ __launch_bounds__(64 * CHAIN_WAVES) void bwd_chains_kernel(BwdParams 
 // wave-private LDS tile. dKD = A^T dW is one product per tile of the V loop's accumulators;
 // the rest of the chunk's algebra (16 x 16 and 16 x K) is scalar, the pairs of G and Mqk in
 // one pass per key dim.
-template <int K, int V>
+template <int K, int V, bool SCALAR>
 struct alignas(16) LocalShare {
-    float q[16][K + 1], k[16][K + 1], gm[16][K + 1];   // q, k, Gam (cumsum of g)
+    float q[16][K + 1], k[16][K + 1], gm[SCALAR ? 1 : 16][K + 1];   // q, k, Gam (cumsum of g)
     float kd[16][K + 1];                               // KD = k e^Gam
     union alignas(16) {                                // two phases, one region
         struct {                                       // the V loop
@@ -123,12 +123,15 @@ struct BlockOps {
     f32x4 doc, doa, vc, va;                     // dO, v: C-layout (rows 4g+i) and row r
 };
 
-template <int K, int V, typename T>
+// SCALAR: one log decay per token and value head (fp32 [T][HV], no gate): a pair's decay is then a number that
+// its products share, and dg is one sum a token.
+template <int K, int V, typename T, bool SCALAR = false>
 __global__ __launch_bounds__(256) void bwd_local_kernel(BwdParams b)
 {
     const FwdParams &p = b.f;
     constexpr int TPW = BlockOps<K>::TPW, NB = V / 16;
-    __shared__ LocalShare<K, V> sh;
+    __shared__ LocalShare<K, V, SCALAR> sh;
+    __shared__ ScalarDecays dec;
     const int tid = threadIdx.x;
     const int slot = blockIdx.x, j = blockIdx.y, h = j / p.G;
     int s;
@@ -165,9 +168,10 @@ __global__ __launch_bounds__(256) void bwd_local_kernel(BwdParams b)
             const int64_t t = bos + (r < nvalid ? r : nvalid - 1);
             rq[e] = q[(t * p.H + h) * K + d];
             rk[e] = k[(t * p.H + h) * K + d];
-            rg[e] = g[(t * p.HV + j) * K + d];
+            if constexpr (!SCALAR) rg[e] = g[(t * p.HV + j) * K + d];
             rdt[e] = dtp ? dtp[d] : 0.f;
         }
+        if constexpr (SCALAR) dec.load(p, bos, nvalid, j, tid);
         rb = bt[(bos + ((tid & 15) < nvalid ? (tid & 15) : nvalid - 1)) * p.HV + j];
 #pragma unroll
         for (int e = 0; e < NE; ++e) {
@@ -175,9 +179,11 @@ __global__ __launch_bounds__(256) void bwd_local_kernel(BwdParams b)
             const bool ok = r < nvalid;
             sh.q[r][d] = ok ? to_f32(rq[e]) : 0.f;
             sh.k[r][d] = ok ? to_f32(rk[e]) : 0.f;
-            float gv = ok ? to_f32(rg[e]) : 0.f;
-            if (gated && ok) gv = gate_activation(p.pre, gv + rdt[e], aexp);
-            sh.gm[r][d] = gv;
+            if constexpr (!SCALAR) {
+                float gv = ok ? to_f32(rg[e]) : 0.f;
+                if (gated && ok) gv = gate_activation(p.pre, gv + rdt[e], aexp);
+                sh.gm[r][d] = gv;
+            }
         }
         if (tid < 16) {
             float bv = tid < nvalid ? to_f32(rb) : 0.f;
@@ -205,10 +211,14 @@ __global__ __launch_bounds__(256) void bwd_local_kernel(BwdParams b)
         }
         __syncthreads();
     }
-    for (int d = tid; d < K; d += 256) {
-        float acc = 0.f;
-        for (int r = 0; r < 16; ++r) { acc += sh.gm[r][d]; sh.gm[r][d] = acc; }
-        sh.E[d] = __expf(acc);
+    if constexpr (SCALAR) {
+        dec.form(tid);
+    } else {
+        for (int d = tid; d < K; d += 256) {
+            float acc = 0.f;
+            for (int r = 0; r < 16; ++r) { acc += sh.gm[r][d]; sh.gm[r][d] = acc; }
+            sh.E[d] = __expf(acc);
+        }
     }
     // ---- the chunk's inverse X, Gram G and Mqk from its record (the prepare kernel's)
     using WSB = WsF32B<K, V>;
@@ -221,7 +231,7 @@ __global__ __launch_bounds__(256) void bwd_local_kernel(BwdParams b)
     sh.A[i16][j16] = sh.X[i16][j16] * sh.beta[j16];
     for (int idx = tid; idx < 16 * K; idx += 256) {
         const int t = idx / K, d = idx % K;
-        sh.kd[t][d] = sh.k[t][d] * __expf(sh.gm[t][d]);
+        sh.kd[t][d] = sh.k[t][d] * (SCALAR ? dec.head[t] : __expf(sh.gm[SCALAR ? 0 : t][d]));
     }
     __syncthreads();
 
@@ -413,6 +423,41 @@ __global__ __launch_bounds__(256) void bwd_local_kernel(BwdParams b)
     }
     __syncthreads();
 
+    if constexpr (SCALAR) {
+        // dg: a decay crosses token t in the pairs i >= t > j of G and Mqk, in KD and QD of i >= t, in KR
+        // of j < t and in E.
+        const int i = i16, c = j16;
+        const float z = i > c ? sh.T1[i][c] * sh.G[i][c] + sh.dMq[i][c] * sh.Mq[i][c] : 0.f;
+        float from = 0.f, upto = 0.f, whole = 0.f;
+        for (int d = c; d < K; d += 16) {
+            from += sh.dkd[i][d] * sh.kd[i][d] + sc * sh.dqd[i][d] * sh.q[i][d] * dec.head[i];
+            upto += sh.dkr[i][d] * sh.k[i][d] * dec.D[15][i];
+            whole += sh.dE[d];
+        }
+#pragma unroll
+        for (int m = 1; m < 16; m <<= 1) {
+            from += __shfl_xor(from, m);
+            upto += __shfl_xor(upto, m);
+            whole += __shfl_xor(whole, m);
+        }
+        // from here on T1 and dMq with the pairs' decays (and the scale) in them; below the diagonal of A
+        // (no longer needed) the pairs' shares of dg
+        sh.T1[i][c] *= dec.D[i][c];
+        if (i > c) sh.dMq[i][c] *= sc * dec.D[i][c];
+        sh.A[i][c] = z;
+        sh.P[i][c] = c == 0 ? from : c == 1 ? upto : whole * dec.head[15];
+        __syncthreads();
+        if (tid < nvalid) {
+            float acc = sh.P[0][2];
+            for (int t = 0; t < 16; ++t) acc += sh.P[t][1];
+            for (int t = 15; t >= tid; --t) {
+                acc += sh.P[t][0] - sh.P[t][1];
+                for (int u = 0; u < 16; ++u) acc += sh.A[t][u] - sh.A[u][t];
+            }
+            b.dg[(bos + tid) * p.HV + j] = acc;
+        }
+    }
+
     // ---- per key dim d: dk, dq and dGam of the 16 tokens, from the chunk-level gradients
     // (dQD, dKR, dKD) and the pairs (i > j) of G and Mqk, each pair's e^{Gam_i - Gam_j}
     // evaluated once. The P = 256 / K waves-groups of a key dim share the rows i between them
@@ -426,7 +471,7 @@ __global__ __launch_bounds__(256) void bwd_local_kernel(BwdParams b)
         for (int t = 0; t < 16; ++t) {
             kk[t] = sh.k[t][d];
             qq[t] = sh.q[t][d];
-            gg[t] = sh.gm[t][d];
+            gg[t] = SCALAR ? 0.f : sh.gm[SCALAR ? 0 : t][d];
             ak[t] = aqv[t] = ag[t] = 0.f;
         }
         // rows {15,14,1,0}, {13,12,3,2}, {11,10,5,4}, {9,8,7,6}: 30 pairs each (P = 4);
@@ -435,6 +480,19 @@ __global__ __launch_bounds__(256) void bwd_local_kernel(BwdParams b)
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
             if (own4[i] * P / 4 != pp) continue;
+            if constexpr (SCALAR) {
+                const float wd = sh.dMq[i][i] * sc;
+                ak[i] += sh.dkd[i][d] * dec.head[i] + sh.dkr[i][d] * dec.D[15][i] + wd * qq[i];
+                aqv[i] += sc * sh.dqd[i][d] * dec.head[i] + wd * kk[i];
+#pragma unroll
+                for (int jx = 0; jx < i; ++jx) {
+                    const float w1 = sh.T1[i][jx], w2 = sh.dMq[i][jx];
+                    ak[i] += w1 * kk[jx];
+                    aqv[i] += w2 * kk[jx];
+                    ak[jx] += w1 * kk[i] + w2 * qq[i];
+                }
+                continue;
+            }
             const float ei = __expf(gg[i]), eri = __expf(gg[15] - gg[i]);
             const float dkd = sh.dkd[i][d], dkr = sh.dkr[i][d], dqd = sh.dqd[i][d];
             const float wd = sh.dMq[i][i] * sc;            // diagonal of Mqk: q_i k_i
@@ -459,7 +517,7 @@ __global__ __launch_bounds__(256) void bwd_local_kernel(BwdParams b)
         float *dk_out = via_part ? b.part_k : b.dk;
         const int qk_heads = via_part ? p.HV : p.H, qk_head = via_part ? j : h;
 #pragma unroll
-        for (int which = 0; which < 3; ++which) {         // dk, dq, dGam in turn
+        for (int which = 0; which < (SCALAR ? 2 : 3); ++which) {    // dk, dq, dGam in turn
             __syncthreads();
 #pragma unroll
             for (int t = 0; t < 16; ++t)
@@ -483,7 +541,7 @@ __global__ __launch_bounds__(256) void bwd_local_kernel(BwdParams b)
     // ---- dgam = dE E + sum_t dKR KR; dg_tau = sum_{t >= tau} dGam_t + dgam; through the
     // gate (raw g reloaded): dg_raw = dg * slope, and this chunk's share of dA_log, ddt_bias
     float gA = 0.f;
-    for (int d = tid; d < K; d += 256) {
+    for (int d = tid; d < K && !SCALAR; d += 256) {
         float dgam = sh.dE[d] * sh.E[d];
         for (int t = 0; t < 16; ++t) dgam += sh.dkr[t][d] * rec[WSB::KR / 4 + t * K + d];
         float acc = dgam, adt = 0.f;
@@ -614,12 +672,12 @@ __global__ __launch_bounds__(256) void bwd_param_kernel(BwdParams b)
 }  // namespace
 
 template <int K, int V>
-hipError_t launch_backward(const BwdParams &b, bool in_bf16, hipStream_t st)
+hipError_t launch_backward(const BwdParams &b, bool in_bf16, bool scalar, hipStream_t st)
 {
     const FwdParams &p = b.f;
     hipError_t e;
     if (p.seq.T_total > 0 &&
-        (e = launch_prepare_f32<K, V>(p, st, in_bf16, true)) != hipSuccess)
+        (e = launch_prepare_f32<K, V>(p, st, in_bf16, true, scalar)) != hipSuccess)
         return e;
     const int64_t units = (int64_t)p.seq.N * p.HV;
     if (units == 0) return hipSuccess;
@@ -628,7 +686,9 @@ hipError_t launch_backward(const BwdParams &b, bool in_bf16, hipStream_t st)
     if ((e = hipGetLastError()) != hipSuccess) return e;
     if (p.seq.T_total > 0) {
         dim3 grid(p.seq.n_slots, p.HV);
-        if (in_bf16)
+        if (scalar)
+            bwd_local_kernel<K, V, float, true><<<grid, dim3(256), 0, st>>>(b);
+        else if (in_bf16)
             bwd_local_kernel<K, V, uint16_t><<<grid, dim3(256), 0, st>>>(b);
         else
             bwd_local_kernel<K, V, float><<<grid, dim3(256), 0, st>>>(b);
@@ -650,7 +710,7 @@ hipError_t launch_backward(const BwdParams &b, bool in_bf16, hipStream_t st)
 }
 
 #define KDA_INST(K, V) \
-    template hipError_t launch_backward<K, V>(const BwdParams &, bool, hipStream_t);
+    template hipError_t launch_backward<K, V>(const BwdParams &, bool, bool, hipStream_t);
 KDA_INST(64, 64)
 KDA_INST(64, 128)
 KDA_INST(128, 64)

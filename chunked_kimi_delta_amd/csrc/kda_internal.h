@@ -23,6 +23,8 @@
 
 #include <utility>
 
+#include "kda_fwd.h"
+
 namespace kda {
 
 typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8;
@@ -447,6 +449,32 @@ __device__ __forceinline__ float l2norm_factor(float sumsq) {
     return __builtin_amdgcn_rsqf(sumsq + L2NORM_EPS);
 }
 
+// ------------------------------------------------------------------------- scalar decays
+
+// The decays of a 16-token chunk with one log decay a token (the fp32 gradients of the gated delta rule), by 256
+// threads. Each is the exponential of its own tokens' sum, in 64 bits: as a difference of an fp32 cumsum a
+// mild decay behind strong ones would keep only what their sum leaves of its bits.
+struct ScalarDecays {
+    float g[16];                // log decays, rows past the sequence end zero
+    float D[16][17];            // D[i][j] = e^{g_{j+1} + .. + g_i}, i >= j
+    float head[16];             // e^{g_0 + .. + g_i}
+    // A decay below e^-100000 is zero whatever its size; -inf would make later sums NaN.
+    __device__ __forceinline__ void load(const FwdParams &p, int64_t bos, int nvalid, int j, int tid) {
+        if (tid >= 16) return;
+        float x = ((const float *)p.g)[(bos + (tid < nvalid ? tid : nvalid - 1)) * p.HV + j];
+        x = x < -1e5f ? -1e5f : x;
+        g[tid] = tid < nvalid ? x : 0.f;
+    }
+    // behind a barrier, and to be read behind another one
+    __device__ __forceinline__ void form(int tid) {
+        const int i = tid >> 4, j = tid & 15;
+        double s = 0.0;
+        for (int t = j + 1; t <= i; ++t) s += (double)g[t];
+        D[i][j] = i >= j ? expf((float)s) : 0.f;
+        if (j == 0) head[i] = expf((float)(s + (double)g[0]));
+    }
+};
+
 // ----------------------------------------------------------------------------- exact Gram
 
 // The bf16 prepare kernels factor e^{Gam_i - Gam_j} = e^{Gam_i - ref} e^{ref - Gam_j} around a
@@ -665,10 +693,11 @@ namespace kda {
 int current_device_cus();
 template <int K, int V> hipError_t launch_prepare_bf16(const FwdParams &p, hipStream_t st);
 template <int K, int V> hipError_t launch_state_bf16(const FwdParams &p, hipStream_t st);
-// fp32 chunk records from fp32 or (in_bf16) bf16 inputs: WsF32, or WsF32B for the backward
+// fp32 chunk records from fp32 or (in_bf16) bf16 inputs: WsF32, or WsF32B for the backward (scalar: from
+// one log decay per token and value head, fp32 inputs)
 template <int K, int V>
 hipError_t launch_prepare_f32(const FwdParams &p, hipStream_t st, bool in_bf16 = false,
-                              bool for_backward = false);
+                              bool for_backward = false, bool scalar = false);
 template <int K, int V> hipError_t launch_state_f32(const FwdParams &p, hipStream_t st);
 template <int K, int V> hipError_t launch_prepare32_bf16(const FwdParams &p, hipStream_t st);
 template <int K, int V> hipError_t launch_state32_bf16(const FwdParams &p, hipStream_t st);
@@ -676,5 +705,10 @@ template <int K, int V> hipError_t launch_prepare64_bf16(const FwdParams &p, hip
 template <int K, int V> hipError_t launch_state64_bf16(const FwdParams &p, hipStream_t st);
 template <int K, int V> hipError_t launch_recurrent(const FwdParams &p, int io, hipStream_t st);
 template <int K, int V>
-hipError_t launch_backward(const BwdParams &b, bool in_bf16, hipStream_t st);
+hipError_t launch_backward(const BwdParams &b, bool in_bf16, bool scalar, hipStream_t st);
+// kda_bwd; with `scalar` (fp32 io, no gate) for one log decay per token and value head: a->g and dg are
+// fp32 [B, T, HV].
+kda_status run_backward(const kda_fwd_args *a, bool scalar, const void *d_o, const float *dht, void *workspace,
+                        size_t ws_bytes, float *dq, float *dk, float *dv, float *dg, float *dbeta,
+                        float *dh0, float *dA_log, float *ddt_bias, void *stream);
 }  // namespace kda

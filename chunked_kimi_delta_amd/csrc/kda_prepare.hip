@@ -310,14 +310,17 @@ __device__ __forceinline__ void rows_times_a(const float (*A)[20], const float (
     }
 }
 
-template <int K, int V, typename T, bool BWD>
+// SCALAR: g is one log decay per token and value head, fp32 [T][HV] (the gated delta rule's gradients,
+// backward only); every decay is then a number of the chunk (ScalarDecays).
+template <int K, int V, typename T, bool BWD, bool SCALAR = false>
 __global__ __launch_bounds__(256) void prepare_f32_kernel(FwdParams p)
 {
+    static_assert(!SCALAR || BWD, "scalar decays: the backward's records");
     using WS = WsF32<K, V>;
     constexpr int STRIDE = BWD ? WsF32B<K, V>::BYTES : WS::BYTES;
     // rows padded to a multiple of 16 bytes (4 dims at a time in the Gram loop); a padding of
     // 4 floats also puts the 16 rows of one dim in distinct banks
-    __shared__ __attribute__((aligned(16))) float sq[16][K + 4], sk[16][K + 4], sG[16][K + 4];
+    __shared__ __attribute__((aligned(16))) float sq[16][K + 4], sk[16][K + 4], sG[SCALAR ? 1 : 16][K + 4];
     __shared__ float sv[16][V + 1];
     __shared__ float sb[16], sL[16][17], sI[16][17], sT[16][17];
     __shared__ __attribute__((aligned(16))) float sP[16][20];    // 16-byte rows
@@ -339,7 +342,7 @@ __global__ __launch_bounds__(256) void prepare_f32_kernel(FwdParams p)
     const int64_t sqk = (int64_t)p.H * K, sgk = (int64_t)p.HV * K, svv = (int64_t)p.HV * V;
     const auto rs_q = rows_in((const T *)p.q + (bos * p.H + h) * K, nvalid, sqk, K);
     const auto rs_k = rows_in((const T *)p.k + (bos * p.H + h) * K, nvalid, sqk, K);
-    const auto rs_g = rows_in((const T *)p.g + (bos * p.HV + j) * K, nvalid, sgk, K);
+    const auto rs_g = SCALAR ? rs_k : rows_in((const T *)p.g + (bos * p.HV + j) * K, nvalid, sgk, K);
     const auto rs_v = rows_in((const T *)p.v + (bos * p.HV + j) * V, nvalid, svv, V);
     const auto rs_b = rows_in((const T *)p.beta + bos * p.HV + j, nvalid, p.HV, 1);
     T rq[NE], rk[NE], rg[NE], rv[NEV], rb;
@@ -348,8 +351,10 @@ __global__ __launch_bounds__(256) void prepare_f32_kernel(FwdParams p)
         const int idx = tid + 256 * e, rr = idx / K, d = idx % K;
         bload_elem(rs_q, (int)(rr * sqk + d) * SZ, rq[e]);
         bload_elem(rs_k, (int)(rr * sqk + d) * SZ, rk[e]);
-        bload_elem(rs_g, (int)(rr * sgk + d) * SZ, rg[e]);
+        if constexpr (!SCALAR) bload_elem(rs_g, (int)(rr * sgk + d) * SZ, rg[e]);
     }
+    __shared__ ScalarDecays dec;
+    if constexpr (SCALAR) dec.load(p, bos, nvalid, j, tid);
 #pragma unroll
     for (int e = 0; e < NEV; ++e) {
         const int idx = tid + 256 * e, rr = idx / V, d = idx % V;
@@ -373,10 +378,12 @@ __global__ __launch_bounds__(256) void prepare_f32_kernel(FwdParams p)
         const bool ok = rr < nvalid;
         sq[rr][d] = ok ? to_f32(rq[e]) : 0.f;
         sk[rr][d] = ok ? to_f32(rk[e]) : 0.f;
-        float gv = ok ? to_f32(rg[e]) : 0.f;
-        if (gated && ok)
-            gv = gate_activation(p.pre, gv + rdt, aexp);
-        sG[rr][d] = gv;
+        if constexpr (!SCALAR) {
+            float gv = ok ? to_f32(rg[e]) : 0.f;
+            if (gated && ok)
+                gv = gate_activation(p.pre, gv + rdt, aexp);
+            sG[rr][d] = gv;
+        }
     }
 #pragma unroll
     for (int e = 0; e < NEV; ++e) {
@@ -408,9 +415,13 @@ __global__ __launch_bounds__(256) void prepare_f32_kernel(FwdParams p)
         }
         __syncthreads();
     }
-    for (int d = tid; d < K; d += 256) {               // inclusive cumsum per key dim
-        float acc = 0.f;
-        for (int rr = 0; rr < 16; ++rr) { acc += sG[rr][d]; sG[rr][d] = acc; }
+    if constexpr (SCALAR) {
+        dec.form(tid);
+    } else {
+        for (int d = tid; d < K; d += 256) {           // inclusive cumsum per key dim
+            float acc = 0.f;
+            for (int rr = 0; rr < 16; ++rr) { acc += sG[rr][d]; sG[rr][d] = acc; }
+        }
     }
     __syncthreads();
 
@@ -424,9 +435,14 @@ __global__ __launch_bounds__(256) void prepare_f32_kernel(FwdParams p)
     float Lij = 0.f, Mij = 0.f;
 #pragma unroll 2
     for (int d = dlo; d < dlo + K / 2; d += 4) {
-        const float4 ga = *(const float4 *)&sG[pa][d], gb = *(const float4 *)&sG[pb][d];
         const float4 ka = *(const float4 *)&sk[pa][d], kb = *(const float4 *)&sk[pb][d];
         const float4 qa = *(const float4 *)&sq[pa][d];
+        if constexpr (SCALAR) {
+            Lij += ka.x * kb.x; Lij += ka.y * kb.y; Lij += ka.z * kb.z; Lij += ka.w * kb.w;
+            Mij += qa.x * kb.x; Mij += qa.y * kb.y; Mij += qa.z * kb.z; Mij += qa.w * kb.w;
+            continue;
+        }
+        const float4 ga = *(const float4 *)&sG[pa][d], gb = *(const float4 *)&sG[pb][d];
         const float e[4] = {__expf(ga.x - gb.x), __expf(ga.y - gb.y), __expf(ga.z - gb.z),
                             __expf(ga.w - gb.w)};
         const float kd[4] = {kb.x * e[0], kb.y * e[1], kb.z * e[2], kb.w * e[3]};
@@ -444,6 +460,10 @@ __global__ __launch_bounds__(256) void prepare_f32_kernel(FwdParams p)
     if (i > jj) {
         Lij += sT[jj][i];
         Mij += sP[jj][i];
+        if constexpr (SCALAR) {
+            Lij *= dec.D[i][jj];
+            Mij *= dec.D[i][jj];
+        }
     } else if (i == jj) {
         Lij = 0.f;
         Mij = Mdiag;
@@ -472,16 +492,16 @@ __global__ __launch_bounds__(256) void prepare_f32_kernel(FwdParams p)
     float *ws = (float *)(p.ws + ((size_t)j * p.seq.n_slots + slot) * (size_t)STRIDE);
     for (int idx = tid; idx < 16 * K; idx += 256) {   // qd, kr; KD = k e^Gam over q's slot
         const int t = idx / K, d = idx % K;
-        const float e = __expf(sG[t][d]);
+        const float e = SCALAR ? dec.head[t] : __expf(sG[SCALAR ? 0 : t][d]);
         ws[WS::QD / 4 + t * K + d] = p.scale * sq[t][d] * e;
-        ws[WS::KR / 4 + t * K + d] = sk[t][d] * __expf(sG[15][d] - sG[t][d]);
+        ws[WS::KR / 4 + t * K + d] = sk[t][d] * (SCALAR ? dec.D[15][t] : __expf(sG[SCALAR ? 0 : 15][d] - sG[SCALAR ? 0 : t][d]));
         sq[t][d] = sk[t][d] * e;
     }
     __syncthreads();
     rows_times_a<K>(sP, sq, ws + WS::W / 4, tid);        // w = A KD
     rows_times_a<V>(sP, sv, ws + WS::U / 4, tid);        // u = A v
     ws[WS::MQK / 4 + i * 16 + jj] = Mv;
-    for (int d = tid; d < K; d += 256) ws[WS::EG / 4 + d] = __expf(sG[15][d]);
+    for (int d = tid; d < K; d += 256) ws[WS::EG / 4 + d] = SCALAR ? dec.head[15] : __expf(sG[SCALAR ? 0 : 15][d]);
     if (BWD) {                        // the inverse and the Gram, for the local gradients
         ws[WsF32B<K, V>::XM / 4 + i * 16 + jj] = sI[i][jj];
         ws[WsF32B<K, V>::GM / 4 + i * 16 + jj] = i > jj ? Lij : 0.f;
@@ -511,10 +531,12 @@ hipError_t launch_prepare_bf16(const FwdParams &p, hipStream_t st)
 
 template <int K, int V>
 hipError_t launch_prepare_f32(const FwdParams &p, hipStream_t st, bool in_bf16,
-                              bool for_backward)
+                              bool for_backward, bool scalar)
 {
     dim3 grid(p.seq.n_slots, p.HV);
-    if (in_bf16 && for_backward)
+    if (scalar)
+        prepare_f32_kernel<K, V, float, true, true><<<grid, dim3(256), 0, st>>>(p);
+    else if (in_bf16 && for_backward)
         prepare_f32_kernel<K, V, uint16_t, true><<<grid, dim3(256), 0, st>>>(p);
     else if (in_bf16)
         prepare_f32_kernel<K, V, uint16_t, false><<<grid, dim3(256), 0, st>>>(p);
@@ -527,7 +549,7 @@ hipError_t launch_prepare_f32(const FwdParams &p, hipStream_t st, bool in_bf16,
 
 #define KDA_INST(K, V)                                                               \
     template hipError_t launch_prepare_bf16<K, V>(const FwdParams &, hipStream_t);  \
-    template hipError_t launch_prepare_f32<K, V>(const FwdParams &, hipStream_t, bool, bool);
+    template hipError_t launch_prepare_f32<K, V>(const FwdParams &, hipStream_t, bool, bool, bool);
 KDA_INST(64, 64)
 KDA_INST(64, 128)
 KDA_INST(128, 64)

@@ -1,0 +1,50 @@
+"""fp32 gradients of the gated delta rule on the inputs that are hardest for them, against autograd through
+the fp64 token recurrence: decays of any strength next to mild ones, long and ragged sequences. The bar is the
+fp32 one of the other gradient tests, 2^-16 relative L2."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+import chunked_kimi_delta_amd as kda
+from gdn_cases import make, to
+from oracle.gdn import gdn_gradients
+from test_gpu_gdn_backward import LEAVES, OUTS, compare, cotangents
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+FP = torch.float32
+
+
+def check(a):
+    d_o, dh = cotangents(a)
+    got = dict(zip(OUTS, kda.gdn_bwd(**to(a, DEV), d_o=d_o.to(DEV), dht=dh.to(DEV),
+                                     want_dh0="initial_state" in a)))
+    leaves = {n: a[n] for n in LEAVES if a.get(n) is not None}
+    ref = gdn_gradients(leaves, d_o, dh, **{n: x for n, x in a.items() if n not in LEAVES})
+    # fp32 has its 24 bits from 2^-126 up: what 64 bits hold below (e^-100, e^-600) is not compared
+    normal = lambda d: {n: torch.where(x.abs() < 2.0 ** -126, 0.0, x) for n, x in d.items() if x is not None}
+    compare(normal(got), normal(ref), FP)
+
+
+@pytest.mark.parametrize("K,V", [(64, 64), (128, 128)])
+@pytest.mark.parametrize("kind", ["mixed", "none", "bursts", "clears"])
+def test_decays(kind, K, V):
+    a = make(T=150, H=2, K=K, V=V, h0=True, seed=3, dtype=FP)
+    g = a["g"]
+    if kind == "mixed":           # one huge decay, then slow ones
+        g[:, 5] = -3000.0
+    elif kind == "bursts":          # some strong ones, then slow ones among the same few tokens
+        for t in range(0, 150, 16):
+            g[:, t:t + 6] = -100.0
+    elif kind == "clears":
+        g[:, 2::37] = -torch.inf
+    else:
+        g.zero_()
+    check(a)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(T=1030, G=1, K=128, V=128), dict(lens=[900, 0, 64, 600, 1], G=2, K=64, V=64, raw=True, gate="bounded")])
+def test_long(kw):
+    check(make(H=1, h0=True, dtype=FP, **kw))
