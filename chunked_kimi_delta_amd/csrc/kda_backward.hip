@@ -171,7 +171,9 @@ __global__ __launch_bounds__(256) void bwd_local_kernel(BwdParams b)
             if constexpr (!SCALAR) rg[e] = g[(t * p.HV + j) * K + d];
             rdt[e] = dtp ? dtp[d] : 0.f;
         }
-        if constexpr (SCALAR) dec.load(p, bos, nvalid, j, tid);
+        float rsg = 0.f;
+        if constexpr (SCALAR)
+            rsg = ((const float *)p.g)[(bos + ((tid & 15) < nvalid ? (tid & 15) : nvalid - 1)) * p.HV + j];
         rb = bt[(bos + ((tid & 15) < nvalid ? (tid & 15) : nvalid - 1)) * p.HV + j];
 #pragma unroll
         for (int e = 0; e < NE; ++e) {
@@ -189,6 +191,7 @@ __global__ __launch_bounds__(256) void bwd_local_kernel(BwdParams b)
             float bv = tid < nvalid ? to_f32(rb) : 0.f;
             if (p.pre.beta_sigmoid && tid < nvalid) bv = sigmoid_f(bv);
             sh.beta[tid] = bv;
+            if constexpr (SCALAR) dec.put(tid, nvalid, rsg);
             sh.dbeta[tid] = 0.f;
         }
     }

@@ -459,9 +459,7 @@ struct ScalarDecays {
     float D[16][17];            // D[i][j] = e^{g_{j+1} + .. + g_i}, i >= j
     float head[16];             // e^{g_0 + .. + g_i}
     // A decay below e^-100000 is zero whatever its size; -inf would make later sums NaN.
-    __device__ __forceinline__ void load(const FwdParams &p, int64_t bos, int nvalid, int j, int tid) {
-        if (tid >= 16) return;
-        float x = ((const float *)p.g)[(bos + (tid < nvalid ? tid : nvalid - 1)) * p.HV + j];
+    __device__ __forceinline__ void put(int tid, int nvalid, float x) {     // threads 0 .. 15: their row's
         x = x < -1e5f ? -1e5f : x;
         g[tid] = tid < nvalid ? x : 0.f;
     }

@@ -354,7 +354,9 @@ __global__ __launch_bounds__(256) void prepare_f32_kernel(FwdParams p)
         if constexpr (!SCALAR) bload_elem(rs_g, (int)(rr * sgk + d) * SZ, rg[e]);
     }
     __shared__ ScalarDecays dec;
-    if constexpr (SCALAR) dec.load(p, bos, nvalid, j, tid);
+    float rsg = 0.f;
+    if constexpr (SCALAR)
+        bload_elem(rows_in((const float *)p.g + bos * p.HV + j, nvalid, p.HV, 1), (tid & 15) * p.HV * 4, rsg);
 #pragma unroll
     for (int e = 0; e < NEV; ++e) {
         const int idx = tid + 256 * e, rr = idx / V, d = idx % V;
@@ -394,6 +396,7 @@ __global__ __launch_bounds__(256) void prepare_f32_kernel(FwdParams p)
         float b = tid < nvalid ? to_f32(rb) : 0.f;
         if (p.pre.beta_sigmoid && tid < nvalid) b = sigmoid_f(b);
         sb[tid] = b;
+        if constexpr (SCALAR) dec.put(tid, nvalid, rsg);
     }
     __syncthreads();
     if (p.pre.qk_l2norm) {
