@@ -427,8 +427,9 @@ __global__ __launch_bounds__(256) void bwd_local_kernel(BwdParams b)
     __syncthreads();
 
     if constexpr (SCALAR) {
-        // dg: a decay crosses token t in the pairs i >= t > j of G and Mqk, in KD and QD of i >= t, in KR
-        // of j < t and in E.
+        // dg_t: what a decay over t is part of, the pairs i >= t > j of G and Mqk, KD and QD of i >= t, KR of
+        // j < t and E. (As suffix sums of what each token gains and loses the other pairs would cancel
+        // only to rounding, which is all that is left of dg where t's decay is strong.)
         const int i = i16, c = j16;
         const float z = i > c ? sh.T1[i][c] * sh.G[i][c] + sh.dMq[i][c] * sh.Mq[i][c] : 0.f;
         float from = 0.f, upto = 0.f, whole = 0.f;
@@ -452,10 +453,12 @@ __global__ __launch_bounds__(256) void bwd_local_kernel(BwdParams b)
         __syncthreads();
         if (tid < nvalid) {
             float acc = sh.P[0][2];
-            for (int t = 0; t < 16; ++t) acc += sh.P[t][1];
-            for (int t = 15; t >= tid; --t) {
-                acc += sh.P[t][0] - sh.P[t][1];
-                for (int u = 0; u < 16; ++u) acc += sh.A[t][u] - sh.A[u][t];
+            for (int t = 0; t < 16; ++t) {
+                acc += t >= tid ? sh.P[t][0] : sh.P[t][1];
+                float row = 0.f;
+#pragma unroll
+                for (int u = 0; u < 15; ++u) row += u < tid ? sh.A[t][u] : 0.f;
+                acc += t >= tid ? row : 0.f;
             }
             b.dg[(bos + tid) * p.HV + j] = acc;
         }

@@ -1,6 +1,6 @@
 """fp32 gradients of the gated delta rule on the inputs that are hardest for them, against autograd through
-the fp64 token recurrence: decays of any strength next to mild ones, long and ragged sequences. The bar is the
-fp32 one of the other gradient tests, 2^-16 relative L2."""
+the fp64 token recurrence: decays of any strength next to mild ones, cleared states, long and ragged sequences.
+The bar is the fp32 one of the other gradient tests, 2^-16 relative L2."""
 from __future__ import annotations
 
 import pytest
@@ -28,11 +28,13 @@ def check(a):
 
 
 @pytest.mark.parametrize("K,V", [(64, 64), (128, 128)])
-@pytest.mark.parametrize("kind", ["mixed", "none", "bursts", "clears"])
+@pytest.mark.parametrize("kind", ["strong", "mixed", "none", "bursts", "clears"])
 def test_decays(kind, K, V):
     a = make(T=150, H=2, K=K, V=V, h0=True, seed=3, dtype=FP)
     g = a["g"]
-    if kind == "mixed":           # one huge decay, then slow ones
+    if kind == "strong":
+        g.mul_(0).sub_(40.0)
+    elif kind == "mixed":           # one huge decay, then slow ones
         g[:, 5] = -3000.0
     elif kind == "bursts":          # some strong ones, then slow ones among the same few tokens
         for t in range(0, 150, 16):
@@ -42,6 +44,19 @@ def test_decays(kind, K, V):
     else:
         g.zero_()
     check(a)
+
+
+def test_a_cleared_state_passes_no_gradient_at_all():
+    # at g = -inf the state starts anew: nothing before it sees what follows, in dg either
+    a = make(T=100, H=1, K=64, V=64, dtype=FP, h0=True)
+    a["g"][:, 70] = -torch.inf
+    d_o, dh = cotangents(a)
+    d_o[:, :70] = 0
+    out = dict(zip(OUTS, kda.gdn_bwd(**to(a, DEV), d_o=d_o.to(DEV), dht=dh.to(DEV))))
+    for n in ("q", "k", "v", "g", "beta"):
+        assert (out[n][:, :70] == 0).all(), n
+    assert (out["g"][:, 70] == 0).all() and (out["initial_state"] == 0).all()
+    compare(out, gdn_gradients({n: a[n] for n in LEAVES if n in a}, d_o, dh), FP)
 
 
 @pytest.mark.parametrize("kw", [
