@@ -476,7 +476,23 @@ __global__ __launch_bounds__(256) void prepare_f32_kernel(FwdParams p)
     sL[i][jj] = Lv;                   // P = L
     sI[i][jj] = (i == jj ? 1.f : 0.f) - Lv;
     __syncthreads();
-    for (int it = 0; it < 3; ++it) {  // P <- P^2 ; INV <- INV + INV P
+    if constexpr (SCALAR) {
+        // Forward substitution, a column a thread: backward stable, where the powers of L grow far beyond the
+        // inverse for keys that resemble each other and lose digits (1e-4 of gradients at 16 such keys).
+        if (tid < 16) {
+            float x[16];
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                float acc = r == tid ? 1.f : 0.f;
+#pragma unroll
+                for (int m = 0; m < r; ++m) acc -= sL[r][m] * x[m];
+                x[r] = acc;
+                sI[r][tid] = acc;
+            }
+        }
+        __syncthreads();
+    }
+    for (int it = 0; it < 3 && !SCALAR; ++it) {  // P <- P^2 ; INV <- INV + INV P
         float acc = 0.f;
         for (int m = 0; m < 16; ++m) acc += sL[i][m] * sL[m][jj];
         __syncthreads();

@@ -1,6 +1,8 @@
 """fp32 gradients of the gated delta rule on the inputs that are hardest for them, against autograd through
-the fp64 token recurrence: decays of any strength next to mild ones, cleared states, long and ragged sequences.
-The bar is the fp32 one of the other gradient tests, 2^-16 relative L2."""
+the fp64 token recurrence: decays of any strength next to mild ones, keys that resemble each other (whose
+powers of L grow while the inverse stays of size one), cleared states, long and ragged sequences. The bar is
+the fp32 one of the other gradient tests, 2^-16 relative L2: fp32 sums behind each other, and inverses formed
+by substitution, which lose no digits to the powers of L."""
 from __future__ import annotations
 
 import pytest
@@ -44,6 +46,43 @@ def test_decays(kind, K, V):
     else:
         g.zero_()
     check(a)
+
+
+def decayed_states(a, d_o, dh):
+    """By token and head in fp64: the norms of the state behind its decay and of the loss's gradient by that state."""
+    q, k, v, g, beta = (a[n][0].double() for n in ("q", "k", "v", "g", "beta"))
+    S, bumps, norms, loss = torch.zeros(dh.shape[1:], dtype=torch.float64), [], [], 0.0
+    for t in range(len(q)):
+        bumps.append(torch.zeros_like(S, requires_grad=True))
+        S = torch.exp(g[t])[:, None, None] * S + bumps[-1]
+        norms.append(S.detach().flatten(1).norm(dim=1))
+        r = v[t] - (S * k[t][:, :, None]).sum(1)
+        S = S + (beta[t][:, None] * k[t])[:, :, None] * r[:, None, :]
+        loss = loss + (k.shape[-1] ** -0.5 * (S * q[t][:, :, None]).sum(1) * d_o[0, t].double()).sum()
+    grads = torch.autograd.grad(loss + (S * dh[0].double()).sum(), bumps)
+    return torch.stack(norms), torch.stack([x.flatten(1).norm(dim=1) for x in grads])
+
+
+@pytest.mark.parametrize("spread", [0.0, 0.02, 0.1])
+def test_keys_that_resemble_each_other(spread):
+    a = make(T=130, H=2, K=64, V=64, seed=4, dtype=FP)
+    gen = torch.Generator().manual_seed(11)
+    k = a["k"][:, :1] + spread * a["k"]
+    a["k"] = k / k.norm(dim=-1, keepdim=True)
+    a["beta"] = 0.9 + 0.1 * torch.rand(a["beta"].shape, generator=gen)
+    a["g"] = torch.full_like(a["g"], -0.005)
+    d_o, dh = cotangents(a)
+    got = dict(zip(OUTS, kda.gdn_bwd(**to(a, DEV), d_o=d_o.to(DEV), dht=dh.to(DEV), want_dh0=False)))
+    ref = gdn_gradients({n: a[n] for n in LEAVES if n in a}, d_o, dh)
+    # dg_t = <S, dS> of the state behind the decay and its gradient. With errors dS' and S' of 2^-16 each it is off
+    # by |<S', dS> + <S, dS'>| <= 2 x 2^-16 |S| |dS|. Where all keys are one, dg is some millionths of |S| |dS|
+    # (each write takes back what the decay left, so the gradient hardly meets the state), and plain fp32 steps
+    # of the recurrence give 1.2e-4 relative to it; there that bound alone is held.
+    S, dS = decayed_states(a, d_o, dh)
+    assert ((got["g"][0].double().cpu() - ref["g"][0]).abs() <= 2.0 ** -15 * S * dS).all()
+    if spread == 0.0:
+        del ref["g"]
+    compare(got, ref, FP)
 
 
 def test_a_cleared_state_passes_no_gradient_at_all():
