@@ -19,10 +19,10 @@
 // Launches: the chunk records (gdn_prepare.hip), both passes over the chunks (the forward one for
 // S and e, the reverse one for dS' and dR; they are independent, one launch), the chunks' tokens.
 // The passes carry two bf16 parts of every operand as the forward does (dh0 is an fp32 result).
-// What they leave for the chunks is scaled fp16 (2^-12 a rounding, against the 2^-8 of the bf16
+// What they leave for the chunks is scaled fp16 (2^-11 a rounding, against the 2^-8 of the bf16
 // gradients that it enters; bf16 there cost up to 5e-3 of dg, whose terms cancel), multiplied with
-// dO as fp16 (exact: a bf16 value scaled by a power of two); the 64 x 64 matrices take two bf16
-// parts against the stored q and k.
+// dO as fp16 (bf16 values scaled by a power of two a token: exact down to 2^-28 of the token's largest); the
+// 64 x 64 matrices take two bf16 parts against the stored q and k.
 //
 // Measured, 16 heads x 4096 tokens, K = V = 128: records 18 us, segments' ends 62, their joining 16, both
 // passes 62, tokens 78 (227 for the call; without segments and with four 64 x 64 matrices 519). The passes are
@@ -90,11 +90,9 @@ __device__ __forceinline__ void reverse_chain(const BwdParams &b, int s, int j, 
     for (int c = c1 - 1; c >= c0; --c) {
         uint8_t *const buf = lds + (c1 - 1 - c) % BUFS * L::BYTES;
         if constexpr (KEPT) {
-            const float x = largest(S), y = largest(D);
-            if (lane == 0) {
-                mx->state[c & 1][wave] = x;
-                mx->rows[c & 1][wave] = y;
-            }
+            const float x = largest(S);
+            if (lane == 0) mx->state[c & 1][wave] = x;
+            mx->rows[c & 1][wave][scale_token(grp, r)] = largest_of_tokens(D, r);
         }
         kda::vm_drain();
         __syncthreads();
@@ -102,8 +100,8 @@ __device__ __forceinline__ void reverse_chain(const BwdParams &b, int s, int j, 
         if constexpr (KEPT) {
         keep_state<KP>(S, mx->scale(mx->state[c & 1]), kept(c) + KP::DS, (float *)(kept(c) + KP::SCALE) + 1, col0 + r, grp);
         if (c < c1 - 1)
-            keep_rows<KP>(D, mx->scale(mx->rows[c & 1]), kept(c + 1) + KP::DR, (float *)(kept(c + 1) + KP::SCALE) + 3,
-                      col0 + r, grp);
+            keep_rows<KP>(D, mx->rows[c & 1], kept(c + 1) + KP::DR, (float *)(kept(c + 1) + KP::SCALE) + KP::SR,
+                          col0 + r, grp, r);
         }
         const uint8_t *const rec = buf + L::REC - R::REV;
         const float *const ra = (const float *)(rec + R::RA), *const rb = (const float *)(rec + R::RB),
@@ -175,11 +173,10 @@ __device__ __forceinline__ void reverse_chain(const BwdParams &b, int s, int j, 
         }
     }
     if (KEPT && c0 < c1) {
-        const float y = largest(D);
-        if (lane == 0) mx->rows[(c0 - 1) & 1][wave] = y;
+        mx->rows[(c0 - 1) & 1][wave][scale_token(grp, r)] = largest_of_tokens(D, r);
         __syncthreads();
-        keep_rows<KP>(D, mx->scale(mx->rows[(c0 - 1) & 1]), kept(c0) + KP::DR, (float *)(kept(c0) + KP::SCALE) + 3,
-                  col0 + r, grp);
+        keep_rows<KP>(D, mx->rows[(c0 - 1) & 1], kept(c0) + KP::DR, (float *)(kept(c0) + KP::SCALE) + KP::SR,
+                      col0 + r, grp, r);
     }
     if (end) {
 #pragma unroll
@@ -277,9 +274,20 @@ struct LocalScalars {
     float diag[64];                         // of U
     float cross[64];                        // sum_{i >= t > j} beta_j U_ij within t's own tile
     float qs[ND][64], ks[ND][64], kt[ND][64];   // per 16 key dims: q.dQ[S part], k.dK[S part], k.T
-    float sd[NW], most[NW];                 // per wave: <S, dS'>, the largest |dO|
+    float sd[NW];                           // per wave: <S, dS'>
+    float so[64];                           // what undoes the scale of a token's dO
     float dot[2][ND][64];                   // per 16 key dims: q.dq, k.dk (L2 norm)
 };
+
+// The largest of 8 or 16 neighbouring lanes' values (every one gets it).
+template <int N>
+__device__ __forceinline__ uint32_t row_max(uint32_t u) {
+    u = max(u, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)u, 0xb1, 0xf, 0xf, false));    // quad_perm 1,0,3,2
+    u = max(u, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)u, 0x4e, 0xf, 0xf, false));    // quad_perm 2,3,0,1
+    u = max(u, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)u, 0x141, 0xf, 0xf, false));   // row_half_mirror
+    if (N == 16) u = max(u, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)u, 0x140, 0xf, 0xf, false));  // row_mirror
+    return u;
+}
 
 // Within 16 lanes: the sum of the lanes before this one, and of this one and those behind it.
 __device__ __forceinline__ float row_shift(float x) {      // the value of the lane before, or zero
@@ -387,33 +395,23 @@ __global__ __launch_bounds__(K * 8) void local_kernel(BwdParams b)
         asm volatile("s_waitcnt vmcnt(%0)" :: "n"(LATE) : "memory");
         __syncthreads();
         const float *const inv = (const float *)(lds + L::INV);
-        const float fs = inv[0], fds = inv[1], fe = inv[2], fdr = inv[3];
+        const float fs = inv[0], fds = inv[1];
+        const float *const fe = inv + KP::SE, *const fdr = inv + KP::SR, *const so = sc.so;
         const float whi = ghi[63], wlo = glo[63];
-        // dO as fp16, in place
-        constexpr int NP = (64 * V / 8 + NTH - 1) / NTH;
-        uint4 ob[NP];
-        float most = 0.f;
+        // dO as fp16, in place: a thread a 16-byte piece, the V / 8 threads of a token side by side
 #pragma unroll
-        for (int q = 0; q < NP; ++q) {
-            const int at = (q * NTH + tid) * 16;
-            ob[q] = at < L::MV ? *(const uint4 *)(lds + L::DO + at) : make_uint4(0, 0, 0, 0);
+        for (int q = 0; q < (64 * V / 8 + NTH - 1) / NTH; ++q) {
+            const int n = q * NTH + tid;
+            if (n >= 64 * V / 8) break;             // (whole waves)
+            uint8_t *const piece = lds + L::DO + n * 16;
+            const uint4 ob = *(const uint4 *)piece;
             f32x4 x, y;
-            kda::unpack_bf16x4(make_uint2(ob[q].x, ob[q].y), (float *)&x);
-            kda::unpack_bf16x4(make_uint2(ob[q].z, ob[q].w), (float *)&y);
-            most = max_abs(y, max_abs(x, most));
-        }
-        most = wave_max(most);
-        if (lane == 0) sc.most[wave] = most;
-        __syncthreads();
-        const Scale so = Maxima<NW>::scale(sc.most);
-#pragma unroll
-        for (int q = 0; q < NP; ++q) {
-            const int at = (q * NTH + tid) * 16;
-            f32x4 x, y;
-            kda::unpack_bf16x4(make_uint2(ob[q].x, ob[q].y), (float *)&x);
-            kda::unpack_bf16x4(make_uint2(ob[q].z, ob[q].w), (float *)&y);
-            const uint2 a = half4(x, so.f), c = half4(y, so.f);
-            if (at < L::MV) *(uint4 *)(lds + L::DO + at) = make_uint4(a.x, a.y, c.x, c.y);
+            kda::unpack_bf16x4(make_uint2(ob.x, ob.y), (float *)&x);
+            kda::unpack_bf16x4(make_uint2(ob.z, ob.w), (float *)&y);
+            const Scale f = scale_for(__uint_as_float(row_max<V / 8>(__float_as_uint(max_abs(y, max_abs(x, 0.f))))));
+            const uint2 a = half4(x, f.f), c = half4(y, f.f);
+            *(uint4 *)piece = make_uint4(a.x, a.y, c.x, c.y);
+            if (n % (V / 8) == 0) sc.so[n / (V / 8)] = f.inv;
         }
         __syncthreads();
 
@@ -444,7 +442,7 @@ __global__ __launch_bounds__(K * 8) void local_kernel(BwdParams b)
             }
             __builtin_amdgcn_sched_barrier(0);
             const int jj = 16 * tj + r;
-            const float bj = beta[jj], rkj = rk[jj], f1 = so.inv * fe * p.scale, f2 = -fdr * fe;
+            const float bj = beta[jj], rkj = rk[jj], fej = fe[jj], fej1 = fej * p.scale;
             float col = 0.f;
             f32x4 bu;
 #pragma unroll
@@ -453,8 +451,8 @@ __global__ __launch_bounds__(K * 8) void local_kernel(BwdParams b)
                 const float d = i >= jj && i < nv
                                     ? __builtin_amdgcn_exp2f((ghi[i] - ghi[jj]) + (glo[i] - glo[jj]))
                                     : 0.f;
-                const float y1 = d != 0.f ? x1[e] * d * f1 : 0.f;
-                const float y2 = d != 0.f && i > jj ? x2[e] * d * f2 : 0.f;
+                const float y1 = d != 0.f ? x1[e] * so[i] * d * fej1 : 0.f;
+                const float y2 = d != 0.f && i > jj ? x2[e] * fdr[i] * d * -fej : 0.f;
                 const float uu = rkj * (y1 * rq[i] * qk[e] + y2 * rk[i] * kk[e]);
                 if (i == jj) sc.diag[i] = uu;
                 col += i > jj ? uu : 0.f;
@@ -515,9 +513,9 @@ __global__ __launch_bounds__(K * 8) void local_kernel(BwdParams b)
             const bool live = i < nv;
             const float head = __builtin_amdgcn_exp2f(ghi[i] + glo[i]);
             const float tail = __builtin_amdgcn_exp2f((whi - ghi[i]) + (wlo - glo[i]));
-            const f32x4 x = xs[u] * (live ? fs * so.inv * p.scale * head * rq[i] : 0.f),
-                        y = ys[u] * (live ? -fs * fdr * head * rk[i] : 0.f),
-                        z = zs[u] * (live ? fds * fe * tail * rk[i] : 0.f);
+            const f32x4 x = xs[u] * so[i] * (live ? fs * p.scale * head * rq[i] : 0.f),
+                        y = ys[u] * fdr[i] * (live ? -fs * head * rk[i] : 0.f),
+                        z = zs[u] * fe[i] * (live ? fds * tail * rk[i] : 0.f);
             const f32x4 qr = row_of(L::Q, t), kr = row_of(L::KM, t);
             const float qs = sum_groups(dot4(qr, x)), ks = sum_groups(dot4(kr, y)), kt = sum_groups(dot4(kr, z));
             if (grp == 0) {
@@ -534,7 +532,7 @@ __global__ __launch_bounds__(K * 8) void local_kernel(BwdParams b)
             const int job = q * NW + wave, t = job & 3, c0 = 16 * (job >> 2);
             const s16x4 x = lds_tr(lds + L::DR + KP::row_at(c0 + 4 * grp + (r >> 2), 16 * t + 4 * (r & 3)));
             const kda::f16x4 y = __builtin_bit_cast(kda::f16x4, x);
-            const f32x4 z = f32x4{(float)y[0], (float)y[1], (float)y[2], (float)y[3]} * fdr;
+            const f32x4 z = f32x4{(float)y[0], (float)y[1], (float)y[2], (float)y[3]} * fdr[16 * t + r];
             if (16 * t + r < nv)
                 *(uint2 *)(b.dv + ((bos + 16 * t + r) * p.HV + j) * V + c0 + 4 * grp) =
                     __builtin_bit_cast(uint2, kda::to_bf16x4(z));

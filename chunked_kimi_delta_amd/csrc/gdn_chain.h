@@ -16,6 +16,8 @@
 // without segments from 205 to 196 us; interleaving the two kinds of instructions by hand 209.
 #pragma once
 
+#include <type_traits>
+
 #include "gdn_internal.h"
 
 namespace gdn {
@@ -46,12 +48,12 @@ __device__ __forceinline__ int state_row(int t, int i, int grp) {
     return 32 * (t / 2) + 8 * grp + 4 * (t % 2) + i;
 }
 
-// The scales of what a pass keeps: every wave leaves the largest value of its columns in LDS before
-// the barrier that each chunk has anyway, and behind it all take the largest of those. Two sets in
-// turn, as a wave may be one barrier ahead.
+// The scales of what a pass keeps: every wave leaves the largest value of its columns (of a state, and of each
+// token of e or dR) in LDS before the barrier that each chunk has anyway, and behind it all take the largest
+// of those. Two sets in turn, as a wave may be one barrier ahead.
 template <int NW>
 struct Maxima {
-    float state[2][NW], rows[2][NW];
+    float state[2][NW], rows[2][NW][64];
     static __device__ __forceinline__ Scale scale(const float (&m)[NW]) {
         uint32_t x = __float_as_uint(m[0]);
 #pragma unroll
@@ -70,6 +72,32 @@ __device__ __forceinline__ float largest(const f32x4 (&x)[N]) {
     return wave_max(__uint_as_float(m));
 }
 
+// The token whose maximum and scale a lane holds: those of element i of tile t are in lane 4 t + i of the 16
+// that share its tokens.
+__device__ __forceinline__ int scale_token(int grp, int r) { return 16 * (r >> 2) + 4 * grp + (r & 3); }
+
+// The largest magnitude of each token over the wave's 16 columns, in scale_token order: halves of the 16 values
+// are exchanged between lanes of a 16-lane row, then quarters, and so on.
+__device__ __forceinline__ float largest_of_tokens(const f32x4 (&x)[4], int r)
+{
+    uint32_t v[16];
+#pragma unroll
+    for (int n = 0; n < 16; ++n) v[n] = __float_as_uint(x[n / 4][n % 4]) & 0x7fffffffu;    // NaN counts
+    auto halve = [&](int bit, auto exchange) {
+#pragma unroll
+        for (int n = 0; n < 8; ++n) {
+            if (n >= bit) break;
+            const uint32_t keep = r & bit ? v[n + bit] : v[n], send = r & bit ? v[n] : v[n + bit];
+            v[n] = max(keep, exchange(send));
+        }
+    };
+    halve(8, [](uint32_t y) { return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)y, 0x128, 0xf, 0xf, false); });  // row_ror:8
+    halve(4, [](uint32_t y) { return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)y, 0x141, 0xf, 0xf, false); });  // row_half_mirror
+    halve(2, [](uint32_t y) { return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)y, 0x4e, 0xf, 0xf, false); });   // quad_perm 2,3,0,1
+    halve(1, [](uint32_t y) { return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)y, 0xb1, 0xf, 0xf, false); });   // quad_perm 1,0,3,2
+    return __uint_as_float(v[0]);
+}
+
 // A wave's columns of the state, or of a [64 tokens][V] matrix in C-layout, to the workspace (`col`: this
 // lane's column).
 template <class KP, int NT>
@@ -83,14 +111,31 @@ __device__ __forceinline__ void keep_state(const f32x4 (&S)[NT], Scale f, uint8_
     if (threadIdx.x == 0) *inv = f.inv;
 }
 
-template <class KP>
-__device__ __forceinline__ void keep_rows(const f32x4 (&E)[4], Scale f, uint8_t *base, float *inv, int col, int grp)
+// Each token has a scale of its own: betas, values or gradients of o of the tokens of a chunk may differ by any
+// factor, and so may their e and dR (one scale a chunk cost less, 124 against 131 us for the gradients of 16 heads x
+// 4096 tokens at K = V = 64, 214 against 216 us at 128, and lost the rows 2^-40 below the largest).
+template <class KP, int NW>
+__device__ __forceinline__ void keep_rows(const f32x4 (&E)[4], const float (&most)[NW][64], uint8_t *base, float *inv,
+                                          int col, int grp, int r)
 {
-    const auto rs = kda::buffer_rsrc(base, KP::BYTES);
+    const int tok = scale_token(grp, r);
+    uint32_t x = __float_as_uint(most[0][tok]);
 #pragma unroll
-    for (int t = 0; t < 4; ++t)
-        kda::bstore8<0>(rs, KP::row_at(col, 16 * t + 4 * grp), 0, half4(E[t], f.f));
-    if (threadIdx.x == 0) *inv = f.inv;
+    for (int w = 1; w < NW; ++w) x = max(x, __float_as_uint(most[w][tok]));
+    const Scale f = scale_for(__uint_as_float(x));
+    const auto rs = kda::buffer_rsrc(base, KP::BYTES);
+    auto put = [&](auto tile) {
+        constexpr int t = decltype(tile)::value;
+        const f32x4 s = {kda::row_bcast<4 * t>(f.f), kda::row_bcast<4 * t + 1>(f.f), kda::row_bcast<4 * t + 2>(f.f),
+                         kda::row_bcast<4 * t + 3>(f.f)};
+        kda::bstore8<0>(rs, KP::row_at(col, 16 * t + 4 * grp), 0,
+                        __builtin_bit_cast(uint2, kda::to_f16x4(E[t] * s)));
+    };
+    put(std::integral_constant<int, 0>());
+    put(std::integral_constant<int, 1>());
+    put(std::integral_constant<int, 2>());
+    put(std::integral_constant<int, 3>());
+    if (threadIdx.x < 64) inv[tok] = f.inv;
 }
 
 // One segment: its sequence, its place in it, and its chunks [c0, c1).
@@ -182,11 +227,9 @@ __device__ __forceinline__ void forward_chain(const Params &p, int s, int j, int
         const int64_t t0 = bos + (int64_t)CT * c;
         const int nv = (int)(eos - t0 < CT ? eos - t0 : CT);
         if constexpr (M == KEEP) {
-            const float a = largest(S), b = largest(E);
-            if (lane == 0) {
-                mx->state[c & 1][wave] = a;
-                mx->rows[c & 1][wave] = b;
-            }
+            const float a = largest(S);
+            if (lane == 0) mx->state[c & 1][wave] = a;
+            mx->rows[c & 1][wave][scale_token(grp, r)] = largest_of_tokens(E, r);
         }
         kda::vm_drain();                    // chunk c has arrived (all of this wave's copies)
         __syncthreads();
@@ -195,8 +238,8 @@ __device__ __forceinline__ void forward_chain(const Params &p, int s, int j, int
             float *const inv = (float *)(kept(c) + KP::SCALE);
             keep_state<KP>(S, mx->scale(mx->state[c & 1]), kept(c) + KP::S, inv, cbase + col0 + r, grp);
             if (c > c0)
-                keep_rows<KP>(E, mx->scale(mx->rows[c & 1]), kept(c - 1) + KP::E, (float *)(kept(c - 1) + KP::SCALE) + 2,
-                          cbase + col0 + r, grp);
+                keep_rows<KP>(E, mx->rows[c & 1], kept(c - 1) + KP::E, (float *)(kept(c - 1) + KP::SCALE) + KP::SE,
+                              cbase + col0 + r, grp, r);
         }
         const uint8_t *const rec = buf + L::REC;
         const float *const ra = (const float *)(rec + R::RA), *const rb = (const float *)(rec + R::RB);
@@ -354,11 +397,10 @@ __device__ __forceinline__ void forward_chain(const Params &p, int s, int j, int
     }
     if constexpr (M == KEEP) {
         if (c0 < c1) {
-            const float b = largest(E);
-            if (lane == 0) mx->rows[c1 & 1][wave] = b;
+            mx->rows[c1 & 1][wave][scale_token(grp, r)] = largest_of_tokens(E, r);
             __syncthreads();
-            keep_rows<KP>(E, mx->scale(mx->rows[c1 & 1]), kept(c1 - 1) + KP::E, (float *)(kept(c1 - 1) + KP::SCALE) + 2,
-                      cbase + col0 + r, grp);
+            keep_rows<KP>(E, mx->rows[c1 & 1], kept(c1 - 1) + KP::E, (float *)(kept(c1 - 1) + KP::SCALE) + KP::SE,
+                          cbase + col0 + r, grp, r);
         }
     }
     if (end) {

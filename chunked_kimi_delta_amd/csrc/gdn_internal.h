@@ -123,16 +123,17 @@ struct RecB {
 __host__ __device__ constexpr int frag_index_t(int t, int s) { return t < 2 ? 2 * t + s : 2 + t; }
 
 // What the backward's two passes leave for one (value head, chunk slot), fp16 with a power of two
-// for each of four matrices (16-bit values of 11 significant bits: the products that use them then
-// add little to the rounding of a bf16 gradient): the state at the chunk's start and the gradient of
-// the state at its end, e, and the gradient of R (which is v's); then the factors that undo the
-// scales, fp32, in that order. Stored in blocks of 16 columns, as a wave of the passes holds them (a
+// for each of the two states and for each token of e and dR (16-bit values of 11 significant bits: the
+// products that use them then add little to the rounding of a bf16 gradient): the state at the chunk's start
+// and the gradient of the state at its end, e, and the gradient of R (which is v's); then the factors that
+// undo the scales, fp32: the two states', from SE on the 64 tokens' of e, from SR on of dR. What lies 2^-28
+// and more below the largest value of its state or its token's row has fewer bits. Stored in blocks of 16 columns, as a wave of the passes holds them (a
 // lane: consecutive key dims or tokens of one column), so that it stores whole lines:
 //   S, DS [V/16][K/32][16 columns][32 key dims],  E, DR [V/16][4][16 columns][16 tokens].
 template <int K, int V>
 struct Keep {
     static constexpr int S = 0, DS = V * K * 2, E = 2 * DS, DR = E + V * 128, SCALE = DR + V * 128;
-    static constexpr int BYTES = SCALE + 1024;          // (copied to LDS as one KiB)
+    static constexpr int SE = 64, SR = 128, BYTES = SCALE + 1024;   // (copied to LDS as one KiB)
     // bytes to four key dims from `dim`, or four tokens from `tok`, of column `col`
     static __host__ __device__ constexpr int state_at(int col, int dim) {
         return ((col >> 4) * (K / 32) + (dim >> 5)) * 1024 + (col & 15) * 64 + (dim & 31) * 2;

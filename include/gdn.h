@@ -85,7 +85,8 @@ kda_status gdn_fwd(const gdn_args *args, void *workspace, size_t ws_bytes, void 
                              NULL; ignored without
    bf16 io: the states and their gradients travel in two bf16 parts as in gdn_fwd (dh0 carries
    about 17 bits); for the other gradients the states, their gradients, e and v's gradient are kept
-   with 11 bits (scaled fp16). fp32 io: fp32 throughout, in 16-token chunks. Deterministic. Tokens behind the last sequence
+   with 11 bits (fp16, scaled by the chunk's state and by the token's row of e, v's gradient and d_o; what lies
+   2^-28 and more below the largest value of that has fewer). fp32 io: fp32 throughout, in 16-token chunks. Deterministic. Tokens behind the last sequence
    are left as they were. `workspace`: gdn_bwd_workspace_bytes(args) bytes, 256-byte aligned. */
 size_t gdn_bwd_workspace_bytes(const gdn_args *args);
 
