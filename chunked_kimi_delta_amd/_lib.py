@@ -98,6 +98,9 @@ def load():
     lib.gdn_bwd_packed.restype = ctypes.c_int
     lib.gdn_step.argtypes = [gdn, ptr, ptr, ctypes.c_int32, ptr]
     lib.gdn_step.restype = ctypes.c_int
+    lib.gdn_zero_tail.argtypes = [ptr, ctypes.c_int32, ctypes.c_int64, ctypes.c_int32,
+                                  ctypes.POINTER(ctypes.c_void_p), ctypes.POINTER(ctypes.c_int64), ptr]
+    lib.gdn_zero_tail.restype = ctypes.c_int
     lib.act8_pack.argtypes = [ptr, ctypes.c_int32, ctypes.c_int64, ctypes.c_int32, ptr, ptr, ptr]
     lib.act8_pack.restype = ctypes.c_int
     lib.act8_unpack.argtypes = [ptr, ptr, ctypes.c_int32, ctypes.c_int64, ctypes.c_int32, ptr, ptr]

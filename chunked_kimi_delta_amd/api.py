@@ -49,6 +49,17 @@ def _on(dev, fn, *args):
         return fn(*args)
 
 
+def _zero_tail(cu_seqlens, *tensors):
+    """Rows behind the last packed sequence of tensors [1, T, ..] set to zero (nothing for a dense batch)."""
+    if cu_seqlens is None:
+        return
+    n, T = len(tensors), tensors[0].shape[1]
+    rows = [x.numel() * x.element_size() // T if T else 2 for x in tensors]
+    _call(load().gdn_zero_tail, "gdn_zero_tail", cu_seqlens.device, None, cu_seqlens.data_ptr(),
+          cu_seqlens.numel() - 1, T, n, (ctypes.c_void_p * n)(*(x.data_ptr() for x in tensors)),
+          (ctypes.c_int64 * n)(*rows))
+
+
 class KdaFwdPlan:
     """Validated arguments for repeated kda_fwd calls on the same tensors.
 

@@ -6,7 +6,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from .act8 import Packed8, pack8, unpack8
-from .api import kda_bwd, kda_fwd
+from .api import _zero_tail, kda_bwd, kda_fwd
 from .gdn import GdnBwdPlan, GdnFwdPlan
 
 
@@ -43,6 +43,7 @@ class ChunkKDAFunction(torch.autograd.Function):
                    A_log=A_log, dt_bias=dt_bias, gate_lower_bound=gate_lower_bound)
         o, fin = kda_fwd(q, k, v, g, beta, scale=scale, cu_seqlens=cu_seqlens,
                          initial_state=initial_state, output_final_state=True, **pre)
+        _zero_tail(cu_seqlens, o)           # the kernels leave rows behind the last sequence alone
         _save(ctx, checkpoint, q, k, v, g, beta, initial_state, A_log, dt_bias, cu_seqlens)
         ctx.scale = scale
         ctx.pre = dict(use_qk_l2norm=use_qk_l2norm, use_beta_sigmoid=use_beta_sigmoid, gate=gate,
@@ -59,6 +60,7 @@ class ChunkKDAFunction(torch.autograd.Function):
         dq, dk, dv, dg, db, dh0, dA, ddt = kda_bwd(
             q, k, v, g, beta, d_o, dht, scale=ctx.scale, cu_seqlens=cu, initial_state=h0,
             want_dh0=h0 is not None, A_log=A_log, dt_bias=dt_bias, **ctx.pre)
+        _zero_tail(cu, dq, dk, dv, dg, db)
         cast = lambda x, ref: None if x is None or ref is None else x.to(ref.dtype)
         return (cast(dq, q), cast(dk, k), cast(dv, v), cast(dg, g), cast(db, beta),
                 cast(dh0, h0), cast(dA, A_log), cast(ddt, dt_bias),
@@ -71,7 +73,8 @@ def chunk_kda(q, k, v, g, beta, scale=None, initial_state=None, cu_seqlens=None,
     """Differentiable KDA forward; returns (o, final_state). Shapes as KdaFwdPlan; every
     tensor argument may require grad (cu_seqlens excepted). The forward uses the library's
     default chunk; the backward always uses 16-token chunks. checkpoint="int8" keeps q, k and v
-    for the backward in 8 bits (pack8), which then gives the gradients at those values."""
+    for the backward in 8 bits (pack8), which then gives the gradients at those values. Rows behind the
+    last packed sequence are zero in o and in the gradients."""
     return ChunkKDAFunction.apply(q, k, v, g, beta, initial_state, A_log, dt_bias, scale,
                                   cu_seqlens, use_qk_l2norm, use_beta_sigmoid, gate,
                                   gate_lower_bound, checkpoint)

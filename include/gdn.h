@@ -112,6 +112,12 @@ kda_status gdn_bwd_packed(const gdn_args *args, const float *q_scale, const floa
 kda_status gdn_step(const gdn_args *args, float *state, const int32_t *state_indices,
                     int32_t slots, void *stream);
 
+/* Rows cu_seqlens[N] .. T - 1 of n (at most 8) tensors of T rows set to zero: those behind the last packed
+   sequence, which the calls above and kda_fwd's and kda_bwd's leave as they were. x[i] device, 8-byte
+   aligned, contiguous; row_bytes[i] even; both arrays on the host, read before the call returns. */
+kda_status gdn_zero_tail(const int64_t *cu_seqlens, int32_t N, int64_t T, int32_t n, void *const *x,
+                         const int64_t *row_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
