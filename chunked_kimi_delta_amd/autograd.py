@@ -91,9 +91,8 @@ class ChunkGDNFunction(torch.autograd.Function):
                        gate_lower_bound=gate_lower_bound)
         plan = GdnFwdPlan(q, k, v, g, beta, scale=scale, cu_seqlens=cu_seqlens,
                           initial_state=initial_state, A_log=A_log, dt_bias=dt_bias, **ctx.pre)
-        if cu_seqlens is not None:
-            plan.o.zero_()                  # the kernels leave rows behind the last sequence alone
         o, fin = plan()
+        _zero_tail(cu_seqlens, o)
         _save(ctx, checkpoint, q, k, v, g, beta, initial_state, A_log, dt_bias, cu_seqlens)
         ctx.scale = scale
         return o, fin
@@ -106,10 +105,8 @@ class ChunkGDNFunction(torch.autograd.Function):
         plan = GdnBwdPlan(
             q, k, v, g, beta, d_o, d_fin.float().contiguous(), scale=ctx.scale, cu_seqlens=cu,
             initial_state=h0, want_dh0=h0 is not None, A_log=A_log, dt_bias=dt_bias, **ctx.pre)
-        if cu is not None:
-            for x in (plan.dq, plan.dk, plan.dv, plan.dg, plan.dbeta):
-                x.zero_()
         dq, dk, dv, dg, db, dh0, dA, ddt = plan()
+        _zero_tail(cu, dq, dk, dv, dg, db)
         return (dq, dk, dv, dg, db, dh0, dA, None if dt_bias is None else ddt,
                 None, None, None, None, None, None, None)
 
