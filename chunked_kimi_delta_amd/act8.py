@@ -20,7 +20,8 @@ class Packed8(NamedTuple):
 
 def pack8(x) -> Packed8:
     """x (bf16 or fp32, contiguous, last dim a multiple of 8 up to 512) as whole numbers in
-    [-127, 127] of its row's largest magnitude / 127. An element is off by at most half of that;
+    [-127, 127] of its row's largest magnitude / 127. An element is off by at most half of that
+    (rows whose largest magnitude is below 2^-119: and by what a subnormal fp32 scale loses);
     a row with a NaN or an infinity comes back as NaN."""
     if x.dtype not in _IO:
         raise TypeError(f"unsupported dtype {x.dtype} (bf16 or fp32)")

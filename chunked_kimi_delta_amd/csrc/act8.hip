@@ -178,7 +178,8 @@ kda_status check(const void *x, int32_t io, int64_t rows, int32_t D, const void 
 {
     if (rows < 0 || D < 8 || D % 8) return KDA_ERR_INVALID_ARG;
     if (D > 512 || (io != KDA_BF16 && io != KDA_FP32)) return KDA_ERR_UNSUPPORTED;
-    if (rows >= ((int64_t)1 << 33) / D) return KDA_ERR_UNSUPPORTED;     // less than 2^32 lanes
+    // less than 2^32 lanes: below D / 4 a row, but four for D = 8, in whole blocks of up to 64 rows
+    if (rows >= ((int64_t)1 << 33) / D || rows > ((int64_t)1 << 30) - 64) return KDA_ERR_UNSUPPORTED;
     if (rows == 0) return KDA_OK;
     if (!x || !data || !scale || ((uintptr_t)x & 15u) || ((uintptr_t)data & 7u) || ((uintptr_t)scale & 3u))
         return KDA_ERR_INVALID_ARG;

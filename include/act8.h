@@ -4,7 +4,7 @@
  *
  * A row x[0..D) becomes n[i] = round(127 x[i] / m) (ties to even) with m = max |x[i]|, and the
  * scale m / 127; a zero row has scale 0. The value a row holds is n[i] * scale, rounded to the
- * io type. A row with a NaN or an infinity gets a NaN scale and comes back as NaN throughout.
+ * io type (below m = 2^-119 the scale is subnormal and has fewer bits, at last none). A row with a NaN or an infinity gets a NaN scale and comes back as NaN throughout.
  */
 #ifndef ACT8_H
 #define ACT8_H
@@ -18,7 +18,7 @@ extern "C" {
 #endif
 
 /* x [rows, D] (io dtype) -> data [rows, D] int8, scale [rows] fp32. D: a multiple of 8, 8 .. 512;
-   rows * D below 2^33. x and data 16- and 8-byte aligned, scale 4-byte aligned. */
+   rows * D below 2^33, at most 2^30 - 64 rows. x and data 16- and 8-byte aligned, scale 4-byte aligned. */
 kda_status act8_pack(const void *x, int32_t io, int64_t rows, int32_t D, int8_t *data,
                      float *scale, void *stream);
 
