@@ -69,7 +69,10 @@ kda_status check_chunks(const gdn_args *a)
 bool recurrent(const gdn_args *a) { return !a->cu_seqlens && a->T <= 16; }
 
 // What a chunk takes, us, by kernel: a workgroup of the whole-sequence pass alone, of the last pass over
-// segments with every compute unit busy, and of the first pass (two workgroups a compute unit).
+// segments with every compute unit busy, and of the first pass (bf16 io: two workgroups a compute unit; fp32 io:
+// its three planes leave LDS for one, and counting two understates that pass. Counted in rounds of one, fp32
+// forwards took 84 -> 80 us for 2 x 1000 tokens of 8 heads, 124 -> 110 for 4096 of 4, 217 -> 193 for 16384 of 2,
+// but 148 -> 163 for 8192 of 8 at K = 64, whose chunks cost less than these times say: kept as it is).
 struct ChunkTimes {
     double whole, last, first;
 };
@@ -91,7 +94,7 @@ Segments plan_segments(int64_t tt, int64_t N, bool packed, int64_t HV, int K, in
                        ChunkTimes us)
 {
     Segments g = {};
-    if (N == 0 || tt == 0) return g;
+    if (tt == 0) return g;
     const int64_t n = (tt / N + CT - 1) / CT, units = N * HV, cus = kda::current_device_cus();
     auto rounds = [](int64_t x, int64_t y) { return (double)((x + y - 1) / y); };
     double best = 0.95 * rounds(units * last_parts, cus) * n * us.whole;
@@ -328,7 +331,6 @@ kda_status gdn_bwd(const gdn_args *a, const void *d_o, const float *dht, void *w
     if (f32 && L.kda_bytes == 0) return KDA_ERR_UNSUPPORTED;
     if (L.f.tt > 0 && (!workspace || ws_bytes < L.total || !aligned(workspace, 256)))
         return KDA_ERR_WORKSPACE;
-    if (a->N == 0) return KDA_OK;
     uint8_t *const ws = (uint8_t *)workspace;
     hipStream_t hs = (hipStream_t)stream;
     Params p = params_of(a, L.f);
@@ -425,10 +427,7 @@ kda_status gdn_fwd(const gdn_args *a, void *workspace, size_t ws_bytes, void *st
     if (st != KDA_OK) return st;
     if ((st = check_tensors(a)) != KDA_OK) return st;
     hipStream_t hs = (hipStream_t)stream;
-    if (recurrent(a)) {
-        if (a->N == 0) return KDA_OK;
-        return run_recurrent(a, a->initial_state, a->final_state, nullptr, 0, hs);
-    }
+    if (recurrent(a)) return run_recurrent(a, a->initial_state, a->final_state, nullptr, 0, hs);
     if ((st = check_chunks(a)) != KDA_OK) return st;
     const Layout L = layout(a);
     if (L.tt > 0 && (!workspace || ws_bytes < L.total || !aligned(workspace, 256)))

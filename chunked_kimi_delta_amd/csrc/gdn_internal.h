@@ -37,8 +37,8 @@ constexpr int CT = 64;                  // tokens per chunk
 //     E_i <- PHI_i E_{i-1} + E_i,
 // and in reverse the gradients before the segments G_i <- PHI_i^T G_{i+1} + G_i, G_i from zero (the last
 // segment: from dht). First pass: E, G and PHI of all segments side by side; the few products above; then
-// every segment from its true start. The last segment's slot of E and the first one's of G are not
-// needed for that and hold copies of the initial state (which final_state may overwrite).
+// every segment from its true start. The last segment's slot of E is not needed
+// for that and holds a copy of the initial state (which final_state may overwrite); the first one's of G is unused.
 struct Segments {
     int32_t chunks, slots;
     float *E, *G, *PHI;                 // [slots][HV][K][V], the same, [slots][HV][2][K][K] (and transposed)
