@@ -7,7 +7,7 @@ from torch.autograd.function import once_differentiable
 
 from .act8 import Packed8, pack8, unpack8
 from .api import _zero_tail, kda_bwd, kda_fwd
-from .gdn import GdnBwdPlan, GdnFwdPlan
+from .gdn import GdnBwdPlan, GdnFwdPlan, _aligned
 
 
 def _save(ctx, checkpoint, q, k, v, *rest):
@@ -89,6 +89,7 @@ class ChunkGDNFunction(torch.autograd.Function):
                 use_qk_l2norm, use_beta_sigmoid, gate, gate_lower_bound, checkpoint=None):
         ctx.pre = dict(use_qk_l2norm=use_qk_l2norm, use_beta_sigmoid=use_beta_sigmoid, gate=gate,
                        gate_lower_bound=gate_lower_bound)
+        g, beta = _aligned(g, beta)
         plan = GdnFwdPlan(q, k, v, g, beta, scale=scale, cu_seqlens=cu_seqlens,
                           initial_state=initial_state, A_log=A_log, dt_bias=dt_bias, **ctx.pre)
         o, fin = plan()

@@ -57,13 +57,19 @@ def _arguments(q, k, v, g, beta, scale, cu_seqlens, initial_state, use_qk_l2norm
                    _GATES[gate], float(gate_lower_bound), A, bias)
 
 
+def _aligned(*tensors):
+    """The tensors, copied where they do not begin at a multiple of 16 bytes as the C ABI asks (g and beta of some
+    tokens of a longer batch, for a call that reads them once)."""
+    return (x if x.data_ptr() % 16 == 0 else x.clone() for x in tensors)
+
+
 class GdnFwdPlan:
     """Validated arguments for repeated gdn_fwd calls on the same tensors.
 
     q, k [B,T,H,K]; v [B,T,HV,V]; g, beta [B,T,HV] (all bf16 or all fp32, contiguous, on one HIP
     device): g is the log decay of a token's whole state. cu_seqlens, initial_state, the outputs
     o and final_state and the pre-stage keywords are KdaFwdPlan's, with dt_bias fp32 [HV]. K and
-    V are 64 or 128; any length, zero included.
+    V are 64 or 128; any length, zero included. A plan's tensors begin at multiples of 16 bytes.
     """
 
     def __init__(self, q, k, v, g, beta, scale=None, cu_seqlens=None, initial_state=None,
@@ -110,6 +116,7 @@ def gdn_fwd(q, k, v, g, beta, scale=None, cu_seqlens=None, initial_state=None,
     """Gated delta rule forward. Returns (o, final_state or None; rows of o behind the last packed
     sequence hold anything); see GdnFwdPlan for shapes and the pre-stage keywords (use_qk_l2norm,
     use_beta_sigmoid, gate, A_log, dt_bias, gate_lower_bound)."""
+    g, beta = _aligned(g, beta)
     return GdnFwdPlan(q, k, v, g, beta, scale, cu_seqlens, initial_state, output_final_state,
                       workspace, **prestage)()
 
@@ -192,6 +199,7 @@ def gdn_bwd(q, k, v, g, beta, d_o, dht=None, scale=None, cu_seqlens=None, initia
     packed = [isinstance(x, Packed8) for x in (q, k, v)]
     if not all(packed):
         q, k, v = (unpack8(x) if p else x for x, p in zip((q, k, v), packed))
+    g, beta = _aligned(g, beta)
     return GdnBwdPlan(q, k, v, g, beta, d_o, dht, scale, cu_seqlens, initial_state, want_dh0,
                       **prestage)()
 
@@ -203,7 +211,8 @@ class GdnStepPlan:
     q, k [B,T,H,K]; v [B,T,HV,V]; g, beta [B,T,HV]: T new tokens of B rows; state fp32
     [slots,HV,K,V], updated in place; state_indices int32 [B] on the device, or None for slot b
     of row b. A row whose index is negative or >= slots is padding: zeros in o, no state touched.
-    Indices of other rows must differ. o [B,T,HV,V] is allocated once and reused.
+    Indices of other rows must differ. o [B,T,HV,V] is allocated once and reused. A plan's tensors begin
+    at multiples of 16 bytes.
     """
 
     def __init__(self, q, k, v, g, beta, state, state_indices=None, scale=None, o=None,
@@ -235,4 +244,5 @@ class GdnStepPlan:
 def gdn_step(q, k, v, g, beta, state, state_indices=None, scale=None, **prestage):
     """A serving step of the gated delta rule: returns o and updates `state` in place; see
     GdnStepPlan."""
+    g, beta = _aligned(g, beta)
     return GdnStepPlan(q, k, v, g, beta, state, state_indices, scale, **prestage)()
