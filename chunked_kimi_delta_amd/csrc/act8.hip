@@ -6,8 +6,9 @@
 // |2 d| < m. Where a wave holds a value that may not, it divides (correctly rounded, which decides every
 // case of bf16 exactly); fp32 rows divide in 64 bits. A lane takes eight values of a row, and a row's
 // maximum is a butterfly over its lanes. Unpacking writes eight bytes a lane, whole lines a store. 4096 x 48 rows
-// of 128 bf16: packing 19.4 us (4.0 TB/s, its vector instructions; two rows a lane 21, four 24 us: loads in
-// flight are not what it lacks), unpacking 15.0 us (5.1 TB/s, what a copy reaches).
+// of 128 bf16: packing 18.3 us (4.2 TB/s, its vector instructions; first calls 19.4, with two rows a lane 21, with
+// four 24 us: loads in flight are not what it lacks), unpacking 14.4 us (5.3 TB/s, what a copy reaches). fp32 rows: 23.5
+// and 20.3 us (5.4 and 6.2 TB/s, part of it from the last-level cache).
 #include "act8.h"
 #include "kda_internal.h"
 

@@ -82,7 +82,8 @@ struct ChunkTimes {
 // two more launches about 6 us. The first pass's workgroups share compute units two by two and take 15% longer
 // once a third waits. Measured, 16 heads x 4096, bf16 io, state pass of the forward: whole 206 us; 4 segments
 // 97, 6: 87, 8: 77, 11: 103, 16: 97 us. Whole backward in segments of 32 chunks 374 us, 16: 262, 11: 224, 8:
-// 216, 4: 234, 2: 284; 8 heads x 16384: 32: 532, 16: 422, 8: 441. 8 packed sequences x 32 heads: whole 465 us,
+// 216, 4: 234, 2: 284; 8 heads x 16384: 32: 532, 16: 422, 8: 441 (calls repeated on one set of inputs; 229 for 216
+// with inputs that change). 8 packed sequences x 32 heads: whole 465 us,
 // two or more segments 660 us and up (512 workgroups fill the device already).
 //
 // Packed sequences that would go whole, and leave no compute unit two workgroups, are cut at one and a half

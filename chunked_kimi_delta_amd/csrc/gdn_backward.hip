@@ -24,11 +24,13 @@
 // dO as fp16 (bf16 values scaled by a power of two a token: exact down to 2^-28 of the token's largest); the
 // 64 x 64 matrices take two bf16 parts against the stored q and k.
 //
-// Measured, 16 heads x 4096 tokens, K = V = 128: records 18 us, segments' ends 62, their joining 16, both
-// passes 62, tokens 78 (227 for the call; without segments and with four 64 x 64 matrices 519). The passes are
-// bound by a chunk's dependent products with two waves a SIMD (7 us a chunk with every compute unit busy), the
-// tokens' kernel by LDS: of a workgroup's 36 thousand cycles 8 load, 6 form the matrices, 9 multiply with the
-// states (520 KB of LDS reads), 5 do the other products.
+// Measured, 16 heads x 4096 tokens, K = V = 128: records 17 us, segments' ends 57, their joining 15, both
+// passes 57, tokens 72 (216 for the call repeated, 229 with inputs that change; without segments and with four
+// 64 x 64 matrices 519). The passes are bound by a chunk's dependent products with two waves a SIMD (7 us a chunk
+// with every compute unit busy: vector instructions issue 41% of it, LDS works 30%, the matrix core 25%). The
+// tokens' kernel has one workgroup a compute unit, which takes 37 thousand clocks; vector instructions issue in 20
+// of them, LDS works 12 (4 of bank conflicts) and the matrix core 4: the phases between its barriers wait for each
+// other. By timestamps 8 thousand go to loading, 6 to forming the matrices, 9 to the products with the states.
 #include <type_traits>
 
 #include "gdn_segments.h"
@@ -312,7 +314,7 @@ __device__ __forceinline__ int w_at(int row, int piece) { return piece_at<64>(ro
 // One workgroup per (chunk slot, q/k head), over the head's value heads, one wave per 16 key dims and half
 // of the tokens: dQ and dK stay in registers, transposed (a lane: four consecutive dims of one token). A
 // chunk fills the LDS of a compute unit, so the waves of one workgroup are all there is to hide latencies:
-// 16 waves took 78 us for 16 heads x 4096 tokens, eight waves with all tokens each 81 us.
+// 16 waves took 78 us for 16 heads x 4096 tokens, eight waves with all tokens each 81 us (first calls).
 template <int K, int V>
 __global__ __launch_bounds__(K * 8) void local_kernel(BwdParams b)
 {

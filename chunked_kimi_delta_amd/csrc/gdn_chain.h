@@ -11,8 +11,9 @@
 // four consecutive columns of one token and stores eight bytes.
 //
 // What bounds it: a chunk is a chain of dependent products and splits, 3.2 us for 64 columns alone (K = 128,
-// bf16 io); by count the matrix core works 0.9 of them, LDS reads of K, Q and the record (290 KB) 1.2 and the
-// splits 0.7. With every compute unit busy 4.1 us. Reading operands a phase ahead took 16 heads x 4096 tokens
+// bf16 io) and 3.5 with every compute unit busy (8.3 thousand clocks). By the counters the matrix core works 2.1
+// thousand of those, LDS 2.2 (290 KB of K, Q and the record; 37% of it bank conflicts) and the vector
+// instructions 2.2, each in turn. Reading operands a phase ahead took 16 heads x 4096 tokens
 // without segments from 205 to 196 us; interleaving the two kinds of instructions by hand 209.
 #pragma once
 

@@ -260,8 +260,9 @@ __device__ __forceinline__ f32x4 widen(s16x4 a) {
 // p ^ swizzle(r) of its row. Sixteen lanes of a transposing read take four neighbouring rows of two
 // or four pieces, sixteen lanes of a 16-byte read one piece of sixteen rows: the two low bits of the
 // row spread the former over the banks (a row of 64 values fills only half of them, so there the
-// lowest bit does without), the next two the latter. With p ^ (r % 16) the transposing reads of
-// K met four to a bank (36% of the LDS cycles of the state pass).
+// lowest bit does without), the next two the latter. Against p ^ (r % 16) the first pass over segments loses 38
+// instead of 47% of its LDS cycles to bank conflicts, the state pass as many (37 and 36%): gradients of 16 heads x
+// 4096 tokens 220 -> 216 us, the forward as fast.
 template <int W>
 __device__ __forceinline__ int swizzle(int row) {
     return W == 128 ? (row & 3) << 2 | (row >> 2 & 3) : (row & 2) << 1 | (row >> 2 & 3);

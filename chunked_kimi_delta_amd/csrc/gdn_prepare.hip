@@ -9,12 +9,12 @@
 // block forward substitution between them on the fp32 matrix core: both backward stable,
 // where a product of powers of L loses digits for keys that resemble each other.
 //
-// Measured (K = V = 128, bf16 io): 32 heads of 21412 packed tokens 150 us for 620 MB, 16 heads x 4096 tokens
-// 17 us for 58 MB: about 80% and 65% of what a large copy reaches; a workgroup alone takes 6 us (two to
-// three of them in the loads, one in the diagonal blocks' substitution), and four share a compute unit (102
-// registers). With Q staged in LDS next to K, also four, 184 and 18 us; with Q in registers, the gate's parameters
-// loaded behind the decays, every key tile read twice and seven workgroups a compute unit (72 registers) 151
-// and 19.9 us: fewer waits did as much as more waves.
+// Measured (K = V = 128, bf16 io): 32 heads of 21412 packed tokens 131 us for 620 MB, 16 heads x 4096 tokens
+// 16 us for 58 MB: about 91% and 70% of what a large copy reaches (first calls 147 and 18 us); a workgroup alone
+// takes 6 us (two to three of them in the loads, one in the diagonal blocks' substitution), and four share a
+// compute unit (102 registers). First calls with Q staged in LDS next to K, also four, 184 and 18 us; with Q in
+// registers, the gate's parameters loaded behind the decays, every key tile read twice and seven workgroups a
+// compute unit (72 registers) 151 and 19.9 us: fewer waits did as much as more waves.
 #include <type_traits>
 
 #include "gdn_internal.h"

@@ -19,6 +19,8 @@
 //   bwd_qk_finalize_kernel         dq, dk summed over the value heads of a q/k head (G > 1)
 //                                  and carried through the q/k L2 norm (when it is on)
 //   bwd_param_kernel               dA_log, dt_bias: per-chunk partials summed (gate on)
+// With one decay per token and value head (SCALAR, the fp32 gradients of gdn.h) the same launches take each decay
+// as a number of the chunk.
 // With the pre-stage on, the kernels read raw inputs and apply it on load (prepare_f32 and the
 // local kernel), and the gradients leave through its reverse mode: dbeta times
 // sigma (1 - sigma), dg times the gate's slope (with dA_log and dt_bias summed over all tokens),

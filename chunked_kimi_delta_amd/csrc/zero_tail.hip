@@ -2,7 +2,8 @@
 //
 // The forward and backward kernels leave those rows as they were, and the differentiable calls want zeros there.
 // Where they begin lies on the device, so clearing whole tensors ahead would write every output twice; this
-// launch writes the tail alone (chunk_gdn, forward and backward, 21412 packed tokens of 32 heads: 2450 -> 2310 us).
+// launch writes the tail alone (chunk_gdn, forward and backward, 21412 packed tokens of 32 heads: 2450 -> 2310
+// us; a call without a tail takes 6 us, most of it in Python).
 #include "gdn.h"
 #include "kda_internal.h"
 

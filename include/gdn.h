@@ -70,7 +70,8 @@ size_t gdn_fwd_workspace_bytes(const gdn_args *args);
    sequence's chunks, split into segments where the batch is too small to fill the device), or,
    for a dense batch of at most 16 tokens a sequence, the recurrence itself. Products take bf16
    operands in parts: two for bf16 io (the states and o carry about 17 bits before their own
-   rounding), three for fp32 io (24 bits). Tokens behind the last sequence are left as they were.
+   rounding), three for fp32 io (24 bits): for final states to fp32 accuracy from bf16 values pass them as
+   fp32. Tokens behind the last sequence are left as they were.
    The chunked form takes less than 2^28 tokens, 2^21 (sequence, value head) pairs and, with fp32
    io, 2^26 (token, value head) pairs a call; so does gdn_bwd, for any length. */
 kda_status gdn_fwd(const gdn_args *args, void *workspace, size_t ws_bytes, void *stream);
@@ -96,7 +97,8 @@ kda_status gdn_bwd(const gdn_args *args, const void *d_o, const float *dht, void
 
 /* gdn_bwd with q, k and v kept as 8-bit checkpoints (act8.h): args->q, k, v are their int8 rows, q_scale,
    k_scale [B, T, H] and v_scale [B, T, HV] fp32 (4-byte aligned) the rows' scales. They are unpacked to
-   the io type into the workspace; the gradients are those at these values. */
+   the io type into the workspace; the gradients are those at these values. q, k and v together have less
+   than 2^33 values. */
 size_t gdn_bwd_packed_workspace_bytes(const gdn_args *args);
 
 kda_status gdn_bwd_packed(const gdn_args *args, const float *q_scale, const float *k_scale,
