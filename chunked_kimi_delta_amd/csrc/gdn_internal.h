@@ -278,11 +278,15 @@ __device__ __forceinline__ int piece_at(int row, int piece) {
 // read of LDS, also where the copies go to the other buffer. The kernels wait themselves (vm_drain)
 // before the barrier behind which the data is read. M0 takes its value one cycle before the copy
 // reads it (s_nop).
+// (The compiler keeps M0 for itself and warns of the clobber, which is what tells it of the write.)
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void copy16_to_lds(const void *base, uint32_t off, uint8_t *dst) {
     const uint32_t at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_u8 *)dst);
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
                  :: "s"(at), "v"(off), "s"(base) : "memory", "m0");
 }
+#pragma clang diagnostic pop
 
 // Stages 64 rows of W 16-bit values (rows `stride` values apart) into LDS, layout piece_at, NW waves
 // sharing the work. A wave's steps are NW * (64 / pieces) rows apart, a multiple of the rows after
