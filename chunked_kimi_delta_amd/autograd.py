@@ -32,7 +32,7 @@ def _saved(ctx):
 
 
 class ChunkKDAFunction(torch.autograd.Function):
-    """o, final_state = KDA(q, k, v, g, beta; initial_state), differentiable in q, k, v, g, beta,
+    """o, final_state = KDA(q, k, v, g, beta; initial_state), differentiable (once) in q, k, v, g, beta,
     initial_state and (with a gate) A_log, dt_bias. Gradients come back in the dtype of each
     input (the kernels compute them in fp32)."""
 
@@ -51,6 +51,7 @@ class ChunkKDAFunction(torch.autograd.Function):
         return o, fin
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, d_o, d_fin):
         q, k, v, g, beta, h0, A_log, dt_bias, cu = _saved(ctx)
         if ctx.packed:
