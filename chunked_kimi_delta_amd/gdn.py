@@ -70,6 +70,7 @@ class GdnFwdPlan:
     device): g is the log decay of a token's whole state. cu_seqlens, initial_state, the outputs
     o and final_state and the pre-stage keywords are KdaFwdPlan's, with dt_bias fp32 [HV]. K and
     V are 64 or 128; any length, zero included. A plan's tensors begin at multiples of 16 bytes.
+    final_state errs by about 4e-6 of itself for bf16 inputs, by 3e-7 where they are passed as fp32.
     """
 
     def __init__(self, q, k, v, g, beta, scale=None, cu_seqlens=None, initial_state=None,

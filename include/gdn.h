@@ -70,8 +70,8 @@ size_t gdn_fwd_workspace_bytes(const gdn_args *args);
    sequence's chunks, split into segments where the batch is too small to fill the device), or,
    for a dense batch of at most 16 tokens a sequence, the recurrence itself. Products take bf16
    operands in parts: two for bf16 io (the states and o carry about 17 bits before their own
-   rounding), three for fp32 io (24 bits): for final states to fp32 accuracy from bf16 values pass them as
-   fp32. Tokens behind the last sequence are left as they were.
+   rounding), three for fp32 io (24 bits). For final states to fp32 accuracy from bf16 values pass
+   them as fp32. Tokens behind the last sequence are left as they were.
    The chunked form takes less than 2^28 tokens, 2^21 (sequence, value head) pairs and, with fp32
    io, 2^26 (token, value head) pairs a call; so does gdn_bwd, for any length. */
 kda_status gdn_fwd(const gdn_args *args, void *workspace, size_t ws_bytes, void *stream);
@@ -85,10 +85,11 @@ kda_status gdn_fwd(const gdn_args *args, void *workspace, size_t ws_bytes, void 
      dA_log, ddt_bias        [HV] fp32 (4-byte aligned): with a gate, dA_log required, ddt_bias or
                              NULL; ignored without
    bf16 io: the states and their gradients travel in two bf16 parts as in gdn_fwd (dh0 carries
-   about 17 bits); for the other gradients the states, their gradients, e and v's gradient are kept
-   with 11 bits (fp16, scaled by the chunk's state and by the token's row of e, v's gradient and d_o; what lies
-   2^-28 and more below the largest value of that has fewer). fp32 io: fp32 throughout, in 16-token chunks. Deterministic. Tokens behind the last sequence
-   are left as they were. `workspace`: gdn_bwd_workspace_bytes(args) bytes, 256-byte aligned. */
+   about 17 bits); for the other gradients the states, their gradients, e, v's gradient and d_o enter
+   with 11 bits (fp16 with a power of two for each state, and for each token's row of the others; what
+   lies 2^-28 and more below the largest value of its state or row has fewer). fp32 io: fp32
+   throughout, in 16-token chunks. Deterministic. Tokens behind the last sequence are left as they
+   were. `workspace`: gdn_bwd_workspace_bytes(args) bytes, 256-byte aligned. */
 size_t gdn_bwd_workspace_bytes(const gdn_args *args);
 
 kda_status gdn_bwd(const gdn_args *args, const void *d_o, const float *dht, void *workspace,
