@@ -49,6 +49,27 @@ class GdnArgs(ctypes.Structure):
     ]
 
 
+class GlrArgs(ctypes.Structure):
+    """Mirror of glr_args (include/glr.h)."""
+    _fields_ = [
+        ("B", ctypes.c_int32), ("T", ctypes.c_int32), ("N", ctypes.c_int32),
+        ("D", ctypes.c_int32), ("io", ctypes.c_int32),
+        ("x", ctypes.c_void_p), ("g", ctypes.c_void_p), ("beta", ctypes.c_void_p),
+        ("x_stride", ctypes.c_int64), ("g_stride", ctypes.c_int64),
+        ("beta_stride", ctypes.c_int64),
+        ("cu_seqlens", ctypes.c_void_p), ("initial_state", ctypes.c_void_p),
+        ("y", ctypes.c_void_p), ("final_state", ctypes.c_void_p),
+        ("beta_sigmoid", ctypes.c_int32), ("gate", ctypes.c_int32),
+        ("gate_lower_bound", ctypes.c_float),
+        ("A_log", ctypes.c_void_p), ("dt_bias", ctypes.c_void_p),
+    ]
+
+
+class PoolRef(ctypes.Structure):
+    """Mirror of pool_ref (include/pool.h)."""
+    _fields_ = [("data", ctypes.c_void_p), ("bytes", ctypes.c_int64)]
+
+
 def library_path() -> str:
     return os.environ.get("KDA_FWD_LIB", os.path.join(HERE, LIB_NAME))
 
@@ -105,6 +126,23 @@ def load():
     lib.act8_pack.restype = ctypes.c_int
     lib.act8_unpack.argtypes = [ptr, ptr, ctypes.c_int32, ctypes.c_int64, ctypes.c_int32, ptr, ptr]
     lib.act8_unpack.restype = ctypes.c_int
+    glr = ctypes.POINTER(GlrArgs)
+    for name in ("glr_fwd_workspace_bytes", "glr_bwd_workspace_bytes"):
+        getattr(lib, name).argtypes = [glr]
+        getattr(lib, name).restype = ctypes.c_size_t
+    lib.glr_fwd.argtypes = [glr, ptr, ctypes.c_size_t, ptr]
+    lib.glr_bwd.argtypes = [glr, ptr, ptr, ptr, ctypes.c_size_t] + [ptr] * 7
+    lib.glr_step.argtypes = [glr, ptr, ptr, ctypes.c_int32, ptr]
+    pools = [ctypes.POINTER(PoolRef), ctypes.c_int32, ctypes.c_int32]
+    sources = [ctypes.POINTER(ctypes.c_void_p), ctypes.c_int32]
+    lib.pool_copy.argtypes = pools + sources + [ptr, ptr, ctypes.c_int64, ptr]
+    lib.pool_fork.argtypes = pools + sources + [ptr, ptr, ptr, ctypes.c_int64, ptr]
+    lib.pool_free.argtypes = pools + [ptr, ptr, ctypes.c_int64, ptr]
+    lib.pool_compact.argtypes = pools + [ptr, ptr, ctypes.c_int64, ptr, ptr, ctypes.c_size_t, ptr]
+    for name in ("glr_fwd", "glr_bwd", "glr_step", "pool_copy", "pool_fork", "pool_free", "pool_compact"):
+        getattr(lib, name).restype = ctypes.c_int
+    lib.pool_compact_workspace_bytes.argtypes = [ctypes.c_int32]
+    lib.pool_compact_workspace_bytes.restype = ctypes.c_size_t
     lib.kda_strerror.argtypes = [ctypes.c_int]
     lib.kda_strerror.restype = ctypes.c_char_p
     lib.kda_version.argtypes = []

@@ -8,6 +8,7 @@ from torch.autograd.function import once_differentiable
 from .act8 import Packed8, pack8, unpack8
 from .api import _zero_tail, kda_bwd, kda_fwd
 from .gdn import GdnBwdPlan, GdnFwdPlan, _aligned
+from .glr import GlrBwdPlan, GlrFwdPlan
 
 
 def _save(ctx, checkpoint, q, k, v, *rest):
@@ -124,3 +125,37 @@ def chunk_gdn(q, k, v, g, beta, scale=None, initial_state=None, cu_seqlens=None,
     return ChunkGDNFunction.apply(q, k, v, g, beta, initial_state, A_log, dt_bias, scale,
                                   cu_seqlens, use_qk_l2norm, use_beta_sigmoid, gate,
                                   gate_lower_bound, checkpoint)
+
+
+class ChunkGLRFunction(torch.autograd.Function):
+    """y, final_state = gated linear recurrence(x, g, beta; initial_state), differentiable (once) in every
+    tensor argument but cu_seqlens."""
+
+    @staticmethod
+    def forward(ctx, x, g, beta, initial_state, A_log, dt_bias, cu_seqlens, use_beta_sigmoid, gate,
+                gate_lower_bound):
+        ctx.pre = dict(use_beta_sigmoid=use_beta_sigmoid, gate=gate, gate_lower_bound=gate_lower_bound)
+        y, fin = GlrFwdPlan(x, g, beta, cu_seqlens, initial_state, A_log=A_log, dt_bias=dt_bias, **ctx.pre)()
+        _zero_tail(cu_seqlens, y)
+        ctx.save_for_backward(None if beta is None else x, g, beta, initial_state, A_log, dt_bias, cu_seqlens, y)
+        return y, fin
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, d_y, d_fin):
+        x, g, beta, h0, A_log, dt_bias, cu, y = ctx.saved_tensors
+        plan = GlrBwdPlan(x, g, y, d_y.to(g.dtype).contiguous(), beta, d_fin.float().contiguous(), cu, h0,
+                          want_dh0=h0 is not None, A_log=A_log, dt_bias=dt_bias, **ctx.pre)
+        dx, dg, db, dh0, dA, ddt = plan()
+        _zero_tail(cu, dx, dg, *(() if db is None else (db,)))
+        return dx, dg, db, dh0, dA, None if dt_bias is None else ddt, None, None, None, None
+
+
+def chunk_glr(x, g, beta=None, initial_state=None, cu_seqlens=None, use_beta_sigmoid=False, gate=None, A_log=None,
+              dt_bias=None, gate_lower_bound=-5.0):
+    """Differentiable gated linear recurrence (one state a channel); returns (y, final_state). Shapes as
+    GlrFwdPlan; every tensor argument may require grad (cu_seqlens excepted). The backward takes the states from
+    y, which must not be changed in place before it. Rows behind the last packed sequence are zero in y and in the
+    gradients."""
+    return ChunkGLRFunction.apply(x, g, beta, initial_state, A_log, dt_bias, cu_seqlens, use_beta_sigmoid, gate,
+                                  gate_lower_bound)

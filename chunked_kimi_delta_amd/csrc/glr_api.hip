@@ -1,0 +1,178 @@
+// glr_api.hip -- the extern "C" boundary of the gated linear recurrence (include/glr.h): argument
+// checks, workspace layout and the launches on the caller's stream. Host side only.
+#include <math.h>
+
+#include "glr_scan.h"
+
+namespace kda {
+int current_device_cus();
+}
+
+namespace {
+
+using namespace glr;
+
+constexpr int64_t MOST = 1 << 18;       // channels, and elements from one token to the next
+
+bool aligned(const void *p, uintptr_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
+size_t align256(size_t x) { return (x + 255) / 256 * 256; }
+
+kda_status check_shapes(const glr_args *a)
+{
+    if (!a) return KDA_ERR_INVALID_ARG;
+    if (a->B < 1 || a->T < 0 || a->N < 0 || a->D < 1) return KDA_ERR_INVALID_ARG;
+    if (a->cu_seqlens) {
+        if (a->B != 1 || a->N < 1 || !aligned(a->cu_seqlens, 8)) return KDA_ERR_INVALID_ARG;
+    } else if (a->N != a->B) {
+        return KDA_ERR_INVALID_ARG;
+    }
+    if (a->io != KDA_BF16 && a->io != KDA_FP32) return KDA_ERR_UNSUPPORTED;
+    if (a->D > MOST) return KDA_ERR_UNSUPPORTED;
+    if (a->gate != KDA_GATE_NONE && a->gate != KDA_GATE_SOFTPLUS && a->gate != KDA_GATE_BOUNDED)
+        return KDA_ERR_UNSUPPORTED;
+    return KDA_OK;
+}
+
+kda_status check_tensors(const glr_args *a, bool x_read)
+{
+    const uintptr_t e = a->io == KDA_FP32 ? 4 : 2;
+    if ((int64_t)a->B * a->T > 0) {
+        if ((x_read && !a->x) || !a->g || !a->y) return KDA_ERR_INVALID_ARG;
+        if (!aligned(a->x, e) || !aligned(a->g, e) || !aligned(a->beta, e) || !aligned(a->y, e)) return KDA_ERR_INVALID_ARG;
+        const int64_t strides[] = {x_read ? a->x_stride : a->D, a->g_stride, a->beta ? a->beta_stride : a->D};
+        for (int64_t s : strides) {
+            if (s < a->D) return KDA_ERR_INVALID_ARG;
+            if (s > MOST) return KDA_ERR_UNSUPPORTED;
+        }
+    }
+    if (!aligned(a->initial_state, 4) || !aligned(a->final_state, 4)) return KDA_ERR_INVALID_ARG;
+    if (a->gate == KDA_GATE_NONE) return KDA_OK;
+    if (!a->A_log || !aligned(a->A_log, 4) || !aligned(a->dt_bias, 4)) return KDA_ERR_INVALID_ARG;
+    if (a->gate == KDA_GATE_BOUNDED && !(a->gate_lower_bound < 0.f && a->gate_lower_bound > -INFINITY))
+        return KDA_ERR_INVALID_ARG;
+    return KDA_OK;
+}
+
+// Two channels a lane where every row begins at a multiple of two elements.
+int vec_of(const glr_args *a, bool x_read, const void *const *more, int n)
+{
+    const uintptr_t e = a->io == KDA_FP32 ? 8 : 4;
+    bool two = a->D % 2 == 0 && a->g_stride % 2 == 0 && aligned(a->g, e) && aligned(a->y, e);
+    if (x_read) two = two && a->x_stride % 2 == 0 && aligned(a->x, e);
+    if (a->beta) two = two && a->beta_stride % 2 == 0 && aligned(a->beta, e);
+    for (int i = 0; i < n; ++i) two = two && aligned(more[i], e);
+    return two ? 2 : 1;
+}
+
+// Narrow strips where wide ones would leave compute units without work.
+Shape shape_of(const glr_args *a, int vec)
+{
+    const int64_t wide = (a->D + 32 * vec - 1) / (32 * vec) * (int64_t)a->N;
+    return Shape{a->io == KDA_FP32, vec, wide >= 2 * kda::current_device_cus() ? 32 : 8};
+}
+
+Params params_of(const glr_args *a, Shape s)
+{
+    Params p = {};
+    p.seq.cu = a->cu_seqlens;
+    p.seq.T = a->T;
+    p.seq.T_total = (int64_t)a->B * a->T;
+    p.seq.N = a->N;
+    p.D = a->D;
+    p.strips = (a->D + s.vec * s.lanes - 1) / (s.vec * s.lanes);
+    p.x = a->x;
+    p.g = a->g;
+    p.beta = a->beta;
+    p.xs = a->x_stride;
+    p.gs = a->g_stride;
+    p.bs = a->beta_stride;
+    p.h0 = a->initial_state;
+    p.y = a->y;
+    p.ht = a->final_state;
+    p.pre = Pre{a->beta_sigmoid != 0, a->gate, a->gate_lower_bound, a->A_log, a->dt_bias};
+    return p;
+}
+
+// A launch has less than 2^32 threads.
+bool fits(const glr_args *a, Shape s)
+{
+    const int ch = s.vec * s.lanes;
+    return unit_grid((a->D + ch - 1) / ch, a->N, near_of(ch * (s.f32 ? 4 : 2))) < ((int64_t)1 << 32) / (64 * W);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t glr_fwd_workspace_bytes(const glr_args *) { return 0; }
+
+kda_status glr_fwd(const glr_args *a, void *, size_t, void *stream)
+{
+    kda_status st = check_shapes(a);
+    if (st != KDA_OK || (st = check_tensors(a, true)) != KDA_OK) return st;
+    const Shape s = shape_of(a, vec_of(a, true, nullptr, 0));
+    if (!fits(a, s)) return KDA_ERR_UNSUPPORTED;
+    if (a->N == 0) return KDA_OK;
+    return launch_fwd(params_of(a, s), s, (hipStream_t)stream) == hipSuccess ? KDA_OK : KDA_ERR_HIP;
+}
+
+size_t glr_bwd_workspace_bytes(const glr_args *a)
+{
+    if (check_shapes(a) != KDA_OK || a->gate == KDA_GATE_NONE) return 0;
+    return 2 * align256((size_t)a->N * a->D * 4);
+}
+
+kda_status glr_bwd(const glr_args *a, const void *d_y, const float *dht, void *workspace, size_t ws_bytes,
+                   void *dx, void *dg, void *dbeta, float *dh0, float *dA_log, float *ddt_bias, void *stream)
+{
+    kda_status st = check_shapes(a);
+    if (st != KDA_OK || (st = check_tensors(a, a->beta != nullptr)) != KDA_OK) return st;
+    const uintptr_t e = a->io == KDA_FP32 ? 4 : 2;
+    const bool gated = a->gate != KDA_GATE_NONE;
+    const void *io[] = {d_y, dx, dg, a->beta ? dbeta : dg};
+    if ((int64_t)a->B * a->T > 0)
+        for (const void *p : io)
+            if (!p || !aligned(p, e)) return KDA_ERR_INVALID_ARG;
+    if (!aligned(dht, 4) || !aligned(dh0, 4)) return KDA_ERR_INVALID_ARG;
+    if (gated && (!dA_log || !aligned(dA_log, 4) || !aligned(ddt_bias, 4))) return KDA_ERR_INVALID_ARG;
+    const Shape s = shape_of(a, vec_of(a, a->beta != nullptr, io, 4));
+    if (!fits(a, s)) return KDA_ERR_UNSUPPORTED;
+    const size_t need = glr_bwd_workspace_bytes(a);
+    if (need && (!workspace || ws_bytes < need || !aligned(workspace, 256))) return KDA_ERR_WORKSPACE;
+    BwdParams q = {};
+    q.f = params_of(a, s);
+    q.d_y = d_y;
+    q.dht = dht;
+    q.dx = dx;
+    q.dg = dg;
+    q.dbeta = dbeta;
+    q.dh0 = dh0;
+    q.part_A = (float *)workspace;
+    q.part_b = (float *)((uint8_t *)workspace + need / 2);
+    hipStream_t hs = (hipStream_t)stream;
+    if (a->N > 0 && launch_bwd(q, s, hs) != hipSuccess) return KDA_ERR_HIP;
+    if (gated && launch_params(q, dA_log, ddt_bias, hs) != hipSuccess) return KDA_ERR_HIP;
+    return KDA_OK;
+}
+
+kda_status glr_step(const glr_args *a, float *state, const int32_t *state_indices, int32_t slots, void *stream)
+{
+    kda_status st = check_shapes(a);
+    if (st != KDA_OK) return st;
+    if (a->cu_seqlens || slots < 0 || (!state_indices && slots < a->B)) return KDA_ERR_INVALID_ARG;
+    if ((st = check_tensors(a, true)) != KDA_OK) return st;
+    if (a->T == 0) return KDA_OK;
+    if ((slots > 0 && !state) || !aligned(state, 4) || !aligned(state_indices, 4)) return KDA_ERR_INVALID_ARG;
+    const int vec = vec_of(a, true, nullptr, 0);
+    StepParams p = {};
+    p.f = params_of(a, Shape{a->io == KDA_FP32, vec, 1});
+    p.state = state;
+    p.index = state_indices;
+    p.B = a->B;
+    p.T = a->T;
+    p.slots = slots;
+    if ((int64_t)a->B * p.f.strips >= ((int64_t)1 << 32) - 256) return KDA_ERR_UNSUPPORTED;
+    return launch_step(p, a->io == KDA_FP32, vec, (hipStream_t)stream) == hipSuccess ? KDA_OK : KDA_ERR_HIP;
+}
+
+}  // extern "C"

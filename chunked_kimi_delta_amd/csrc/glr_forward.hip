@@ -1,0 +1,170 @@
+// glr_forward.hip -- the forward of the gated linear recurrence and its serving step (include/glr.h):
+//     h <- e^g h + beta x;   y = h
+#include "glr_scan.h"
+
+namespace glr {
+
+namespace {
+
+template <typename T, int VEC, bool BETA>
+struct Rows {
+    Raw<T, VEC> x[K], g[K], b[BETA ? K : 1];
+};
+
+template <typename T, int VEC, int LPR, bool BETA>
+__global__ __launch_bounds__(64 * W) void scan_kernel(Params p)
+{
+    constexpr int CH = LPR * VEC, R = 64 / LPR, STEP = R * K * W, E = sizeof(T);
+    __shared__ Totals<CH> tot[2];
+    int seq, strip;
+    if (!unit_of(blockIdx.x, p.strips, p.seq.N, near_of(CH * E), seq, strip)) return;
+    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+    const int64_t bos = kda::seq_bos(p.seq, seq), n = kda::seq_eos(p.seq, seq, bos) - bos;
+    const int ch = strip * CH + lane % LPR * VEC;
+    const bool on = ch < p.D;
+    const int d = on ? ch : 0, tok = (wave * R + lane / LPR) * K;
+    const Gate<T> gate0 = gate_of<T>(p.pre, d), gate1 = gate_of<T>(p.pre, VEC == 2 && on ? ch + 1 : d);
+    float carry[VEC];
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) carry[v] = p.h0 && on ? p.h0[(int64_t)seq * p.D + d + v] : 0.f;
+
+    // offsets of this lane's first token in a step; a resource spans the step's rows
+    const uint32_t xs = (uint32_t)p.xs * E, gs = (uint32_t)p.gs * E, bs = (uint32_t)p.bs * E, ys = (uint32_t)p.D * E;
+    auto rows = [&](const void *base, int64_t stride, int64_t s0) {
+        const int64_t left = n - s0;
+        return kda::rows_in((const T *)base + (bos + s0) * stride, (int)(left < STEP ? left : STEP), stride, p.D);
+    };
+    Rows<T, VEC, BETA> next;
+    auto fetch = [&](int64_t s0) {
+        const auto xr = rows(p.x, p.xs, s0), gr = rows(p.g, p.gs, s0);
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            load(next.g[k], gr, (tok + k) * gs + d * E);
+            load(next.x[k], xr, (tok + k) * xs + d * E);
+        }
+        if constexpr (BETA) {
+            const auto br = rows(p.beta, p.bs, s0);
+#pragma unroll
+            for (int k = 0; k < K; ++k) load(next.b[k], br, (tok + k) * bs + d * E);
+        }
+    };
+    if (n > 0) fetch(0);
+    int buf = 0;
+    for (int64_t s0 = 0; s0 < n; s0 += STEP, buf ^= 1) {
+        const Rows<T, VEC, BETA> cur = next;
+        if (s0 + STEP < n) fetch(s0 + STEP);
+        float c[K][VEC], s[K][VEC], w[K][VEC], G[VEC], end[VEC], h[VEC];
+        const int64_t live = n - s0 - tok;      // tokens of the sequence from this lane's first on
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) {
+            const Gate<T> &gate = v ? gate1 : gate0;
+            G[v] = end[v] = 0.f;
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                float g = gate.active(value(cur.g[k], v));
+                if (p.pre.gate && k >= live) g = 0.f;
+                w[k][v] = value(cur.x[k], v);
+                if constexpr (BETA) {
+                    const float b = value(cur.b[k], v);
+                    w[k][v] *= p.pre.beta_sigmoid ? sigmoid<T>(b).s : b;
+                }
+                decay<T>(g, c[k][v], s[k][v]);
+                G[v] += g;
+                end[v] = fmaf(c[k][v], end[v], fmaf(s[k][v], end[v], w[k][v]));
+            }
+        }
+        join<T, LPR, VEC>(G, end, carry, h, tot[buf], wave, lane);
+        const auto yr = rows(p.y, p.D, s0);
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) h[v] = fmaf(c[k][v], h[v], fmaf(s[k][v], h[v], w[k][v]));
+            // channels past the last lie past every range
+            store<T, VEC>(h, yr, on ? (tok + k) * ys + d * E : 0x80000000u);
+        }
+    }
+    if (p.ht && on && tid < LPR) {
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) p.ht[(int64_t)seq * p.D + d + v] = carry[v];
+    }
+}
+
+__device__ __forceinline__ void put(uint16_t *y, const float (&h)[1]) { *y = (uint16_t)bf16_bits(h[0]); }
+__device__ __forceinline__ void put(uint16_t *y, const float (&h)[2]) { *(uint32_t *)y = bf16_bits(h[0]) | bf16_bits(h[1]) << 16; }
+__device__ __forceinline__ void put(float *y, const float (&h)[1]) { *y = h[0]; }
+__device__ __forceinline__ void put(float *y, const float (&h)[2]) { *(float2 *)y = make_float2(h[0], h[1]); }
+
+// A row's state on VEC channels a thread, its tokens one behind the other.
+template <typename T, int VEC>
+__global__ __launch_bounds__(256) void step_kernel(StepParams p)
+{
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, per = p.f.strips;
+    if (i >= p.B * per) return;
+    const int b = (int)(i / per), d = (int)(i % per) * VEC, D = p.f.D;
+    const int at = p.index ? p.index[b] : b;
+    const bool live = at >= 0 && at < p.slots;
+    float h[VEC];
+    Gate<T> gate[VEC];
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) {
+        h[v] = live ? p.state[(int64_t)at * D + d + v] : 0.f;
+        gate[v] = gate_of<T>(p.f.pre, d + v);
+    }
+    for (int t = 0; t < p.T; ++t) {
+        const int64_t tok = (int64_t)b * p.T + t;
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) {
+            if (live) {
+                const float g = gate[v].active(kda::to_f32(((const T *)p.f.g)[tok * p.f.gs + d + v]));
+                float w = kda::to_f32(((const T *)p.f.x)[tok * p.f.xs + d + v]), c, s;
+                if (p.f.beta) {
+                    const float x = kda::to_f32(((const T *)p.f.beta)[tok * p.f.bs + d + v]);
+                    w *= p.f.pre.beta_sigmoid ? sigmoid<T>(x).s : x;
+                }
+                decay<T>(g, c, s);
+                h[v] = fmaf(c, h[v], fmaf(s, h[v], w));
+            }
+        }
+        put((T *)p.f.y + tok * D + d, h);
+    }
+    if (live) {
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) p.state[(int64_t)at * D + d + v] = h[v];
+    }
+}
+
+template <typename T, int VEC, int LPR>
+hipError_t launch(const Params &p, hipStream_t st)
+{
+    const dim3 grid((unsigned)unit_grid(p.strips, p.seq.N, near_of(LPR * VEC * (int)sizeof(T))));
+    if (p.beta)
+        scan_kernel<T, VEC, LPR, true><<<grid, dim3(64 * W), 0, st>>>(p);
+    else
+        scan_kernel<T, VEC, LPR, false><<<grid, dim3(64 * W), 0, st>>>(p);
+    return hipGetLastError();
+}
+template <typename T>
+hipError_t launch_io(const Params &p, Shape s, hipStream_t st)
+{
+    if (s.vec == 2) return s.lanes == 8 ? launch<T, 2, 8>(p, st) : launch<T, 2, 32>(p, st);
+    return s.lanes == 8 ? launch<T, 1, 8>(p, st) : launch<T, 1, 32>(p, st);
+}
+
+}  // namespace
+
+hipError_t launch_fwd(const Params &p, Shape s, hipStream_t st)
+{
+    return s.f32 ? launch_io<float>(p, s, st) : launch_io<uint16_t>(p, s, st);
+}
+
+hipError_t launch_step(const StepParams &p, bool f32, int vec, hipStream_t st)
+{
+    const dim3 grid((unsigned)(((int64_t)p.B * p.f.strips + 255) / 256));
+    if (f32 && vec == 2) step_kernel<float, 2><<<grid, dim3(256), 0, st>>>(p);
+    else if (f32) step_kernel<float, 1><<<grid, dim3(256), 0, st>>>(p);
+    else if (vec == 2) step_kernel<uint16_t, 2><<<grid, dim3(256), 0, st>>>(p);
+    else step_kernel<uint16_t, 1><<<grid, dim3(256), 0, st>>>(p);
+    return hipGetLastError();
+}
+
+}  // namespace glr

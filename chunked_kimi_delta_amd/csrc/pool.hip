@@ -1,0 +1,296 @@
+// pool.hip -- slots of state pools copied, forked, freed and compacted (include/pool.h).
+//
+// What moves a state is one kernel: a launch goes over (pair, piece) items, a piece 16 KiB of one slot of
+// one pool, with 16 bytes a lane and load. Which slots, one workgroup decides ahead of it in a launch of its
+// own (prefix sums over `used`): the lists stay on the device.
+#include "pool.h"
+#include "kda_internal.h"
+
+namespace {
+
+constexpr int MAX_POOLS = 32, PIECE = 16384, MOST = 1 << 24;
+
+struct Pools {
+    uint8_t *to[MAX_POOLS];
+    const uint8_t *from[MAX_POOLS];
+    int64_t bytes[MAX_POOLS];
+    int32_t first[MAX_POOLS + 1];       // a pair's pieces: pool i has first[i] .. first[i + 1] - 1
+    int32_t n;
+};
+
+struct Pairs {
+    const int32_t *src, *dst;           // null: i
+    int32_t from_slots, to_slots;
+    int64_t n;
+    const int32_t *count;               // pairs, on the device (null: n)
+};
+
+enum Mode { COPY, MOVE, CLEAR };        // MOVE: the source is cleared behind the copy
+
+template <Mode M, typename U>
+__device__ __forceinline__ void piece_of(uint8_t *to, uint8_t *from, int len) {
+    const int n = len / (int)sizeof(U);
+    for (int i = threadIdx.x; i < n; i += 256) {
+        if (M != CLEAR) ((U *)to)[i] = ((const U *)from)[i];
+        if (M != COPY) ((U *)(M == MOVE ? from : to))[i] = 0;
+    }
+}
+
+// Whole 16-byte units, all of a thread's loads ahead of its stores.
+template <Mode M>
+__device__ __forceinline__ void piece16(uint8_t *to, uint8_t *from, int len) {
+    constexpr int N = PIECE / 4096;
+    const auto tr = kda::buffer_rsrc(to, len), fr = kda::buffer_rsrc(from, M == CLEAR ? 0 : len);
+    const int at = threadIdx.x * 16;
+    kda::u32x4 v[N] = {};
+    if (M != CLEAR) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = kda::bload16(fr, at + 4096 * i, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) kda::bstore16<0>(tr, at + 4096 * i, 0, v[i]);
+    if (M == MOVE) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) kda::bstore16<0>(fr, at + 4096 * i, 0, kda::u32x4{0, 0, 0, 0});
+    }
+}
+
+template <Mode M>
+__global__ __launch_bounds__(256) void slots_kernel(Pools p, Pairs q)
+{
+    const int64_t per = p.first[p.n], items = (q.count ? *q.count : q.n) * per;
+    for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+        const int64_t pair = item / per;
+        const int part = (int)(item - pair * per);
+        const int64_t a = q.src ? q.src[pair] : pair, b = q.dst ? q.dst[pair] : pair;
+        if (b < 0 || b >= q.to_slots) continue;
+        if (M != CLEAR && (a < 0 || a >= q.from_slots)) continue;
+        int j = 0;
+        while (j + 1 < p.n && part >= p.first[j + 1]) ++j;
+        const int64_t bytes = p.bytes[j], off = (int64_t)(part - p.first[j]) * PIECE;
+        const int len = (int)(bytes - off < PIECE ? bytes - off : PIECE);
+        uint8_t *const to = p.to[j] + b * bytes + off;
+        uint8_t *const from = M == CLEAR ? to : const_cast<uint8_t *>(p.from[j]) + a * bytes + off;
+        if (M != CLEAR && to == from) continue;
+        const uintptr_t unit = (uintptr_t)to | (uintptr_t)from | (uintptr_t)len;
+        if (unit % 16 == 0) piece16<M>(to, from, len);
+        else if (unit % 4 == 0) piece_of<M, uint32_t>(to, from, len);
+        else piece_of<M, uint8_t>(to, from, len);
+    }
+}
+
+// ----------------------------------------------------------------------------- one workgroup's plans
+
+constexpr int NT = 1024;
+
+// Rank of `on` among the workgroup's threads, behind `base`; base moves on by all of them. Two barriers.
+__device__ __forceinline__ int rank_of(bool on, int &base, int (&waves)[NT / 64]) {
+    const uint64_t b = __builtin_amdgcn_ballot_w64(on);
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    if (lane == 0) waves[wave] = __builtin_popcountll(b);
+    __syncthreads();
+    int r = base + __builtin_popcountll(b & ((1ull << lane) - 1)), all = 0;
+#pragma unroll
+    for (int w = 0; w < NT / 64; ++w) {
+        if (w < wave) r += waves[w];
+        all += waves[w];
+    }
+    base += all;
+    __syncthreads();
+    return r;
+}
+
+struct Fork {
+    uint8_t *used;
+    const int32_t *src;
+    int32_t *dst;
+    int64_t n;
+    int32_t slots, from_slots;
+    bool own;                           // the sources are the pools: a free slot is none
+};
+
+// dst first holds the free slots in order; then, from the last requests to the first, each request reads
+// its own (no later than at its own place, so what it overwrites is read already).
+__global__ __launch_bounds__(NT) void fork_kernel(Fork f)
+{
+    __shared__ int waves[NT / 64];
+    const int tid = threadIdx.x;
+    auto wants = [&](int64_t i) {
+        if (i >= f.n) return false;
+        if (!f.src) return f.own || i < f.from_slots;
+        const int s = f.src[i];
+        return s >= 0 && s < f.from_slots && (!f.own || f.used[s]);
+    };
+    int want = 0, free = 0;
+    for (int64_t i = 0; i < f.n; i += NT) rank_of(wants(i + tid), want, waves);
+    for (int64_t s = 0; s < f.slots && free < want; s += NT) {
+        const bool on = s + tid < f.slots && !f.used[s + tid];
+        const int r = rank_of(on, free, waves);
+        if (on && r < want) f.dst[r] = (int)s + tid;
+    }
+    __syncthreads();
+    int left = want;
+    for (int64_t i = (f.n - 1) / NT * NT; i >= 0; i -= NT) {
+        const bool on = wants(i + tid);
+        int here = 0;
+        int r = rank_of(on, here, waves);
+        r += left - here;
+        left -= here;
+        const int slot = on && r < free ? f.dst[r] : -1;
+        __syncthreads();
+        if (i + tid < f.n) f.dst[i + tid] = slot;
+        __syncthreads();
+    }
+    for (int64_t i = tid; i < f.n; i += NT)
+        if (f.dst[i] >= 0) f.used[f.dst[i]] = 1;
+}
+
+__global__ __launch_bounds__(256) void unuse_kernel(uint8_t *used, const int32_t *indices, int64_t n, int32_t slots)
+{
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i < n && indices[i] >= 0 && indices[i] < slots) used[indices[i]] = 0;
+}
+
+struct Compact {
+    uint8_t *used;
+    int32_t *indices, *count, *moves, *src, *dst, *place;   // place[slot]: its move, or -1
+    int64_t n;
+    int32_t slots;
+};
+
+__global__ __launch_bounds__(NT) void compact_kernel(Compact c)
+{
+    __shared__ int waves[NT / 64];
+    const int tid = threadIdx.x;
+    int live = 0, holes = 0, moves = 0;
+    for (int64_t s = 0; s < c.slots; s += NT) rank_of(s + tid < c.slots && c.used[s + tid], live, waves);
+    for (int64_t s0 = 0; s0 < c.slots; s0 += NT) {
+        const int s = (int)s0 + tid;
+        const bool in = s < c.slots, used = in && c.used[s], hole = in && !used && s < live, tail = used && s >= live;
+        const int h = rank_of(hole, holes, waves), t = rank_of(tail, moves, waves);
+        if (hole) c.dst[h] = s;
+        if (tail) c.src[t] = s;
+        if (in) {
+            c.place[s] = tail ? t : -1;
+            c.used[s] = s < live;
+        }
+    }
+    if (tid == 0) {
+        *c.count = live;
+        *c.moves = moves;
+    }
+    __syncthreads();
+    for (int64_t i = tid; i < c.n; i += NT) {
+        const int s = c.indices[i];
+        if (s >= 0 && s < c.slots && c.place[s] >= 0) c.indices[i] = c.dst[c.place[s]];
+    }
+}
+
+// ----------------------------------------------------------------------------- host side
+
+bool aligned(const void *p, uintptr_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
+
+kda_status check(const pool_ref *pools, int32_t n_pools, int32_t slots, const void *const *sources,
+                 int32_t source_slots, int64_t n)
+{
+    if (n_pools < 0 || slots < 0 || n < 0 || (n_pools > 0 && !pools) || (sources && source_slots < 0))
+        return KDA_ERR_INVALID_ARG;
+    if (slots > MOST || n > MOST || (sources && source_slots > MOST)) return KDA_ERR_UNSUPPORTED;
+    for (int i = 0; i < n_pools; ++i) {
+        if (pools[i].bytes < 1 || (slots > 0 && !pools[i].data)) return KDA_ERR_INVALID_ARG;
+        if (pools[i].bytes > (int64_t)1 << 40) return KDA_ERR_UNSUPPORTED;
+        if (sources && source_slots > 0 && !sources[i]) return KDA_ERR_INVALID_ARG;
+    }
+    return KDA_OK;
+}
+
+template <Mode M>
+kda_status move_slots(const pool_ref *pools, int32_t n_pools, const void *const *sources, const Pairs &q,
+                      hipStream_t st)
+{
+    if (q.n == 0) return KDA_OK;
+    for (int i0 = 0; i0 < n_pools; i0 += MAX_POOLS) {
+        Pools p = {};
+        int64_t pieces = 0;
+        for (int i = i0; i < n_pools && i < i0 + MAX_POOLS; ++i) {
+            p.to[p.n] = (uint8_t *)pools[i].data;
+            p.from[p.n] = sources ? (const uint8_t *)sources[i] : p.to[p.n];
+            p.bytes[p.n] = pools[i].bytes;
+            p.first[p.n] = (int32_t)pieces;
+            pieces += (pools[i].bytes + PIECE - 1) / PIECE;
+            if (pieces > INT32_MAX) return KDA_ERR_UNSUPPORTED;
+            p.first[++p.n] = (int32_t)pieces;
+        }
+        const int64_t items = q.n * pieces, grid = items < 16384 ? items : 16384;
+        slots_kernel<M><<<dim3((unsigned)grid), dim3(256), 0, st>>>(p, q);
+        if (hipGetLastError() != hipSuccess) return KDA_ERR_HIP;
+    }
+    return KDA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+kda_status pool_copy(const pool_ref *pools, int32_t n_pools, int32_t slots, const void *const *sources,
+                     int32_t source_slots, const int32_t *src, const int32_t *dst, int64_t n, void *stream)
+{
+    const kda_status st = check(pools, n_pools, slots, sources, source_slots, n);
+    if (st != KDA_OK) return st;
+    if (!aligned(src, 4) || !aligned(dst, 4)) return KDA_ERR_INVALID_ARG;
+    const Pairs q = {src, dst, sources ? source_slots : slots, slots, n, nullptr};
+    return move_slots<COPY>(pools, n_pools, sources, q, (hipStream_t)stream);
+}
+
+kda_status pool_fork(const pool_ref *pools, int32_t n_pools, int32_t slots, const void *const *sources,
+                     int32_t source_slots, uint8_t *used, const int32_t *src, int32_t *dst, int64_t n, void *stream)
+{
+    const kda_status st = check(pools, n_pools, slots, sources, source_slots, n);
+    if (st != KDA_OK) return st;
+    if ((slots > 0 && !used) || !aligned(src, 4) || !aligned(dst, 4) || (n > 0 && !dst)) return KDA_ERR_INVALID_ARG;
+    if (n == 0) return KDA_OK;
+    const Fork f = {used, src, dst, n, slots, sources ? source_slots : slots, !sources};
+    fork_kernel<<<dim3(1), dim3(NT), 0, (hipStream_t)stream>>>(f);
+    if (hipGetLastError() != hipSuccess) return KDA_ERR_HIP;
+    if (!src && !sources) return KDA_OK;
+    const Pairs q = {src, dst, f.from_slots, slots, n, nullptr};
+    return move_slots<COPY>(pools, n_pools, sources, q, (hipStream_t)stream);
+}
+
+kda_status pool_free(const pool_ref *pools, int32_t n_pools, int32_t slots, uint8_t *used, const int32_t *indices,
+                     int64_t n, void *stream)
+{
+    const kda_status st = check(pools, n_pools, slots, nullptr, 0, n);
+    if (st != KDA_OK) return st;
+    if ((slots > 0 && !used) || (n > 0 && !indices) || !aligned(indices, 4)) return KDA_ERR_INVALID_ARG;
+    if (n == 0) return KDA_OK;
+    unuse_kernel<<<dim3((unsigned)((n + 255) / 256)), dim3(256), 0, (hipStream_t)stream>>>(used, indices, n, slots);
+    if (hipGetLastError() != hipSuccess) return KDA_ERR_HIP;
+    const Pairs q = {nullptr, indices, 0, slots, n, nullptr};
+    return move_slots<CLEAR>(pools, n_pools, nullptr, q, (hipStream_t)stream);
+}
+
+size_t pool_compact_workspace_bytes(int32_t slots)
+{
+    if (slots < 0 || slots > MOST) return 0;
+    return (((size_t)slots * 12 + 4) + 255) / 256 * 256;
+}
+
+kda_status pool_compact(const pool_ref *pools, int32_t n_pools, int32_t slots, uint8_t *used, int32_t *indices,
+                        int64_t n, int32_t *count, void *workspace, size_t ws_bytes, void *stream)
+{
+    const kda_status st = check(pools, n_pools, slots, nullptr, 0, n);
+    if (st != KDA_OK) return st;
+    if ((slots > 0 && !used) || (n > 0 && !indices) || !aligned(indices, 4) || !count || !aligned(count, 4))
+        return KDA_ERR_INVALID_ARG;
+    if (!workspace || !aligned(workspace, 256) || ws_bytes < pool_compact_workspace_bytes(slots)) return KDA_ERR_WORKSPACE;
+    int32_t *const ws = (int32_t *)workspace;
+    const Compact c = {used, indices, count, ws, ws + 1, ws + 1 + slots, ws + 1 + 2 * (int64_t)slots, n, slots};
+    compact_kernel<<<dim3(1), dim3(NT), 0, (hipStream_t)stream>>>(c);
+    if (hipGetLastError() != hipSuccess) return KDA_ERR_HIP;
+    // at most half of the slots move
+    const Pairs q = {c.src, c.dst, slots, slots, slots / 2, c.moves};
+    return move_slots<MOVE>(pools, n_pools, nullptr, q, (hipStream_t)stream);
+}
+
+}  // extern "C"
