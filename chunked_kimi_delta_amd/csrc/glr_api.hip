@@ -64,9 +64,27 @@ int vec_of(const glr_args *a, bool x_read, const void *const *more, int n)
     return two ? 2 : 1;
 }
 
-// Narrow strips where wide ones would leave compute units without work.
-Shape shape_of(const glr_args *a, int vec)
+// Tiles that hand states to each other, or strips of whole sequences? Strips are one launch and no workspace (13 us a
+// call, tiles 18), but take a sequence's 512 tokens in 3 to 5 us however few strips there are, and a packed batch's
+// longest sequence alone. bf16, us, strips and tiles: 2048 tokens x 2048 channels 15 and 18 (gradients 20 and 22), 4096 x
+// 2048 25 and 21 (35 and 25), 4096 x 4096 27 and 30 (57 and 42; with raw gates 51 and 41; fp32 49 and 41), 131072 x 2048 943 and 373, 8 x 2048 x
+// 4096 90 and 99. Packed, 16 x 2048 tokens 183 and 197, 7 x 512 + 16384 tokens of 2048 channels 125 and 70; lengths lie on the
+// device, so raggedness is assumed.
+bool use_tiles(const glr_args *a, bool back)
 {
+    const int64_t tokens = (int64_t)a->B * a->T, mean = a->N > 0 ? tokens / a->N : 0;
+    if (a->cu_seqlens && a->N > 1) return mean >= 1024 && tokens >= 8192;
+    const bool fill = (int64_t)a->N * a->D >= 16 * (int64_t)kda::current_device_cus();  // narrow strips, every compute unit
+    return mean >= (fill && !back && !a->beta && a->io == KDA_BF16 ? 8192 : 4096);
+}
+
+// Lanes a token: 64 in tiles; 8 in narrow strips, where wide ones (32) would leave compute units without work.
+// Channels a lane: `vec`, but in tiles one where two would take the registers of a second workgroup on a compute unit (fp32
+// gradients 102 -> 71 us for 8192 x 2048, bf16 with beta 280 -> 250 for 4 x 8192 x 4096; without, 373 against 407 for 131072 x 2048;
+// bf16 gradients 324 -> 281 for 4 x 8192 x 4096, with beta 155 against 161 for 4 x 4096 x 2048).
+Shape shape_of(const glr_args *a, int vec, bool back)
+{
+    if (use_tiles(a, back)) return Shape{a->io == KDA_FP32, a->io == KDA_BF16 && back == (a->beta != nullptr) ? vec : 1, 64};
     const int64_t wide = (a->D + 32 * vec - 1) / (32 * vec) * (int64_t)a->N;
     return Shape{a->io == KDA_FP32, vec, wide >= 2 * kda::current_device_cus() ? 32 : 8};
 }
@@ -97,29 +115,54 @@ Params params_of(const glr_args *a, Shape s)
 bool fits(const glr_args *a, Shape s)
 {
     const int ch = s.vec * s.lanes;
-    return unit_grid((a->D + ch - 1) / ch, a->N, near_of(ch * (s.f32 ? 4 : 2))) < ((int64_t)1 << 32) / (64 * W);
+    const int64_t strips = (a->D + ch - 1) / ch, most = ((int64_t)1 << 32) - 1;
+    if (s.lanes == 64)          // tiles of at least 64 tokens, workgroups of at most 512 threads
+        return (((int64_t)a->B * a->T) / 64 + a->N) * strips <= most / 512;
+    return unit_grid(strips, a->N, near_of(ch * (s.f32 ? 4 : 2))) <= most / (64 * W);
+}
+
+// Workspace of the tiles for either number of channels a lane (alignments are not known yet).
+size_t tiles_workspace(const glr_args *a, bool back)
+{
+    int64_t most = 0;
+    for (int vec = 1; vec <= 2; ++vec) {
+        const Shape s = {a->io == KDA_FP32, vec, 64};
+        const Params p = params_of(a, s);
+        const int64_t n = back ? tiles_back_bytes(p, s) : tiles_bytes(p, s);
+        most = n > most ? n : most;
+    }
+    return align256((size_t)most);
 }
 
 }  // namespace
 
 extern "C" {
 
-size_t glr_fwd_workspace_bytes(const glr_args *) { return 0; }
+size_t glr_fwd_workspace_bytes(const glr_args *a)
+{
+    return check_shapes(a) == KDA_OK && use_tiles(a, false) ? tiles_workspace(a, false) : 0;
+}
 
-kda_status glr_fwd(const glr_args *a, void *, size_t, void *stream)
+kda_status glr_fwd(const glr_args *a, void *workspace, size_t ws_bytes, void *stream)
 {
     kda_status st = check_shapes(a);
     if (st != KDA_OK || (st = check_tensors(a, true)) != KDA_OK) return st;
-    const Shape s = shape_of(a, vec_of(a, true, nullptr, 0));
+    const Shape s = shape_of(a, vec_of(a, true, nullptr, 0), false);
     if (!fits(a, s)) return KDA_ERR_UNSUPPORTED;
+    const size_t need = glr_fwd_workspace_bytes(a);
+    if (need && (!workspace || ws_bytes < need || !aligned(workspace, 256))) return KDA_ERR_WORKSPACE;
     if (a->N == 0) return KDA_OK;
-    return launch_fwd(params_of(a, s), s, (hipStream_t)stream) == hipSuccess ? KDA_OK : KDA_ERR_HIP;
+    const Params p = params_of(a, s);
+    hipStream_t hs = (hipStream_t)stream;
+    return (s.lanes == 64 ? launch_fwd_tiles(p, s, workspace, hs) : launch_fwd(p, s, hs)) == hipSuccess ? KDA_OK : KDA_ERR_HIP;
 }
 
 size_t glr_bwd_workspace_bytes(const glr_args *a)
 {
-    if (check_shapes(a) != KDA_OK || a->gate == KDA_GATE_NONE) return 0;
-    return 2 * align256((size_t)a->N * a->D * 4);
+    if (check_shapes(a) != KDA_OK) return 0;
+    const bool tiles = use_tiles(a, true);
+    const int64_t rows = tiles ? tiles_back_rows(params_of(a, Shape{a->io == KDA_FP32, 1, 64})) : a->N;
+    return (a->gate ? 2 * align256((size_t)rows * a->D * 4) : 0) + (tiles ? tiles_workspace(a, true) : 0);
 }
 
 kda_status glr_bwd(const glr_args *a, const void *d_y, const float *dht, void *workspace, size_t ws_bytes,
@@ -135,7 +178,7 @@ kda_status glr_bwd(const glr_args *a, const void *d_y, const float *dht, void *w
             if (!p || !aligned(p, e)) return KDA_ERR_INVALID_ARG;
     if (!aligned(dht, 4) || !aligned(dh0, 4)) return KDA_ERR_INVALID_ARG;
     if (gated && (!dA_log || !aligned(dA_log, 4) || !aligned(ddt_bias, 4))) return KDA_ERR_INVALID_ARG;
-    const Shape s = shape_of(a, vec_of(a, a->beta != nullptr, io, 4));
+    const Shape s = shape_of(a, vec_of(a, a->beta != nullptr, io, 4), true);
     if (!fits(a, s)) return KDA_ERR_UNSUPPORTED;
     const size_t need = glr_bwd_workspace_bytes(a);
     if (need && (!workspace || ws_bytes < need || !aligned(workspace, 256))) return KDA_ERR_WORKSPACE;
@@ -147,11 +190,15 @@ kda_status glr_bwd(const glr_args *a, const void *d_y, const float *dht, void *w
     q.dg = dg;
     q.dbeta = dbeta;
     q.dh0 = dh0;
-    q.part_A = (float *)workspace;
-    q.part_b = (float *)((uint8_t *)workspace + need / 2);
+    const bool tiles = s.lanes == 64;
+    const int64_t rows = tiles ? tiles_back_rows(q.f) : a->N;
+    const size_t part = gated ? align256((size_t)rows * a->D * 4) : 0;
+    uint8_t *const ws = (uint8_t *)workspace;
+    q.part_A = (float *)ws;
+    q.part_b = (float *)(ws + part);
     hipStream_t hs = (hipStream_t)stream;
-    if (a->N > 0 && launch_bwd(q, s, hs) != hipSuccess) return KDA_ERR_HIP;
-    if (gated && launch_params(q, dA_log, ddt_bias, hs) != hipSuccess) return KDA_ERR_HIP;
+    if (a->N > 0 && (tiles ? launch_bwd_tiles(q, s, ws + 2 * part, hs) : launch_bwd(q, s, hs)) != hipSuccess) return KDA_ERR_HIP;
+    if (gated && launch_params(q, rows, dA_log, ddt_bias, hs) != hipSuccess) return KDA_ERR_HIP;
     return KDA_OK;
 }
 

@@ -23,7 +23,9 @@ __global__ __launch_bounds__(64 * W) void scan_back_kernel(BwdParams q)
     const int ch = strip * CH + lane % LPR * VEC;
     const bool on = ch < p.D, gated = p.pre.gate != 0;
     const int d = on ? ch : 0, tok = (wave * R + lane / LPR) * K;
-    const Gate<T> gate0 = gate_of<T>(p.pre, d), gate1 = gate_of<T>(p.pre, VEC == 2 && on ? ch + 1 : d);
+    Gate gate[VEC];
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) gate[v] = gate_of(p.pre, d + v);
     float carry[VEC], first[VEC];           // m, and the state ahead of the first token
     double dA[VEC], db[VEC];
 #pragma unroll
@@ -34,7 +36,7 @@ __global__ __launch_bounds__(64 * W) void scan_back_kernel(BwdParams q)
     }
     // A step takes the rows [max(lo, 0), hi) of the sequence, hi = n - s0 and lo = hi - STEP; token k of a
     // lane is row hi - 1 - tok - k, and rows before the sequence lie past every range (as unsigned
-    // offsets).
+    // offsets below zero).
     const uint32_t ds = (uint32_t)p.D * E;
     auto rows = [&](const void *base, int64_t stride, int64_t at, int64_t hi) {
         return kda::rows_in((const T *)base + (bos + at) * stride, (int)(hi - at), stride, p.D);
@@ -43,11 +45,11 @@ __global__ __launch_bounds__(64 * W) void scan_back_kernel(BwdParams q)
     auto fetch = [&](int64_t s0) {
         const int64_t hi = n - s0, at = hi > STEP ? hi - STEP : 0;
         const auto gr = rows(p.g, p.gs, at, hi), dr = rows(q.d_y, p.D, at, hi);
-        const int row = (int)(hi - at) - 1 - tok;
+        const uint32_t row = (uint32_t)((int)(hi - at) - 1 - tok), gs = (uint32_t)p.gs * E;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            load(ng[k], gr, row - k < 0 ? 0x80000000u : (uint32_t)(row - k) * (uint32_t)p.gs * E + d * E);
-            load(nd[k], dr, row - k < 0 ? 0x80000000u : (uint32_t)(row - k) * ds + d * E);
+            load(ng[k], gr, row * gs + d * E - k * gs);
+            load(nd[k], dr, row * ds + d * E - k * ds);
         }
     };
     if (n > 0) fetch(0);
@@ -66,67 +68,68 @@ __global__ __launch_bounds__(64 * W) void scan_back_kernel(BwdParams q)
         const auto yr = rows(p.y, p.D, yat, hi);
         const int yrow = row - (at > 0 ? 0 : 1);
 #pragma unroll
-        for (int k = 0; k < K; ++k) load(cy[k], yr, yrow - k < 0 ? 0x80000000u : (uint32_t)(yrow - k) * ds + d * E);
+        for (int k = 0; k < K; ++k) load(cy[k], yr, (uint32_t)yrow * ds + d * E - k * ds);
         if constexpr (BETA) {
             const auto xr = rows(p.x, p.xs, at, hi), br = rows(p.beta, p.bs, at, hi);
+            const uint32_t xs = (uint32_t)p.xs * E, bs = (uint32_t)p.bs * E;
 #pragma unroll
             for (int k = 0; k < K; ++k) {
-                load(cx[k], xr, row - k < 0 ? 0x80000000u : (uint32_t)(row - k) * (uint32_t)p.xs * E + d * E);
-                load(cb[k], br, row - k < 0 ? 0x80000000u : (uint32_t)(row - k) * (uint32_t)p.bs * E + d * E);
+                load(cx[k], xr, (uint32_t)row * xs + d * E - k * xs);
+                load(cb[k], br, (uint32_t)row * bs + d * E - k * bs);
             }
         }
         if (s0 + STEP < n) fetch(s0 + STEP);
-        float c[K][VEC], s[K][VEC], G[VEC], end[VEC], m[VEC];
+        float c[K][VEC], act[K][VEC], G[VEC], end[VEC], m[VEC], least, most;
+        log_decays<T>(cg, gate, p.pre.gate, row + 1, c, G, least, most);
 #pragma unroll
-        for (int v = 0; v < VEC; ++v) {
-            const Gate<T> &gate = v ? gate1 : gate0;
-            G[v] = end[v] = 0.f;
+        for (int k = 0; k < K; ++k)
 #pragma unroll
-            for (int k = 0; k < K; ++k) {
-                float g = gate.active(value(cg[k], v));
-                if (gated && k > row) g = 0.f;
-                decay<T>(g, c[k][v], s[k][v]);
-                G[v] += g;
-                const float u = end[v] + value(cd[k], v);
-                end[v] = fmaf(c[k][v], u, s[k][v] * u);
+            for (int v = 0; v < VEC; ++v) act[k][v] = c[k][v];
+        const Form form = form_of<T>(least, most);
+        uint32_t s = 0;
+        by_form(form, [&](auto f) {
+            constexpr Form F = decltype(f)::value;
+            s = decays<T, F>(c);
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) {
+                end[v] = 0.f;
+#pragma unroll
+                for (int k = 0; k < K; ++k) end[v] = apply<F>(c[k][v], s, k * VEC + v, end[v] + value(cd[k], v), 0.f);
             }
-        }
+        });
         join<T, LPR, VEC>(G, end, carry, m, tot[buf], wave, lane);
         const auto dxr = rows(q.dx, p.D, at, hi), dgr = rows(q.dg, p.D, at, hi), dbr = rows(BETA ? q.dbeta : q.dx, p.D, at, hi);
+        const uint32_t o0 = on ? (uint32_t)row * ds + d * E : PAST;
         float sA[VEC], sb[VEC];
 #pragma unroll
         for (int v = 0; v < VEC; ++v) sA[v] = sb[v] = 0.f;
+        by_kind(p.pre.gate, [&](auto kind) { by_form(form, [&](auto f) {
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-            float dx[VEC], dg[VEC], dbt[VEC];
+            for (int k = 0; k < K; ++k) {
+                float dx[VEC], dg[VEC], dbt[VEC];
 #pragma unroll
-            for (int v = 0; v < VEC; ++v) {
-                const Gate<T> &gate = v ? gate1 : gate0;
-                const float dh = value(cd[k], v) + m[v];
-                m[v] = fmaf(c[k][v], dh, s[k][v] * dh);
-                const float before = yrow - k == -1 && at == 0 ? first[v] : value(cy[k], v);
-                dx[v] = dh;
-                dg[v] = before * m[v];
-                if constexpr (BETA) {
-                    const float b = value(cb[k], v);
-                    const Sigmoid r = p.pre.beta_sigmoid ? sigmoid<T>(b) : Sigmoid{b, 1.f};
-                    dx[v] *= r.s;
-                    dbt[v] = value(cx[k], v) * dh * r.ds;
-                }
-                if (gated) {
-                    float a = 0.f, o = 0.f;
-                    dg[v] = gate.back(value(cg[k], v), dg[v], a, o);
-                    if (k <= row) {
-                        sA[v] += a;
-                        sb[v] += o;
+                for (int v = 0; v < VEC; ++v) {
+                    const float dh = value(cd[k], v) + m[v];
+                    m[v] = apply<decltype(f)::value>(c[k][v], s, k * VEC + v, dh, 0.f);
+                    const float before = yrow - k == -1 && at == 0 ? first[v] : value(cy[k], v);
+                    dx[v] = dh;
+                    dg[v] = before * m[v];
+                    if constexpr (BETA) {
+                        const float b = value(cb[k], v);
+                        const Sigmoid r = p.pre.beta_sigmoid ? sigmoid<T>(b) : Sigmoid{b, 1.f};
+                        dx[v] *= r.s;
+                        dbt[v] = value(cx[k], v) * dh * r.ds;
                     }
+                    // (behind a sequence's end m is no token's gradient)
+                    if (decltype(kind)::value != NONE)
+                        dg[v] = gate[v].template back<T, decltype(kind)::value>(value(cg[k], v), act[k][v], k <= row ? dg[v] : 0.f, sA[v], sb[v]);
                 }
+                const uint32_t off = o0 - k * ds;
+                store<T, VEC>(dx, dxr, off);
+                store<T, VEC>(dg, dgr, off);
+                if constexpr (BETA) store<T, VEC>(dbt, dbr, off);
             }
-            const uint32_t off = on && row - k >= 0 ? (uint32_t)(row - k) * ds + d * E : 0x80000000u;
-            store<T, VEC>(dx, dxr, off);
-            store<T, VEC>(dg, dgr, off);
-            if constexpr (BETA) store<T, VEC>(dbt, dbr, off);
-        }
+        }); });
 #pragma unroll
         for (int v = 0; v < VEC; ++v) {
             dA[v] += sA[v];
@@ -160,19 +163,29 @@ __global__ __launch_bounds__(64 * W) void scan_back_kernel(BwdParams q)
     }
 }
 
-// The sums of all sequences.
-__global__ __launch_bounds__(256) void params_kernel(const float *part_A, const float *part_b, int N, int D,
-                                                     float *dA_log, float *ddt_bias)
+// The sums of all rows of partial sums: 64 channels a workgroup, every sixteenth row a wave.
+__global__ __launch_bounds__(1024) void params_kernel(const float *part_A, const float *part_b, int64_t rows, int D,
+                                                      float *dA_log, float *ddt_bias)
 {
-    const int d = blockIdx.x * 256 + threadIdx.x;
-    if (d >= D) return;
+    __shared__ double sums[2][16][64];
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, d = blockIdx.x * 64 + lane;
     double a = 0.0, b = 0.0;
-    for (int i = 0; i < N; ++i) {
-        a += part_A[(int64_t)i * D + d];
-        b += part_b[(int64_t)i * D + d];
+    if (d < D) {
+#pragma unroll 4
+        for (int64_t i = wave; i < rows; i += 16) {
+            a += part_A[i * D + d];
+            b += part_b[i * D + d];
+        }
     }
-    dA_log[d] = (float)a;
-    if (ddt_bias) ddt_bias[d] = (float)b;
+    sums[0][wave][lane] = a;
+    sums[1][wave][lane] = b;
+    __syncthreads();
+    if (wave > 1 || d >= D) return;
+    double x = 0.0;
+#pragma unroll
+    for (int w = 0; w < 16; ++w) x += sums[wave][w][lane];
+    if (wave == 0) dA_log[d] = (float)x;
+    else if (ddt_bias) ddt_bias[d] = (float)x;
 }
 
 template <typename T, int VEC, int LPR>
@@ -199,9 +212,9 @@ hipError_t launch_bwd(const BwdParams &q, Shape s, hipStream_t st)
     return s.f32 ? launch_io<float>(q, s, st) : launch_io<uint16_t>(q, s, st);
 }
 
-hipError_t launch_params(const BwdParams &q, float *dA_log, float *ddt_bias, hipStream_t st)
+hipError_t launch_params(const BwdParams &q, int64_t rows, float *dA_log, float *ddt_bias, hipStream_t st)
 {
-    params_kernel<<<dim3((q.f.D + 255) / 256), dim3(256), 0, st>>>(q.part_A, q.part_b, q.f.seq.N, q.f.D, dA_log, ddt_bias);
+    params_kernel<<<dim3((q.f.D + 63) / 64), dim3(1024), 0, st>>>(q.part_A, q.part_b, rows, q.f.D, dA_log, ddt_bias);
     return hipGetLastError();
 }
 

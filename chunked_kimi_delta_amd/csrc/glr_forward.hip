@@ -23,7 +23,9 @@ __global__ __launch_bounds__(64 * W) void scan_kernel(Params p)
     const int ch = strip * CH + lane % LPR * VEC;
     const bool on = ch < p.D;
     const int d = on ? ch : 0, tok = (wave * R + lane / LPR) * K;
-    const Gate<T> gate0 = gate_of<T>(p.pre, d), gate1 = gate_of<T>(p.pre, VEC == 2 && on ? ch + 1 : d);
+    Gate gate[VEC];
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) gate[v] = gate_of(p.pre, d + v);
     float carry[VEC];
 #pragma unroll
     for (int v = 0; v < VEC; ++v) carry[v] = p.h0 && on ? p.h0[(int64_t)seq * p.D + d + v] : 0.f;
@@ -37,15 +39,17 @@ __global__ __launch_bounds__(64 * W) void scan_kernel(Params p)
     Rows<T, VEC, BETA> next;
     auto fetch = [&](int64_t s0) {
         const auto xr = rows(p.x, p.xs, s0), gr = rows(p.g, p.gs, s0);
+        const uint32_t g0 = opaque(tok * gs + d * E), x0 = opaque(tok * xs + d * E);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            load(next.g[k], gr, (tok + k) * gs + d * E);
-            load(next.x[k], xr, (tok + k) * xs + d * E);
+            load(next.g[k], gr, g0 + k * gs);
+            load(next.x[k], xr, x0 + k * xs);
         }
         if constexpr (BETA) {
             const auto br = rows(p.beta, p.bs, s0);
+            const uint32_t b0 = opaque(tok * bs + d * E);
 #pragma unroll
-            for (int k = 0; k < K; ++k) load(next.b[k], br, (tok + k) * bs + d * E);
+            for (int k = 0; k < K; ++k) load(next.b[k], br, b0 + k * bs);
         }
     };
     if (n > 0) fetch(0);
@@ -53,35 +57,36 @@ __global__ __launch_bounds__(64 * W) void scan_kernel(Params p)
     for (int64_t s0 = 0; s0 < n; s0 += STEP, buf ^= 1) {
         const Rows<T, VEC, BETA> cur = next;
         if (s0 + STEP < n) fetch(s0 + STEP);
-        float c[K][VEC], s[K][VEC], w[K][VEC], G[VEC], end[VEC], h[VEC];
-        const int64_t live = n - s0 - tok;      // tokens of the sequence from this lane's first on
+        float c[K][VEC], w[BETA ? K : 1][VEC], G[VEC], end[VEC], h[VEC], least, most;
+        log_decays<T>(cur.g, gate, p.pre.gate, (int)(n - s0 < STEP ? n - s0 : STEP) - tok, c, G, least, most);
+        if constexpr (BETA) gated_inputs<T>(cur.x, cur.b, p.pre.beta_sigmoid, w);
+        auto in = [&](int k, int v) {
+            if constexpr (BETA) return w[k][v]; else return value(cur.x[k], v);
+        };
+        const Form form = form_of<T>(least, most);
+        uint32_t s = 0;
+        auto local = [&](auto f) {
+            constexpr Form F = decltype(f)::value;
+            s = decays<T, F>(c);
 #pragma unroll
-        for (int v = 0; v < VEC; ++v) {
-            const Gate<T> &gate = v ? gate1 : gate0;
-            G[v] = end[v] = 0.f;
+            for (int v = 0; v < VEC; ++v) {
+                end[v] = in(0, v);
 #pragma unroll
-            for (int k = 0; k < K; ++k) {
-                float g = gate.active(value(cur.g[k], v));
-                if (p.pre.gate && k >= live) g = 0.f;
-                w[k][v] = value(cur.x[k], v);
-                if constexpr (BETA) {
-                    const float b = value(cur.b[k], v);
-                    w[k][v] *= p.pre.beta_sigmoid ? sigmoid<T>(b).s : b;
-                }
-                decay<T>(g, c[k][v], s[k][v]);
-                G[v] += g;
-                end[v] = fmaf(c[k][v], end[v], fmaf(s[k][v], end[v], w[k][v]));
+                for (int k = 1; k < K; ++k) end[v] = apply<F>(c[k][v], s, k * VEC + v, end[v], in(k, v));
             }
-        }
+        };
+        by_form(form, local);
         join<T, LPR, VEC>(G, end, carry, h, tot[buf], wave, lane);
         const auto yr = rows(p.y, p.D, s0);
+        const uint32_t y0 = opaque(on ? tok * ys + d * E : PAST);    // channels past the last lie past every range
+        by_form(form, [&](auto f) {
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
+            for (int k = 0; k < K; ++k) {
 #pragma unroll
-            for (int v = 0; v < VEC; ++v) h[v] = fmaf(c[k][v], h[v], fmaf(s[k][v], h[v], w[k][v]));
-            // channels past the last lie past every range
-            store<T, VEC>(h, yr, on ? (tok + k) * ys + d * E : 0x80000000u);
-        }
+                for (int v = 0; v < VEC; ++v) h[v] = apply<decltype(f)::value>(c[k][v], s, k * VEC + v, h[v], in(k, v));
+                store<T, VEC>(h, yr, y0 + k * ys);
+            }
+        });
     }
     if (p.ht && on && tid < LPR) {
 #pragma unroll
@@ -90,7 +95,7 @@ __global__ __launch_bounds__(64 * W) void scan_kernel(Params p)
 }
 
 __device__ __forceinline__ void put(uint16_t *y, const float (&h)[1]) { *y = (uint16_t)bf16_bits(h[0]); }
-__device__ __forceinline__ void put(uint16_t *y, const float (&h)[2]) { *(uint32_t *)y = bf16_bits(h[0]) | bf16_bits(h[1]) << 16; }
+__device__ __forceinline__ void put(uint16_t *y, const float (&h)[2]) { *(uint32_t *)y = bf16_bits(h[0], h[1]); }
 __device__ __forceinline__ void put(float *y, const float (&h)[1]) { *y = h[0]; }
 __device__ __forceinline__ void put(float *y, const float (&h)[2]) { *(float2 *)y = make_float2(h[0], h[1]); }
 
@@ -104,22 +109,23 @@ __global__ __launch_bounds__(256) void step_kernel(StepParams p)
     const int at = p.index ? p.index[b] : b;
     const bool live = at >= 0 && at < p.slots;
     float h[VEC];
-    Gate<T> gate[VEC];
+    Gate gate[VEC];
 #pragma unroll
     for (int v = 0; v < VEC; ++v) {
         h[v] = live ? p.state[(int64_t)at * D + d + v] : 0.f;
-        gate[v] = gate_of<T>(p.f.pre, d + v);
+        gate[v] = gate_of(p.f.pre, d + v);
     }
     for (int t = 0; t < p.T; ++t) {
         const int64_t tok = (int64_t)b * p.T + t;
 #pragma unroll
         for (int v = 0; v < VEC; ++v) {
             if (live) {
-                const float g = gate[v].active(kda::to_f32(((const T *)p.f.g)[tok * p.f.gs + d + v]));
+                float g = kda::to_f32(((const T *)p.f.g)[tok * p.f.gs + d + v]);
+                by_kind(p.f.pre.gate, [&](auto n) { g = gate[v].template active<T, decltype(n)::value>(g); });
                 float w = kda::to_f32(((const T *)p.f.x)[tok * p.f.xs + d + v]), c, s;
                 if (p.f.beta) {
                     const float x = kda::to_f32(((const T *)p.f.beta)[tok * p.f.bs + d + v]);
-                    w *= p.f.pre.beta_sigmoid ? sigmoid<T>(x).s : x;
+                    w *= p.f.pre.beta_sigmoid ? logistic<T>(x) : x;
                 }
                 decay<T>(g, c, s);
                 h[v] = fmaf(c, h[v], fmaf(s, h[v], w));

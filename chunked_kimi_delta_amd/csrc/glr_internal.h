@@ -7,6 +7,8 @@
 // distance from 1 to 24 bits as well as a itself.
 #pragma once
 
+#include <type_traits>
+
 #include "glr.h"
 #include "kda_internal.h"
 
@@ -35,7 +37,7 @@ struct BwdParams {
     const float *dht;
     void *dx, *dg, *dbeta;
     float *dh0;
-    float *part_A, *part_b;             // [N][D] a sequence's sums for dA_log and ddt_bias
+    float *part_A, *part_b;             // [rows][D] sums for dA_log and ddt_bias: of a sequence, or of a tile's slot
 };
 
 struct StepParams {
@@ -47,16 +49,50 @@ struct StepParams {
 
 // ----------------------------------------------------------------------------- scalar functions
 //
-// bf16 io takes the hardware's base-2 functions (1 ulp each), fp32 io the library's: an fp32 output
-// shows what a product with log2 e rounds away from a large argument, a bf16 one does not.
+// On the hardware's base-2 exponential and its reciprocal (1 ulp each). fp32 io adds what the product
+// with log2 e rounds away and a Newton step, since an fp32 output would show them; bf16 io does not.
 
-template <typename T> __device__ __forceinline__ float exp_(float x);
-template <> __device__ __forceinline__ float exp_<uint16_t>(float x) { return __builtin_amdgcn_exp2f(x * kda::LOG2E); }
-template <> __device__ __forceinline__ float exp_<float>(float x) { return expf(x); }
-
-template <typename T> __device__ __forceinline__ float inverse(float x);
-template <> __device__ __forceinline__ float inverse<uint16_t>(float x) { return __builtin_amdgcn_rcpf(x); }
-template <> __device__ __forceinline__ float inverse<float>(float x) { return 1.f / x; }
+template <typename T>
+__device__ __forceinline__ float exp_(float x) {
+    const float t = x * kda::LOG2E, r = __builtin_amdgcn_exp2f(t);
+    if constexpr (sizeof(T) == 2) return r;
+    // x log2 e = t + lo; behind the finite exponentials lo must not make a NaN of infinities
+    const float lo = fmaf(x, 1.925963033500931e-8f, fmaf(x, kda::LOG2E, -t));
+    return fabsf(t) < 160.f ? fmaf(r, lo * 0.6931471805599453f, r) : r;
+}
+template <typename T>
+__device__ __forceinline__ float inverse(float x) {     // of x in [1, 2]
+    const float r = __builtin_amdgcn_rcpf(x);
+    if constexpr (sizeof(T) == 2) return r;
+    return fmaf(fmaf(-x, r, 1.f), r, r);
+}
+// log(1 + e) of e in [0, 1]: e p(e), p fitted there (bf16 io 2^-22 of it off, fp32 io 2^-24)
+template <typename T>
+__device__ __forceinline__ float log1p_(float e) {
+    float p;
+    if constexpr (sizeof(T) == 2) {
+        p = -0.00857467577f;
+        p = fmaf(p, e, 0.0442141928f);
+        p = fmaf(p, e, -0.107853681f);
+        p = fmaf(p, e, 0.177570239f);
+        p = fmaf(p, e, -0.244996116f);
+        p = fmaf(p, e, 0.332761765f);
+        p = fmaf(p, e, -0.499974489f);
+        p = fmaf(p, e, 0.999999821f);
+    } else {
+        p = -0.00325637846f;
+        p = fmaf(p, e, 0.0199071616f);
+        p = fmaf(p, e, -0.0570642017f);
+        p = fmaf(p, e, 0.106142648f);
+        p = fmaf(p, e, -0.153118625f);
+        p = fmaf(p, e, 0.196781173f);
+        p = fmaf(p, e, -0.249545589f);
+        p = fmaf(p, e, 0.333300054f);
+        p = fmaf(p, e, -0.499999046f);
+        p = fmaf(p, e, 1.f);
+    }
+    return e * p;
+}
 
 // sigmoid and its derivative from e^-|x|, each to a few roundings of itself
 struct Sigmoid {
@@ -68,59 +104,67 @@ __device__ __forceinline__ Sigmoid sigmoid(float x) {
     return Sigmoid{x < 0.f ? o : r, o * r};
 }
 
-// e^g as (c, s). On (-1/2, 0] e^g - 1 = g + g^2 q(g), with a q of degree 4 fitted there (2^-26 of
-// e^g - 1 off).
+// the sigmoid alone
 template <typename T>
-__device__ __forceinline__ void decay(float g, float &c, float &s) {
+__device__ __forceinline__ float logistic(float x) {
+    if constexpr (sizeof(T) == 2) return __builtin_amdgcn_rcpf(1.f + exp_<T>(-x));
+    return sigmoid<T>(x).s;
+}
+
+// e^g - 1 for g in [-1/2, 0]: g + g^2 q(g), q fitted there (2^-26 of the whole off)
+__device__ __forceinline__ float expm1_slow(float g) {
     float q = 0.0011646067f;
     q = fmaf(q, g, 0.008238542f);
     q = fmaf(q, g, 0.04165003f);
     q = fmaf(q, g, 0.16666564f);
     q = fmaf(q, g, 0.5f);
-    const bool slow = g > -0.5f && g <= 0.f;
-    c = slow ? fmaf(g * g, q, g) : exp_<T>(g);
+    return fmaf(g * g, q, g);
+}
+
+// e^g as (c, s)
+template <typename T>
+__device__ __forceinline__ void decay(float g, float &c, float &s) {
+    const bool slow = fabsf(g + 0.25f) <= 0.25f;
+    float d = expm1_slow(g), a = exp_<T>(g);
+    asm("" : "+v"(d), "+v"(a));         // both, and no branch around either
+    c = slow ? d : a;
     s = slow ? 1.f : 0.f;
 }
 
-// A channel's gate. active() is the log decay of a raw input; back() takes the gradient of the active
-// decay to that of the raw input and adds to the gradients of A_log and dt_bias.
-template <typename T>
+// A channel's gate. active() is the log decay of a raw input; back() takes the gradient dg of the active
+// decay `act` to that of the raw input and adds to the gradients of A_log and dt_bias. The kind is a type, so
+// that a lane's tokens go through one branch together.
+enum Kind { NONE, SOFTPLUS, BOUNDED };
+
 struct Gate {
-    int kind;
     float ea, bias, lb;
 
-    // log(1 + e^u) from e = e^-|u|: log1p(e) = log w + (e - (w - 1)) / w, w = 1 + e rounded
-    __device__ __forceinline__ float softplus(float u) const {
-        if constexpr (sizeof(T) == 4) {
-            return fmaxf(u, 0.f) + log1pf(expf(-fabsf(u)));
-        } else {
-            const float e = exp_<T>(-fabsf(u)), w = 1.f + e;
-            return fmaxf(u, 0.f) + fmaf(__builtin_amdgcn_logf(w), 0.6931471805599453f, (e - (w - 1.f)) * inverse<T>(w));
-        }
-    }
+    template <typename T, Kind N>
     __device__ __forceinline__ float active(float g) const {
-        if (kind == 0) return g;
+        if (N == NONE) return g;
         const float u = g + bias;
-        return kind == 1 ? -ea * softplus(u) : lb * sigmoid<T>(ea * u).s;
+        if (N == SOFTPLUS) return -ea * (fmaxf(u, 0.f) + log1p_<T>(exp_<T>(-fabsf(u))));
+        return lb * logistic<T>(ea * u);
     }
-    __device__ __forceinline__ float back(float g, float dg, float &dA, float &db) const {
+    template <typename T, Kind N>
+    __device__ __forceinline__ float back(float g, float act, float dg, float &dA, float &db) const {
+        if (N == NONE) return dg;
         const float u = g + bias;
-        if (kind == 1) {
-            const float du = -ea * sigmoid<T>(u).s * dg;
-            dA -= ea * softplus(u) * dg;
-            db += du;
-            return du;
-        }
-        const float du = ea * lb * sigmoid<T>(ea * u).ds * dg;
-        dA += du * u;
+        const float du = N == SOFTPLUS ? -ea * logistic<T>(u) * dg : ea * lb * sigmoid<T>(ea * u).ds * dg;
+        dA += N == SOFTPLUS ? act * dg : du * u;
         db += du;
         return du;
     }
 };
+template <class Fn>
+__device__ __forceinline__ void by_kind(int kind, Fn fn) {
+    if (kind == 0) fn(std::integral_constant<Kind, NONE>());
+    else if (kind == 1) fn(std::integral_constant<Kind, SOFTPLUS>());
+    else fn(std::integral_constant<Kind, BOUNDED>());
+}
 
-template <typename T>
-__device__ __forceinline__ Gate<T> gate_of(const Pre &pre, int d) {
-    Gate<T> g = {pre.gate, 1.f, 0.f, pre.lower_bound};
+__device__ __forceinline__ Gate gate_of(const Pre &pre, int d) {
+    Gate g = {1.f, 0.f, pre.lower_bound};
     if (pre.gate) {
         g.ea = expf(pre.A_log[d]);
         if (pre.dt_bias) g.bias = pre.dt_bias[d];
@@ -132,6 +176,9 @@ __device__ __forceinline__ Gate<T> gate_of(const Pre &pre, int d) {
 //
 // VEC neighbouring channels of one token, as they are stored; loads past a resource's range give zeros,
 // stores past it are dropped.
+
+// No resource reaches PAST (2^29 bytes at most: 512 rows of 2^18 fp32 values), nor do PAST less or more as much.
+constexpr uint32_t PAST = 0xc0000000u;
 
 template <typename T, int VEC> struct Raw;
 template <int VEC> struct Raw<uint16_t, VEC> { uint32_t v; };
@@ -158,16 +205,85 @@ template <int VEC>
 __device__ __forceinline__ float value(const Raw<float, VEC> &r, int i) { return r.v[i]; }
 
 __device__ __forceinline__ uint32_t bf16_bits(float x) { return __builtin_bit_cast(uint16_t, (__bf16)x); }
+__device__ __forceinline__ uint32_t bf16_bits(float x, float y) {
+    typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2;
+    return __builtin_bit_cast(uint32_t, bf16x2{(__bf16)x, (__bf16)y});
+}
 template <typename T, int VEC>
 __device__ __forceinline__ void store(const float (&v)[VEC], __amdgpu_buffer_rsrc_t b, uint32_t off) {
     if constexpr (sizeof(T) == 2 && VEC == 1)
         __builtin_amdgcn_raw_buffer_store_b16((uint16_t)bf16_bits(v[0]), b, off, 0, 0);
     else if constexpr (sizeof(T) == 2)
-        __builtin_amdgcn_raw_buffer_store_b32(bf16_bits(v[0]) | bf16_bits(v[1]) << 16, b, off, 0, 0);
+        __builtin_amdgcn_raw_buffer_store_b32(bf16_bits(v[0], v[1]), b, off, 0, 0);
     else if constexpr (VEC == 1)
         __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v[0]), b, off, 0, 0);
     else
         __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(kda::u32x2, kda::f32v2{v[0], v[1]}), b, off, 0, 0);
+}
+
+// The same offset, which the compiler knows nothing of: a loop would otherwise keep its sums with every token's
+// distance in registers, 8 to 32 of them.
+__device__ __forceinline__ uint32_t opaque(uint32_t x) {
+    asm("" : "+v"(x));
+    return x;
+}
+
+// Behind every fourth of a row of evaluations: the compiler would take all of them side by side, a few registers
+// each, and leave room for half as many waves.
+__device__ __forceinline__ void few_at_once(int i) {
+    if (i % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+}
+
+// A lane's log decays of N tokens, and the sums, least and largest of them. live: tokens that the sequence has
+// from the lane's first on (a raw gate input of zero is no log decay of zero).
+template <typename T, int N, int VEC>
+__device__ __forceinline__ void log_decays(const Raw<T, VEC> (&raw)[N], const Gate (&gate)[VEC], int kind, int live,
+                                           float (&g)[N][VEC], float (&G)[VEC], float &least, float &most) {
+    by_kind(kind, [&](auto n) {
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) {
+                g[k][v] = gate[v].template active<T, decltype(n)::value>(value(raw[k], v));
+                if (decltype(n)::value != NONE) few_at_once(k * VEC + v);
+            }
+    });
+    if (kind != 0 && live < N) {
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) g[k][v] = k < live ? g[k][v] : 0.f;
+    }
+    least = most = g[0][0];
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) {
+        G[v] = 0.f;
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            G[v] += g[k][v];
+            least = fminf(least, g[k][v]);
+            most = fmaxf(most, g[k][v]);
+        }
+    }
+}
+// x beta
+template <typename T, int N, int VEC>
+__device__ __forceinline__ void gated_inputs(const Raw<T, VEC> (&x)[N], const Raw<T, VEC> (&beta)[N], int is_logit,
+                                             float (&w)[N][VEC]) {
+    if (is_logit) {
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) {
+                w[k][v] = value(x[k], v) * logistic<T>(value(beta[k], v));
+                few_at_once(k * VEC + v);
+            }
+    } else {
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) w[k][v] = value(x[k], v) * value(beta[k], v);
+    }
 }
 
 // Host-side launchers (defined next to their kernels). vec: channels a lane; lanes: lanes a token
@@ -178,9 +294,15 @@ struct Shape {
 };
 hipError_t launch_fwd(const Params &p, Shape s, hipStream_t st);
 hipError_t launch_bwd(const BwdParams &p, Shape s, hipStream_t st);
-hipError_t launch_params(const BwdParams &p, float *dA_log, float *ddt_bias, hipStream_t st);
+hipError_t launch_params(const BwdParams &p, int64_t rows, float *dA_log, float *ddt_bias, hipStream_t st);
+// the same in tiles (Shape.lanes 64): workspace bytes, and for the backward rows of its partial sums
+int64_t tiles_bytes(const Params &p, Shape s);
+hipError_t launch_fwd_tiles(const Params &p, Shape s, void *ws, hipStream_t st);
+int64_t tiles_back_bytes(const Params &p, Shape s);
+int64_t tiles_back_rows(const Params &p);
+hipError_t launch_bwd_tiles(const BwdParams &p, Shape s, void *ws, hipStream_t st);
 hipError_t launch_step(const StepParams &p, bool f32, int vec, hipStream_t st);
 
-constexpr int W = 8, K = 8;             // waves a workgroup, tokens a lane and step
+constexpr int W = 8, K = 8;             // waves a workgroup and tokens a lane and step of the strips' kernels
 
 }  // namespace glr

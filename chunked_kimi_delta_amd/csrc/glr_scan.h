@@ -8,6 +8,8 @@
 // for another.
 #pragma once
 
+#include <type_traits>
+
 #include "glr_internal.h"
 
 namespace glr {
@@ -18,53 +20,61 @@ struct Totals {
     float c[W][CH], s[W][CH], E[W][CH];
 };
 
+// The values that the lower and the upper of each two neighbouring blocks of M lanes hold, in both.
+template <int M>
+__device__ __forceinline__ void both(float x, float &lo, float &up) {
+    if constexpr (M == 8) {             // the halves of a row of 16 lanes: banks 0, 1 and 2, 3
+        lo = __builtin_amdgcn_update_dpp(x, x, 0x118, 0xf, 0xc, false);     // row_shr:8
+        up = __builtin_amdgcn_update_dpp(x, x, 0x108, 0xf, 0x3, false);     // row_shl:8
+    } else {
+        const uint32_t u = __builtin_bit_cast(uint32_t, x);
+        const auto r = M == 16 ? __builtin_amdgcn_permlane16_swap(u, u, false, false)
+                               : __builtin_amdgcn_permlane32_swap(u, u, false, false);
+        lo = __builtin_bit_cast(float, (uint32_t)r[0]);
+        up = __builtin_bit_cast(float, (uint32_t)r[1]);
+    }
+}
+
+// A lane's tokens, and those of the groups before its own in its wave: h <- A h + E. G: sum of log decays.
+struct Part {
+    float A, E, G, A0, E0;
+};
+template <int M>
+__device__ __forceinline__ void level(Part &p, int lane) {
+    float al, au, el, eu, gl, gu;
+    both<M>(p.A, al, au);
+    both<M>(p.E, el, eu);
+    both<M>(p.G, gl, gu);
+    const bool upper = lane & M;
+    p.E0 = fmaf(p.A0, upper ? el : 0.f, p.E0);
+    p.A0 *= upper ? al : 1.f;
+    p.E = fmaf(au, el, eu);
+    p.A = al * au;
+    p.G = gl + gu;
+}
+
 // From each lane's own tokens (sum G of log decays, end E of a zero state) to the state `in` that they
 // start from; `carry`, the workgroup's state, moves behind the step's last token.
 template <typename T, int LPR, int VEC>
 __device__ __forceinline__ void join(const float (&G)[VEC], const float (&E)[VEC], float (&carry)[VEC],
                                      float (&in)[VEC], Totals<LPR * VEC> &tot, int wave, int lane) {
     const int at = lane % LPR;
-    float A[VEC], e[VEC], g[VEC];
+    Part p[VEC];
 #pragma unroll
     for (int v = 0; v < VEC; ++v) {
-        g[v] = G[v];
-        e[v] = E[v];
-        A[v] = exp_<T>(G[v]);
+        p[v] = Part{exp_<T>(G[v]), E[v], G[v], 1.f, 0.f};
+        if constexpr (LPR <= 8) level<8>(p[v], lane);
+        if constexpr (LPR <= 16) level<16>(p[v], lane);
+        if constexpr (LPR <= 32) level<32>(p[v], lane);
     }
-#pragma unroll
-    for (int m = LPR; m < 64; m *= 2) {
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) {
-            const float a0 = __shfl_up(A[v], m), e0 = __shfl_up(e[v], m), g0 = __shfl_up(g[v], m);
-            if (lane >= m) {
-                e[v] = fmaf(A[v], e0, e[v]);
-                A[v] *= a0;
-                g[v] += g0;
-            }
-        }
-    }
-    if (lane >= 64 - LPR) {
+    if (lane < LPR) {
 #pragma unroll
         for (int v = 0; v < VEC; ++v) {
             float c, s;
-            decay<T>(g[v], c, s);
+            decay<T>(p[v].G, c, s);
             tot.c[wave][at * VEC + v] = c;
             tot.s[wave][at * VEC + v] = s;
-            tot.E[wave][at * VEC + v] = e[v];
-        }
-    }
-    // the groups before this one
-    float A0[VEC], e0[VEC];
-#pragma unroll
-    for (int v = 0; v < VEC; ++v) {
-        A0[v] = 1.f;
-        e0[v] = 0.f;
-        if constexpr (LPR < 64) {
-            const float a = __shfl_up(A[v], LPR), x = __shfl_up(e[v], LPR);
-            if (lane >= LPR) {
-                A0[v] = a;
-                e0[v] = x;
-            }
+            tot.E[wave][at * VEC + v] = p[v].E;
         }
     }
     __syncthreads();
@@ -77,8 +87,62 @@ __device__ __forceinline__ void join(const float (&G)[VEC], const float (&E)[VEC
             h = fmaf(tot.c[w][at * VEC + v], h, fmaf(tot.s[w][at * VEC + v], h, tot.E[w][at * VEC + v]));
         }
         carry[v] = h;
-        in[v] = fmaf(A0[v], mine, e0[v]);
+        in[v] = fmaf(p[v].A0, mine, p[v].E0);
     }
+}
+
+// How a wave's decays of a step are held, by what they all are:
+//   FAST   a alone, where rounding it to 24 bits costs at most 2^-17 of a state in all (bf16 io:
+//          every |g| >= 2^-8; fp32 io, whose results would show that: every g < -1/2)
+//   SLOW   e^g - 1 alone: every g in [-1/2, 0]
+//   MIXED  (c, s)
+// SLOW takes 6 instructions a decay and FAST the exponential's 5, with one or two a step; MIXED 15 and two.
+enum Form { FAST, SLOW, MIXED };
+
+template <typename T>
+__device__ __forceinline__ Form form_of(float least, float most) {
+    constexpr float FAST_MOST = sizeof(T) == 2 ? -0.00390625f : -0.5f;
+    const bool fast = most <= FAST_MOST, slow = least >= -0.5f && most <= 0.f;
+    if (__builtin_amdgcn_ballot_w64(!fast) == 0) return FAST;
+    return __builtin_amdgcn_ballot_w64(!slow) == 0 ? SLOW : MIXED;
+}
+
+// A lane's decays of a step: c in place of the log decays, and a bit of s each.
+template <typename T, Form F, int N, int VEC>
+__device__ __forceinline__ uint32_t decays(float (&c)[N][VEC]) {
+    static_assert(N * VEC <= 32, "a bit a decay");
+    uint32_t s = 0;
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) {
+            const float g = c[k][v];
+            if (F == FAST) {
+                c[k][v] = exp_<T>(g);
+            } else if (F == SLOW) {
+                c[k][v] = expm1_slow(g);
+            } else {
+                float one;
+                decay<T>(g, c[k][v], one);
+                s |= one != 0.f ? 1u << (k * VEC + v) : 0u;
+                asm("" : "+v"(s));      // bit by bit: together they would take a register each
+            }
+            few_at_once(k * VEC + v);
+        }
+    return s;
+}
+template <class Fn>
+__device__ __forceinline__ void by_form(Form f, Fn fn) {
+    if (f == FAST) fn(std::integral_constant<Form, FAST>());
+    else if (f == SLOW) fn(std::integral_constant<Form, SLOW>());
+    else fn(std::integral_constant<Form, MIXED>());
+}
+// (s + c) h + w
+template <Form F>
+__device__ __forceinline__ float apply(float c, uint32_t s, int i, float h, float w) {
+    if (F == FAST) return fmaf(c, h, w);
+    if (F == SLOW) return fmaf(c, h, h + w);
+    return fmaf(c, h, w + __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, h) & (uint32_t)((int32_t)(s << (31 - i)) >> 31)));
 }
 
 // Workgroup -> (sequence, strip). Workgroups go to the 8 XCDs in turn, and each XCD has its own L2:

@@ -23,6 +23,7 @@ struct Pairs {
     int32_t from_slots, to_slots;
     int64_t n;
     const int32_t *count;               // pairs, on the device (null: n)
+    uint8_t *used;                      // CLEAR: marks of the slots, which become free (or null)
 };
 
 enum Mode { COPY, MOVE, CLEAR };        // MOVE: the source is cleared behind the copy
@@ -72,6 +73,7 @@ __global__ __launch_bounds__(256) void slots_kernel(Pools p, Pairs q)
         uint8_t *const to = p.to[j] + b * bytes + off;
         uint8_t *const from = M == CLEAR ? to : const_cast<uint8_t *>(p.from[j]) + a * bytes + off;
         if (M != CLEAR && to == from) continue;
+        if (M == CLEAR && part == 0 && q.used && threadIdx.x == 0) q.used[b] = 0;
         const uintptr_t unit = (uintptr_t)to | (uintptr_t)from | (uintptr_t)len;
         if (unit % 16 == 0) piece16<M>(to, from, len);
         else if (unit % 4 == 0) piece_of<M, uint32_t>(to, from, len);
@@ -238,7 +240,7 @@ kda_status pool_copy(const pool_ref *pools, int32_t n_pools, int32_t slots, cons
     const kda_status st = check(pools, n_pools, slots, sources, source_slots, n);
     if (st != KDA_OK) return st;
     if (!aligned(src, 4) || !aligned(dst, 4)) return KDA_ERR_INVALID_ARG;
-    const Pairs q = {src, dst, sources ? source_slots : slots, slots, n, nullptr};
+    const Pairs q = {src, dst, sources ? source_slots : slots, slots, n, nullptr, nullptr};
     return move_slots<COPY>(pools, n_pools, sources, q, (hipStream_t)stream);
 }
 
@@ -253,7 +255,7 @@ kda_status pool_fork(const pool_ref *pools, int32_t n_pools, int32_t slots, cons
     fork_kernel<<<dim3(1), dim3(NT), 0, (hipStream_t)stream>>>(f);
     if (hipGetLastError() != hipSuccess) return KDA_ERR_HIP;
     if (!src && !sources) return KDA_OK;
-    const Pairs q = {src, dst, f.from_slots, slots, n, nullptr};
+    const Pairs q = {src, dst, f.from_slots, slots, n, nullptr, nullptr};
     return move_slots<COPY>(pools, n_pools, sources, q, (hipStream_t)stream);
 }
 
@@ -264,9 +266,11 @@ kda_status pool_free(const pool_ref *pools, int32_t n_pools, int32_t slots, uint
     if (st != KDA_OK) return st;
     if ((slots > 0 && !used) || (n > 0 && !indices) || !aligned(indices, 4)) return KDA_ERR_INVALID_ARG;
     if (n == 0) return KDA_OK;
-    unuse_kernel<<<dim3((unsigned)((n + 255) / 256)), dim3(256), 0, (hipStream_t)stream>>>(used, indices, n, slots);
-    if (hipGetLastError() != hipSuccess) return KDA_ERR_HIP;
-    const Pairs q = {nullptr, indices, 0, slots, n, nullptr};
+    if (n_pools == 0) {
+        unuse_kernel<<<dim3((unsigned)((n + 255) / 256)), dim3(256), 0, (hipStream_t)stream>>>(used, indices, n, slots);
+        return hipGetLastError() == hipSuccess ? KDA_OK : KDA_ERR_HIP;
+    }
+    const Pairs q = {nullptr, indices, 0, slots, n, nullptr, used};
     return move_slots<CLEAR>(pools, n_pools, nullptr, q, (hipStream_t)stream);
 }
 
@@ -289,7 +293,7 @@ kda_status pool_compact(const pool_ref *pools, int32_t n_pools, int32_t slots, u
     compact_kernel<<<dim3(1), dim3(NT), 0, (hipStream_t)stream>>>(c);
     if (hipGetLastError() != hipSuccess) return KDA_ERR_HIP;
     // at most half of the slots move
-    const Pairs q = {c.src, c.dst, slots, slots, slots / 2, c.moves};
+    const Pairs q = {c.src, c.dst, slots, slots, slots / 2, c.moves, nullptr};
     return move_slots<MOVE>(pools, n_pools, nullptr, q, (hipStream_t)stream);
 }
 

@@ -68,6 +68,10 @@ def _arguments(x, g, beta, cu_seqlens, initial_state, use_beta_sigmoid, gate, A_
                    int(bool(use_beta_sigmoid)), _GATES[gate], float(gate_lower_bound), A, bias)
 
 
+def _like(g):
+    return torch.empty_like(g, memory_format=torch.contiguous_format)
+
+
 def _workspace(given, need, dev):
     if given is None:
         return torch.empty(need, dtype=torch.uint8, device=dev) if need else None
@@ -99,7 +103,7 @@ class GlrFwdPlan:
         a = _arguments(x, g, beta, cu_seqlens, initial_state, use_beta_sigmoid, gate, A_log, dt_bias,
                        gate_lower_bound)
         dev = self.device = g.device
-        self.y = torch.empty(g.shape, dtype=g.dtype, device=dev) if y is None else y
+        self.y = _like(g) if y is None else y
         if y is not None:
             _check(y, "y", g.dtype, g.shape, dev)
         a.y = self.y.data_ptr()
@@ -154,9 +158,8 @@ class GlrBwdPlan:
         if dht is not None:
             _check(dht, "dht", torch.float32, (a.N, a.D), dev)
         a.y = y.data_ptr()
-        new = lambda: torch.empty(g.shape, dtype=g.dtype, device=dev)
         f32 = dict(dtype=torch.float32, device=dev)
-        self.dx, self.dg, self.dbeta = new(), new(), None if beta is None else new()
+        self.dx, self.dg, self.dbeta = _like(g), _like(g), None if beta is None else _like(g)
         self.dh0 = torch.empty((a.N, a.D), **f32) if want_dh0 else None
         self.dA_log = torch.empty(a.D, **f32) if gate is not None else None
         self.ddt_bias = torch.empty(a.D, **f32) if gate is not None else None
@@ -201,7 +204,7 @@ class GlrStepPlan:
             _check(state_indices, "state_indices", torch.int32, (a.B,), g.device)
         elif state.shape[0] < a.B:
             raise ValueError(f"state has {state.shape[0]} slots for {a.B} rows")
-        self.y = torch.empty(g.shape, dtype=g.dtype, device=g.device) if y is None else y
+        self.y = _like(g) if y is None else y
         if y is not None:
             _check(y, "y", g.dtype, g.shape, g.device)
         a.y = self.y.data_ptr()

@@ -31,8 +31,9 @@ def _pools(pools, device=None):
             raise ValueError("pools of one call must have one number of slots")
         slots, device = p.shape[0], p.device
         r.data = p.data_ptr()
-        r.bytes = p[:1].numel() * p.element_size() if slots else p.element_size()
-        if r.bytes == 0:
+        size = p.numel() // slots if slots else 1
+        r.bytes = size * p.element_size()
+        if size == 0:
             raise ValueError("a pool's slots must not be empty")
     return refs, len(pools), slots, device
 
@@ -94,7 +95,7 @@ def pool_fork(pools, used, src=None, sources=None):
     if src is not None:
         _indices(src, "src", dev)
     n = m if src is None else src.numel()
-    dst = torch.empty(n, dtype=torch.int32, device=dev)
+    dst = used.new_empty(n, dtype=torch.int32)
     _call(load().pool_fork, "pool_fork", dev, None, refs, n_pools, slots, ptrs, m, used.data_ptr(), _ptr(src),
           dst.data_ptr(), n)
     return dst
@@ -128,8 +129,8 @@ def pool_compact(pools, used, indices):
     refs, n_pools, slots, dev = _pools(pools)
     slots, dev = _used(used, slots, dev)
     _indices(indices, "indices", dev)
-    count = torch.empty(1, dtype=torch.int32, device=dev)
-    ws = torch.empty(load().pool_compact_workspace_bytes(slots) or 256, dtype=torch.uint8, device=dev)
+    count = indices.new_empty(1)
+    ws = used.new_empty(load().pool_compact_workspace_bytes(slots) or 256, dtype=torch.uint8)
     _call(load().pool_compact, "pool_compact", dev, None, refs, n_pools, slots, used.data_ptr(), indices.data_ptr(),
           indices.numel(), count.data_ptr(), ws.data_ptr(), ws.numel())
     return count

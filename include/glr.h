@@ -10,7 +10,7 @@
  * and final_state[s, d] is h after the last token (initial_state for a sequence of no tokens).
  *
  * Conventions are kda_fwd.h's: device pointers, caller-owned; nothing is allocated, nothing
- * synchronises, no atomics, errors only through the return value; concurrent calls use distinct
+ * synchronises, errors only through the return value; concurrent calls use distinct
  * workspaces and outputs. A tensor's channels are contiguous. x, g and beta may be columns of wider
  * rows (x_stride and so on: elements from one token to the next); everything else is contiguous. io
  * tensors are aligned to their elements, fp32 tensors to 4 bytes, cu_seqlens to 8. A NaN or an
@@ -54,14 +54,16 @@ typedef struct {
     const float *dt_bias;     /* [D] fp32, or NULL for zeros                                         */
 } glr_args;
 
-/* Bytes of device workspace glr_fwd / glr_bwd need (only shapes, io, gate, whether cu_seqlens is
-   there, and the current device's compute-unit count are read): may be 0, and is 0 for arguments that
-   the calls reject. */
+/* Bytes of device workspace glr_fwd / glr_bwd need (only shapes, io, gate, whether beta and cu_seqlens
+   are there, and the current device's compute-unit count are read): may be 0, and is 0 for arguments that
+   the calls reject. Its contents need not be kept between calls. */
 size_t glr_fwd_workspace_bytes(const glr_args *args);
 size_t glr_bwd_workspace_bytes(const glr_args *args);
 
-/* Enqueue the forward on `stream`. States and sums are fp32. Tokens behind the last sequence are left
-   as they were. D and the strides are at most 2^18. */
+/* Enqueue the forward on `stream`: strips of channels that take a sequence in one workgroup each, or for
+   long sequences tiles of 64 or 128 tokens that hand states to each other within the launch (they wait for tiles
+   that have begun only). States and sums are fp32; results do not depend on the order in which tiles run.
+   Tokens behind the last sequence are left as they were. D and the strides are at most 2^18. */
 kda_status glr_fwd(const glr_args *args, void *workspace, size_t ws_bytes, void *stream);
 
 /* Gradients of glr_fwd's inputs from the gradients of a loss with respect to y (d_y, like y) and to

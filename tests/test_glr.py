@@ -101,6 +101,8 @@ def test_packed_arguments(lib):
 def test_launches_that_do_not_fit_are_refused(lib):
     a = args(D=4096, x_stride=4096, g_stride=4096, beta_stride=4096, N=1 << 20, cu_seqlens=FAKE)
     assert lib.glr_fwd(ctypes.byref(a), FAKE, 1 << 50, None) == back(lib, a) == NOT
+    a = args(T=1 << 30, D=1 << 12, x_stride=4096, g_stride=4096, beta_stride=4096)      # tiles
+    assert lib.glr_fwd(ctypes.byref(a), FAKE, 1 << 60, None) == back(lib, a, size=1 << 60) == NOT
     a = args(B=1 << 30, N=1 << 30, T=1)
     assert lib.glr_step(ctypes.byref(a), FAKE, FAKE, 1, None) == NOT
 
@@ -116,6 +118,21 @@ def test_backward_refuses_bad_arguments(lib):
     assert need > 0
     for kw in (dict(ws=None), dict(size=need - 1), dict(ws=FAKE + 64)):
         assert back(lib, g, **kw) == _lib.KDA_ERR_WORKSPACE, kw
+
+
+def test_workspace(lib):
+    long = dict(D=2048, x_stride=2048, g_stride=2048, beta_stride=2048)
+    fwd = lambda **kw: lib.glr_fwd_workspace_bytes(ctypes.byref(args(**kw)))
+    bwd = lambda **kw: lib.glr_bwd_workspace_bytes(ctypes.byref(args(**kw)))
+    assert fwd() == bwd() == fwd(D=0) == bwd(D=0) == 0          # strips, and refused
+    assert bwd(gate=1) >= 2 * 64 * 4                            # partial sums of the gate's gradients
+    # tiles of 64 tokens (with beta), a word of 8 bytes a channel each
+    assert fwd(T=1 << 16, **long) >= (1 << 10) * 2048 * 8 and bwd(T=1 << 16, **long) >= (1 << 10) * 2048 * 8
+    assert fwd(T=1 << 16, beta=None, **long) >= (1 << 9) * 2048 * 8
+    a = args(T=1 << 16, **long)
+    for call, need in ((lambda ws, n: lib.glr_fwd(ctypes.byref(a), ws, n, None), fwd(T=1 << 16, **long)),
+                       (lambda ws, n: back(lib, a, ws=ws, size=n), bwd(T=1 << 16, **long))):
+        assert call(None, need) == call(FAKE, need - 1) == call(FAKE + 64, need) == _lib.KDA_ERR_WORKSPACE
 
 
 def test_step_refuses_bad_pools(lib):
