@@ -65,28 +65,31 @@ int vec_of(const glr_args *a, bool x_read, const void *const *more, int n)
 }
 
 // Tiles that hand states to each other, or strips of whole sequences? Strips are one launch and no workspace (13 us a
-// call, tiles 18), but take a sequence's 512 tokens in 3 to 5 us however few strips there are, and a packed batch's
-// longest sequence alone. bf16, us, strips and tiles: 2048 tokens x 2048 channels 15 and 18 (gradients 20 and 22), 4096 x
-// 2048 25 and 21 (35 and 25), 4096 x 4096 27 and 30 (57 and 42; with raw gates 51 and 41; fp32 49 and 41), 131072 x 2048 943 and 373, 8 x 2048 x
-// 4096 90 and 99. Packed, 16 x 2048 tokens 183 and 197, 7 x 512 + 16384 tokens of 2048 channels 125 and 70; lengths lie on the
-// device, so raggedness is assumed.
-bool use_tiles(const glr_args *a, bool back)
+// call, tiles 18), and the better of the two wherever strips of 64 channels fill the device; narrower ones take longer, and
+// a packed batch's longest sequence takes its time alone. bf16, us, strips and tiles: 4 x 4096 tokens x 4096 channels 86 and 98
+// (gradients 147 and 149, raw 247 and 273); 2560 x 4096 21 and 24 (28 and 27, raw 73 and 60), 3300 x 4096 24 and 29 (51 and 36, raw 92
+// and 76), 7000 x 4096 68 and 50; 3300 x 2048 19 and 19 (28 and 23), 16384 x 1000 83 and 38. Packed, 16 x 2048 tokens x 4096 183 and 185,
+// 7 x 512 + 16384 x 2048 125 and 66; lengths lie on the device, so raggedness is assumed.
+bool use_tiles(const glr_args *a)
 {
     const int64_t tokens = (int64_t)a->B * a->T, mean = a->N > 0 ? tokens / a->N : 0;
+    const int64_t channels = (int64_t)a->N * a->D, cus = kda::current_device_cus();
     if (a->cu_seqlens && a->N > 1) return mean >= 1024 && tokens >= 8192;
-    const bool fill = (int64_t)a->N * a->D >= 16 * (int64_t)kda::current_device_cus();  // narrow strips, every compute unit
-    return mean >= (fill && !back && !a->beta && a->io == KDA_BF16 ? 8192 : 4096);
+    return channels < 64 * cus && mean >= (channels < 16 * cus ? 3584 : 2560);
 }
 
-// Lanes a token: 64 in tiles; 8 in narrow strips, where wide ones (32) would leave compute units without work.
-// Channels a lane: `vec`, but in tiles one where two would take the registers of a second workgroup on a compute unit (fp32
-// gradients 102 -> 71 us for 8192 x 2048, bf16 with beta 280 -> 250 for 4 x 8192 x 4096; without, 373 against 407 for 131072 x 2048;
-// bf16 gradients 324 -> 281 for 4 x 8192 x 4096, with beta 155 against 161 for 4 x 4096 x 2048).
+// Tiles have 64 lanes a token, and one channel a lane where two would take the registers of a second workgroup on a
+// compute unit (fp32 gradients 102 -> 71 us for 8192 x 2048, bf16 with beta 280 -> 250 for 4 x 8192 x 4096; without, 373 against 407
+// for 131072 x 2048; bf16 gradients 324 -> 281 for 4 x 8192 x 4096, with beta 155 against 161 for 4 x 4096 x 2048).
+// Strips have as many lanes a token as leave every compute unit a workgroup: 8 x 1000 tokens x 2048 channels, raw, 38 us with
+// 64, 41, 52 and 68 with 32, 16 and 8; 2048 x 2048 13 us with 8 and 40 with 64.
 Shape shape_of(const glr_args *a, int vec, bool back)
 {
-    if (use_tiles(a, back)) return Shape{a->io == KDA_FP32, a->io == KDA_BF16 && back == (a->beta != nullptr) ? vec : 1, 64};
-    const int64_t wide = (a->D + 32 * vec - 1) / (32 * vec) * (int64_t)a->N;
-    return Shape{a->io == KDA_FP32, vec, wide >= 2 * kda::current_device_cus() ? 32 : 8};
+    const bool f32 = a->io == KDA_FP32;
+    if (use_tiles(a)) return Shape{f32, true, !f32 && back == (a->beta != nullptr) ? vec : 1, 64};
+    int lanes = 64;
+    while (lanes > 8 && (int64_t)a->N * ((a->D + lanes - 1) / lanes) < kda::current_device_cus()) lanes /= 2;
+    return Shape{f32, false, 1, lanes};
 }
 
 Params params_of(const glr_args *a, Shape s)
@@ -116,7 +119,7 @@ bool fits(const glr_args *a, Shape s)
 {
     const int ch = s.vec * s.lanes;
     const int64_t strips = (a->D + ch - 1) / ch, most = ((int64_t)1 << 32) - 1;
-    if (s.lanes == 64)          // tiles of at least 64 tokens, workgroups of at most 512 threads
+    if (s.tiles)                // of at least 64 tokens, workgroups of at most 512 threads
         return (((int64_t)a->B * a->T) / 64 + a->N) * strips <= most / 512;
     return unit_grid(strips, a->N, near_of(ch * (s.f32 ? 4 : 2))) <= most / (64 * W);
 }
@@ -126,7 +129,7 @@ size_t tiles_workspace(const glr_args *a, bool back)
 {
     int64_t most = 0;
     for (int vec = 1; vec <= 2; ++vec) {
-        const Shape s = {a->io == KDA_FP32, vec, 64};
+        const Shape s = {a->io == KDA_FP32, true, vec, 64};
         const Params p = params_of(a, s);
         const int64_t n = back ? tiles_back_bytes(p, s) : tiles_bytes(p, s);
         most = n > most ? n : most;
@@ -140,7 +143,7 @@ extern "C" {
 
 size_t glr_fwd_workspace_bytes(const glr_args *a)
 {
-    return check_shapes(a) == KDA_OK && use_tiles(a, false) ? tiles_workspace(a, false) : 0;
+    return check_shapes(a) == KDA_OK && use_tiles(a) ? tiles_workspace(a, false) : 0;
 }
 
 kda_status glr_fwd(const glr_args *a, void *workspace, size_t ws_bytes, void *stream)
@@ -154,14 +157,14 @@ kda_status glr_fwd(const glr_args *a, void *workspace, size_t ws_bytes, void *st
     if (a->N == 0) return KDA_OK;
     const Params p = params_of(a, s);
     hipStream_t hs = (hipStream_t)stream;
-    return (s.lanes == 64 ? launch_fwd_tiles(p, s, workspace, hs) : launch_fwd(p, s, hs)) == hipSuccess ? KDA_OK : KDA_ERR_HIP;
+    return (s.tiles ? launch_fwd_tiles(p, s, workspace, hs) : launch_fwd(p, s, hs)) == hipSuccess ? KDA_OK : KDA_ERR_HIP;
 }
 
 size_t glr_bwd_workspace_bytes(const glr_args *a)
 {
     if (check_shapes(a) != KDA_OK) return 0;
-    const bool tiles = use_tiles(a, true);
-    const int64_t rows = tiles ? tiles_back_rows(params_of(a, Shape{a->io == KDA_FP32, 1, 64})) : a->N;
+    const bool tiles = use_tiles(a);
+    const int64_t rows = tiles ? tiles_back_rows(params_of(a, Shape{a->io == KDA_FP32, true, 1, 64})) : a->N;
     return (a->gate ? 2 * align256((size_t)rows * a->D * 4) : 0) + (tiles ? tiles_workspace(a, true) : 0);
 }
 
@@ -190,7 +193,7 @@ kda_status glr_bwd(const glr_args *a, const void *d_y, const float *dht, void *w
     q.dg = dg;
     q.dbeta = dbeta;
     q.dh0 = dh0;
-    const bool tiles = s.lanes == 64;
+    const bool tiles = s.tiles;
     const int64_t rows = tiles ? tiles_back_rows(q.f) : a->N;
     const size_t part = gated ? align256((size_t)rows * a->D * 4) : 0;
     uint8_t *const ws = (uint8_t *)workspace;
@@ -212,7 +215,7 @@ kda_status glr_step(const glr_args *a, float *state, const int32_t *state_indice
     if ((slots > 0 && !state) || !aligned(state, 4) || !aligned(state_indices, 4)) return KDA_ERR_INVALID_ARG;
     const int vec = vec_of(a, true, nullptr, 0);
     StepParams p = {};
-    p.f = params_of(a, Shape{a->io == KDA_FP32, vec, 1});
+    p.f = params_of(a, Shape{a->io == KDA_FP32, false, vec, 1});
     p.state = state;
     p.index = state_indices;
     p.B = a->B;

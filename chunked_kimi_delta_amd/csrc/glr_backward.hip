@@ -9,10 +9,10 @@ namespace glr {
 
 namespace {
 
-template <typename T, int VEC, int LPR, bool BETA>
+template <typename T, int LPR, bool BETA>
 __global__ __launch_bounds__(64 * W) void scan_back_kernel(BwdParams q)
 {
-    constexpr int CH = LPR * VEC, R = 64 / LPR, STEP = R * K * W, E = sizeof(T);
+    constexpr int VEC = 1, CH = LPR, R = 64 / LPR, STEP = R * K * W, E = sizeof(T);
     __shared__ Totals<CH> tot[2];
     __shared__ double sums[2][W][CH];
     const Params &p = q.f;
@@ -188,28 +188,29 @@ __global__ __launch_bounds__(1024) void params_kernel(const float *part_A, const
     else if (ddt_bias) ddt_bias[d] = (float)x;
 }
 
-template <typename T, int VEC, int LPR>
+template <typename T, int LPR>
 hipError_t launch(const BwdParams &q, hipStream_t st)
 {
-    const dim3 grid((unsigned)unit_grid(q.f.strips, q.f.seq.N, near_of(LPR * VEC * (int)sizeof(T))));
+    const dim3 grid((unsigned)unit_grid(q.f.strips, q.f.seq.N, near_of(LPR * (int)sizeof(T))));
     if (q.f.beta)
-        scan_back_kernel<T, VEC, LPR, true><<<grid, dim3(64 * W), 0, st>>>(q);
+        scan_back_kernel<T, LPR, true><<<grid, dim3(64 * W), 0, st>>>(q);
     else
-        scan_back_kernel<T, VEC, LPR, false><<<grid, dim3(64 * W), 0, st>>>(q);
+        scan_back_kernel<T, LPR, false><<<grid, dim3(64 * W), 0, st>>>(q);
     return hipGetLastError();
 }
 template <typename T>
-hipError_t launch_io(const BwdParams &q, Shape s, hipStream_t st)
+hipError_t launch_io(const BwdParams &q, int lanes, hipStream_t st)
 {
-    if (s.vec == 2) return s.lanes == 8 ? launch<T, 2, 8>(q, st) : launch<T, 2, 32>(q, st);
-    return s.lanes == 8 ? launch<T, 1, 8>(q, st) : launch<T, 1, 32>(q, st);
+    if (lanes == 64) return launch<T, 64>(q, st);
+    if (lanes == 32) return launch<T, 32>(q, st);
+    return lanes == 16 ? launch<T, 16>(q, st) : launch<T, 8>(q, st);
 }
 
 }  // namespace
 
 hipError_t launch_bwd(const BwdParams &q, Shape s, hipStream_t st)
 {
-    return s.f32 ? launch_io<float>(q, s, st) : launch_io<uint16_t>(q, s, st);
+    return s.f32 ? launch_io<float>(q, s.lanes, st) : launch_io<uint16_t>(q, s.lanes, st);
 }
 
 hipError_t launch_params(const BwdParams &q, int64_t rows, float *dA_log, float *ddt_bias, hipStream_t st)

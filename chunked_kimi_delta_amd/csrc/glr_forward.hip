@@ -11,10 +11,10 @@ struct Rows {
     Raw<T, VEC> x[K], g[K], b[BETA ? K : 1];
 };
 
-template <typename T, int VEC, int LPR, bool BETA>
+template <typename T, int LPR, bool BETA>
 __global__ __launch_bounds__(64 * W) void scan_kernel(Params p)
 {
-    constexpr int CH = LPR * VEC, R = 64 / LPR, STEP = R * K * W, E = sizeof(T);
+    constexpr int VEC = 1, CH = LPR, R = 64 / LPR, STEP = R * K * W, E = sizeof(T);
     __shared__ Totals<CH> tot[2];
     int seq, strip;
     if (!unit_of(blockIdx.x, p.strips, p.seq.N, near_of(CH * E), seq, strip)) return;
@@ -139,28 +139,29 @@ __global__ __launch_bounds__(256) void step_kernel(StepParams p)
     }
 }
 
-template <typename T, int VEC, int LPR>
+template <typename T, int LPR>
 hipError_t launch(const Params &p, hipStream_t st)
 {
-    const dim3 grid((unsigned)unit_grid(p.strips, p.seq.N, near_of(LPR * VEC * (int)sizeof(T))));
+    const dim3 grid((unsigned)unit_grid(p.strips, p.seq.N, near_of(LPR * (int)sizeof(T))));
     if (p.beta)
-        scan_kernel<T, VEC, LPR, true><<<grid, dim3(64 * W), 0, st>>>(p);
+        scan_kernel<T, LPR, true><<<grid, dim3(64 * W), 0, st>>>(p);
     else
-        scan_kernel<T, VEC, LPR, false><<<grid, dim3(64 * W), 0, st>>>(p);
+        scan_kernel<T, LPR, false><<<grid, dim3(64 * W), 0, st>>>(p);
     return hipGetLastError();
 }
 template <typename T>
-hipError_t launch_io(const Params &p, Shape s, hipStream_t st)
+hipError_t launch_io(const Params &p, int lanes, hipStream_t st)
 {
-    if (s.vec == 2) return s.lanes == 8 ? launch<T, 2, 8>(p, st) : launch<T, 2, 32>(p, st);
-    return s.lanes == 8 ? launch<T, 1, 8>(p, st) : launch<T, 1, 32>(p, st);
+    if (lanes == 64) return launch<T, 64>(p, st);
+    if (lanes == 32) return launch<T, 32>(p, st);
+    return lanes == 16 ? launch<T, 16>(p, st) : launch<T, 8>(p, st);
 }
 
 }  // namespace
 
 hipError_t launch_fwd(const Params &p, Shape s, hipStream_t st)
 {
-    return s.f32 ? launch_io<float>(p, s, st) : launch_io<uint16_t>(p, s, st);
+    return s.f32 ? launch_io<float>(p, s.lanes, st) : launch_io<uint16_t>(p, s.lanes, st);
 }
 
 hipError_t launch_step(const StepParams &p, bool f32, int vec, hipStream_t st)

@@ -289,13 +289,13 @@ __device__ __forceinline__ void gated_inputs(const Raw<T, VEC> (&x)[N], const Ra
 // Host-side launchers (defined next to their kernels). vec: channels a lane; lanes: lanes a token
 // (Params.strips = ceil(D / (vec lanes))).
 struct Shape {
-    bool f32;
+    bool f32, tiles;
     int vec, lanes;
 };
 hipError_t launch_fwd(const Params &p, Shape s, hipStream_t st);
 hipError_t launch_bwd(const BwdParams &p, Shape s, hipStream_t st);
 hipError_t launch_params(const BwdParams &p, int64_t rows, float *dA_log, float *ddt_bias, hipStream_t st);
-// the same in tiles (Shape.lanes 64): workspace bytes, and for the backward rows of its partial sums
+// the same in tiles (64 lanes a token): workspace bytes, and for the backward rows of its partial sums
 int64_t tiles_bytes(const Params &p, Shape s);
 hipError_t launch_fwd_tiles(const Params &p, Shape s, void *ws, hipStream_t st);
 int64_t tiles_back_bytes(const Params &p, Shape s);

@@ -61,20 +61,26 @@ __device__ __forceinline__ void await(const uint64_t *const (&p)[N], const bool 
     }
 }
 
-// Slot -> (sequence, tile of it). Sequence s's tile t lies in slot floor(bos_s / TILE) + s + t; the last
+// Slot -> (sequence, tile of it). Sequence s's tile t lies in slot floor(bos_s / tile) + s + t; the last
 // sequence whose first slot is not behind `slot` is the one. False: a slot with no tile. A sequence of no tokens
-// has one slot with tile 0 and n = 0.
+// has one slot with tile 0 and n = 0. Every lane of a wave calls; the last 64 candidates are looked at at once, one a
+// lane (one after the other their loads took 20 us of 215 for 21412 packed tokens of 4096 channels).
 __device__ __forceinline__ bool tile_of(const kda::SeqGeom &sg, int tile, int64_t slot, int &seq, int64_t &t,
                                         int64_t &bos, int64_t &n) {
     int lo = 0, hi = sg.N - 1;
-    while (lo < hi) {
+    while (hi - lo >= 64) {
         const int mid = (lo + hi + 1) >> 1;
         if (kda::seq_bos(sg, mid) / tile + mid <= slot) lo = mid; else hi = mid - 1;
     }
-    seq = lo;
-    bos = kda::seq_bos(sg, lo);
-    n = kda::seq_eos(sg, lo, bos) - bos;
-    t = slot - (bos / tile + lo);
+    const int mine = lo + (int)(threadIdx.x & 63);
+    const int64_t first = mine <= hi ? kda::seq_bos(sg, mine) : 0, end = mine <= hi ? kda::seq_eos(sg, mine, first) : 0;
+    // (lo's own first slot is not behind: sequence 0's is 0)
+    const uint64_t ahead = __builtin_amdgcn_ballot_w64(mine <= hi && first / tile + mine <= slot) | 1;
+    const int at = 63 - __builtin_clzll(ahead);
+    seq = lo + at;
+    bos = (int64_t)__builtin_amdgcn_readlane((int)(first >> 32), at) << 32 | (uint32_t)__builtin_amdgcn_readlane((int)first, at);
+    n = ((int64_t)__builtin_amdgcn_readlane((int)(end >> 32), at) << 32 | (uint32_t)__builtin_amdgcn_readlane((int)end, at)) - bos;
+    t = slot - (bos / tile + seq);
     return t >= 0 && (t * tile < n || (t == 0 && n == 0));
 }
 // The place of a sequence's group of `size` tiles that tile t is in: injective over all sequences, below

@@ -180,8 +180,9 @@ class GlrBwdPlan:
 
 def glr_bwd(x, g, y, d_y, beta=None, dht=None, cu_seqlens=None, initial_state=None, want_dh0=True, **prestage):
     """Gated linear recurrence backward. Returns (dx, dg, dbeta or None in the io dtype, dh0 fp32 or None,
-    dA_log or None, ddt_bias or None; rows behind the last packed sequence hold anything); see GlrBwdPlan."""
-    return GlrBwdPlan(x, g, y, d_y, beta, dht, cu_seqlens, initial_state, want_dh0, **prestage)()
+    dA_log or None, ddt_bias or None; rows behind the last packed sequence hold anything); see GlrBwdPlan. y and d_y
+    are copied where they are not contiguous."""
+    return GlrBwdPlan(x, g, y.contiguous(), d_y.contiguous(), beta, dht, cu_seqlens, initial_state, want_dh0, **prestage)()
 
 
 class GlrStepPlan:

@@ -85,6 +85,19 @@ def test_columns_of_a_projection(kw, dtype):
         assert torch.equal(*step)
 
 
+def test_backward_takes_y_and_its_gradient_as_views():
+    a = to(make(B=3, T=37, D=10, dtype=torch.float32), DEV)
+    y, _ = kda.glr_fwd(**a)
+    d_y = torch.randn_like(y)
+    padded = lambda t: torch.cat([t, torch.full_like(t[:, :5], float("nan"))], 1)[:, :37]
+    want = kda.glr_bwd(None, a["g"], y, d_y)
+    for p, q in zip(kda.glr_bwd(None, a["g"], padded(y), padded(d_y)), want):
+        assert p is None or torch.equal(p, q)
+    ones = torch.ones((), device=DEV).expand(3, 37, 10)             # what the gradient of a sum is
+    for p, q in zip(kda.glr_bwd(None, a["g"], y, ones), kda.glr_bwd(None, a["g"], y, torch.ones_like(y))):
+        assert p is None or torch.equal(p, q)
+
+
 def test_strides_that_are_refused():
     x = torch.zeros(2, 6, 8, device=DEV)
     for bad in (x.transpose(1, 2)[:, :6, :6], x[:, ::2][:, :, :6].transpose(0, 1), x[:, :, ::2], x[:1].expand(2, 6, 8)):
