@@ -53,6 +53,8 @@ __global__ __launch_bounds__(64 * W) void scan_back_kernel(BwdParams q)
         }
     };
     if (n > 0) fetch(0);
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) asm volatile("" : : "v"(carry[v]));      // read before the first wave may write there
     int buf = 0;
     for (int64_t s0 = 0; s0 < n; s0 += STEP, buf ^= 1) {
         const int64_t hi = n - s0, at = hi > STEP ? hi - STEP : 0;

@@ -12,7 +12,7 @@
 // Waits end: a strip's tiles are numbered by a counter in the order in which its workgroups begin, and a tile waits
 // only for tiles of its strip with lower numbers, which some running workgroup has begun. A word holds its value
 // and its own flag (a sign bit that no value has), so nothing has to be ordered around it: stores and loads of 8
-// bytes at device scope, zeros before the launch. A wait gives up after SPINS polls (about a second) all the same,
+// bytes at device scope, zeros before the launch. A wait gives up after SPINS polls (a tenth of a second) all the same,
 // so that a workspace that two calls share at once gives wrong results and not a hang.
 #pragma once
 
@@ -22,7 +22,7 @@ namespace glr {
 
 constexpr int TILES = 8, WINDOWS = 8, SPAN = TILES * WINDOWS;
 constexpr int TICKET = 64;
-constexpr int SPINS = 1 << 21;
+constexpr int SPINS = 1 << 17;
 
 struct Tiles {
     uint32_t *ticket;                   // a strip's counter, TICKET words apart
@@ -143,6 +143,9 @@ __device__ __forceinline__ void hand_over(const Tiles &x, const float (&G)[VEC],
             sh.G[wave][ch + v] = p[v].G;
         }
     }
+    // every wave has `start` before a word goes out: the sequence's last tile may write where it was read
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) asm volatile("" : : "v"(start[v]));
     __syncthreads();
     const int tile = (int)(t % TILES), window = (int)(t % SPAN) / TILES;   // in the window, in the span
     if (wave == 0 && !last && tile < TILES - 1) {           // (no tile reads a window's last one)

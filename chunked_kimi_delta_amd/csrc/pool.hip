@@ -200,7 +200,7 @@ kda_status check(const pool_ref *pools, int32_t n_pools, int32_t slots, const vo
     if (slots > MOST || n > MOST || (sources && source_slots > MOST)) return KDA_ERR_UNSUPPORTED;
     for (int i = 0; i < n_pools; ++i) {
         if (pools[i].bytes < 1 || (slots > 0 && !pools[i].data)) return KDA_ERR_INVALID_ARG;
-        if (pools[i].bytes > (int64_t)1 << 40) return KDA_ERR_UNSUPPORTED;
+        if (pools[i].bytes > (int64_t)1 << 39) return KDA_ERR_UNSUPPORTED;    // 2^25 pieces, MAX_POOLS times
         if (sources && source_slots > 0 && !sources[i]) return KDA_ERR_INVALID_ARG;
     }
     return KDA_OK;
@@ -220,7 +220,6 @@ kda_status move_slots(const pool_ref *pools, int32_t n_pools, const void *const 
             p.bytes[p.n] = pools[i].bytes;
             p.first[p.n] = (int32_t)pieces;
             pieces += (pools[i].bytes + PIECE - 1) / PIECE;
-            if (pieces > INT32_MAX) return KDA_ERR_UNSUPPORTED;
             p.first[++p.n] = (int32_t)pieces;
         }
         const int64_t items = q.n * pieces, grid = items < 16384 ? items : 16384;

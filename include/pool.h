@@ -10,7 +10,7 @@
  * Conventions are kda_fwd.h's: nothing is allocated, nothing synchronises, no atomics; every index is
  * read on the device, so that calls can be captured in a graph. Index arrays and `used` must not
  * overlap each other or the pools. Host arrays (pools, sources) are read before the call returns. At
- * most 2^24 slots and 2^24 indices a call; pools need no alignment (16 bytes, and slots of a multiple of
+ * most 2^24 slots, 2^24 indices and slots of 2^39 bytes a call; pools need no alignment (16 bytes, and slots of a multiple of
  * 16 bytes, are faster).
  */
 #ifndef POOL_H

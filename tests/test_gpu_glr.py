@@ -341,6 +341,23 @@ def test_other_streams_and_repeats_agree():
         assert torch.equal(p, q) and torch.equal(p, r)
 
 
+@pytest.mark.parametrize("gate", [None, "softplus"])
+def test_no_tokens(gate):
+    a = to(make(B=2, T=3, D=5, h0=True, sigmoid=True, gate=gate), DEV)
+    a |= {n: a[n][:, :0] for n in ("x", "g", "beta")}
+    y, fin = kda.glr_fwd(**a)
+    assert y.shape == (2, 0, 5) and torch.equal(fin, a["initial_state"])
+    dht = torch.randn_like(fin)
+    b = dict(a)
+    dx, dg, db, dh0, dA, ddt = kda.glr_bwd(b.pop("x"), b.pop("g"), y, y.clone(), dht=dht, **b)
+    assert torch.equal(dh0, dht) and dx.shape == dg.shape == db.shape == (2, 0, 5)
+    assert gate is None or (not dA.any() and not ddt.any())
+    state = torch.randn(2, 5, device=DEV)
+    keep = state.clone()
+    b = {n: x for n, x in a.items() if n != "initial_state"}
+    assert kda.glr_step(**b, state=state).shape == (2, 0, 5) and torch.equal(state, keep)
+
+
 def test_sequences_of_a_batch_are_what_they_are_alone():
     """The same sequence alone (narrow strips) and among many (wide strips): the bounds of two evaluations."""
     lens = [900] + [40] * 60

@@ -49,6 +49,25 @@ def test_forward_and_gradients(kw, pre, dtype):
             assert p is None or (torch.equal(p[:, :rows], q[:, :rows]) if p.dim() == 3 else torch.equal(p, q))
 
 
+@pytest.mark.parametrize("n", [64, 65, 150])
+def test_many_packed_sequences(n):
+    gen = torch.Generator().manual_seed(n)
+    lens = [int(x) for x in torch.randint(900, 1400, (n,), generator=gen)]
+    lens[3], lens[4] = 0, 2600
+    a = make(lens=lens, D=2, h0=True, dtype=torch.float32)
+    y, fin = kda.glr_fwd(**to(a, DEV))
+    check_forward(a, y, fin, *glr_recurrent(**a))
+    d_y = torch.randn_like(y)
+    b = to(a, DEV)
+    dx, dg, _, dh0, _, _ = kda.glr_bwd(b.pop("x"), b.pop("g"), y, d_y, **b)
+    for s in (0, 3, 4, 62, 63, n - 1):              # each as it is alone: a batch of its own takes strips
+        lo, hi = int(a["cu_seqlens"][s]), int(a["cu_seqlens"][s + 1])
+        one = {m: a[m][:, lo:hi].contiguous() for m in ("x", "g")} | {"initial_state": a["initial_state"][s:s + 1]}
+        part, d = y[:, lo:hi].cpu(), d_y[:, lo:hi].cpu()
+        got = (dx[:, lo:hi], dg[:, lo:hi], None, dh0[s:s + 1], None, None)
+        check_gradients(one, part, d, None, got, glr_gradients(**one, y=part, d_y=d))
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 def test_slow_strong_and_clearing_decays(dtype):
     T = 20000

@@ -42,7 +42,7 @@ def calls(lib, pools=(GOOD,), n_pools=None, slots=8, sources=None, m=0, used=FAK
 @pytest.mark.parametrize("kw,status", [
     (dict(n_pools=-1), BAD), (dict(slots=-1), BAD), (dict(n=-1), BAD), (dict(slots=(1 << 24) + 1), NOT),
     (dict(n=(1 << 24) + 1), NOT), (dict(pools=((None, 64),)), BAD), (dict(pools=((FAKE, 0),)), BAD),
-    (dict(pools=(GOOD, (FAKE, -4))), BAD), (dict(pools=((FAKE, (1 << 40) + 1),)), NOT), (dict(src=FAKE + 2), BAD)])
+    (dict(pools=(GOOD, (FAKE, -4))), BAD), (dict(pools=((FAKE, (1 << 39) + 1),)), NOT), (dict(src=FAKE + 2), BAD)])
 def test_calls_refuse_bad_arguments(lib, kw, status):
     for name, call in calls(lib, **kw).items():
         assert call() == status, name
