@@ -1,5 +1,14 @@
 // glr_forward.hip -- the forward of the gated linear recurrence and its serving step (include/glr.h):
 //     h <- e^g h + beta x;   y = h
+//
+// The scan over strips (glr_scan.h). A value costs 6 to 15 instructions for its decay, a raw gate 14 and a sigmoid 5 more, and
+// four of the scan's own, so bytes and instructions are of a size: 32 x 500 tokens x 2048 channels fp32 82 us (4.8 TB/s, 93% of
+// what a copy reaches), 8 x 2048 x 4096 bf16 93 us (4.3 TB/s), raw 129 (4.2). Where strips are few it is a step's own time, 2.5 to 4 us
+// for loads, the groups' scan, a barrier and the chain over the waves: 2048 x 2048 in 13 us. Kernel alone, 70 tokens of 256
+// channels, raw: 4.8 us, two memory latencies.
+//
+// The step: a state is read and written once, by a thread of its own for all tokens of the call. 64 rows x 4096 channels 4.2 us
+// (1 row x 2048 3.4): latency of index, state and inputs; the call takes 11.
 #include "glr_scan.h"
 
 namespace glr {
@@ -39,7 +48,7 @@ __global__ __launch_bounds__(64 * W) void scan_kernel(Params p)
     Rows<T, VEC, BETA> next;
     auto fetch = [&](int64_t s0) {
         const auto xr = rows(p.x, p.xs, s0), gr = rows(p.g, p.gs, s0);
-        const uint32_t g0 = opaque(tok * gs + d * E), x0 = opaque(tok * xs + d * E);
+        const uint32_t g0 = tok * gs + d * E, x0 = tok * xs + d * E;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             load(next.g[k], gr, g0 + k * gs);
@@ -47,7 +56,7 @@ __global__ __launch_bounds__(64 * W) void scan_kernel(Params p)
         }
         if constexpr (BETA) {
             const auto br = rows(p.beta, p.bs, s0);
-            const uint32_t b0 = opaque(tok * bs + d * E);
+            const uint32_t b0 = tok * bs + d * E;
 #pragma unroll
             for (int k = 0; k < K; ++k) load(next.b[k], br, b0 + k * bs);
         }
@@ -80,7 +89,7 @@ __global__ __launch_bounds__(64 * W) void scan_kernel(Params p)
         by_form(form, local);
         join<T, LPR, VEC>(G, end, carry, h, tot[buf], wave, lane);
         const auto yr = rows(p.y, p.D, s0);
-        const uint32_t y0 = opaque(on ? tok * ys + d * E : PAST);    // channels past the last lie past every range
+        const uint32_t y0 = on ? tok * ys + d * E : PAST;    // channels past the last lie past every range
         by_form(form, [&](auto f) {
 #pragma unroll
             for (int k = 0; k < K; ++k) {

@@ -221,19 +221,6 @@ __device__ __forceinline__ void store(const float (&v)[VEC], __amdgpu_buffer_rsr
         __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(kda::u32x2, kda::f32v2{v[0], v[1]}), b, off, 0, 0);
 }
 
-// The same offset, which the compiler knows nothing of: a loop would otherwise keep its sums with every token's
-// distance in registers, 8 to 32 of them.
-__device__ __forceinline__ uint32_t opaque(uint32_t x) {
-    asm("" : "+v"(x));
-    return x;
-}
-
-// Behind every fourth of a row of evaluations: the compiler would take all of them side by side, a few registers
-// each, and leave room for half as many waves.
-__device__ __forceinline__ void few_at_once(int i) {
-    if (i % 4 == 3) __builtin_amdgcn_sched_barrier(0);
-}
-
 // A lane's log decays of N tokens, and the sums, least and largest of them. live: tokens that the sequence has
 // from the lane's first on (a raw gate input of zero is no log decay of zero).
 template <typename T, int N, int VEC>
@@ -243,10 +230,7 @@ __device__ __forceinline__ void log_decays(const Raw<T, VEC> (&raw)[N], const Ga
 #pragma unroll
         for (int k = 0; k < N; ++k)
 #pragma unroll
-            for (int v = 0; v < VEC; ++v) {
-                g[k][v] = gate[v].template active<T, decltype(n)::value>(value(raw[k], v));
-                if (decltype(n)::value != NONE) few_at_once(k * VEC + v);
-            }
+            for (int v = 0; v < VEC; ++v) g[k][v] = gate[v].template active<T, decltype(n)::value>(value(raw[k], v));
     });
     if (kind != 0 && live < N) {
 #pragma unroll
@@ -274,10 +258,7 @@ __device__ __forceinline__ void gated_inputs(const Raw<T, VEC> (&x)[N], const Ra
 #pragma unroll
         for (int k = 0; k < N; ++k)
 #pragma unroll
-            for (int v = 0; v < VEC; ++v) {
-                w[k][v] = value(x[k], v) * logistic<T>(value(beta[k], v));
-                few_at_once(k * VEC + v);
-            }
+            for (int v = 0; v < VEC; ++v) w[k][v] = value(x[k], v) * logistic<T>(value(beta[k], v));
     } else {
 #pragma unroll
         for (int k = 0; k < N; ++k)

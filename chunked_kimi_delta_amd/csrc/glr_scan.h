@@ -5,8 +5,8 @@
 // registers of a second workgroup on a compute unit: fp32 gradients of 8 x 1000 x 2048 179 us for 145): a
 // step takes 64 / LPR x K x W tokens in order of (wave, group, token). A lane runs its tokens from a zero
 // state; a scan over the groups and the waves' totals in LDS then give the state that it starts from, and
-// it runs them again. The workgroup's own state goes from step to step in registers: no workgroup waits
-// for another.
+// it runs them again. The workgroup's own state goes from step to step in registers, and the next step's inputs are
+// fetched ahead of the current one's work (behind it: 83 -> 86 us for 16384 x 1000): no workgroup waits for another.
 #pragma once
 
 #include <type_traits>
@@ -128,7 +128,6 @@ __device__ __forceinline__ uint32_t decays(float (&c)[N][VEC]) {
                 s |= one != 0.f ? 1u << (k * VEC + v) : 0u;
                 asm("" : "+v"(s));      // bit by bit: together they would take a register each
             }
-            few_at_once(k * VEC + v);
         }
     return s;
 }

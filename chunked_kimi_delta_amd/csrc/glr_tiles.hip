@@ -1,5 +1,12 @@
-// glr_tiles.hip -- forward and gradients of the gated linear recurrence in tiles (glr_tiles.h). The
-// mathematics is glr_forward.hip's and glr_backward.hip's.
+// glr_tiles.hip -- the forward of the gated linear recurrence in tiles (glr_tiles.h). The
+// mathematics is glr_forward.hip's.
+//
+// 131072 tokens x 2048 channels bf16: 370 us (4.35 TB/s, 84% of what a copy reaches; strips, 16 channels a workgroup, 943): each byte
+// once (1.19 GB in, 0.57 out, words of the tiles among them), 3.6 waves on a SIMD, which wait 59% of their time, for inputs first
+// and then for each other's words (about 2 us a tile). 21412 packed tokens x 4096 channels with raw gates 177 us: vector
+// instructions fill 69% of the SIMDs' time (48 a value). A workgroup that fetched its next tile ahead of its hand-over
+// took 550 us for the former: half the workgroups for its registers. Tiles of half the tokens 450, of words that wait
+// for the window's before them (no spans) 480.
 #include "glr_tiles.h"
 
 namespace glr {
@@ -64,11 +71,7 @@ __global__ __launch_bounds__(64 * waves<BETA>()) void tile_kernel(Params p, Tile
         }
         float c[KT][VEC], w[BETA ? KT : 1][VEC], G[VEC], end[VEC], least, most;
         log_decays<T>(rg, gate, p.pre.gate, have - tok, c, G, least, most);
-        if constexpr (BETA) {
-            __builtin_amdgcn_sched_barrier(0);
-            gated_inputs<T>(rx, rb, p.pre.beta_sigmoid, w);
-            __builtin_amdgcn_sched_barrier(0);
-        }
+        if constexpr (BETA) gated_inputs<T>(rx, rb, p.pre.beta_sigmoid, w);
         auto in = [&](int k, int v) {
             if constexpr (BETA) return w[k][v]; else return value(rx[k], v);
         };

