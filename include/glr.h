@@ -10,8 +10,9 @@
  * and final_state[s, d] is h after the last token (initial_state for a sequence of no tokens).
  *
  * Conventions are kda_fwd.h's: device pointers, caller-owned; nothing is allocated, nothing
- * synchronises, errors only through the return value; concurrent calls use distinct
- * workspaces and outputs. A tensor's channels are contiguous. x, g and beta may be columns of wider
+ * synchronises, results are deterministic (the numbers that a long sequence's tiles take are the only
+ * atomics), errors only through the return value; concurrent calls use distinct workspaces and outputs.
+ * A tensor's channels are contiguous. x, g and beta may be columns of wider
  * rows (x_stride and so on: elements from one token to the next); everything else is contiguous. io
  * tensors are aligned to their elements, fp32 tensors to 4 bytes, cu_seqlens to 8. A NaN or an
  * infinity reaches its own channel of its own sequence, from its token on (in the backward: up to it).
