@@ -56,9 +56,9 @@ template <typename T>
 __device__ __forceinline__ float exp_(float x) {
     const float t = x * kda::LOG2E, r = __builtin_amdgcn_exp2f(t);
     if constexpr (sizeof(T) == 2) return r;
-    // x log2 e = t + lo; behind the finite exponentials lo must not make a NaN of infinities
+    // x log2 e = t + lo. Where r is infinite (t >= 128) or x is, lo must not make a NaN of it: t in (-160, 128) only
     const float lo = fmaf(x, 1.925963033500931e-8f, fmaf(x, kda::LOG2E, -t));
-    return fabsf(t) < 160.f ? fmaf(r, lo * 0.6931471805599453f, r) : r;
+    return fabsf(t + 16.f) < 144.f ? fmaf(r, lo * 0.6931471805599453f, r) : r;
 }
 template <typename T>
 __device__ __forceinline__ float inverse(float x) {     // of x in [1, 2]
