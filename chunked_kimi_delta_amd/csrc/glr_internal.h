@@ -7,6 +7,8 @@
 // distance from 1 to 24 bits as well as a itself.
 #pragma once
 
+#include <float.h>
+
 #include <type_traits>
 
 #include "glr.h"
@@ -133,7 +135,8 @@ __device__ __forceinline__ void decay(float g, float &c, float &s) {
 
 // A channel's gate. active() is the log decay of a raw input; back() takes the gradient dg of the active
 // decay `act` to that of the raw input and adds to the gradients of A_log and dt_bias. The kind is a type, so
-// that a lane's tokens go through one branch together.
+// that a lane's tokens go through one branch together. An infinite input (a state cleared or kept) has no part in
+// A_log's gradient, nor has a far one: there dg or du is zero, and the other factor is taken as finite.
 enum Kind { NONE, SOFTPLUS, BOUNDED };
 
 struct Gate {
@@ -151,7 +154,7 @@ struct Gate {
         if (N == NONE) return dg;
         const float u = g + bias;
         const float du = N == SOFTPLUS ? -ea * logistic<T>(u) * dg : ea * lb * sigmoid<T>(ea * u).ds * dg;
-        dA += N == SOFTPLUS ? act * dg : du * u;
+        dA += N == SOFTPLUS ? fmaxf(act, -FLT_MAX) * dg : du * __builtin_amdgcn_fmed3f(u, -FLT_MAX, FLT_MAX);
         db += du;
         return du;
     }
