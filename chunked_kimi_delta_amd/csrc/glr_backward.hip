@@ -5,8 +5,9 @@
 // forward's, from the last token to the first: "token" below counts from the end.
 //
 // With y at hand no forward state is formed again: a pass over g, dy and y (with beta x and beta). Sums for A_log and dt_bias
-// are fp32 over a lane's K tokens and fp64 from there on, a row a sequence (or tile), added by a second launch of a
-// workgroup for 64 channels. bf16, us: 8 x 1000 tokens x 2048 channels 40 (4.1 TB/s), raw with the gate's gradients 70 (3.7 TB/s; vector
+// are fp32 over a lane's tokens of a step or tile (8 or 16, which its registers hold), fp64 over a sequence's steps and waves (a
+// tile's waves), rounded to an fp32 row a sequence (a tile) and added in fp64 by a second launch of a workgroup for 64
+// channels. bf16, us: 8 x 1000 tokens x 2048 channels 40 (4.1 TB/s), raw with the gate's gradients 70 (3.7 TB/s; vector
 // instructions 57% of the SIMDs' time, with 1.7 waves on one: 512 workgroups' registers). 708 packed tokens x 512 channels fp32 raw:
 // 13.0 + 3.8, two steps of the longest sequence and a launch.
 #include "glr_scan.h"

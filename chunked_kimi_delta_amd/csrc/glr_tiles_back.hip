@@ -129,7 +129,7 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(4))) voi
 #pragma unroll
         for (int v = 0; v < VEC; ++v) q.dh0[(int64_t)seq * p.D + d + v] = out[v];
     }
-    if (gated) {                            // this tile's sums over its tokens
+    if (gated) {                            // this tile's sums over its tokens: fp64 over the waves
         __syncthreads();                    // the maps' LDS is read
 #pragma unroll
         for (int v = 0; v < VEC; ++v) {
@@ -138,10 +138,10 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(4))) voi
         }
         __syncthreads();
         if (tid < 2 * CH && strip * CH + tid % CH < p.D) {
-            float sum = 0.f;
+            double sum = 0.0;
 #pragma unroll
             for (int w = 0; w < W; ++w) sum += tid < CH ? sh.c[w][tid % CH] : sh.s[w][tid % CH];
-            (tid < CH ? q.part_A : q.part_b)[(int64_t)slot * p.D + strip * CH + tid % CH] = sum;
+            (tid < CH ? q.part_A : q.part_b)[(int64_t)slot * p.D + strip * CH + tid % CH] = (float)sum;
         }
     }
 }
