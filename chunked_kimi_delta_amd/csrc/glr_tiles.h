@@ -30,11 +30,16 @@ struct Tiles {
     uint64_t *tile, *window, *span;     // [places][strips * CH] what tiles and windows do, and states behind spans
 };
 
-__device__ __forceinline__ uint64_t word_of(float c, float s, float E) {
-    const uint32_t b = (__builtin_bit_cast(uint32_t, c) & 0x7ffffffeu) | (s != 0.f ? 1u : 0u);
+// What a tile does, as a word: E's 32 bits, the flag, and c without its sign (s == 1: not above zero, else not below),
+// whose last bit is s. c is rounded to 23 bits: up to 2^-23 of it a tile, either way, and as much of a state over the
+// 1 / |c| tiles that it remembers.
+__host__ __device__ __forceinline__ uint64_t word_of(float c, float s, float E) {
+    uint32_t b = __builtin_bit_cast(uint32_t, c) & 0x7fffffffu;
+    b += b >> 1 & 1;                                        // to even; below a sign bit that a NaN would carry into
+    b = ((b < 0x7fffffffu ? b : 0x7fffffffu) & 0x7ffffffeu) | (s != 0.f ? 1u : 0u);
     return (uint64_t)(b | 0x80000000u) << 32 | __builtin_bit_cast(uint32_t, E);
 }
-__device__ __forceinline__ void from_word(uint64_t w, float &c, float &s, float &E) {
+__host__ __device__ __forceinline__ void from_word(uint64_t w, float &c, float &s, float &E) {
     const uint32_t b = (uint32_t)(w >> 32);
     const float x = __builtin_bit_cast(float, b & 0x7ffffffeu);
     c = b & 1 ? -x : x;

@@ -1,0 +1,67 @@
+"""The words in which tiles of the gated linear recurrence hand over what they do to a state, on the CPU: the functions of
+csrc/glr_tiles.h compiled for the host."""
+from __future__ import annotations
+
+import ctypes
+import os
+import subprocess
+
+import numpy as np
+import pytest
+
+from chunked_kimi_delta_amd import build
+
+SOURCE = """
+#include "glr_tiles.h"
+extern "C" void words(const float *c, const float *s, const float *E, int64_t n, uint64_t *w, float *c2, float *s2, float *E2)
+{
+    for (int64_t i = 0; i < n; ++i) {
+        w[i] = glr::word_of(c[i], s[i], E[i]);
+        glr::from_word(w[i], c2[i], s2[i], E2[i]);
+    }
+}
+"""
+
+
+@pytest.fixture(scope="module")
+def words(tmp_path_factory):
+    d = tmp_path_factory.mktemp("words")
+    src, out = d / "words.hip", d / "words.so"
+    src.write_text(SOURCE)
+    subprocess.run([build.hipcc(), *build.HIPCC_FLAGS, "-I", build.CSRC, "-shared", str(src), "-o", str(out)], check=True,
+                   capture_output=True)
+    lib = ctypes.CDLL(os.fspath(out))
+
+    def call(c, s, E):
+        c, s, E = (np.ascontiguousarray(np.broadcast_to(np.asarray(x, np.float32), np.shape(c))) for x in (c, s, E))
+        w = np.zeros(len(c), np.uint64)
+        back = [np.zeros(len(c), np.float32) for _ in range(3)]
+        ptr = lambda a: a.ctypes.data_as(ctypes.c_void_p)
+        lib.words(ptr(c), ptr(s), ptr(E), ctypes.c_int64(len(c)), ptr(w), *map(ptr, back))
+        return (w, *back)
+    return call
+
+
+def test_maps_survive(words):
+    """c is e^g (s zero), or e^g - 1 (s one): to half a step of 23 bits, without a bias; s and E exactly."""
+    first = np.float32(0.4375).view(np.uint32)
+    bits = (first + np.arange(4096, dtype=np.uint32)).view(np.float32)
+    for s, c in ((0.0, bits), (1.0, -bits)):
+        E = np.linspace(-3e38, 3e38, len(c)).astype(np.float32)
+        w, c2, s2, E2 = words(c, s, E)
+        assert (w >> np.uint64(63) == 1).all() and (s2 == s).all() and (E2 == E).all()
+        step = 2.0 ** -25                                   # of 24 bits, at 0.4375
+        off = (c2.astype(np.float64) - c) / step
+        assert np.abs(off).max() <= 1.0 and abs(off.mean()) <= 1e-3
+    for c, s in ((0.0, 0.0), (1.0, 0.0), (0.0, 1.0), (-0.0, 1.0), (-0.5, 1.0), (-2.0 ** -100, 1.0), (2.0 ** 126, 0.0),
+                 (np.inf, 0.0)):
+        _, c2, s2, _ = words([c], s, 0.0)
+        assert c2[0] + s2[0] == c + s and (c2[0] == c or c == 0), (c, s)
+
+
+def test_numbers_that_are_none(words):
+    nans = np.array([0x7fc00000, 0x7fffffff, 0x7f800002, 0xffc00000, 0xffffffff, 0x7fc00001], np.uint32).view(np.float32)
+    w, c, _, E = words(nans, 0.0, nans)
+    assert (w >> np.uint64(63) == 1).all() and np.isnan(c).all() and np.isnan(E).all()
+    _, c, _, E = words(np.array([0.5, 0.5], np.float32), 0.0, np.array([np.inf, -np.inf], np.float32))
+    assert (E == [np.inf, -np.inf]).all() and (c == 0.5).all()
