@@ -32,8 +32,12 @@ struct Tiles {
 
 // What a tile does, as a word: E's 32 bits, the flag, and c without its sign (s == 1: not above zero, else not below),
 // whose last bit is s. c is rounded to 23 bits: up to 2^-23 of it a tile, either way, and as much of a state over the
-// 1 / |c| tiles that it remembers.
+// 1 / |c| tiles that it remembers. A slight growth in the form e^g - 1 > 0 has a sign that the word has no place for: e^g.
 __host__ __device__ __forceinline__ uint64_t word_of(float c, float s, float E) {
+    if (s != 0.f && c > 0.f) {
+        c += 1.f;
+        s = 0.f;
+    }
     uint32_t b = __builtin_bit_cast(uint32_t, c) & 0x7fffffffu;
     b += b >> 1 & 1;                                        // to even; below a sign bit that a NaN would carry into
     b = ((b < 0x7fffffffu ? b : 0x7fffffffu) & 0x7ffffffeu) | (s != 0.f ? 1u : 0u);

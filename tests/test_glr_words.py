@@ -65,3 +65,12 @@ def test_numbers_that_are_none(words):
     assert (w >> np.uint64(63) == 1).all() and np.isnan(c).all() and np.isnan(E).all()
     _, c, _, E = words(np.array([0.5, 0.5], np.float32), 0.0, np.array([np.inf, -np.inf], np.float32))
     assert (E == [np.inf, -np.inf]).all() and (c == 0.5).all()
+
+
+def test_a_slight_growth_does_not_become_a_decay(words):
+    """e^g - 1 above zero, as the least positive log decays and windows of them give it: a decay rounded to 24 bits (half a
+    step is 2^-24) and in the word to 23 (2^-23)."""
+    c = np.array([1e-12, 1e-9, 1.4e-8, 3e-8, 1.1e-7, 1e-6], np.float32)
+    _, c2, s2, _ = words(c, 1.0, 0.0)
+    a = c2.astype(np.float64) + s2
+    assert (a >= 1.0).all() and (np.abs(a - 1.0 - c) <= 2.0 ** -24 + 2.0 ** -23).all()
