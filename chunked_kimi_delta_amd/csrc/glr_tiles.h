@@ -13,8 +13,9 @@
 // only for tiles of its strip with lower numbers, which some running workgroup has begun. (One counter for all strips:
 // 185 -> 282 us for 21412 packed tokens of 4096 channels, raw.) A word holds its value
 // and its own flag (a sign bit that no value has), so nothing has to be ordered around it: stores and loads of 8
-// bytes at device scope, zeros before the launch. A wait gives up after SPINS polls (a tenth of a second) all the same,
-// so that a workspace that two calls share at once gives wrong results and not a hang.
+// bytes at device scope, zeros before the launch. A wait gives up after SPINS polls (a tenth of a second) all the same, so
+// that a workspace that two calls share at once, against the rules, does not hang: what has not come is taken as NaN,
+// and so are all states behind it.
 #pragma once
 
 #include "glr_scan.h"
@@ -53,6 +54,8 @@ __host__ __device__ __forceinline__ void from_word(uint64_t w, float &c, float &
 __device__ __forceinline__ void publish(uint64_t *p, uint64_t w) {
     __hip_atomic_store(p, w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
+// A word as it is, or NaN for one that was not published.
+__host__ __device__ __forceinline__ uint64_t met(uint64_t w) { return w >> 63 ? w : ~0ull; }
 // N maps of VEC channels for every lane that takes part: waits until all are published.
 template <int N, int VEC>
 __device__ __forceinline__ void await(const uint64_t *const (&p)[N], const bool (&on)[N], uint64_t (&w)[N][VEC]) {
@@ -69,6 +72,10 @@ __device__ __forceinline__ void await(const uint64_t *const (&p)[N], const bool 
             for (int v = 0; v < VEC; ++v) missing = missing || !(w[i][v] >> 63);
         if (__builtin_amdgcn_ballot_w64(missing) == 0) return;
     }
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) w[i][v] = met(w[i][v]);
 }
 
 // Slot -> (sequence, tile of it). Sequence s's tile t lies in slot floor(bos_s / tile) + s + t; the last

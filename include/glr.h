@@ -64,6 +64,8 @@ size_t glr_bwd_workspace_bytes(const glr_args *args);
 /* Enqueue the forward on `stream`: strips of channels that take a sequence in one workgroup each, or for
    long sequences tiles of 64 or 128 tokens that hand states to each other within the launch (they wait for tiles
    that have begun only). States and sums are fp32; results do not depend on the order in which tiles run.
+   A wait that is not met within about a tenth of a second, which only a workspace in use by another call
+   at once can bring about, ends with NaN in the states behind it (the call has returned KDA_OK by then).
    Tokens behind the last sequence are left as they were. D and the strides are at most 2^18. */
 kda_status glr_fwd(const glr_args *args, void *workspace, size_t ws_bytes, void *stream);
 

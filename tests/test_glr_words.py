@@ -20,6 +20,11 @@ extern "C" void words(const float *c, const float *s, const float *E, int64_t n,
         glr::from_word(w[i], c2[i], s2[i], E2[i]);
     }
 }
+extern "C" void given_up(uint64_t w, uint64_t *as, float *c, float *s, float *E)
+{
+    *as = glr::met(w);
+    glr::from_word(*as, *c, *s, *E);
+}
 """
 
 
@@ -39,6 +44,7 @@ def words(tmp_path_factory):
         ptr = lambda a: a.ctypes.data_as(ctypes.c_void_p)
         lib.words(ptr(c), ptr(s), ptr(E), ctypes.c_int64(len(c)), ptr(w), *map(ptr, back))
         return (w, *back)
+    call.lib = lib
     return call
 
 
@@ -74,3 +80,17 @@ def test_a_slight_growth_does_not_become_a_decay(words):
     _, c2, s2, _ = words(c, 1.0, 0.0)
     a = c2.astype(np.float64) + s2
     assert (a >= 1.0).all() and (np.abs(a - 1.0 - c) <= 2.0 ** -24 + 2.0 ** -23).all()
+
+
+def test_a_wait_that_gives_up_is_loud(words):
+    """What has not come stands for NaN, as a map and as a state; what has come stays as it is."""
+    def given_up(w):
+        u, f = ctypes.c_uint64(), [ctypes.c_float() for _ in range(3)]
+        words.lib.given_up(ctypes.c_uint64(w), ctypes.byref(u), *map(ctypes.byref, f))
+        return u.value, *(x.value for x in f)
+    w, c, s, E = given_up(0)
+    assert w >> 63 and np.isnan(c) and np.isnan(E) and not np.isfinite(np.float32(c) + np.float32(s))
+    (there, *_) = words(np.array([0.5], np.float32), 0.0, 3.0)
+    assert given_up(int(there[0])) == (int(there[0]), 0.5, 0.0, 3.0)
+    state = 1 << 63 | int(np.float32(-2.5).view(np.uint32))
+    assert given_up(state)[0] == state and given_up(state)[3] == -2.5
