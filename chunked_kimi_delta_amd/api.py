@@ -29,6 +29,12 @@ def _check(t: torch.Tensor, name: str, dtype, shape, device):
         raise ValueError(f"{name} must be contiguous")
 
 
+def _count(n: int, name: str):
+    """Sizes that the C ABI takes in 32 bits."""
+    if n > 2 ** 31 - 1:
+        raise ValueError(f"{name}: at most 2^31 - 1 (got {n})")
+
+
 def _call(fn, name, dev, stream, *args):
     """Enqueue on `stream` (default: torch's current stream of `dev`), with `dev` current."""
     raw = torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream.cuda_stream

@@ -7,7 +7,7 @@ import ctypes
 import torch
 
 from ._lib import GlrArgs, load
-from .api import _GATES, _IO, _call, _check, _on, _ptr
+from .api import _GATES, _IO, _call, _check, _count, _on, _ptr
 
 
 def _rows(t, name, dtype, shape, device):
@@ -32,6 +32,8 @@ def _arguments(x, g, beta, cu_seqlens, initial_state, use_beta_sigmoid, gate, A_
     dt, dev = g.dtype, g.device
     if dt not in _IO:
         raise TypeError(f"unsupported io dtype {dt} (bf16 or fp32)")
+    for n in g.shape:
+        _count(n, "B, T and D")
     if dev.type != "cuda":
         raise ValueError("inputs must be on a HIP device")
     if g.dim() != 3:
@@ -49,6 +51,7 @@ def _arguments(x, g, beta, cu_seqlens, initial_state, use_beta_sigmoid, gate, A_
         if not cu_seqlens.is_contiguous():
             raise ValueError("cu_seqlens must be contiguous")
         N, cu = cu_seqlens.numel() - 1, cu_seqlens.data_ptr()
+        _count(N, "sequences")
     if initial_state is not None:
         _check(initial_state, "initial_state", torch.float32, (N, D), dev)
         h0 = initial_state.data_ptr()
@@ -198,6 +201,7 @@ class GlrStepPlan:
     def __init__(self, x, g, state, beta=None, state_indices=None, y=None, use_beta_sigmoid=False, gate=None,
                  A_log=None, dt_bias=None, gate_lower_bound=-5.0):
         self.lib = load()
+        _count(state.shape[0], "slots")
         a = _arguments(x, g, beta, None, None, use_beta_sigmoid, gate, A_log, dt_bias, gate_lower_bound)
         self.device = g.device
         _check(state, "state", torch.float32, (state.shape[0], a.D), g.device)
