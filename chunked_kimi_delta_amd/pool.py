@@ -127,8 +127,8 @@ def pool_free(pools, used, indices):
 
 def pool_compact(pools, used, indices):
     """The used slots move to the front of every pool, into the free ones there (in order); where they were is
-    clear. indices (int32 [n], the slots of the rows in flight) are renumbered in place. Returns the number of used
-    slots, int32 [1] on the device."""
+    clear. indices (int32 [n], the slots of all rows in flight: a copy kept elsewhere goes stale) are renumbered in
+    place. Returns the number of used slots, int32 [1] on the device."""
     refs, n_pools, slots, dev = _pools(pools)
     slots, dev = _used(used, slots, dev)
     _indices(indices, "indices", dev)
