@@ -20,9 +20,9 @@ size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 kda_status check_shapes(const glr_args *a)
 {
     if (!a) return KDA_ERR_INVALID_ARG;
-    if (a->B < 1 || a->T < 0 || a->N < 0 || a->D < 1) return KDA_ERR_INVALID_ARG;
+    if (a->B < 1 || a->T < 0 || a->N < 1 || a->D < 1) return KDA_ERR_INVALID_ARG;
     if (a->cu_seqlens) {
-        if (a->B != 1 || a->N < 1 || !aligned(a->cu_seqlens, 8)) return KDA_ERR_INVALID_ARG;
+        if (a->B != 1 || !aligned(a->cu_seqlens, 8)) return KDA_ERR_INVALID_ARG;
     } else if (a->N != a->B) {
         return KDA_ERR_INVALID_ARG;
     }
@@ -72,7 +72,7 @@ int vec_of(const glr_args *a, bool x_read, const void *const *more, int n)
 // 7 x 512 + 16384 x 2048 125 and 66; lengths lie on the device, so raggedness is assumed.
 bool use_tiles(const glr_args *a)
 {
-    const int64_t tokens = (int64_t)a->B * a->T, mean = a->N > 0 ? tokens / a->N : 0;
+    const int64_t tokens = (int64_t)a->B * a->T, mean = tokens / a->N;
     const int64_t channels = (int64_t)a->N * a->D, cus = kda::current_device_cus();
     if (a->cu_seqlens && a->N > 1) return mean >= 1024 && tokens >= 8192;
     return channels < 64 * cus && mean >= (channels < 16 * cus ? 3584 : 2560);
@@ -154,7 +154,6 @@ kda_status glr_fwd(const glr_args *a, void *workspace, size_t ws_bytes, void *st
     if (!fits(a, s)) return KDA_ERR_UNSUPPORTED;
     const size_t need = glr_fwd_workspace_bytes(a);
     if (need && (!workspace || ws_bytes < need || !aligned(workspace, 256))) return KDA_ERR_WORKSPACE;
-    if (a->N == 0) return KDA_OK;
     const Params p = params_of(a, s);
     hipStream_t hs = (hipStream_t)stream;
     return (s.tiles ? launch_fwd_tiles(p, s, workspace, hs) : launch_fwd(p, s, hs)) == hipSuccess ? KDA_OK : KDA_ERR_HIP;
@@ -200,7 +199,7 @@ kda_status glr_bwd(const glr_args *a, const void *d_y, const float *dht, void *w
     q.part_A = (float *)ws;
     q.part_b = (float *)(ws + part);
     hipStream_t hs = (hipStream_t)stream;
-    if (a->N > 0 && (tiles ? launch_bwd_tiles(q, s, ws + 2 * part, hs) : launch_bwd(q, s, hs)) != hipSuccess) return KDA_ERR_HIP;
+    if ((tiles ? launch_bwd_tiles(q, s, ws + 2 * part, hs) : launch_bwd(q, s, hs)) != hipSuccess) return KDA_ERR_HIP;
     if (gated && launch_params(q, rows, dA_log, ddt_bias, hs) != hipSuccess) return KDA_ERR_HIP;
     return KDA_OK;
 }

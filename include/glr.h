@@ -56,8 +56,8 @@ typedef struct {
 } glr_args;
 
 /* Bytes of device workspace glr_fwd / glr_bwd need (only shapes, io, gate, whether beta and cu_seqlens
-   are there, and the current device's compute-unit count are read): may be 0, and is 0 for arguments that
-   the calls reject. Its contents need not be kept between calls. */
+   are there, and the current device's compute-unit count are read): may be 0, and is 0 where these are
+   invalid or unsupported by themselves. Its contents need not be kept between calls. */
 size_t glr_fwd_workspace_bytes(const glr_args *args);
 size_t glr_bwd_workspace_bytes(const glr_args *args);
 
