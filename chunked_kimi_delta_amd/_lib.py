@@ -62,6 +62,7 @@ class GlrArgs(ctypes.Structure):
         ("beta_sigmoid", ctypes.c_int32), ("gate", ctypes.c_int32),
         ("gate_lower_bound", ctypes.c_float),
         ("A_log", ctypes.c_void_p), ("dt_bias", ctypes.c_void_p),
+        ("x_batch", ctypes.c_int64), ("g_batch", ctypes.c_int64), ("beta_batch", ctypes.c_int64),
     ]
 
 

@@ -40,9 +40,11 @@ kda_status check_tensors(const glr_args *a, bool x_read)
         if ((x_read && !a->x) || !a->g || !a->y) return KDA_ERR_INVALID_ARG;
         if (!aligned(a->x, e) || !aligned(a->g, e) || !aligned(a->beta, e) || !aligned(a->y, e)) return KDA_ERR_INVALID_ARG;
         const int64_t strides[] = {x_read ? a->x_stride : a->D, a->g_stride, a->beta ? a->beta_stride : a->D};
-        for (int64_t s : strides) {
-            if (s < a->D) return KDA_ERR_INVALID_ARG;
-            if (s > MOST) return KDA_ERR_UNSUPPORTED;
+        const int64_t batches[] = {x_read ? a->x_batch : 0, a->g_batch, a->beta ? a->beta_batch : 0};
+        for (int i = 0; i < 3; ++i) {
+            if (strides[i] < a->D) return KDA_ERR_INVALID_ARG;
+            if (strides[i] > MOST) return KDA_ERR_UNSUPPORTED;
+            if (a->B > 1 && batches[i] != 0 && batches[i] < (a->T - 1) * strides[i] + a->D) return KDA_ERR_INVALID_ARG;
         }
     }
     if (!aligned(a->initial_state, 4) || !aligned(a->final_state, 4)) return KDA_ERR_INVALID_ARG;
@@ -57,9 +59,12 @@ kda_status check_tensors(const glr_args *a, bool x_read)
 int vec_of(const glr_args *a, bool x_read, const void *const *more, int n)
 {
     const uintptr_t e = a->io == KDA_FP32 ? 8 : 4;
-    bool two = a->D % 2 == 0 && a->g_stride % 2 == 0 && aligned(a->g, e) && aligned(a->y, e);
-    if (x_read) two = two && a->x_stride % 2 == 0 && aligned(a->x, e);
-    if (a->beta) two = two && a->beta_stride % 2 == 0 && aligned(a->beta, e);
+    auto even = [&](const void *p, int64_t stride, int64_t batch) {
+        return aligned(p, e) && stride % 2 == 0 && (a->B == 1 || batch % 2 == 0);
+    };
+    bool two = a->D % 2 == 0 && even(a->g, a->g_stride, a->g_batch) && aligned(a->y, e);
+    if (x_read) two = two && even(a->x, a->x_stride, a->x_batch);
+    if (a->beta) two = two && even(a->beta, a->beta_stride, a->beta_batch);
     for (int i = 0; i < n; ++i) two = two && aligned(more[i], e);
     return two ? 2 : 1;
 }
@@ -107,6 +112,10 @@ Params params_of(const glr_args *a, Shape s)
     p.xs = a->x_stride;
     p.gs = a->g_stride;
     p.bs = a->beta_stride;
+    auto beyond = [&](int64_t batch, int64_t stride) { return a->B > 1 && batch != 0 ? batch - a->T * stride : 0; };
+    p.xe = beyond(a->x_batch, a->x_stride);
+    p.ge = beyond(a->g_batch, a->g_stride);
+    p.be = beyond(a->beta_batch, a->beta_stride);
     p.h0 = a->initial_state;
     p.y = a->y;
     p.ht = a->final_state;

@@ -45,13 +45,13 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(sizeof(T
     // lane is row hi - 1 - tok - k, and rows before the sequence lie past every range (as unsigned
     // offsets below zero).
     const uint32_t ds = (uint32_t)p.D * E;
-    auto rows = [&](const void *base, int64_t stride, int64_t at, int64_t hi) {
-        return kda::rows_in((const T *)base + (bos + at) * stride, (int)(hi - at), stride, p.D);
+    auto rows = [&](const void *base, int64_t stride, int64_t at, int64_t hi, int64_t beyond = 0) {
+        return kda::rows_in((const T *)base + (bos + at) * stride + seq * beyond, (int)(hi - at), stride, p.D);
     };
     Raw<T, VEC> ng[K], nd[K];
     auto fetch = [&](int64_t s0) {
         const int64_t hi = n - s0, at = hi > STEP ? hi - STEP : 0;
-        const auto gr = rows(p.g, p.gs, at, hi), dr = rows(q.d_y, p.D, at, hi);
+        const auto gr = rows(p.g, p.gs, at, hi, p.ge), dr = rows(q.d_y, p.D, at, hi);
         const uint32_t row = (uint32_t)((int)(hi - at) - 1 - tok), gs = (uint32_t)p.gs * E;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
@@ -79,7 +79,7 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(sizeof(T
 #pragma unroll
         for (int k = 0; k < K; ++k) load(cy[k], yr, (uint32_t)yrow * ds + d * E - k * ds);
         if constexpr (BETA) {
-            const auto xr = rows(p.x, p.xs, at, hi), br = rows(p.beta, p.bs, at, hi);
+            const auto xr = rows(p.x, p.xs, at, hi, p.xe), br = rows(p.beta, p.bs, at, hi, p.be);
             const uint32_t xs = (uint32_t)p.xs * E, bs = (uint32_t)p.bs * E;
 #pragma unroll
             for (int k = 0; k < K; ++k) {

@@ -41,13 +41,13 @@ __global__ __launch_bounds__(64 * W) void scan_kernel(Params p)
 
     // offsets of this lane's first token in a step; a resource spans the step's rows
     const uint32_t xs = (uint32_t)p.xs * E, gs = (uint32_t)p.gs * E, bs = (uint32_t)p.bs * E, ys = (uint32_t)p.D * E;
-    auto rows = [&](const void *base, int64_t stride, int64_t s0) {
+    auto rows = [&](const void *base, int64_t stride, int64_t s0, int64_t beyond = 0) {
         const int64_t left = n - s0;
-        return kda::rows_in((const T *)base + (bos + s0) * stride, (int)(left < STEP ? left : STEP), stride, p.D);
+        return kda::rows_in((const T *)base + (bos + s0) * stride + seq * beyond, (int)(left < STEP ? left : STEP), stride, p.D);
     };
     Rows<T, VEC, BETA> next;
     auto fetch = [&](int64_t s0) {
-        const auto xr = rows(p.x, p.xs, s0), gr = rows(p.g, p.gs, s0);
+        const auto xr = rows(p.x, p.xs, s0, p.xe), gr = rows(p.g, p.gs, s0, p.ge);
         const uint32_t g0 = tok * gs + d * E, x0 = tok * xs + d * E;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
@@ -55,7 +55,7 @@ __global__ __launch_bounds__(64 * W) void scan_kernel(Params p)
             load(next.x[k], xr, x0 + k * xs);
         }
         if constexpr (BETA) {
-            const auto br = rows(p.beta, p.bs, s0);
+            const auto br = rows(p.beta, p.bs, s0, p.be);
             const uint32_t b0 = tok * bs + d * E;
 #pragma unroll
             for (int k = 0; k < K; ++k) load(next.b[k], br, b0 + k * bs);
@@ -131,11 +131,11 @@ __global__ __launch_bounds__(256) void step_kernel(StepParams p)
 #pragma unroll
         for (int v = 0; v < VEC; ++v) {
             if (live) {
-                float g = kda::to_f32(((const T *)p.f.g)[tok * p.f.gs + d + v]);
+                float g = kda::to_f32(((const T *)p.f.g)[tok * p.f.gs + b * p.f.ge + d + v]);
                 by_kind(p.f.pre.gate, [&](auto n) { g = gate[v].template active<T, decltype(n)::value>(g); });
-                float w = kda::to_f32(((const T *)p.f.x)[tok * p.f.xs + d + v]), c, s;
+                float w = kda::to_f32(((const T *)p.f.x)[tok * p.f.xs + b * p.f.xe + d + v]), c, s;
                 if (p.f.beta) {
-                    const float x = kda::to_f32(((const T *)p.f.beta)[tok * p.f.bs + d + v]);
+                    const float x = kda::to_f32(((const T *)p.f.beta)[tok * p.f.bs + b * p.f.be + d + v]);
                     w *= p.f.pre.beta_sigmoid ? logistic<T>(x) : x;
                 }
                 decay<T>(g, c, s);

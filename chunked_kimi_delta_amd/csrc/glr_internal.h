@@ -27,6 +27,7 @@ struct Params {
     int32_t D, strips;                  // strips: workgroups that share a sequence's channels
     const void *x, *g, *beta;           // beta: null for ones
     int64_t xs, gs, bs;                 // elements from one token to the next
+    int64_t xe, ge, be;                 // and from a dense batch's sequence to the next beyond T times as many
     const float *h0;
     void *y;
     float *ht;

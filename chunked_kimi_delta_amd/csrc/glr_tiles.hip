@@ -46,19 +46,19 @@ __global__ __launch_bounds__(64 * waves<BETA>()) void tile_kernel(Params p, Tile
     float start[VEC], h[VEC], out[VEC];
     if (have > 0) {
         const uint32_t xs = (uint32_t)p.xs * E, gs = (uint32_t)p.gs * E, bs = (uint32_t)p.bs * E, ys = (uint32_t)p.D * E;
-        auto rows = [&](const void *base, int64_t stride) {
-            return kda::rows_in((const T *)base + (bos + s0) * stride, have, stride, p.D);
+        auto rows = [&](const void *base, int64_t stride, int64_t beyond = 0) {
+            return kda::rows_in((const T *)base + (bos + s0) * stride + seq * beyond, have, stride, p.D);
         };
         Raw<T, VEC> rg[KT], rx[KT], rb[BETA ? KT : 1];
         {
-            const auto gr = rows(p.g, p.gs), xr = rows(p.x, p.xs);
+            const auto gr = rows(p.g, p.gs, p.ge), xr = rows(p.x, p.xs, p.xe);
             const uint32_t g0 = tok * gs + d * E, x0 = tok * xs + d * E;
 #pragma unroll
             for (int k = 0; k < KT; ++k) load(rg[k], gr, g0 + k * gs);
 #pragma unroll
             for (int k = 0; k < KT; ++k) load(rx[k], xr, x0 + k * xs);
             if constexpr (BETA) {
-                const auto br = rows(p.beta, p.bs);
+                const auto br = rows(p.beta, p.bs, p.be);
                 const uint32_t b0 = tok * bs + d * E;
 #pragma unroll
                 for (int k = 0; k < KT; ++k) load(rb[k], br, b0 + k * bs);

@@ -46,8 +46,8 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(4))) voi
     const bool last = hi <= TILE;                                               // (that is, its first token's tile)
     const int row = (int)(hi - at) - 1 - tok;                                   // of this lane's token 0, from row `at`
     const uint32_t ds = (uint32_t)p.D * E;
-    auto rows = [&](const void *base, int64_t stride, int64_t from) {
-        return kda::rows_in((const T *)base + (bos + from) * stride, (int)(hi - from), stride, p.D);
+    auto rows = [&](const void *base, int64_t stride, int64_t from, int64_t beyond = 0) {
+        return kda::rows_in((const T *)base + (bos + from) * stride + seq * beyond, (int)(hi - from), stride, p.D);
     };
     // rows before the sequence lie past every range, as unsigned offsets below zero
     auto fetch = [&](Raw<T, VEC> (&r)[KB], __amdgpu_buffer_rsrc_t b, int first, uint32_t stride) {
@@ -56,15 +56,15 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(4))) voi
         for (int k = 0; k < KB; ++k) load(r[k], b, o - k * stride);
     };
     Raw<T, VEC> rg[KB], rd[KB], ry[KB], rx[BETA ? KB : 1], rb[BETA ? KB : 1];
-    fetch(rg, rows(p.g, p.gs, at), row, (uint32_t)p.gs * E);
+    fetch(rg, rows(p.g, p.gs, at, p.ge), row, (uint32_t)p.gs * E);
     fetch(rd, rows(q.d_y, p.D, at), row, ds);
     // y of the row before: from row at - 1 on (from row 0 in the tile that has it)
     const int64_t yat = at > 0 ? at - 1 : 0;
     const int yrow = row - (at > 0 ? 0 : 1);
     fetch(ry, rows(p.y, p.D, yat), yrow, ds);
     if constexpr (BETA) {
-        fetch(rx, rows(p.x, p.xs, at), row, (uint32_t)p.xs * E);
-        fetch(rb, rows(p.beta, p.bs, at), row, (uint32_t)p.bs * E);
+        fetch(rx, rows(p.x, p.xs, at, p.xe), row, (uint32_t)p.xs * E);
+        fetch(rb, rows(p.beta, p.bs, at, p.be), row, (uint32_t)p.bs * E);
     }
     Gate gate[VEC];
     float start[VEC], first[VEC], m[VEC], out[VEC];

@@ -11,7 +11,8 @@ from .api import _GATES, _IO, _call, _check, _count, _on, _ptr
 
 
 def _rows(t, name, dtype, shape, device):
-    """Checks a tensor [B, T, D] whose tokens may be columns of wider rows; elements from token to token."""
+    """Checks a tensor [B, T, D] whose tokens may be columns of wider rows, of a longer batch; elements from token to
+    token, and from row to row of the batch (0: T tokens)."""
     if t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     if t.shape != shape:
@@ -19,12 +20,13 @@ def _rows(t, name, dtype, shape, device):
     if t.device != device:
         raise ValueError(f"{name}: expected device {device}, got {t.device}")
     if t.is_contiguous():
-        return shape[2]
+        return shape[2], 0
     B, T, D = shape
-    per = t.stride(1) if T > 1 else t.stride(0)     # from token to token; one token a row: from row to row
-    if (D > 1 and t.stride(2) != 1) or (B > 1 and t.stride(0) != T * per) or per < D:
-        raise ValueError(f"{name}: channels must be contiguous and tokens evenly spaced")
-    return per
+    per = t.stride(1) if T > 1 else D
+    batch = t.stride(0) if B > 1 else 0
+    if (D > 1 and t.stride(2) != 1) or per < D or (B > 1 and batch < (T - 1) * per + D):
+        raise ValueError(f"{name}: channels must be contiguous, tokens evenly spaced and rows of the batch one behind another")
+    return per, batch
 
 
 def _arguments(x, g, beta, cu_seqlens, initial_state, use_beta_sigmoid, gate, A_log, dt_bias, gate_lower_bound):
@@ -39,9 +41,9 @@ def _arguments(x, g, beta, cu_seqlens, initial_state, use_beta_sigmoid, gate, A_
     if g.dim() != 3:
         raise ValueError("x, g and beta must be [B, T, D]")
     B, T, D = shape = g.shape
-    gs = _rows(g, "g", dt, shape, dev)
-    xs = D if x is None else _rows(x, "x", dt, shape, dev)
-    bs = D if beta is None else _rows(beta, "beta", dt, shape, dev)
+    gs, gb = _rows(g, "g", dt, shape, dev)
+    xs, xb = (D, 0) if x is None else _rows(x, "x", dt, shape, dev)
+    bs, bb = (D, 0) if beta is None else _rows(beta, "beta", dt, shape, dev)
     if use_beta_sigmoid and beta is None:
         raise ValueError("use_beta_sigmoid needs beta")
     N, cu, h0 = B, None, None
@@ -68,7 +70,7 @@ def _arguments(x, g, beta, cu_seqlens, initial_state, use_beta_sigmoid, gate, A_
             bias = dt_bias.data_ptr()
     return GlrArgs(B, T, N, D, _IO[dt], None if x is None else x.data_ptr(), g.data_ptr(),
                    None if beta is None else beta.data_ptr(), xs, gs, bs, cu, h0, None, None,
-                   int(bool(use_beta_sigmoid)), _GATES[gate], float(gate_lower_bound), A, bias)
+                   int(bool(use_beta_sigmoid)), _GATES[gate], float(gate_lower_bound), A, bias, xb, gb, bb)
 
 
 def _like(g):
@@ -89,7 +91,7 @@ class GlrFwdPlan:
     h <- exp(g) h + beta x, y = h, with one state a channel.
 
     x, g, beta [B,T,D] (all bf16 or all fp32, on one HIP device; beta None: ones): g is the log decay.
-    They may be columns of wider rows (slices of one projection). cu_seqlens int64 [N+1] on the device
+    They may be columns of wider rows (slices of one projection) and some tokens of a longer batch. cu_seqlens int64 [N+1] on the device
     (then B == 1) or None; initial_state fp32 [N,D] or None. Outputs y (contiguous, like x) and
     final_state (fp32 [N,D], or None; may be initial_state) are allocated once and reused by every
     call(). Any D up to 2^18 and any length, zero included.

@@ -12,9 +12,9 @@
  * Conventions are kda_fwd.h's: device pointers, caller-owned; nothing is allocated, nothing
  * synchronises, results are deterministic (the numbers that a long sequence's tiles take are the only
  * atomics), errors only through the return value; concurrent calls use distinct workspaces and outputs.
- * A tensor's channels are contiguous. x, g and beta may be columns of wider
- * rows (x_stride and so on: elements from one token to the next); everything else is contiguous. io
- * tensors are aligned to their elements, fp32 tensors to 4 bytes, cu_seqlens to 8. A NaN or an
+ * A tensor's channels are contiguous. x, g and beta may be columns of wider rows (x_stride and so on:
+ * elements from one token to the next) and some tokens of a longer batch (x_batch and so on: from one
+ * sequence's first token to the next's); everything else is contiguous. io tensors are aligned to their elements, fp32 tensors to 4 bytes, cu_seqlens to 8. A NaN or an
  * infinity reaches its own channel of its own sequence, from its token on (in the backward: up to it).
  */
 #ifndef GLR_H
@@ -53,6 +53,9 @@ typedef struct {
     float gate_lower_bound;   /* KDA_GATE_BOUNDED: finite and < 0                                    */
     const float *A_log;       /* [D] fp32; required for a gate                                       */
     const float *dt_bias;     /* [D] fp32, or NULL for zeros                                         */
+    /* Dense batches: elements from one sequence's first token to the next's, at least (T - 1) token strides
+       and D; 0: T token strides. Not read for B == 1.                                               */
+    int64_t x_batch, g_batch, beta_batch;
 } glr_args;
 
 /* Bytes of device workspace glr_fwd / glr_bwd need (only shapes, io, gate, whether beta and cu_seqlens
@@ -66,7 +69,7 @@ size_t glr_bwd_workspace_bytes(const glr_args *args);
    that have begun only). States and sums are fp32; results do not depend on the order in which tiles run.
    A wait that is not met within about a tenth of a second, which only a workspace in use by another call
    at once can bring about, ends with NaN in the states behind it (the call has returned KDA_OK by then).
-   Tokens behind the last sequence are left as they were. D and the strides are at most 2^18. */
+   Tokens behind the last sequence are left as they were. D and the strides from token to token are at most 2^18. */
 kda_status glr_fwd(const glr_args *args, void *workspace, size_t ws_bytes, void *stream);
 
 /* Gradients of glr_fwd's inputs from the gradients of a loss with respect to y (d_y, like y) and to
