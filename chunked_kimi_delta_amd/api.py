@@ -29,10 +29,7 @@ def _check(t: torch.Tensor, name: str, dtype, shape, device):
         raise ValueError(f"{name} must be contiguous")
 
 
-def _count(n: int, name: str):
-    """Sizes that the C ABI takes in 32 bits."""
-    if n > 2 ** 31 - 1:
-        raise ValueError(f"{name}: at most 2^31 - 1 (got {n})")
+_INT32 = 2 ** 31 - 1         # sizes that the C ABI takes in 32 bits
 
 
 def _call(fn, name, dev, stream, *args):

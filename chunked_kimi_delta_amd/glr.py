@@ -7,7 +7,7 @@ import ctypes
 import torch
 
 from ._lib import GlrArgs, load
-from .api import _GATES, _IO, _call, _check, _count, _on, _ptr
+from .api import _GATES, _INT32, _IO, _call, _check, _on, _ptr
 
 
 def _rows(t, name, dtype, shape, device):
@@ -34,13 +34,13 @@ def _arguments(x, g, beta, cu_seqlens, initial_state, use_beta_sigmoid, gate, A_
     dt, dev = g.dtype, g.device
     if dt not in _IO:
         raise TypeError(f"unsupported io dtype {dt} (bf16 or fp32)")
-    for n in g.shape:
-        _count(n, "B, T and D")
-    if dev.type != "cuda":
-        raise ValueError("inputs must be on a HIP device")
     if g.dim() != 3:
         raise ValueError("x, g and beta must be [B, T, D]")
     B, T, D = shape = g.shape
+    if B > _INT32 or T > _INT32 or D > _INT32:
+        raise ValueError(f"B, T and D are at most 2^31 - 1 (got {B}, {T}, {D})")
+    if dev.type != "cuda":
+        raise ValueError("inputs must be on a HIP device")
     gs, gb = _rows(g, "g", dt, shape, dev)
     xs, xb = (D, 0) if x is None else _rows(x, "x", dt, shape, dev)
     bs, bb = (D, 0) if beta is None else _rows(beta, "beta", dt, shape, dev)
@@ -53,7 +53,8 @@ def _arguments(x, g, beta, cu_seqlens, initial_state, use_beta_sigmoid, gate, A_
         if not cu_seqlens.is_contiguous():
             raise ValueError("cu_seqlens must be contiguous")
         N, cu = cu_seqlens.numel() - 1, cu_seqlens.data_ptr()
-        _count(N, "sequences")
+        if N > _INT32:
+            raise ValueError(f"at most 2^31 - 1 sequences (got {N})")
     if initial_state is not None:
         _check(initial_state, "initial_state", torch.float32, (N, D), dev)
         h0 = initial_state.data_ptr()
@@ -68,9 +69,12 @@ def _arguments(x, g, beta, cu_seqlens, initial_state, use_beta_sigmoid, gate, A_
         if dt_bias is not None:
             _check(dt_bias, "dt_bias", torch.float32, (D,), dev)
             bias = dt_bias.data_ptr()
-    return GlrArgs(B, T, N, D, _IO[dt], None if x is None else x.data_ptr(), g.data_ptr(),
-                   None if beta is None else beta.data_ptr(), xs, gs, bs, cu, h0, None, None,
-                   int(bool(use_beta_sigmoid)), _GATES[gate], float(gate_lower_bound), A, bias, xb, gb, bb)
+    a = GlrArgs(B, T, N, D, _IO[dt], None if x is None else x.data_ptr(), g.data_ptr(),
+                None if beta is None else beta.data_ptr(), xs, gs, bs, cu, h0, None, None,
+                int(bool(use_beta_sigmoid)), _GATES[gate], float(gate_lower_bound), A, bias)
+    if xb or gb or bb:
+        a.x_batch, a.g_batch, a.beta_batch = xb, gb, bb
+    return a
 
 
 def _like(g):
@@ -203,7 +207,8 @@ class GlrStepPlan:
     def __init__(self, x, g, state, beta=None, state_indices=None, y=None, use_beta_sigmoid=False, gate=None,
                  A_log=None, dt_bias=None, gate_lower_bound=-5.0):
         self.lib = load()
-        _count(state.shape[0], "slots")
+        if state.shape[0] > _INT32:
+            raise ValueError(f"at most 2^31 - 1 slots (got {state.shape[0]})")
         a = _arguments(x, g, beta, None, None, use_beta_sigmoid, gate, A_log, dt_bias, gate_lower_bound)
         self.device = g.device
         _check(state, "state", torch.float32, (state.shape[0], a.D), g.device)

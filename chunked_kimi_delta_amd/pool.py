@@ -13,7 +13,7 @@ import ctypes
 import torch
 
 from ._lib import PoolRef, load
-from .api import _call, _check, _count, _ptr
+from .api import _INT32, _call, _check, _ptr
 
 
 def _pools(pools, device=None):
@@ -25,12 +25,14 @@ def _pools(pools, device=None):
     for r, p in zip(refs, pools):
         if p.dim() < 1 or not p.is_contiguous():
             raise ValueError("a pool must be contiguous, [slots, ...]")
-        _count(p.shape[0], "slots")
-        if p.device.type != "cuda" or (device is not None and p.device != device):
+        n, d = p.shape[0], p.device
+        if n > _INT32:
+            raise ValueError(f"at most 2^31 - 1 slots (got {n})")
+        if d.type != "cuda" or (device is not None and d != device):
             raise ValueError("pools must be on one HIP device")
-        if slots is not None and p.shape[0] != slots:
+        if slots is not None and n != slots:
             raise ValueError("pools of one call must have one number of slots")
-        slots, device = p.shape[0], p.device
+        slots, device = n, d
         r.data = p.data_ptr()
         size = p.numel() // slots if slots else 1
         r.bytes = size * p.element_size()
@@ -49,8 +51,10 @@ def _sources(sources, pools):
         raise ValueError("as many sources as pools are needed")
     for s, p in zip(sources, pools):
         _check(s, "sources", p.dtype, (sources[0].shape[0], *p.shape[1:]), p.device)
-    _count(sources[0].shape[0], "slots of the sources")
-    return (ctypes.c_void_p * len(sources))(*(s.data_ptr() for s in sources)), sources[0].shape[0]
+    n = sources[0].shape[0]
+    if n > _INT32:
+        raise ValueError(f"sources: at most 2^31 - 1 slots (got {n})")
+    return (ctypes.c_void_p * len(sources))(*(s.data_ptr() for s in sources)), n
 
 
 def _indices(t, name, device, n=None):
@@ -60,7 +64,8 @@ def _indices(t, name, device, n=None):
 def _used(used, slots, device):
     if slots is None:                       # no pools
         slots, device = used.numel(), used.device
-        _count(slots, "slots")
+        if slots > _INT32:
+            raise ValueError(f"at most 2^31 - 1 slots (got {slots})")
         if device.type != "cuda":
             raise ValueError("used must be on a HIP device")
     _check(used, "used", torch.bool, (slots,), device)
