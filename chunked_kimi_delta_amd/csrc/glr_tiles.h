@@ -116,17 +116,18 @@ struct Shared {
 };
 
 // One map after another, for the map of all: decays as a product, and as distances from 1, which are exact
-// enough where the product is near it.
+// enough where the product is near it and no factor is above 1 (e^32 e^-32 - 1 by way of e^32 has no digit left).
 struct Chain {
-    float A = 1.f, D = 0.f, E = 0.f;
+    float A = 1.f, D = 0.f, E = 0.f, most = 0.f;
     __device__ __forceinline__ void then(float c, float s, float e) {
         E = fmaf(c, E, fmaf(s, E, e));
         const float d = s != 0.f ? c : c - 1.f;
         D = fmaf(D, d, D + d);
+        most = fmaxf(most, d);
         A *= s != 0.f ? 1.f + c : c;
     }
     __device__ __forceinline__ uint64_t word() const {
-        const bool slow = A >= 0.625f && A <= 1.f;          // then every factor was (c, 1)
+        const bool slow = A >= 0.625f && most <= 0.f;       // then every factor was (c, 1), c <= 0
         return word_of(slow ? D : A, slow ? 1.f : 0.f, E);
     }
 };
