@@ -73,8 +73,12 @@ int vec_of(const glr_args *a, bool x_read, const void *const *more, int n)
 // call, tiles 18), and the better of the two wherever strips of 64 channels fill the device; narrower ones take longer, and
 // a packed batch's longest sequence takes its time alone. bf16, us, strips and tiles: 4 x 4096 tokens x 4096 channels 86 and 98
 // (gradients 147 and 149, raw 247 and 273); 2560 x 4096 21 and 24 (28 and 27, raw 73 and 60), 3300 x 4096 24 and 29 (51 and 36, raw 92
-// and 76), 7000 x 4096 68 and 50; 3300 x 2048 19 and 19 (28 and 23), 16384 x 1000 83 and 38. Packed, 16 x 2048 tokens x 4096 183 and 185,
-// 7 x 512 + 16384 x 2048 125 and 66; lengths lie on the device, so raggedness is assumed.
+// and 76), 7000 x 4096 68 and 50; 3300 x 2048 19 and 19 (28 and 23), 16384 x 1000 83 and 38. One switch for the forward and the
+// gradients, so near it one of them is a fifth from its better side (forward of 3300 x 4096, gradients of 3300 x 2048).
+// Packed, 16 x 2048 tokens x 4096 183 and 185, 7 x 512 + 16384 x 2048 125 and 66, 32 x 512 x 2048 37 and 45 (gradients 73 and 79, raw
+// 121 and 145). Lengths lie on the device, and the mean stands for them: a batch of one long sequence among many short ones
+// takes strips and the long one's time, 8000 + 31 x 100 x 2048 141 and 42 (gradients 240 and 54, raw 430 and 115), 32768 + 63 x 1
+// x 2048 564 and 118.
 bool use_tiles(const glr_args *a)
 {
     const int64_t tokens = (int64_t)a->B * a->T, mean = tokens / a->N;

@@ -98,7 +98,9 @@ class GlrFwdPlan:
     They may be columns of wider rows (slices of one projection) and some tokens of a longer batch. cu_seqlens int64 [N+1] on the device
     (then B == 1) or None; initial_state fp32 [N,D] or None. Outputs y (contiguous, like x) and
     final_state (fp32 [N,D], or None; may be initial_state) are allocated once and reused by every
-    call(). Any D up to 2^18 and any length, zero included.
+    call(). Any D up to 2^18 and any length, zero included, in fewer than 2^23 pieces: sequences times
+    ceil(D / 64) channels, or for long sequences 64 tokens of 64 channels (2^35 values). What infinities and log
+    decays above zero give, and how far fp32 outputs err, is in include/glr.h.
 
     Pre-stage, done inside the kernels: use_beta_sigmoid takes beta as logits; gate "softplus"
     (g <- -exp(A_log) softplus(g + dt_bias)) or "bounded" (g <- gate_lower_bound * sigmoid(exp(A_log)

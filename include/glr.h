@@ -14,8 +14,17 @@
  * atomics), errors only through the return value; concurrent calls use distinct workspaces and outputs.
  * A tensor's channels are contiguous. x, g and beta may be columns of wider rows (x_stride and so on:
  * elements from one token to the next) and some tokens of a longer batch (x_batch and so on: from one
- * sequence's first token to the next's); everything else is contiguous. io tensors are aligned to their elements, fp32 tensors to 4 bytes, cu_seqlens to 8. A NaN or an
- * infinity reaches its own channel of its own sequence, from its token on (in the backward: up to it).
+ * sequence's first token to the next's); everything else is contiguous. io tensors are aligned to their
+ * elements, fp32 tensors to 4 bytes, cu_seqlens to 8.
+ *
+ * Numbers. A NaN or an infinity reaches its own channel of its own sequence, from its token on (in the
+ * backward: up to it). Behind its token an infinity is an infinity or a NaN: decays are applied as e^g - 1 and
+ * as products, so that e^g times infinity may come out as infinity minus infinity or zero times it.
+ * Log decays above zero are taken too, with e^g rounded to 24 bits, while their sums over up to 1024
+ * neighbouring tokens stay below 88; beyond, where e^88 overflows, states may become NaN even where they are
+ * zero. Final states, dh0, dA_log and ddt_bias are fp32 for either io and err by about 1e-7 of themselves; for
+ * bf16 io a channel that decays by about 2^-8 a token for long may err by up to 2^-17. The last bits of a
+ * channel may depend on the decays of the channels beside it (which form of a decay a wave takes).
  */
 #ifndef GLR_H
 #define GLR_H
@@ -69,7 +78,9 @@ size_t glr_bwd_workspace_bytes(const glr_args *args);
    that have begun only). States and sums are fp32; results do not depend on the order in which tiles run.
    A wait that is not met within about a tenth of a second, which only a workspace in use by another call
    at once can bring about, ends with NaN in the states behind it (the call has returned KDA_OK by then).
-   Tokens behind the last sequence are left as they were. D and the strides from token to token are at most 2^18. */
+   Tokens behind the last sequence are left as they were. D and the strides from token to token are at most 2^18.
+   A launch has fewer than 2^23 workgroups, or the call is KDA_ERR_UNSUPPORTED: about N ceil(D / 64) for strips where
+   sequences are many, at most (B T / 64 + N) ceil(D / 64) for tiles. */
 kda_status glr_fwd(const glr_args *args, void *workspace, size_t ws_bytes, void *stream);
 
 /* Gradients of glr_fwd's inputs from the gradients of a loss with respect to y (d_y, like y) and to
