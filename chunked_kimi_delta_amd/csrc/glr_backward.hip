@@ -8,8 +8,8 @@
 // are fp32 over a lane's tokens of a step or tile (8 or 16, which its registers hold), fp64 over a sequence's steps and waves (a
 // tile's waves), rounded to an fp32 row a sequence (a tile) and added in fp64 by a second launch of a workgroup for 64
 // channels. bf16, us: 8 x 1000 tokens x 2048 channels 40 (4.1 TB/s), raw with the gate's gradients 70 (3.7 TB/s; vector
-// instructions 57% of the SIMDs' time, with 1.7 waves on one: 512 workgroups' registers). 708 packed tokens x 512 channels fp32 raw:
-// 13.0 + 3.8, two steps of the longest sequence and a launch.
+// instructions 57% of the SIMDs' time, with 1.6 waves on one: 512 workgroups' registers). 708 packed tokens x 512 channels fp32 raw:
+// 13.5 + 3.9, two steps of the longest sequence and a launch.
 #include "glr_scan.h"
 
 namespace glr {

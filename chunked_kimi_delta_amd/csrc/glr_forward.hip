@@ -5,7 +5,7 @@
 // four of the scan's own, so bytes and instructions are of a size: 32 x 500 tokens x 2048 channels fp32 82 us (4.8 TB/s, 93% of
 // what a copy reaches), 8 x 2048 x 4096 bf16 93 us (4.3 TB/s), raw 129 (4.2). Where strips are few it is a step's own time, 2.5 to 4 us
 // for loads, the groups' scan, a barrier and the chain over the waves: 2048 x 2048 in 13 us. Kernel alone, 70 tokens of 256
-// channels, raw: 4.8 us, two memory latencies.
+// channels, raw: 5.2 us, two memory latencies.
 //
 // The step: a state is read and written once, by a thread of its own for all tokens of the call. 64 rows x 4096 channels 4.2 us
 // (1 row x 2048 3.4): latency of index, state and inputs; the call takes 11.

@@ -1,10 +1,10 @@
 // glr_tiles.hip -- the forward of the gated linear recurrence in tiles (glr_tiles.h). The
 // mathematics is glr_forward.hip's.
 //
-// 131072 tokens x 2048 channels bf16: 370 us (4.35 TB/s, 84% of what a copy reaches; strips, 16 channels a workgroup, 943): each byte
+// 131072 tokens x 2048 channels bf16: 375 us (4.3 TB/s, 83% of what a copy reaches; strips, 16 channels a workgroup, 943): each byte
 // once (1.19 GB in, 0.57 out, words of the tiles among them), 3.6 waves on a SIMD, which wait 59% of their time, for inputs first
-// and then for each other's words (about 2 us a tile). 21412 packed tokens x 4096 channels with raw gates 177 us: vector
-// instructions fill 69% of the SIMDs' time (48 a value). A workgroup that fetched its next tile ahead of its hand-over
+// and then for each other's words (about 2 us a tile). 21412 packed tokens x 4096 channels with raw gates 179 us: vector
+// instructions fill 70% of the SIMDs' time (49 a value). A workgroup that fetched its next tile ahead of its hand-over
 // took 550 us for the former: half the workgroups for its registers. Tiles of half the tokens 450, of words that wait
 // for the window's before them (no spans) 480.
 #include "glr_tiles.h"

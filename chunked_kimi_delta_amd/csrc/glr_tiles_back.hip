@@ -1,7 +1,7 @@
 // glr_tiles_back.hip -- the gradients of the gated linear recurrence in tiles (glr_tiles.h): glr_backward.hip's
 // mathematics, tiles and tokens counted from a sequence's end.
 //
-// 4 x 8192 tokens x 4096 channels bf16 281 us (4.75 TB/s, 92% of what a copy reaches), 4096 x 2048 21 + 2 us for the cleared words
+// 4 x 8192 tokens x 4096 channels bf16 284 us (4.7 TB/s, 91% of what a copy reaches), 4096 x 2048 22 + 2 us for the cleared words
 // (84 MB: two rounds of tiles, whose first loads and last stores overlap with nothing), fp32 8192 x 2048 71 us (4.7 TB/s).
 #include "glr_tiles.h"
 
