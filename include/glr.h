@@ -77,7 +77,8 @@ size_t glr_bwd_workspace_bytes(const glr_args *args);
    long sequences tiles of 64 or 128 tokens that hand states to each other within the launch (they wait for tiles
    that have begun only). States and sums are fp32; results do not depend on the order in which tiles run.
    A wait that is not met within about a tenth of a second, which only a workspace in use by another call
-   at once can bring about, ends with NaN in the states behind it (the call has returned KDA_OK by then).
+   at once or decreasing offsets can bring about, ends with NaN in the states behind it (the call has
+   returned KDA_OK by then). Outputs overlap no inputs but final_state its initial_state.
    Tokens behind the last sequence are left as they were. D and the strides from token to token are at most 2^18.
    A launch has fewer than 2^23 workgroups, or the call is KDA_ERR_UNSUPPORTED: about N ceil(D / 64) for strips where
    sequences are many, at most (B T / 64 + N) ceil(D / 64) for tiles. */
@@ -90,7 +91,7 @@ kda_status glr_fwd(const glr_args *args, void *workspace, size_t ws_bytes, void 
      dbeta             likewise; with beta only
      dh0               [N, D] fp32, or NULL to skip; may be the buffer of dht
      dA_log, ddt_bias  [D] fp32: with a gate, dA_log required, ddt_bias or NULL; ignored without
-   Deterministic. Tokens behind the last sequence are left as they were. */
+   Deterministic. Tokens behind the last sequence are left as they were. Outputs overlap no inputs but dh0 its dht. */
 kda_status glr_bwd(const glr_args *args, const void *d_y, const float *dht, void *workspace, size_t ws_bytes,
                    void *dx, void *dg, void *dbeta, float *dh0, float *dA_log, float *ddt_bias, void *stream);
 
